@@ -37,7 +37,10 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_set_kernel_events", "bdla_fwd_noalloc", "bdla_noalloc_read_status",
            "bdla_set_seq_split", "bdla_decode", "bdla_set_wait_limit_ns", "bdla_set_test_stall",
            "bdla_workspace_bytes_vec", "bdla_fwd_vec", "bdla_bwd_vec", "bdla_workspace_bytes_delta",
-           "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes")
+           "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes",
+           "bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
+           "bdla_attn_cached", "bdla_workspace_bytes_attn")
+ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED = 0, 1, 2, 3, 4
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
 STALL_NONE, STALL_PRODUCER, STALL_MMA, STALL_EPILOGUE = 0, 1, 2, 3
 
@@ -51,6 +54,25 @@ class BdlaError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int)]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("d", ctypes.c_int)]
+
+
+class QkNormArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("base", ctypes.c_double), ("eps", ctypes.c_float),
+                ("rotary", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_docs", ctypes.c_int)]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page", ctypes.c_int),
+                ("max_pages", ctypes.c_int)]
 
 
 _lib = None
@@ -113,6 +135,17 @@ def lib():
         L.bdla_tile_states_bytes.argtypes = [Dims, ci]
         L.bdla_tile_states_bytes.restype = sz
         L.bdla_bwd_delta.restype = ci
+        L.bdla_qk_norm.argtypes = [QkNormArgs, vp, vp, AttnDims, vp]
+        L.bdla_qk_norm_bwd.argtypes = [QkNormArgs, vp, vp, ci, vp, vp, vp, vp, AttnDims, vp, sz, vp]
+        L.bdla_attn_fwd.argtypes = [vp, vp, vp, vp, ci, f32, vp, vp, AttnDims, vp, sz, vp]
+        L.bdla_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, f32, vp, vp, vp, AttnDims, vp, sz, vp]
+        L.bdla_cache_append.argtypes = [vp, vp, CacheArgs, vp, vp, AttnDims, vp, sz, vp]
+        L.bdla_attn_cached.argtypes = [vp, CacheArgs, vp, f32, vp, vp, AttnDims, vp, sz, vp]
+        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
+                     "bdla_attn_cached"):
+            getattr(L, name).restype = ci
+        L.bdla_workspace_bytes_attn.argtypes = [ci, AttnDims, ci, ctypes.c_int64]
+        L.bdla_workspace_bytes_attn.restype = sz
         del i32
         _lib = L
     return _lib
@@ -554,3 +587,228 @@ def bwd_delta(q, k, v, a, beta, dO, b: float = -5.0, h0=None, dhT=None, cu_seqle
     if st:
         raise BdlaError(st, "bdla_bwd_delta")
     return dq, dk_, dv_, da, dbeta, dh0
+
+
+# ---------------------------------------------------------------- softmax layer
+def _on(t: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
+    """A contiguous CUDA tensor of this type and shape, on the device of `like`."""
+    _check(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _new(shapes, dtypes, device, stream):
+    """Outputs that belong to the stream the call runs on."""
+    if stream is None:
+        return [torch.empty(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
+
+
+def _attn_ws(op, d: AttnDims, n_docs, max_keys, ws, device, stream) -> Workspace:
+    need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
+    if need == 0:
+        raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_attn")
+    if ws is not None and need <= ws.nbytes:
+        return ws
+    if stream is None:
+        return Workspace(need, device) if ws is None else ws.ensure(need)
+    with torch.cuda.stream(stream):
+        return Workspace(need, device) if ws is None else ws.ensure(need)
+
+
+def _documents(cu_seqlens, B, like):
+    if cu_seqlens is None:
+        return 0
+    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if cu_seqlens.device != like.device:
+        raise ValueError("cu_seqlens is on another device")
+    if B != 1:
+        raise ValueError("packed documents need B = 1")
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens needs at least two offsets")
+    return cu_seqlens.numel() - 1
+
+
+def _strided(t: torch.Tensor, name: str):
+    """Element strides (token, head) of a [B, T, H, d] tensor whose features are
+    contiguous and whose batch rows follow each other."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{name} must be bf16 [B, T, H, d]")
+    B, T, H, d = t.shape
+    sb, st, sh, sd = t.stride()
+    if d > 1 and sd != 1:
+        raise ValueError(f"{name}: features must be contiguous")
+    if T == 1:
+        st = sb   # one token a row: the batch stride steps from token to token
+    elif B > 1 and sb != T * st:
+        raise ValueError(f"{name}: batch rows must follow each other (batch stride = T * token stride)")
+    return st, (sh if H > 1 else d)
+
+
+def _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps):
+    qt, qh = _strided(q, "q")
+    kt, kh = _strided(k, "k")
+    B, T, Hq, d = q.shape
+    if k.shape[0] != B or k.shape[1] != T or k.shape[3] != d:
+        raise ValueError("q and k shapes disagree")
+    if k.device != q.device:
+        raise ValueError("q and k are on different devices")
+    _on(wq, "wq", torch.float32, (d,), q)
+    _on(wk, "wk", torch.float32, (d,), q)
+    n_docs = _documents(cu_seqlens, B, q)
+    if positions is not None:
+        _on(positions, "positions", torch.int32, (B, T), q)
+    a = QkNormArgs(q.data_ptr(), k.data_ptr(), qt, qh, kt, kh, wq.data_ptr(), wk.data_ptr(),
+                   None if positions is None else positions.data_ptr(),
+                   None if cu_seqlens is None else cu_seqlens.data_ptr(), base, eps,
+                   d if rotary is None else rotary, int(interleaved), n_docs)
+    return a, AttnDims(B, T, Hq, k.shape[2], d)
+
+
+def qk_norm(q, k, wq, wk, rotary: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
+            positions=None, cu_seqlens=None, eps: float = 1e-6, stream=None):
+    """RMS norm of every head of q [B, T, Hq, d] and k [B, T, Hk, d] (bf16; views
+    of one projection are fine) with weights wq, wk (fp32 [d]), then the
+    rotation of the first `rotary` features (all by default, 0 for none) by
+    the token's position: `positions` (int32 [B, T]), or its index in its
+    document.  Returns (qn, kn), contiguous.  Inputs used on another stream
+    than their own are the caller's to keep alive, as for every call here."""
+    a, d = _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
+    qn, kn = _new((q.shape, k.shape), (q.dtype, q.dtype), q.device, stream)
+    st = lib().bdla_qk_norm(a, _p(qn), _p(kn), d, _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_qk_norm")
+    return qn, kn
+
+
+def qk_norm_bwd(q, k, wq, wk, dqn, dkn, rotary: Optional[int] = None, base: float = 10000.0,
+                interleaved: bool = False, positions=None, cu_seqlens=None, eps: float = 1e-6,
+                ws: Optional[Workspace] = None, stream=None):
+    """Gradient of qk_norm at the same inputs; dqn, dkn both bf16 or both fp32.
+    Returns (dq, dk, dwq, dwk): bf16, bf16 and fp32 [d]."""
+    a, d = _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
+    code = _dtype_code(dqn.dtype)
+    _on(dqn, "dqn", dqn.dtype, q.shape, q)
+    _on(dkn, "dkn", dqn.dtype, k.shape, q)
+    bf, f32 = torch.bfloat16, torch.float32
+    dq, dk, dwq, dwk = _new((q.shape, k.shape, wq.shape, wk.shape), (bf, bf, f32, f32), q.device, stream)
+    ws = _attn_ws(ATTN_NORM_BWD, d, a.n_docs, 0, ws, q.device, stream)
+    st = lib().bdla_qk_norm_bwd(a, _p(dqn), _p(dkn), code, _p(dq), _p(dk), _p(dwq), _p(dwk), d, ws.ptr, ws.nbytes,
+                                _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_qk_norm_bwd")
+    return dq, dk, dwq, dwk
+
+
+def _attn_dims(q, k, v):
+    _check(q, "q", torch.bfloat16, 4)
+    B, T, Hq, d = q.shape
+    _check(k, "k", torch.bfloat16, 4)
+    Hk = k.shape[2]
+    _on(k, "k", torch.bfloat16, (B, T, Hk, d), q)
+    _on(v, "v", torch.bfloat16, (B, T, Hk, d), q)
+    return AttnDims(B, T, Hq, Hk, d)
+
+
+def attn_fwd(q, k, v, scale: Optional[float] = None, cu_seqlens=None, ws: Optional[Workspace] = None, stream=None):
+    """Causal softmax attention of whole documents: q [B, T, Hq, d], k and v
+    [B, T, Hk, d] bf16, Hq a multiple of Hk; packed documents with B = 1 and
+    cu_seqlens.  scale is 1/sqrt(d) unless given.  Returns (o, lse): o like q,
+    lse fp32 [Hq, B*T]."""
+    d = _attn_dims(q, k, v)
+    n_docs = _documents(cu_seqlens, d.B, q)
+    o, lse = _new((q.shape, (d.Hq, d.B * d.T)), (q.dtype, torch.float32), q.device, stream)
+    ws = _attn_ws(ATTN_FWD, d, n_docs, 0, ws, q.device, stream)
+    st = lib().bdla_attn_fwd(_p(q), _p(k), _p(v), _p(cu_seqlens), n_docs, d.d ** -0.5 if scale is None else scale,
+                             _p(o), _p(lse), d, ws.ptr, ws.nbytes, _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_attn_fwd")
+    return o, lse
+
+
+def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None, ws: Optional[Workspace] = None,
+             stream=None):
+    """Gradient of attn_fwd from its inputs, its (o, lse) and dO like o.
+    Returns (dq, dk, dv), bf16.  The same inputs give the same bits."""
+    d = _attn_dims(q, k, v)
+    _on(o, "o", torch.bfloat16, q.shape, q)
+    _on(dO, "dO", torch.bfloat16, q.shape, q)
+    _on(lse, "lse", torch.float32, (d.Hq, d.B * d.T), q)
+    n_docs = _documents(cu_seqlens, d.B, q)
+    dq, dk, dv = _new((q.shape, k.shape, v.shape), (q.dtype,) * 3, q.device, stream)
+    ws = _attn_ws(ATTN_BWD, d, n_docs, 0, ws, q.device, stream)
+    st = lib().bdla_attn_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(dO), _p(cu_seqlens), n_docs,
+                             d.d ** -0.5 if scale is None else scale, _p(dq), _p(dk), _p(dv), d, ws.ptr, ws.nbytes,
+                             _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_attn_bwd")
+    return dq, dk, dv
+
+
+def _cache_args(kcache, vcache, pages, lens, B, like):
+    _check(kcache, "kcache", torch.bfloat16, 4)
+    _on(vcache, "vcache", torch.bfloat16, kcache.shape, like)
+    _check(pages, "pages", torch.int32, 2)
+    _on(pages, "pages", torch.int32, (B, pages.shape[1]), like)
+    _on(lens, "lens", torch.int32, (B,), like)
+    if kcache.device != like.device:
+        raise ValueError("kcache is on another device")
+    return CacheArgs(kcache.data_ptr(), vcache.data_ptr(), pages.data_ptr(), lens.data_ptr(), kcache.shape[0],
+                     kcache.shape[1], pages.shape[1])
+
+
+def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: Optional[Workspace] = None,
+                 stream=None):
+    """Writes k, v [B, T, Hk, d] into the paged cache (kcache, vcache
+    [n_pages, page, Hk, d]) behind each sequence's lens[b] tokens: the rows
+    0 .. T - 1, or the first counts[b] of rows[b] (int32 [B], [B, T]), which is
+    how a verified tree's accepted drafts are made consecutive.  pages is the
+    int32 page table [B, max_pages]; lens is left as it is."""
+    _check(k, "k", torch.bfloat16, 4)
+    B, T, Hk, d = k.shape
+    _on(v, "v", torch.bfloat16, k.shape, k)
+    c = _cache_args(kcache, vcache, pages, lens, B, k)
+    if tuple(kcache.shape[2:]) != (Hk, d):
+        raise ValueError("kcache must be [n_pages, page, Hk, d] with the heads of k")
+    if rows is not None:
+        _on(rows, "rows", torch.int32, (B, T), k)
+    if counts is not None:
+        _on(counts, "counts", torch.int32, (B,), k)
+    dims = AttnDims(B, T, Hk, Hk, d)
+    ws = _attn_ws(ATTN_APPEND, dims, 0, 0, ws, k.device, stream)
+    st = lib().bdla_cache_append(_p(k), _p(v), c, _p(rows), _p(counts), dims, ws.ptr, ws.nbytes,
+                                 _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_cache_append")
+
+
+def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float] = None,
+                ws: Optional[Workspace] = None, stream=None):
+    """Attention of each sequence's T newest tokens (q [B, T, Hq, d], T <= 64)
+    over the paged cache, their own keys and values already appended at
+    positions lens[b] .. lens[b] + T - 1.  tree: int64 [B, T] bit masks of the
+    new tokens each one sees (None: those up to and with itself).  Returns
+    (o like q, lse fp32 [B, T, Hq]); a token that sees nothing gets 0 and -inf."""
+    _check(q, "q", torch.bfloat16, 4)
+    B, T, Hq, d = q.shape
+    c = _cache_args(kcache, vcache, pages, lens, B, q)
+    Hk = kcache.shape[2]
+    if kcache.shape[3] != d:
+        raise ValueError("kcache and q have different widths")
+    if tree is not None:
+        _on(tree, "tree", torch.int64, (B, T), q)
+    dims = AttnDims(B, T, Hq, Hk, d)
+    o, lse = _new((q.shape, (B, T, Hq)), (q.dtype, torch.float32), q.device, stream)
+    ws = _attn_ws(ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, q.device, stream)
+    st = lib().bdla_attn_cached(_p(q), c, _p(tree), d ** -0.5 if scale is None else scale, _p(o), _p(lse), dims,
+                                ws.ptr, ws.nbytes, _stream_handle(stream))
+    if st:
+        raise BdlaError(st, "bdla_attn_cached")
+    return o, lse

@@ -36,7 +36,8 @@ def _sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(ROOT, "include", "bdla.h"))
+    inc = os.path.join(ROOT, "include")
+    hs.extend(os.path.join(inc, f) for f in sorted(os.listdir(inc)) if f.endswith(".h"))
     return hs
 
 
