@@ -1,65 +1,409 @@
-// Causal softmax attention over whole documents, forward.
+// Causal softmax attention over whole documents, forward, on the sm_100-family
+// tensor cores.
+//
+//   s_ij = scale q_i . k_j (j <= i),  p_ij = e^{s_ij - m_i},  o_i = (sum_j p_ij v_j) / l_i,
+//   l_i = sum_j p_ij,  lse_i = m_i + log l_i
+// in one pass over the keys with a reference m_i that follows the running
+// maximum.
+//
+// One CTA takes 256 consecutive queries of one document and head as two tiles
+// of 128, and walks the keys in tiles of 128 up to the diagonal.  The two query
+// tiles share every key and value tile and run in turn: while the tensor cores
+// multiply for one, the four warps of the other turn scores into weights, so
+// that neither pipe waits for a whole tile of the other.  Warp 0 loads (TMA,
+// a ring of key and value tiles), warp 1 issues the MMAs, warps 2-5 and 6-9
+// are the softmax of tile 0 and 1, one thread a query row.
+//
+// Tensor memory: scores of either tile (128 columns each), outputs (D columns
+// each).  A thread reads its 128 scores, and writes the bf16 weights over them,
+// from where the P V product takes its A operand.  m_i moves only when a score
+// exceeds it by more than a factor 2^8 (kSlack): weights then stay below 2^8,
+// far from overflow, sums lose nothing in fp32, and the output is rescaled in
+// tensor memory in the first tiles only instead of in every one.  The order of
+// the MMAs makes that safe without a barrier of its own: Q K of tile j is
+// issued after P V of tile j - 1, so the scores' arrival says that the output
+// is at rest.
+//
+// Rounding: scores, maxima, sums and outputs are fp32; the weights enter the
+// P V product as bf16 (half a step, 2^-8 of each), as the tensor cores take
+// them; the sum adds them before that rounding.
+//
+// Rows past a document's end hold the next document.  Their scores are masked
+// by selection, and the values of the last tile's rows past the end are
+// cleared in shared memory, so that 0 times another document's infinity or NaN
+// never enters a sum.
+#include <cudaTypedefs.h>
+
 #include "bdla_attn_internal.h"
+#include "bdla_sm100.cuh"
 
 namespace bdla {
 
+bool make_token_map(CUtensorMap *map, const void *ptr, int d, int H, int64_t tokens);
+
 namespace {
 
-// One warp per (token, query head), each lane d/32 features.
-template <int D>
-__global__ void __launch_bounds__(128)
-attn_fwd_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
-                const __nv_bfloat16 *__restrict__ v, const int32_t *__restrict__ cu, int n_docs, int T, int64_t tokens,
-                int Hq, int Hk, float scale, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse)
+using namespace sm100;
+
+constexpr int BT = 128;                          // rows of a tile
+constexpr int kPairBlocks = 2;                   // query tiles of a CTA
+constexpr int kThreads = 64 + kPairBlocks * BT;  // loader, MMA issuer, softmax
+constexpr uint32_t kPanel = 16384;               // 128 rows x 128 swizzled bytes
+constexpr float kSlack = 8.0f;                   // log2 of how far weights may exceed 1
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// drains of a CTA's own copies and MMAs before it exits keep the full limit
+constexpr uint64_t kWaitNs = kDefaultWaitNs;
+
+template <int D> struct FwdSmem {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kTile = kPanels * kPanel;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    alignas(1024) unsigned char q[kPairBlocks][kTile];   // queries, then the output's staging
+    alignas(1024) unsigned char ring[kStages][kTile];    // K_0 V_0 K_1 V_1 ...
+    uint64_t full_q, full[kStages], empty[kStages], s_full[kPairBlocks], p_ready[kPairBlocks], o_done[kPairBlocks];
+    uint64_t drain, never;
+    uint64_t wait_ns;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+constexpr size_t kMaxSmem = 232448;   // 227 KB opt-in shared memory per CTA
+static_assert(sizeof(FwdSmem<128>) <= kMaxSmem && sizeof(FwdSmem<64>) <= kMaxSmem, "shared memory of a CTA");
+
+__device__ __forceinline__ float ex2(float x)
 {
-    constexpr int E = D / 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (item >= tokens * Hq)
-        return;
-    const int64_t t = item / Hq;
-    const int h = (int)(item % Hq), kh = h / (Hq / Hk);
-    int64_t start = t / (T > 0 ? T : 1) * T;
-    if (cu != nullptr) {
-        start = -1;
-        for (int n = 0; n < n_docs; ++n) {
-            const DocSpan s = doc_span(cu, n, T);
-            if (doc_valid(s, tokens) && t >= s.start && t < s.start + s.len)
-                start = s.start;
-        }
-        if (start < 0)
-            return;
-    }
-    float x[E], acc[E], m = -INFINITY, z = 0.0f;
-    for (int e = 0; e < E; ++e) {
-        x[e] = bf2f(q[item * D + lane * E + e]) * scale;
-        acc[e] = 0.0f;
-    }
-    for (int64_t j = start; j <= t; ++j) {
-        const int64_t off = (j * Hk + kh) * D + lane * E;
-        float s = 0.0f;
-        for (int e = 0; e < E; ++e)
-            s = fmaf(x[e], bf2f(k[off + e]), s);
-        for (int w = 16; w > 0; w >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float mn = fmaxf(m, s);
-        const float a = m == -INFINITY ? 0.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(s - mn);
-        z = z * a + p;
-        for (int e = 0; e < E; ++e)
-            acc[e] = acc[e] * a + p * bf2f(v[off + e]);
-        m = mn;
-    }
-    for (int e = 0; e < E; ++e)
-        o[item * D + lane * E + e] = __float2bfloat16_rn(z == 0.0f ? 0.0f : acc[e] / z);
-    if (lane == 0)
-        lse[h * tokens + t] = z == 0.0f ? -INFINITY : m + logf(z);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const int32_t *__restrict__ cu, int n_docs, int T,
+                int64_t tokens, int Hq, int group, int n_slots, float scale, __nv_bfloat16 *__restrict__ o,
+                float *__restrict__ lse, DeviceStatus *st, uint64_t wait_ns, int stall)
+{
+    using Smem = FwdSmem<D>;
+    constexpr int NS = Smem::kStages, NP = Smem::kPanels;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && cu != nullptr)
+        for (int n = tid; n < n_docs; n += kThreads)
+            if (cu[n + 1] < cu[n] || (n == 0 && cu[0] != 0) || (n == n_docs - 1 && cu[n_docs] != tokens))
+                set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
+    // heads fastest, so that the CTAs in flight share keys; late (long) query
+    // blocks first, so that the short ones fill the end
+    const int h = blockIdx.x % Hq;
+    const SegSpan span = seg_span(cu, T, tokens, n_docs, n_slots - 1 - (int)(blockIdx.x / Hq), kPairBlocks);
+    if (!span.valid || span.len <= 0)
+        return;
+    if ((smem_u32(smem_raw) & 1023u) != 0u) {
+        if (tid == 0)
+            set_status(st, BDLA_ERR_DEVICE, 0xA11u);
+        return;
+    }
+    const int kh = h / group;
+    // key tiles of each query tile: up to and with its own (0: no such tile)
+    const int n_kv[2] = {span.blk_base + 1, span.len > BT ? span.blk_base + 2 : 0};
+    const int n_max = n_kv[1] ? n_kv[1] : n_kv[0];
+    const int64_t doc_start = span.doc_start;
+
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(&sm.full_q, 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int w = 0; w < kPairBlocks; ++w) {
+            mbar_init(&sm.s_full[w], 1);
+            mbar_init(&sm.p_ready[w], BT);
+            mbar_init(&sm.o_done[w], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.never, 1);
+        sm.abort_flag = 0;
+        sm.wait_ns = wait_ns;
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int *abort_flag = &sm.abort_flag;
+    const int stall_at = n_max > 1 ? 1 : 0;   // test hook: the key tile at which a role stalls
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loader
+        if (lane == 0) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&tk);
+            tma_prefetch_desc(&tv);
+            const int tiles_q = n_kv[1] ? 2 : 1;
+            mbar_arrive_expect_tx(&sm.full_q, (uint32_t)(tiles_q * Smem::kTile));
+            for (int w = 0; w < tiles_q; ++w)
+                for (int p = 0; p < NP; ++p)
+                    tma_load_3d(sm.q[w] + p * kPanel, &tq, &sm.full_q, p * 64, h, (int)(span.start + w * BT));
+            int issued = 0;
+            bool ok = true;
+            for (int it = 0; it < 2 * n_max; ++it) {
+                const int s = it % NS;
+                const bool hook = stall == BDLA_STALL_PRODUCER && it == 2 * stall_at;
+                if (*abort_flag ||
+                    ((it >= NS || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
+                                                          hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns))) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.full[s], (uint32_t)Smem::kTile);
+                for (int p = 0; p < NP; ++p)
+                    tma_load_3d(sm.ring[s] + p * kPanel, (it & 1) ? &tv : &tk, &sm.full[s], p * 64, kh,
+                                (int)(doc_start + (int64_t)(it >> 1) * BT));
+                issued = it + 1;
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                set_status(st, BDLA_ERR_TIMEOUT, 0x10u);
+                // the copies this thread started land before the CTA exits
+                mbar_wait(&sm.full_q, 0, kWaitNs);
+                for (int it = issued > NS ? issued - NS : 0; it < issued; ++it)
+                    mbar_wait(&sm.full[it % NS], (it / NS) & 1, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t id_qk = idesc_bf16_f32(BT, BT, false, false);
+            const uint32_t id_pv = idesc_bf16_f32(BT, D, false, true);
+            bool ok = mbar_wait_lim(&sm.full_q, 0, &sm.wait_ns);
+            // S_w = Q_w K_j^T over the scores (and weights) of tile j - 1
+            auto issue_qk = [&](int w, int j) {
+                const int it = 2 * j;
+                if (!mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns))
+                    return false;
+                tc_fence_after();
+                const uint32_t a = smem_u32(sm.q[w]), b = smem_u32(sm.ring[it % NS]);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
+                    umma_bf16(tmem + BT * w, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id_qk,
+                              ks > 0);
+                }
+                umma_commit(&sm.s_full[w]);
+                if (w == 1 || j >= n_kv[1])   // the last reader of this key tile
+                    umma_commit(&sm.empty[it % NS]);
+                return true;
+            };
+            for (int w = 0; ok && w < 2; ++w)
+                if (n_kv[w] > 0)
+                    ok = issue_qk(w, 0);
+            for (int j = 0; ok && j < n_max; ++j) {
+                for (int w = 0; ok && w < 2; ++w) {
+                    if (j >= n_kv[w])
+                        continue;
+                    const int it = 2 * j + 1;
+                    const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
+                    ok = !*abort_flag &&
+                         mbar_wait_lim(hook ? &sm.never : &sm.p_ready[w], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns) &&
+                         mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t b = smem_u32(sm.ring[it % NS]);
+                    for (int ks = 0; ks < BT / 16; ++ks)
+                        umma_bf16_ts(tmem + 2 * BT + BT * w, tmem + BT * w + ks * 8,
+                                     sdesc_sw128(b + ks * 2048, kPanel, 1024), id_pv, j > 0 || ks > 0);
+                    if (w == 1 || j >= n_kv[1])
+                        umma_commit(&sm.empty[it % NS]);
+                    if (j + 1 < n_kv[w])
+                        ok = issue_qk(w, j + 1);
+                    else
+                        umma_commit(&sm.o_done[w]);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                set_status(st, BDLA_ERR_TIMEOUT, 0x11u);
+            }
+            // every MMA issued above has completed before TMEM is released
+            umma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, kWaitNs);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int w = (warp - 2) >> 2;
+        const int q4 = warp & 3;
+        const int r = 32 * q4 + lane;   // row of the tile, TMEM lane
+        const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+        const uint32_t t_s = tmem + BT * w + lane_off, t_o = tmem + 2 * BT + BT * w + lane_off;
+        const int n = n_kv[w];
+        const int valid = (int)(span.len - w * BT);   // rows of the tile inside the document (may exceed 128)
+        const float c = scale * kLog2e;
+        float m = -INFINITY, mc = -INFINITY, l = 0.0f;   // reference, times c; sum of the weights
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
+            ok = __all_sync(0xffffffffu, mbar_wait_lim(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(j & 1),
+                                                       &sm.wait_ns)) &&
+                 !*abort_flag;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tmem_ld32(t_s + 32 * k, x[k]);
+            tmem_ld_wait();
+            if (j == n - 1) {   // the diagonal tile: keys past the query (and with them all past the end)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[k][i] = 32 * k + i > r ? 0xff800000u : x[k][i];
+            }
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                mx[k] = __uint_as_float(x[k][0]);
+#pragma unroll
+                for (int i = 1; i < 32; ++i)
+                    mx[k] = fmaxf(mx[k], __uint_as_float(x[k][i]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool move = (top - m) * c > kSlack;
+            if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? ex2(mc - top * c) : 1.0f;
+                if (move) {
+                    m = top;
+                    mc = top * c;
+                }
+                l *= f;
+                if (j > 0) {
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t y[32];
+                        tmem_ld32(t_o + 32 * k, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                        tmem_st32(t_o + 32 * k, y);
+                    }
+                }
+            }
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t u[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = ex2(fmaf(__uint_as_float(x[k][2 * i]), c, -mc));
+                    const float b = ex2(fmaf(__uint_as_float(x[k][2 * i + 1]), c, -mc));
+                    sum[i & 3] += a + b;
+                    u[i] = pack_bf16(a, b);
+                }
+                tmem_st16(t_s + 16 * k, u);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (j == n - 1 && valid < BT) {
+                // this tile alone reads the document's last values: clear the rows past the end
+                const int it = 2 * j + 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns));
+                if (!ok)
+                    break;
+                for (int e = r; e < (BT - valid) * 8 * NP; e += BT) {
+                    const int p = e / ((BT - valid) * 8), f = e % ((BT - valid) * 8);
+                    *reinterpret_cast<uint4 *>(sm.ring[it % NS] + p * kPanel + (valid + (f >> 3)) * 128 + (f & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.p_ready[w]);
+        }
+        if (ok && n > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_lim(&sm.o_done[w], 0, &sm.wait_ns)) && !*abort_flag;
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (ok && n > 0) {
+            tc_fence_after();
+            const int64_t t0 = span.start + w * BT;
+            if (r < valid)
+                lse[(int64_t)h * tokens + t0 + r] = (mc + log2f(l)) * kLn2;
+            const float inv = 1.0f / l;
+            // a warp stages its own 32 rows of 128 bytes in its tile's queries (read by now), then writes whole rows
+            uint4 *stage = reinterpret_cast<uint4 *>(sm.q[w] + q4 * 4096);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                uint32_t y[2][32];
+                tmem_ld32(t_o + 64 * p, y[0]);
+                tmem_ld32(t_o + 64 * p + 32, y[1]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = pack_bf16(__uint_as_float(y[k >> 2][8 * (k & 3) + 2 * i]) * inv,
+                                         __uint_as_float(y[k >> 2][8 * (k & 3) + 2 * i + 1]) * inv);
+                    stage[lane * 8 + (k ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                __syncwarp();
+                __nv_bfloat16 *dst = o + ((size_t)(t0 + 32 * q4) * Hq + h) * D + p * 64;
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int row = 4 * it + (lane >> 3), c8 = lane & 7;
+                    const uint4 v = stage[row * 8 + (c8 ^ (row & 7))];
+                    if (32 * q4 + row < valid)
+                        *reinterpret_cast<uint4 *>(dst + (size_t)row * Hq * D + 8 * c8) = v;
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x12u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+// The check of a packed call that has no tokens (and so no attention CTA).
 __global__ void doc_report_kernel(const int32_t *cu, int n_docs, int64_t tokens, DeviceStatus *st)
 {
     for (int n = threadIdx.x; n < n_docs; n += blockDim.x)
         if (cu[n + 1] < cu[n] || (n == 0 && cu[0] != 0) || (n == n_docs - 1 && cu[n_docs] != tokens))
             set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
+}
+
+template <int D>
+cudaError_t go(const AttnProblem &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+               __nv_bfloat16 *o, float *lse)
+{
+    auto kern = attn_fwd_kernel<D>;
+    const size_t smem = sizeof(FwdSmem<D>);
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t rows = kPairBlocks * BT;
+    const int64_t n_slots = (p.tokens + rows - 1) / rows + p.n_docs;
+    if (n_slots * p.Hq > INT32_MAX)
+        return cudaErrorInvalidValue;
+    kern<<<(unsigned)(n_slots * p.Hq), kThreads, smem, p.stream>>>(
+        mq, mk, mv, p.cu, p.n_docs, p.T, p.tokens, p.Hq, p.Hq / p.Hk, (int)n_slots, p.scale, o, lse, p.st,
+        g_wait_ns.load(), g_test_stall[BDLA_KERNEL_ATTN_FWD].load());
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -74,15 +418,14 @@ cudaError_t launch_doc_report(const AttnProblem &p)
 cudaError_t launch_attn_fwd(const AttnProblem &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                             const __nv_bfloat16 *v, __nv_bfloat16 *o, float *lse)
 {
-    const cudaError_t err = launch_doc_report(p);
-    if (err != cudaSuccess || p.tokens == 0)
-        return err;
-    const unsigned grid = (unsigned)((p.tokens * p.Hq + 3) / 4);
-    if (p.d == 64)
-        attn_fwd_kernel<64><<<grid, 128, 0, p.stream>>>(q, k, v, p.cu, p.n_docs, p.T, p.tokens, p.Hq, p.Hk, p.scale, o, lse);
-    else
-        attn_fwd_kernel<128><<<grid, 128, 0, p.stream>>>(q, k, v, p.cu, p.n_docs, p.T, p.tokens, p.Hq, p.Hk, p.scale, o, lse);
-    return cudaGetLastError();
+    KernelMark mark_(BDLA_KERNEL_ATTN_FWD, p.stream);
+    if (p.tokens == 0)
+        return launch_doc_report(p);
+    CUtensorMap mq, mk, mv;
+    if (!make_token_map(&mq, q, p.d, p.Hq, p.tokens) || !make_token_map(&mk, k, p.d, p.Hk, p.tokens) ||
+        !make_token_map(&mv, v, p.d, p.Hk, p.tokens))
+        return cudaErrorInvalidValue;
+    return p.d == 64 ? go<64>(p, mq, mk, mv, o, lse) : go<128>(p, mq, mk, mv, o, lse);
 }
 
 }  // namespace bdla

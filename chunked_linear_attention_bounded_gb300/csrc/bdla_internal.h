@@ -78,7 +78,8 @@ extern KernelEvents g_kernel_events[BDLA_KERNEL_COUNT];
 inline const char *kernel_range_name(int kernel)
 {
     static const char *names[BDLA_KERNEL_COUNT] = {"bdla:decay", "bdla:fwd", "bdla:bwd",
-                                                   "bdla:states", "bdla:seg"};
+                                                   "bdla:states", "bdla:seg", "bdla:attn_fwd",
+                                                   "bdla:attn_bwd"};
     return names[kernel];
 }
 // Bounded waits (bdla_set_wait_limit_ns, bdla_set_test_stall): the limit of
