@@ -1,123 +1,621 @@
-// Causal softmax attention over whole documents, gradient.
-#include "bdla_attn_internal.h"
+// Causal softmax attention over whole documents, gradient, on the sm_100-family
+// tensor cores.
+//
+//   p_ij = e^{s_ij - lse_i},  delta_i = dO_i . o_i,  dp_ij = dO_i . v_j,  ds_ij = p_ij (dp_ij - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,   dv_j = sum_i p_ij dO_i
+//   (dk, dv also summed over the query heads of the key head)
+//
+// Two kernels, each of which owns what it sums into: one per tile of queries
+// that walks its keys (dq, and delta for the second), one per tile of keys that
+// walks the queries of all heads of its group (dk, dv).  Scores and dp are
+// formed in both, seven products of the pairs instead of five, and in return
+// nothing is added through memory: no fp32 copy of dq (four bytes an element
+// written and read again for every key tile), no atomics, and the same bits
+// from the same inputs.
+//
+// Both kernels: warp 0 loads (TMA, a ring of tiles), warp 1 issues the MMAs,
+// warps 2-9 form the weights, two warps for every 32 rows, 64 columns each.
+// The rows of the accumulators are the rows of what is summed into (queries, or
+// keys: the scores are then formed transposed), so that p and ds go back to
+// tensor memory as the A operand of the next product and never pass through
+// shared memory.  They are written over the scores (or dp) that they were
+// formed from, each warp inside its own 64 columns.
+//
+// Rounding: scores, dp, delta and the accumulators are fp32; p and ds enter
+// their products as bf16 (half a step, 2^-8 of each); ds is formed from the
+// fp32 p.
+//
+// Rows past a document's end hold the next document.  Their p and ds are
+// zeroed by selection, and where such rows are the summed side of a product
+// their operand rows are cleared in shared memory, so that another document's
+// infinity or NaN never enters a sum.
+#include <cudaTypedefs.h>
+
+#include "bdla_attn_sm100.cuh"
 
 namespace bdla {
 
 namespace {
 
-struct Span2 {
-    int64_t start, end;
+using namespace sm100;
+using namespace attn;
+
+constexpr int kEpi = 256;              // weight threads
+constexpr int kThreads = 64 + kEpi;    // + loader and MMA issuer
+
+template <int D> struct BwdSmem {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kTile = kPanels * kPanel;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    alignas(1024) unsigned char own[2][kTile];          // Q, dO of the query tile, or K, V of the key tile
+    alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 ..., or Q_0 dO_0 Q_1 ...
+    float col[2][2][BT];   // key tiles: lse * log2 e and delta of a query tile; query tiles: [0] halves of delta
+    uint64_t full_own, full[kStages], empty[kStages], s_full[2], ready[2], dp_full, dp_free, done;
+    uint64_t drain, never;
+    uint64_t wait_ns;
+    uint32_t tmem_base;
+    int abort_flag;
 };
+static_assert(sizeof(BwdSmem<128>) <= kMaxSmem && sizeof(BwdSmem<64>) <= kMaxSmem, "shared memory of a CTA");
 
-__device__ Span2 document_of(const int32_t *cu, int n_docs, int T, int64_t tokens, int64_t t)
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// The same barrier, which also says whether every thread still runs.
+__device__ __forceinline__ bool epi_all(bool v)
 {
-    if (cu == nullptr)
-        return {t / T * T, t / T * T + T};
-    Span2 r = {-1, -1};
-    for (int n = 0; n < n_docs; ++n) {
-        const DocSpan s = doc_span(cu, n, T);
-        if (doc_valid(s, tokens) && t >= s.start && t < s.start + s.len)
-            r = {s.start, s.start + s.len};
-    }
-    return r;
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
 }
 
-__device__ __forceinline__ float warp_sum(float s)
+// Tensor memory: both kernels hold two 128-column tiles of scores or dp and
+// their accumulators.
+template <typename Smem>
+__device__ __forceinline__ void setup(Smem &sm, int tid, uint64_t wait_ns)
 {
-    for (int w = 16; w > 0; w >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, w);
-    return s;
-}
-
-// One warp per (token, query head): delta = dO . o, then dq.
-template <int D>
-__global__ void __launch_bounds__(128)
-attn_dq_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
-               const __nv_bfloat16 *__restrict__ v, const __nv_bfloat16 *__restrict__ o, const float *__restrict__ lse,
-               const __nv_bfloat16 *__restrict__ dO, const int32_t *__restrict__ cu, int n_docs, int T, int64_t tokens,
-               int Hq, int Hk, float scale, __nv_bfloat16 *__restrict__ dq, float *__restrict__ delta)
-{
-    constexpr int E = D / 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (item >= tokens * Hq)
-        return;
-    const int64_t t = item / Hq;
-    const int h = (int)(item % Hq), kh = h / (Hq / Hk);
-    const Span2 doc = document_of(cu, n_docs, T, tokens, t);
-    if (doc.start < 0)
-        return;
-    float x[E], g[E], acc[E], dl = 0.0f;
-    for (int e = 0; e < E; ++e) {
-        const int64_t off = item * D + lane * E + e;
-        x[e] = bf2f(q[off]) * scale;
-        g[e] = bf2f(dO[off]);
-        dl = fmaf(g[e], bf2f(o[off]), dl);
-        acc[e] = 0.0f;
+    if ((tid >> 5) == 1) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
     }
-    dl = warp_sum(dl);
-    const float l = lse[h * tokens + t];
-    for (int64_t j = doc.start; j <= t; ++j) {
-        const int64_t off = (j * Hk + kh) * D + lane * E;
-        float s = 0.0f, dp = 0.0f;
-        for (int e = 0; e < E; ++e) {
-            s = fmaf(x[e], bf2f(k[off + e]), s);
-            dp = fmaf(g[e], bf2f(v[off + e]), dp);
+    if (tid == 0) {
+        mbar_init(&sm.full_own, 1);
+        for (int s = 0; s < Smem::kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
         }
-        const float ds = expf(warp_sum(s) - l) * (warp_sum(dp) - dl) * scale;
-        for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(ds, bf2f(k[off + e]), acc[e]);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.s_full[b], 1);
+            mbar_init(&sm.ready[b], kEpi);
+        }
+        mbar_init(&sm.dp_full, 1);
+        mbar_init(&sm.dp_free, kEpi);
+        mbar_init(&sm.done, 1);
+        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.never, 1);
+        sm.abort_flag = 0;
+        sm.wait_ns = wait_ns;
+        mbar_fence_init();
     }
-    for (int e = 0; e < E; ++e)
-        dq[item * D + lane * E + e] = __float2bfloat16_rn(acc[e]);
-    if (lane == 0)
-        delta[h * tokens + t] = dl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
 }
 
-// One warp per (token, key head).
-template <int D>
-__global__ void __launch_bounds__(128)
-attn_dkv_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
-                const __nv_bfloat16 *__restrict__ v, const float *__restrict__ lse,
-                const __nv_bfloat16 *__restrict__ dO, const float *__restrict__ delta, const int32_t *__restrict__ cu,
-                int n_docs, int T, int64_t tokens, int Hq, int Hk, float scale, __nv_bfloat16 *__restrict__ dk,
-                __nv_bfloat16 *__restrict__ dv)
+// The loader's ring: `n` tiles, tile `it` fetched by load(it, slot).  Lets its
+// copies land before it returns from a wait that ran out.
+template <typename Smem, typename Load>
+__device__ __forceinline__ void run_loader(Smem &sm, int n, int stall_it, DeviceStatus *st, Load load)
 {
-    constexpr int E = D / 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (item >= tokens * Hk)
-        return;
-    const int64_t t = item / Hk;
-    const int kh = (int)(item % Hk), G = Hq / Hk;
-    const Span2 doc = document_of(cu, n_docs, T, tokens, t);
-    if (doc.start < 0)
-        return;
-    float x[E], y[E], ak[E], av[E];
-    for (int e = 0; e < E; ++e) {
-        x[e] = bf2f(k[item * D + lane * E + e]) * scale;
-        y[e] = bf2f(v[item * D + lane * E + e]);
-        ak[e] = av[e] = 0.0f;
-    }
-    for (int h = kh * G; h < (kh + 1) * G; ++h)
-        for (int64_t i = t; i < doc.end; ++i) {
-            const int64_t off = (i * Hq + h) * D + lane * E;
-            float s = 0.0f, dp = 0.0f;
-            for (int e = 0; e < E; ++e) {
-                s = fmaf(x[e], bf2f(q[off + e]), s);
-                dp = fmaf(y[e], bf2f(dO[off + e]), dp);
-            }
-            const float p = expf(warp_sum(s) - lse[h * tokens + i]);
-            const float ds = p * (warp_sum(dp) - delta[h * tokens + i]) * scale;
-            for (int e = 0; e < E; ++e) {
-                ak[e] = fmaf(ds, bf2f(q[off + e]), ak[e]);
-                av[e] = fmaf(p, bf2f(dO[off + e]), av[e]);
-            }
+    constexpr int NS = Smem::kStages;
+    volatile int *abort_flag = &sm.abort_flag;
+    int issued = 0;
+    bool ok = true;
+    for (int it = 0; it < n; ++it) {
+        const int s = it % NS;
+        const bool hook = it == stall_it;
+        if (*abort_flag || ((it >= NS || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
+                                                                 hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns))) {
+            ok = false;
+            break;
         }
-    for (int e = 0; e < E; ++e) {
-        dk[item * D + lane * E + e] = __float2bfloat16_rn(ak[e]);
-        dv[item * D + lane * E + e] = __float2bfloat16_rn(av[e]);
+        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)Smem::kTile);
+        load(it, s);
+        issued = it + 1;
     }
+    if (!ok) {
+        *abort_flag = 1;
+        set_status(st, BDLA_ERR_TIMEOUT, 0x20u);
+        mbar_wait(&sm.full_own, 0, kDrainNs);
+        for (int it = issued > NS ? issued - NS : 0; it < issued; ++it)
+            mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
+    }
+}
+
+// D[acc] = A B^T of two tiles whose rows are the operands' rows (features summed).
+template <int D> __device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b)
+{
+    constexpr uint32_t id = idesc_bf16_f32(BT, BT, false, false);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
+        umma_bf16(acc, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id, ks > 0);
+    }
+}
+
+// D[acc] += A B: A bf16 [128 x 128] in tensor memory (the first and second 64
+// columns' pairs at `a` and `a + 64`), B a tile whose rows are summed over.
+template <int D> __device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t a, uint32_t b, bool accumulate)
+{
+    constexpr uint32_t id = idesc_bf16_f32(BT, D, false, true);
+#pragma unroll
+    for (int ks = 0; ks < BT / 16; ++ks)
+        umma_bf16_ts(acc, a + (ks >> 2) * 64 + (ks & 3) * 8, sdesc_sw128(b + ks * 2048, kPanel, 1024), id,
+                     accumulate || ks > 0);
+}
+
+// ---------------------------------------------------------------- dq
+// Tensor memory: scores of even and odd key tiles (ds over them), dp, dq.  While
+// the weights of tile j are formed, the tensor cores run S of j + 1, dp of j + 1
+// (dp is free once it is in registers) and dq of j - 1.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+               const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+               const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dO, const float *__restrict__ lse,
+               const int32_t *__restrict__ cu, int n_docs, int T, int64_t tokens, int Hq, int group, int n_slots,
+               float scale, __nv_bfloat16 *__restrict__ dq, float *__restrict__ delta, DeviceStatus *st,
+               uint64_t wait_ns, int stall)
+{
+    using Smem = BwdSmem<D>;
+    constexpr int NS = Smem::kStages, NP = Smem::kPanels;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && cu != nullptr)
+        check_offsets(cu, n_docs, tokens, st);
+    // late (long) query tiles first
+    const int h = blockIdx.x % Hq;
+    const SegSpan span = seg_span(cu, T, tokens, n_docs, n_slots - 1 - (int)(blockIdx.x / Hq), 1);
+    if (!span.valid || span.len <= 0)
+        return;
+    if ((smem_u32(smem_raw) & 1023u) != 0u) {
+        if (tid == 0)
+            set_status(st, BDLA_ERR_DEVICE, 0xA11u);
+        return;
+    }
+    const int kh = h / group;
+    const int n = span.blk_base + 1;       // key tiles up to the diagonal
+    const int valid = (int)span.len;       // rows of the tile (and keys of the diagonal one) inside the document
+    const int stall_at = n > 1 ? 1 : 0;
+    setup(sm, tid, wait_ns);
+    const uint32_t tmem = sm.tmem_base, t_dp = tmem + 2 * BT, t_dq = tmem + 3 * BT;
+    volatile int *abort_flag = &sm.abort_flag;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.full_own, 2u * Smem::kTile);
+            for (int p = 0; p < NP; ++p) {
+                tma_load_3d(sm.own[0] + p * kPanel, &tq, &sm.full_own, p * 64, h, (int)span.start);
+                tma_load_3d(sm.own[1] + p * kPanel, &tdo, &sm.full_own, p * 64, h, (int)span.start);
+            }
+            run_loader(sm, 2 * n, stall == BDLA_STALL_PRODUCER ? 2 * stall_at : -1, st, [&](int it, int s) {
+                for (int p = 0; p < NP; ++p)
+                    tma_load_3d(sm.ring[s] + p * kPanel, (it & 1) ? &tv : &tk, &sm.full[s], p * 64, kh,
+                                (int)(span.doc_start + (int64_t)(it >> 1) * BT));
+            });
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t q = smem_u32(sm.own[0]), g = smem_u32(sm.own[1]);
+            auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
+            auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
+            auto issue_s = [&](int j) {
+                if (!landed(2 * j))
+                    return false;
+                tc_fence_after();
+                mma_rows<D>(tmem + BT * (j & 1), q, tile(2 * j));
+                umma_commit(&sm.s_full[j & 1]);
+                return true;
+            };
+            auto issue_dp = [&](int j) {
+                if (!landed(2 * j + 1))
+                    return false;
+                tc_fence_after();
+                mma_rows<D>(t_dp, g, tile(2 * j + 1));
+                umma_commit(&sm.dp_full);
+                umma_commit(&sm.empty[(2 * j + 1) % NS]);
+                return true;
+            };
+            bool ok = mbar_wait_lim(&sm.full_own, 0, &sm.wait_ns) && issue_s(0) && issue_dp(0);
+            for (int j = 0; ok && j < n; ++j) {
+                const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
+                if (j + 1 < n)
+                    ok = issue_s(j + 1) && mbar_wait_lim(&sm.dp_free, j & 1, &sm.wait_ns) && issue_dp(j + 1);
+                ok = ok && !*abort_flag &&
+                     mbar_wait_lim(hook ? &sm.never : &sm.ready[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma_sum<D>(t_dq, tmem + BT * (j & 1), tile(2 * j), j > 0);
+                umma_commit(&sm.empty[(2 * j) % NS]);
+            }
+            if (ok) {
+                umma_commit(&sm.done);
+            } else {
+                *abort_flag = 1;
+                set_status(st, BDLA_ERR_TIMEOUT, 0x21u);
+            }
+            umma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, kDrainNs);
+        }
+    } else {
+        const int half = (warp - 2) >> 2, q4 = warp & 3, r = 32 * q4 + lane, e = 128 * half + r;
+        const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+        const int64_t t = span.start + r;
+        // delta of the row, half the features each
+        float dl = 0.0f, l2 = 0.0f;
+        if (r < valid) {
+            const size_t off = ((size_t)t * Hq + h) * D + half * (D / 2);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(o + off + 8 * i);
+                const uint4 b = *reinterpret_cast<const uint4 *>(dO + off + 8 * i);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    dl = fmaf(bf16_hi(x[u]), bf16_hi(y[u]), fmaf(bf16_lo(x[u]), bf16_lo(y[u]), dl));
+            }
+            l2 = lse[(int64_t)h * tokens + t] * kLog2e;
+        }
+        sm.col[0][half][r] = dl;
+        epi_sync();
+        dl = sm.col[0][0][r] + sm.col[0][1][r];
+        if (half == 0 && r < valid)
+            delta[(int64_t)h * tokens + t] = dl;
+        const float c = scale * kLog2e;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
+            const uint32_t t_s = tmem + BT * (j & 1) + lane_off + 64 * half;
+            ok = warp_wait(hook ? &sm.never : &sm.s_full[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns, abort_flag);
+            if (!ok)
+                break;
+            tc_fence_after();
+            uint32_t x[2][32], y[2][32];
+            tmem_ld32(t_s, x[0]);
+            tmem_ld32(t_s + 32, x[1]);
+            ok = warp_wait(&sm.dp_full, j & 1, &sm.wait_ns, abort_flag);
+            if (!ok)
+                break;
+            tc_fence_after();
+            tmem_ld32(t_dp + lane_off + 64 * half, y[0]);
+            tmem_ld32(t_dp + lane_off + 64 * half + 32, y[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.dp_free);
+            const bool diag = j == n - 1;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t u[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float ds[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int m = 2 * i + b;
+                        const float p = ex2(fmaf(__uint_as_float(x[k][m]), c, -l2));
+                        ds[b] = p * (__uint_as_float(y[k][m]) - dl);
+                        if (diag && 64 * half + 32 * k + m > r)
+                            ds[b] = 0.0f;
+                    }
+                    u[i] = pack_bf16(ds[0], ds[1]);
+                }
+                tmem_st16(t_s + 16 * k, u);
+            }
+            if (diag && valid < BT) {
+                // this product sums over the diagonal tile's keys: clear those past the end (S has read them)
+                clear_rows(sm.ring[(2 * j) % NS], NP, valid, e, kEpi);
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.ready[j & 1]);
+        }
+        if (ok)
+            ok = warp_wait(&sm.done, 0, &sm.wait_ns, abort_flag);
+        if (ok && half < NP) {
+            tc_fence_after();
+            // 64 features a half, staged in the query tile (read by now)
+            store_rows64(t_dq + lane_off + 64 * half, scale, sm.own[0] + half * kPanel + q4 * 4096,
+                         dq + ((size_t)(span.start + 32 * q4) * Hq + h) * D + 64 * half, (size_t)Hq * D, valid - 32 * q4,
+                         lane);
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x22u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- dk, dv
+// Tensor memory: S^T (p over it), dp^T (ds over it), dv, dk.  The two halves of
+// a tile's work alternate with the tensor cores: dv of t and S^T of t + 1 run
+// while ds of t is formed, dk of t and dp^T of t + 1 while p of t + 1 is.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                const float *__restrict__ lse, const float *__restrict__ delta, const int32_t *__restrict__ cu,
+                int n_docs, int T, int64_t tokens, int Hk, int group, float scale, __nv_bfloat16 *__restrict__ dk,
+                __nv_bfloat16 *__restrict__ dv, DeviceStatus *st, uint64_t wait_ns, int stall)
+{
+    using Smem = BwdSmem<D>;
+    constexpr int NS = Smem::kStages, NP = Smem::kPanels;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // early key tiles, which the most queries see, first
+    const int kh = blockIdx.x % Hk;
+    const SegSpan span = seg_span(cu, T, tokens, n_docs, (int)(blockIdx.x / Hk), 1);
+    if (!span.valid || span.len <= 0)
+        return;
+    if ((smem_u32(smem_raw) & 1023u) != 0u) {
+        if (tid == 0)
+            set_status(st, BDLA_ERR_DEVICE, 0xA11u);
+        return;
+    }
+    const int64_t doc_len = doc_span(cu, span.n, T).len;
+    const int nq = (int)((doc_len + BT - 1) / BT) - span.blk_base;   // query tiles from the diagonal on
+    const int n = nq * group;                                        // of every head of the group in turn
+    const int stall_at = n > 1 ? 1 : 0;
+    setup(sm, tid, wait_ns);
+    const uint32_t tmem = sm.tmem_base, t_dp = tmem + BT, t_dv = tmem + 2 * BT, t_dk = tmem + 3 * BT;
+    volatile int *abort_flag = &sm.abort_flag;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.full_own, 2u * Smem::kTile);
+            for (int p = 0; p < NP; ++p) {
+                tma_load_3d(sm.own[0] + p * kPanel, &tk, &sm.full_own, p * 64, kh, (int)span.start);
+                tma_load_3d(sm.own[1] + p * kPanel, &tv, &sm.full_own, p * 64, kh, (int)span.start);
+            }
+            run_loader(sm, 2 * n, stall == BDLA_STALL_PRODUCER ? 2 * stall_at : -1, st, [&](int it, int s) {
+                const int g = (it >> 1) / nq, i = (it >> 1) % nq;
+                for (int p = 0; p < NP; ++p)
+                    tma_load_3d(sm.ring[s] + p * kPanel, (it & 1) ? &tdo : &tq, &sm.full[s], p * 64, kh * group + g,
+                                (int)(span.start + (int64_t)i * BT));
+            });
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t k = smem_u32(sm.own[0]), v = smem_u32(sm.own[1]);
+            auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
+            auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
+            auto issue_s = [&](int t) {
+                if (!landed(2 * t))
+                    return false;
+                tc_fence_after();
+                mma_rows<D>(tmem, k, tile(2 * t));
+                umma_commit(&sm.s_full[0]);
+                return true;
+            };
+            auto issue_dp = [&](int t) {
+                if (!landed(2 * t + 1))
+                    return false;
+                tc_fence_after();
+                mma_rows<D>(t_dp, v, tile(2 * t + 1));
+                umma_commit(&sm.dp_full);
+                return true;
+            };
+            bool ok = mbar_wait_lim(&sm.full_own, 0, &sm.wait_ns) && issue_s(0) && issue_dp(0);
+            for (int t = 0; ok && t < n; ++t) {
+                const bool hook = stall == BDLA_STALL_MMA && t == stall_at;
+                ok = !*abort_flag &&
+                     mbar_wait_lim(hook ? &sm.never : &sm.ready[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma_sum<D>(t_dv, tmem, tile(2 * t + 1), t > 0);
+                umma_commit(&sm.empty[(2 * t + 1) % NS]);
+                if (t + 1 < n && !(ok = issue_s(t + 1)))
+                    break;
+                if (!(ok = mbar_wait_lim(&sm.ready[1], t & 1, &sm.wait_ns)))
+                    break;
+                tc_fence_after();
+                mma_sum<D>(t_dk, t_dp, tile(2 * t), t > 0);
+                umma_commit(&sm.empty[(2 * t) % NS]);
+                if (t + 1 < n)
+                    ok = issue_dp(t + 1);
+            }
+            if (ok) {
+                umma_commit(&sm.done);
+            } else {
+                *abort_flag = 1;
+                set_status(st, BDLA_ERR_TIMEOUT, 0x23u);
+            }
+            umma_commit(&sm.drain);
+            mbar_wait(&sm.drain, 0, kDrainNs);
+        }
+    } else {
+        const int half = (warp - 2) >> 2, q4 = warp & 3, r = 32 * q4 + lane, e = 128 * half + r;
+        const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+        const uint32_t t_s = tmem + lane_off + 64 * half, t_d = t_dp + lane_off + 64 * half;
+        const float c = scale * kLog2e;
+        // this thread's entry of a query tile's lse (half 0) or delta (half 1), fetched one tile ahead
+        const float *src = half ? delta : lse;
+        auto fetch = [&](int t) {
+            const int g = t / nq, i = t % nq;
+            const int64_t row = (int64_t)(span.blk_base + i) * BT + r;
+            if (row >= doc_len)
+                return 0.0f;
+            const float x = src[(int64_t)(kh * group + g) * tokens + span.doc_start + row];
+            return half ? x : x * kLog2e;
+        };
+        float next = fetch(0);
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            const bool hook = stall == BDLA_STALL_EPILOGUE && t == stall_at;
+            const int i_tile = t % nq;
+            // queries of the tile inside the document
+            const int valid = (int)(doc_len - (int64_t)(span.blk_base + i_tile) * BT);
+            sm.col[t & 1][half][r] = next;
+            // Every thread is done with the entries of two tiles before.  A warp whose wait ran out skips the
+            // rest of its tile and leaves with all the others here.
+            if (!(ok = epi_all(ok)))
+                break;
+            if (t + 1 < n)
+                next = fetch(t + 1);
+            ok = warp_wait(hook ? &sm.never : &sm.s_full[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns, abort_flag);
+            float p[64];
+            if (ok) {
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld32(t_s, x[0]);
+                tmem_ld32(t_s + 32, x[1]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int m4 = 0; m4 < 16; ++m4) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(&sm.col[t & 1][0][64 * half + 4 * m4]);
+                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        p[4 * m4 + b] = ex2(fmaf(__uint_as_float(x[m4 >> 3][(4 * m4 + b) & 31]), c, -lv[b]));
+                }
+                if (i_tile == 0 || valid < BT) {   // the diagonal, or queries past the end
+#pragma unroll
+                    for (int m = 0; m < 64; ++m) {
+                        const int q = 64 * half + m;
+                        if ((i_tile == 0 && q < r) || q >= valid)
+                            p[m] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        u[i] = pack_bf16(p[32 * k + 2 * i], p[32 * k + 2 * i + 1]);
+                    tmem_st16(t_s + 16 * k, u);
+                }
+                if (valid < BT) {
+                    // dv and dk sum over this tile's queries: clear those past the end once S and dp have read them
+                    ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
+                    if (ok) {
+                        clear_rows(sm.ring[(2 * t) % NS], NP, valid, e, kEpi);
+                        clear_rows(sm.ring[(2 * t + 1) % NS], NP, valid, e, kEpi);
+                        fence_proxy_async_smem();
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                if (ok)
+                    mbar_arrive(&sm.ready[0]);
+            }
+            if (ok)
+                ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
+            if (!ok) {
+                *abort_flag = 1;
+                continue;
+            }
+            tc_fence_after();
+            uint32_t y[2][32];
+            tmem_ld32(t_d, y[0]);
+            tmem_ld32(t_d + 32, y[1]);
+            tmem_ld_wait();
+            const bool mask = i_tile == 0 || valid < BT;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t u[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 d4 = *reinterpret_cast<const float4 *>(&sm.col[t & 1][1][64 * half + 32 * k + 2 * i]);
+                    const float dv4[4] = {d4.x, d4.y, d4.z, d4.w};
+                    float ds[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int m = 32 * k + 2 * i + b;
+                        ds[b] = p[m] * (__uint_as_float(y[k][2 * i + b]) - dv4[b]);
+                        if (mask) {   // 0 times another document's NaN
+                            const int q = 64 * half + m;
+                            if ((i_tile == 0 && q < r) || q >= valid)
+                                ds[b] = 0.0f;
+                        }
+                    }
+                    u[i] = pack_bf16(ds[0], ds[1]);
+                    u[i + 1] = pack_bf16(ds[2], ds[3]);
+                }
+                tmem_st16(t_d + 16 * k, u);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.ready[1]);
+        }
+        if (ok)
+            ok = warp_wait(&sm.done, 0, &sm.wait_ns, abort_flag);
+        if (ok) {
+            tc_fence_after();
+            const int rows = (int)span.len - 32 * q4;
+            const size_t row0 = ((size_t)(span.start + 32 * q4) * Hk + kh) * D;
+            unsigned char *stage = sm.own[half] + q4 * 4096;   // K and V have been read
+            // 128 features: each half takes 64 of both; 64 features: one tensor each
+            if (NP == 2 || half == 0)
+                store_rows64(t_dv + lane_off + 64 * (NP == 2 ? half : 0), 1.0f, stage, dv + row0 + 64 * (NP == 2 ? half : 0),
+                             (size_t)Hk * D, rows, lane);
+            if (NP == 2 || half == 1)
+                store_rows64(t_dk + lane_off + 64 * (NP == 2 ? half : 0), scale, stage, dk + row0 + 64 * (NP == 2 ? half : 0),
+                             (size_t)Hk * D, rows, lane);
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x24u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t go(const AttnProblem &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+               const CUtensorMap &mdo, const __nv_bfloat16 *o, const __nv_bfloat16 *dO, const float *lse,
+               __nv_bfloat16 *dq, __nv_bfloat16 *dk, __nv_bfloat16 *dv, float *delta)
+{
+    const size_t smem = sizeof(BwdSmem<D>);
+    cudaError_t err = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(attn_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t n_slots = (p.tokens + BT - 1) / BT + p.n_docs;
+    if (n_slots * p.Hq > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const uint64_t ns = g_wait_ns.load();
+    const int stall = g_test_stall[BDLA_KERNEL_ATTN_BWD].load(), group = p.Hq / p.Hk;
+    attn_dq_kernel<D><<<(unsigned)(n_slots * p.Hq), kThreads, smem, p.stream>>>(
+        mq, mk, mv, mdo, o, dO, lse, p.cu, p.n_docs, p.T, p.tokens, p.Hq, group, (int)n_slots, p.scale, dq, delta, p.st,
+        ns, stall);
+    err = cudaGetLastError();
+    if (err != cudaSuccess)
+        return err;
+    attn_dkv_kernel<D><<<(unsigned)(n_slots * p.Hk), kThreads, smem, p.stream>>>(
+        mq, mk, mv, mdo, lse, delta, p.cu, p.n_docs, p.T, p.tokens, p.Hk, group, p.scale, dk, dv, p.st, ns, stall);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -127,23 +625,15 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, const __nv_bfloat16 *q, const 
                             const __nv_bfloat16 *dO, __nv_bfloat16 *dq, __nv_bfloat16 *dk, __nv_bfloat16 *dv,
                             float *delta)
 {
-    const cudaError_t err = launch_doc_report(p);
-    if (err != cudaSuccess || p.tokens == 0)
-        return err;
-    const unsigned gq = (unsigned)((p.tokens * p.Hq + 3) / 4), gk = (unsigned)((p.tokens * p.Hk + 3) / 4);
-#define BDLA_GO(D_)                                                                                                  \
-    do {                                                                                                             \
-        attn_dq_kernel<D_><<<gq, 128, 0, p.stream>>>(q, k, v, o, lse, dO, p.cu, p.n_docs, p.T, p.tokens, p.Hq, p.Hk, \
-                                                     p.scale, dq, delta);                                            \
-        attn_dkv_kernel<D_><<<gk, 128, 0, p.stream>>>(q, k, v, lse, dO, delta, p.cu, p.n_docs, p.T, p.tokens, p.Hq,  \
-                                                      p.Hk, p.scale, dk, dv);                                        \
-    } while (0)
-    if (p.d == 64)
-        BDLA_GO(64);
-    else
-        BDLA_GO(128);
-#undef BDLA_GO
-    return cudaGetLastError();
+    KernelMark mark_(BDLA_KERNEL_ATTN_BWD, p.stream);
+    if (p.tokens == 0)
+        return launch_doc_report(p);
+    CUtensorMap mq, mk, mv, mdo;
+    if (!make_token_map(&mq, q, p.d, p.Hq, p.tokens) || !make_token_map(&mk, k, p.d, p.Hk, p.tokens) ||
+        !make_token_map(&mv, v, p.d, p.Hk, p.tokens) || !make_token_map(&mdo, dO, p.d, p.Hq, p.tokens))
+        return cudaErrorInvalidValue;
+    return p.d == 64 ? go<64>(p, mq, mk, mv, mdo, o, dO, lse, dq, dk, dv, delta)
+                     : go<128>(p, mq, mk, mv, mdo, o, dO, lse, dq, dk, dv, delta);
 }
 
 }  // namespace bdla

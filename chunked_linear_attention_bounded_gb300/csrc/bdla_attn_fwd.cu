@@ -34,25 +34,18 @@
 // never enters a sum.
 #include <cudaTypedefs.h>
 
-#include "bdla_attn_internal.h"
-#include "bdla_sm100.cuh"
+#include "bdla_attn_sm100.cuh"
 
 namespace bdla {
-
-bool make_token_map(CUtensorMap *map, const void *ptr, int d, int H, int64_t tokens);
 
 namespace {
 
 using namespace sm100;
+using namespace attn;
 
-constexpr int BT = 128;                          // rows of a tile
 constexpr int kPairBlocks = 2;                   // query tiles of a CTA
 constexpr int kThreads = 64 + kPairBlocks * BT;  // loader, MMA issuer, softmax
-constexpr uint32_t kPanel = 16384;               // 128 rows x 128 swizzled bytes
 constexpr float kSlack = 8.0f;                   // log2 of how far weights may exceed 1
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// drains of a CTA's own copies and MMAs before it exits keep the full limit
-constexpr uint64_t kWaitNs = kDefaultWaitNs;
 
 template <int D> struct FwdSmem {
     static constexpr int kPanels = D / 64;
@@ -67,15 +60,7 @@ template <int D> struct FwdSmem {
     int abort_flag;
 };
 
-constexpr size_t kMaxSmem = 232448;   // 227 KB opt-in shared memory per CTA
 static_assert(sizeof(FwdSmem<128>) <= kMaxSmem && sizeof(FwdSmem<64>) <= kMaxSmem, "shared memory of a CTA");
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -90,9 +75,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0 && cu != nullptr)
-        for (int n = tid; n < n_docs; n += kThreads)
-            if (cu[n + 1] < cu[n] || (n == 0 && cu[0] != 0) || (n == n_docs - 1 && cu[n_docs] != tokens))
-                set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
+        check_offsets(cu, n_docs, tokens, st);
     // heads fastest, so that the CTAs in flight share keys; late (long) query
     // blocks first, so that the short ones fill the end
     const int h = blockIdx.x % Hq;
@@ -170,9 +153,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 *abort_flag = 1;
                 set_status(st, BDLA_ERR_TIMEOUT, 0x10u);
                 // the copies this thread started land before the CTA exits
-                mbar_wait(&sm.full_q, 0, kWaitNs);
+                mbar_wait(&sm.full_q, 0, kDrainNs);
                 for (int it = issued > NS ? issued - NS : 0; it < issued; ++it)
-                    mbar_wait(&sm.full[it % NS], (it / NS) & 1, kWaitNs);
+                    mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
             }
         }
     } else if (warp == 1) {
@@ -231,7 +214,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             }
             // every MMA issued above has completed before TMEM is released
             umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, kWaitNs);
+            mbar_wait(&sm.drain, 0, kDrainNs);
         }
     } else {
         // ---------------------------------------------------------------- softmax
@@ -247,10 +230,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
-            ok = __all_sync(0xffffffffu, mbar_wait_lim(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(j & 1),
-                                                       &sm.wait_ns)) &&
-                 !*abort_flag;
-            ok = __all_sync(0xffffffffu, ok);
+            ok = warp_wait(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
             if (!ok)
                 break;
             tc_fence_after();
@@ -313,58 +293,29 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (j == n - 1 && valid < BT) {
                 // this tile alone reads the document's last values: clear the rows past the end
                 const int it = 2 * j + 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns));
+                ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag);
                 if (!ok)
                     break;
-                for (int e = r; e < (BT - valid) * 8 * NP; e += BT) {
-                    const int p = e / ((BT - valid) * 8), f = e % ((BT - valid) * 8);
-                    *reinterpret_cast<uint4 *>(sm.ring[it % NS] + p * kPanel + (valid + (f >> 3)) * 128 + (f & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
+                clear_rows(sm.ring[it % NS], NP, valid, r, BT);
                 fence_proxy_async_smem();
             }
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.p_ready[w]);
         }
-        if (ok && n > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_lim(&sm.o_done[w], 0, &sm.wait_ns)) && !*abort_flag;
-            ok = __all_sync(0xffffffffu, ok);
-        }
+        if (ok && n > 0)
+            ok = warp_wait(&sm.o_done[w], 0, &sm.wait_ns, abort_flag);
         if (ok && n > 0) {
             tc_fence_after();
             const int64_t t0 = span.start + w * BT;
             if (r < valid)
                 lse[(int64_t)h * tokens + t0 + r] = (mc + log2f(l)) * kLn2;
             const float inv = 1.0f / l;
-            // a warp stages its own 32 rows of 128 bytes in its tile's queries (read by now), then writes whole rows
-            uint4 *stage = reinterpret_cast<uint4 *>(sm.q[w] + q4 * 4096);
+            // the tile's queries have been read: a warp stages its own 32 rows of 128 bytes there
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                uint32_t y[2][32];
-                tmem_ld32(t_o + 64 * p, y[0]);
-                tmem_ld32(t_o + 64 * p + 32, y[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = pack_bf16(__uint_as_float(y[k >> 2][8 * (k & 3) + 2 * i]) * inv,
-                                         __uint_as_float(y[k >> 2][8 * (k & 3) + 2 * i + 1]) * inv);
-                    stage[lane * 8 + (k ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-                __syncwarp();
-                __nv_bfloat16 *dst = o + ((size_t)(t0 + 32 * q4) * Hq + h) * D + p * 64;
-#pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int row = 4 * it + (lane >> 3), c8 = lane & 7;
-                    const uint4 v = stage[row * 8 + (c8 ^ (row & 7))];
-                    if (32 * q4 + row < valid)
-                        *reinterpret_cast<uint4 *>(dst + (size_t)row * Hq * D + 8 * c8) = v;
-                }
-                __syncwarp();
-            }
+            for (int p = 0; p < NP; ++p)
+                store_rows64(t_o + 64 * p, inv, sm.q[w] + q4 * 4096, o + ((size_t)(t0 + 32 * q4) * Hq + h) * D + p * 64,
+                             (size_t)Hq * D, valid - 32 * q4, lane);
         }
         if (!ok) {
             *abort_flag = 1;
@@ -382,9 +333,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 // The check of a packed call that has no tokens (and so no attention CTA).
 __global__ void doc_report_kernel(const int32_t *cu, int n_docs, int64_t tokens, DeviceStatus *st)
 {
-    for (int n = threadIdx.x; n < n_docs; n += blockDim.x)
-        if (cu[n + 1] < cu[n] || (n == 0 && cu[0] != 0) || (n == n_docs - 1 && cu[n_docs] != tokens))
-            set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
+    check_offsets(cu, n_docs, tokens, st);
 }
 
 template <int D>

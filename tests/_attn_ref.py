@@ -8,7 +8,7 @@ import torch
 
 H = 2.0 ** -8      # half a step of bf16, relative
 S = 2.0 ** -14     # a few hundred steps of fp32: sums of d products, exponentials, row sums
-TINY = 2.0 ** -126  # relative steps hold for normal numbers of bf16 and fp32; below the smallest, results may be 0
+TINY = 2.0 ** -126  # relative steps hold for normal numbers of bf16 and fp32: below the smallest, a weight may be 0
 F64 = torch.float64
 
 
@@ -44,7 +44,7 @@ def attn(q, k, v, scale, cu=None, dO=None):
             p = torch.exp(x - lse[:, None])
             o = p @ vv
             out["o"][0][r, h] = o
-            out["o"][1][r, h] = H * o.abs() + (H + S) * (p @ vv.abs())
+            out["o"][1][r, h] = H * o.abs() + (H + S) * (p @ vv.abs()) + TINY * vv.abs().sum(0)
             out["lse"][0][h, r] = lse
             out["lse"][1][h, r] = 2.0 ** -17 * (1 + lse.abs() + amp.amax(1))
             if dO is None:
@@ -55,13 +55,13 @@ def attn(q, k, v, scale, cu=None, dO=None):
             # delta is taken from the o that the forward rounded
             d_err = H * (g * o).abs().sum(1, keepdim=True)
             ds = p * (dp - delta)
-            ds_err = H * ds.abs() + p * (d_err + S * (g.abs() @ vv.abs().T + delta.abs()))
+            ds_err = H * ds.abs() + p * (d_err + S * (g.abs() @ vv.abs().T + delta.abs())) + TINY * (dp - delta).abs()
             out["dq"][0][r, h] = scale * (ds @ kk)
             out["dq"][1][r, h] = scale * (ds_err @ kk.abs())
             out["dk"][0][r, h // G] += scale * (ds.T @ qq)
             out["dk"][1][r, h // G] += scale * (ds_err.T @ qq.abs())
             out["dv"][0][r, h // G] += p.T @ g
-            out["dv"][1][r, h // G] += (H + S) * (p.T @ g.abs())
+            out["dv"][1][r, h // G] += (H + S) * (p.T @ g.abs()) + TINY * g.abs().sum(0)
     for x in ("dq", "dk", "dv"):
         if x in out:
             out[x][1].add_(H * out[x][0].abs())
