@@ -227,6 +227,8 @@ bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, 
         return BDLA_ERR_SHAPE;
     if (d.T > 64)
         return BDLA_ERR_UNSUPPORTED;
+    if ((int64_t)d.B * d.T * d.Hq > INT32_MAX)   // rows are a grid extent
+        return BDLA_ERR_TOO_LARGE;
     BDLA_TRY(check_scale(scale));
     BDLA_TRY(check_cache(c));
     if (!q || !o || !lse)

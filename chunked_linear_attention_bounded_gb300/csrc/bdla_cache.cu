@@ -72,65 +72,395 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
     }
 }
 
-// One warp per (sequence, new token, query head), each lane d/32 features.
+// ---------------------------------------------------------------- attention over the cache
+//
+//   s = scale q . k over the visible positions,  o = (sum_t e^{s_t - m} v_t) / sum_t e^{s_t - m}
+//
+// A key head's cache is read once for all rows that use it: the new tokens of a
+// sequence times the query heads of the group, in blocks of 16, 32 or 64 rows
+// (the smallest that holds them).  With few rows the pass is bound by HBM: 16
+// rows of weights cost nothing beside 512 bytes of keys and values a position,
+// so the products run as warp MMAs (m16n8k16) straight from the tiles that
+// cp.async brings in, three tiles of 64 positions in flight.  A CTA's four
+// warps split the rows first and the positions of the tile with what is left,
+// and join through shared memory at the end.
+//
+// The long axis is split: every sequence into at most `ns` pieces of equal
+// length, at least kMinSplit positions each, as the lengths on the device say.
+// A sequence of one piece is finished by its CTA; the others leave an fp32 sum
+// per row and piece, which combine_kernel joins in the order of the pieces.
+//
+// Positions are looked up in the page table two tiles ahead of their load, by
+// 64 threads into shared memory, so any page size works and no tile has to end
+// with a page.  A position that nobody may see is not loaded: its rows are
+// zeros.
+constexpr int kKeys = 64;         // positions of a tile
+constexpr int kCStages = 3;
+constexpr int kCThreads = 128;
+constexpr int kMinSplit = 128;
+
+template <int D> struct CachedSmem {
+    alignas(128) unsigned char kv[kCStages][2][kKeys * D * 2];
+    int64_t row[4][kKeys];        // cache row of a tile's positions, -1: not seen
+    uint32_t valid[4][2];
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// How a sequence's positions are cut.
+struct Cut {
+    int len, end;   // committed positions; all positions inside the table
+    int size, used; // positions a piece, pieces
+};
+__device__ __forceinline__ Cut cut_of(const bdla_cache &c, int b, int T, int ns)
+{
+    Cut k;
+    k.len = c.lens[b];
+    const int64_t cap = (int64_t)c.max_pages * c.page, all = (int64_t)k.len + T;
+    k.end = k.len < 0 ? 0 : (int)(all < cap ? all : cap);
+    const int even = (int)(((int64_t)k.end + ns - 1) / ns);
+    k.size = even < kMinSplit ? kMinSplit : (even + kKeys - 1) / kKeys * kKeys;
+    k.used = k.end > 0 ? (k.end + k.size - 1) / k.size : 1;
+    return k;
+}
+
+// New tokens that token i sees (bit j: token j).
+__device__ __forceinline__ uint64_t sees(const uint64_t *tree, int64_t b, int T, int i)
+{
+    const uint64_t m = tree != nullptr ? tree[b * T + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+    return T < 64 ? m & ((1ull << T) - 1) : m;
+}
+
+template <int D, int WR>
+__global__ void __launch_bounds__(kCThreads)
+cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_cache c,
+              const uint64_t *__restrict__ tree, float scale, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
+              float *__restrict__ part_o, float *__restrict__ part_ml, int T, int Hq, int Hk, int row_blocks, int ns,
+              DeviceStatus *st)
+{
+    constexpr int WK = 4 / WR;          // warps along the positions
+    constexpr int KW = kKeys / WK;      // positions of a warp
+    constexpr int MR = 16 * WR;         // rows of the CTA
+    constexpr int kChunks = D / 8;      // 16-byte chunks of a row
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    CachedSmem<D> &sm = *reinterpret_cast<CachedSmem<D> *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wr = warp % WR, wk = warp / WR;
+    // heads of one position lie next to each other in the cache: keep them together in time
+    int idx = blockIdx.x;
+    const int rb = idx % row_blocks;
+    idx /= row_blocks;
+    const int kh = idx % Hk;
+    idx /= Hk;
+    const int piece = idx % ns, b = idx / ns;
+    const Cut cut = cut_of(c, b, T, ns);
+    if (piece >= cut.used)
+        return;
+    if (piece == 0 && kh == 0 && rb == 0 && tid == 0 && (cut.len < 0 || (int64_t)cut.len + T > (int64_t)c.max_pages * c.page))
+        set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
+    const int G = Hq / Hk, R = T * G;
+    const int k0 = piece * cut.size, k1 = min(cut.end, k0 + cut.size);
+    const int nt = (k1 - k0 + kKeys - 1) / kKeys;
+    const int32_t *table = c.pages + (int64_t)b * c.max_pages;
+    const bool drafts = k1 > cut.len;   // the piece holds new tokens
+    uint64_t seen = 0;                  // new tokens that any of the sequence's sees
+    if (drafts) {
+        for (int i = lane; i < T; i += 32)
+            seen |= sees(tree, b, T, i);
+        for (int w = 16; w > 0; w >>= 1)
+            seen |= __shfl_xor_sync(0xffffffffu, seen, w);
+    }
+
+    // page table entry of position t (a tile's 64 positions, by the first 64 threads)
+    auto lookup = [&](int t) { return t < k1 ? table[t / c.page] : -1; };
+    auto place = [&](int n, int t, int pg) {
+        bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
+        if (live && (pg < 0 || pg >= c.n_pages)) {
+            set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
+            live = false;
+        }
+        sm.row[n & 3][tid] = live ? (int64_t)pg * c.page + t % c.page : -1;
+        const uint32_t m = __ballot_sync(0xffffffffu, live);
+        if (lane == 0)
+            sm.valid[n & 3][tid >> 5] = m;
+    };
+    auto load = [&](int n) {
+        if (n < nt) {
+            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(sm.kv[n % kCStages][0]));
+#pragma unroll
+            for (int u = 0; u < kKeys * kChunks / kCThreads; ++u) {
+                const int e = tid + u * kCThreads, r = e / kChunks, ch = e % kChunks;
+                const int64_t row = sm.row[n & 3][r];
+                const int64_t off = ((row < 0 ? 0 : row) * Hk + kh) * D + 8 * ch;
+                const uint32_t to = dst + (r * kChunks + (ch ^ (r & 7))) * 16;
+                cp16(to, static_cast<const __nv_bfloat16 *>(c.k) + off, row >= 0);
+                cp16(to + kKeys * D * 2, static_cast<const __nv_bfloat16 *>(c.v) + off, row >= 0);
+            }
+        }
+        cp_commit();
+    };
+    if (tid < kKeys)
+        for (int n = 0; n < 3; ++n) {
+            const int t = k0 + n * kKeys + tid;
+            place(n, t, lookup(t));
+        }
+    __syncthreads();
+    load(0);
+    load(1);
+
+    // query fragments: rows lane/4 and lane/4 + 8 of the warp's 16
+    const int r0 = rb * MR + 16 * wr + (lane >> 2), r1 = r0 + 8;
+    const int i0 = min(r0, R - 1) / G, i1 = min(r1, R - 1) / G;
+    const __nv_bfloat16 *qa = q + (((int64_t)b * T + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qb = q + (((int64_t)b * T + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
+    uint32_t fq[D / 16][4];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        fq[ks][0] = *reinterpret_cast<const uint32_t *>(qa + 16 * ks);
+        fq[ks][1] = *reinterpret_cast<const uint32_t *>(qb + 16 * ks);
+        fq[ks][2] = *reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8);
+        fq[ks][3] = *reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8);
+    }
+    const uint64_t see0 = drafts ? sees(tree, b, T, i0) : 0, see1 = drafts ? sees(tree, b, T, i1) : 0;
+    const float cs = scale * 1.4426950408889634f;
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+
+    for (int n = 0; n < nt; ++n) {
+        cp_wait<kCStages - 2>();
+        __syncthreads();   // tile n is here, tile n - 1 is done with, the rows of tile n + 2 are known
+        load(n + 2);
+        const int t3 = k0 + (n + 3) * kKeys + tid;
+        const int pg3 = tid < kKeys ? lookup(t3) : -1;
+        const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(sm.kv[n % kCStages][0]));
+        const uint32_t sv = sk + kKeys * D * 2;
+        float s[KW / 8][4];
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int nb = 0; nb < KW / 16; ++nb) {
+                const int row = wk * KW + nb * 16 + (lane & 7) + ((lane >> 4) << 3), ch = 2 * ks + ((lane >> 3) & 1);
+                uint32_t f[4];
+                ldm4(f, sk + (row * kChunks + (ch ^ (row & 7))) * 16);
+                mma16816(s[2 * nb], fq[ks], f[0], f[1]);
+                mma16816(s[2 * nb + 1], fq[ks], f[2], f[3]);
+            }
+        const uint64_t ok = (uint64_t)sm.valid[n & 3][0] | ((uint64_t)sm.valid[n & 3][1] << 32);
+        const int t0 = k0 + n * kKeys;
+        if (ok != ~0ull || t0 + kKeys > cut.len) {
+#pragma unroll
+            for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = wk * KW + 8 * i + 2 * (lane & 3) + u, j = t0 + kk - cut.len;
+                    const bool live = (ok >> kk) & 1;
+                    if (!(live && (j < 0 || ((see0 >> j) & 1))))
+                        s[i][u] = -INFINITY;
+                    if (!(live && (j < 0 || ((see1 >> j) & 1))))
+                        s[i][2 + u] = -INFINITY;
+                }
+        }
+        float x0 = s[0][0], x1 = s[0][2];
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i) {
+            x0 = fmaxf(x0, fmaxf(s[i][0], s[i][1]));
+            x1 = fmaxf(x1, fmaxf(s[i][2], s[i][3]));
+        }
+#pragma unroll
+        for (int w = 1; w < 4; w <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
+        }
+        if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float a0 = n0 == m0 ? 1.0f : ex2((m0 - n0) * cs), a1 = n1 == m1 ? 1.0f : ex2((m1 - n1) * cs);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                acc[i][0] *= a0;
+                acc[i][1] *= a0;
+                acc[i][2] *= a1;
+                acc[i][3] *= a1;
+            }
+        }
+        // rows that have seen nothing yet: every weight is e^(-inf)
+        const float b0 = m0 == -INFINITY ? 0.0f : m0 * cs, b1 = m1 == -INFINITY ? 0.0f : m1 * cs;
+#pragma unroll
+        for (int nb = 0; nb < KW / 16; ++nb) {
+            uint32_t fp[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float *x = s[2 * nb + u];
+                const float p0 = ex2(fmaf(x[0], cs, -b0)), p1 = ex2(fmaf(x[1], cs, -b0));
+                const float p2 = ex2(fmaf(x[2], cs, -b1)), p3 = ex2(fmaf(x[3], cs, -b1));
+                l0 += p0 + p1;
+                l1 += p2 + p3;
+                fp[2 * u] = sm100::pack_bf16(p0, p1);
+                fp[2 * u + 1] = sm100::pack_bf16(p2, p3);
+            }
+            const int row = wk * KW + nb * 16 + (lane & 15);
+#pragma unroll
+            for (int dn = 0; dn < D / 16; ++dn) {
+                const int ch = 2 * dn + (lane >> 4);
+                uint32_t f[4];
+                ldm4t(f, sv + (row * kChunks + (ch ^ (row & 7))) * 16);
+                mma16816(acc[2 * dn], fp, f[0], f[1]);
+                mma16816(acc[2 * dn + 1], fp, f[2], f[3]);
+            }
+        }
+        if (tid < kKeys)
+            place(n + 3, t3, pg3);
+    }
+    cp_wait<0>();
+    __syncthreads();   // the tiles' memory is free for the join
+
+    float *jo = reinterpret_cast<float *>(sm.kv[0][0]);          // [WK][MR][D]
+    float *jm = jo + WK * MR * D;                                // [WK][MR][2]
+#pragma unroll
+    for (int w = 1; w < 4; w <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+    }
+    {
+        const int ra = 16 * wr + (lane >> 2);
+        float *a = jo + (wk * MR + ra) * D + 2 * (lane & 3), *e = a + 8 * D;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            *reinterpret_cast<float2 *>(a + 8 * i) = make_float2(acc[i][0], acc[i][1]);
+            *reinterpret_cast<float2 *>(e + 8 * i) = make_float2(acc[i][2], acc[i][3]);
+        }
+        if ((lane & 3) == 0) {
+            *reinterpret_cast<float2 *>(jm + 2 * (wk * MR + ra)) = make_float2(m0, l0);
+            *reinterpret_cast<float2 *>(jm + 2 * (wk * MR + ra + 8)) = make_float2(m1, l1);
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < MR * (D / 4); e += kCThreads) {
+        const int r = e / (D / 4), d4 = 4 * (e % (D / 4)), row = rb * MR + r;
+        if (row >= R)
+            break;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w)
+            m = fmaxf(m, jm[2 * (w * MR + r)]);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const float2 ml = *reinterpret_cast<const float2 *>(jm + 2 * (w * MR + r));
+            const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * cs);
+            const float4 y = *reinterpret_cast<const float4 *>(jo + (w * MR + r) * D + d4);
+            l = fmaf(ml.y, f, l);
+            v.x = fmaf(y.x, f, v.x);
+            v.y = fmaf(y.y, f, v.y);
+            v.z = fmaf(y.z, f, v.z);
+            v.w = fmaf(y.w, f, v.w);
+        }
+        if (cut.used > 1) {
+            const int64_t at = (((int64_t)b * Hk + kh) * ns + piece) * R + row;
+            *reinterpret_cast<float4 *>(part_o + at * D + d4) = v;
+            if (d4 == 0)
+                *reinterpret_cast<float2 *>(part_ml + 2 * at) = make_float2(m, l);
+        } else {
+            const int64_t at = ((int64_t)b * T + row / G) * Hq + kh * G + row % G;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            *reinterpret_cast<uint2 *>(o + at * D + d4) =
+                make_uint2(sm100::pack_bf16(v.x * inv, v.y * inv), sm100::pack_bf16(v.z * inv, v.w * inv));
+            if (d4 == 0)
+                lse[at] = l == 0.0f ? -INFINITY : fmaf(m, scale, logf(l));
+        }
+    }
+}
+
+// Joins the pieces of one row: one CTA a row, four warps over the pieces.
 template <int D>
 __global__ void __launch_bounds__(128)
-attn_cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_cache c,
-                   const uint64_t *__restrict__ tree, float scale, __nv_bfloat16 *__restrict__ o,
-                   float *__restrict__ lse, int T, int Hq, int Hk, int64_t total, DeviceStatus *st)
+combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ml, const __grid_constant__ bdla_cache c,
+               float scale, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int T, int Hq, int Hk, int ns)
 {
     constexpr int E = D / 32;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (item >= total)
-        return;
-    const int h = (int)(item % Hq), i = (int)(item / Hq % T), b = (int)(item / Hq / T);
-    const int kh = h / (Hq / Hk);
-    const int32_t *table = c.pages + (int64_t)b * c.max_pages;
-    int len = c.lens[b];
-    const int64_t cap = (int64_t)c.max_pages * c.page;
-    if (len < 0 || len + (int64_t)T > cap) {
-        if (lane == 0)
-            set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
-    }
-    uint64_t see = tree != nullptr ? tree[(int64_t)b * T + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-    if (T < 64)
-        see &= (1ull << T) - 1;
-    int end = (int)(len + (int64_t)T < cap ? len + (int64_t)T : cap);
-    if (len < 0)
-        end = 0;
-    float x[E], acc[E], m = -INFINITY, z = 0.0f;
-    for (int e = 0; e < E; ++e) {
-        x[e] = bf2f(q[item * D + lane * E + e]) * scale;
-        acc[e] = 0.0f;
-    }
-    for (int t = 0; t < end; ++t) {
-        if (t >= len && !((see >> (t - len)) & 1))
-            continue;
-        const int64_t row = cache_row(c, table, t);
-        if (row < 0) {
-            if (lane == 0)
-                set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
-            continue;
-        }
-        const int64_t off = (row * Hk + kh) * D + lane * E;
-        float s = 0.0f;
-        for (int e = 0; e < E; ++e)
-            s = fmaf(x[e], bf2f(static_cast<const __nv_bfloat16 *>(c.k)[off + e]), s);
-        for (int w = 16; w > 0; w >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float mn = fmaxf(m, s);
-        const float a = m == -INFINITY ? 0.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(s - mn);
-        z = z * a + p;
-        for (int e = 0; e < E; ++e)
-            acc[e] = acc[e] * a + p * bf2f(static_cast<const __nv_bfloat16 *>(c.v)[off + e]);
-        m = mn;
-    }
-    const float inv = z > 0.0f ? 1.0f / z : (z == 0.0f ? 0.0f : z);
-    for (int e = 0; e < E; ++e)
-        o[item * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
+    __shared__ float red_m[4], red_l[4], red_o[4][D];
+    const int64_t at = blockIdx.x;
+    const int h = (int)(at % Hq), i = (int)(at / Hq % T), b = (int)(at / Hq / T);
+    const Cut cut = cut_of(c, b, T, ns);
+    if (cut.used < 2)
+        return;   // finished by its own CTA
+    const int G = Hq / Hk, kh = h / G, R = T * G, row = i * G + h % G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t base = ((int64_t)b * Hk + kh) * ns;
+    const float cs = scale * 1.4426950408889634f;
+    float m = -INFINITY;
+    for (int s = threadIdx.x; s < cut.used; s += 128)
+        m = fmaxf(m, part_ml[2 * ((base + s) * R + row)]);
+    for (int w = 16; w > 0; w >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
     if (lane == 0)
-        lse[item] = z == 0.0f ? -INFINITY : m + logf(z);
+        red_m[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
+    float l = 0.0f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        v[e] = 0.0f;
+#pragma unroll 4
+    for (int s = warp; s < cut.used; s += 4) {
+        const int64_t p = (base + s) * R + row;
+        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + 2 * p);
+        const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * cs);
+        l = fmaf(ml.y, f, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] = fmaf(part_o[p * D + lane + 32 * e], f, v[e]);
+    }
+    if (lane == 0)
+        red_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        red_o[warp][lane + 32 * e] = v[e];
+    __syncthreads();
+    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (threadIdx.x < D)
+        o[at * D + threadIdx.x] = __float2bfloat16_rn(((red_o[0][threadIdx.x] + red_o[1][threadIdx.x]) +
+                                                       (red_o[2][threadIdx.x] + red_o[3][threadIdx.x])) * inv);
+    if (threadIdx.x == 0)
+        lse[at] = l == 0.0f ? -INFINITY : fmaf(m, scale, logf(l));
 }
 
 }  // namespace
@@ -149,20 +479,78 @@ cudaError_t launch_cache_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v, 
     return cudaGetLastError();
 }
 
-int cached_splits(const bdla_attn_dims &, int64_t) { return 1; }
-size_t cached_partial_bytes(const bdla_attn_dims &, int) { return 0; }
+// Rows of a CTA: the smallest block that holds a key head's rows, at most 64.
+static int cached_rows(const bdla_attn_dims &d)
+{
+    const int R = d.T * (d.Hq / d.Hk);
+    return R <= 16 ? 16 : R <= 32 ? 32 : 64;
+}
+
+// Pieces of a sequence: enough for eight CTAs an SM, and pieces of at most 2048
+// positions so that long and short sequences end together; no more than there
+// are kMinSplit positions, than 256 MB of partial sums, or than keep the grid
+// within 2^17 CTAs (more only where the sequences alone are more).
+int cached_splits(const bdla_attn_dims &d, int64_t max_keys)
+{
+    const int mr = cached_rows(d), R = d.T * (d.Hq / d.Hk);
+    const int64_t units = (int64_t)d.B * d.Hk * ((R + mr - 1) / mr);
+    int64_t ns = ((int64_t)sm_count() * 8 + units - 1) / units;
+    const int64_t even = (max_keys + 2047) / 2048;
+    ns = ns > even ? ns : even;
+    const int64_t most[3] = {(max_keys + kMinSplit - 1) / kMinSplit,
+                             ((int64_t)256 << 20) / ((int64_t)d.B * d.T * d.Hq * (d.d + 2) * 4), (1 << 17) / units};
+    for (int i = 0; i < 3; ++i)
+        ns = ns < most[i] ? ns : most[i];
+    return ns < 1 ? 1 : (int)ns;
+}
+
+size_t cached_partial_bytes(const bdla_attn_dims &d, int splits)
+{
+    return splits > 1 ? (size_t)splits * d.B * d.T * d.Hq * (d.d + 2) * 4 : 0;
+}
+
+template <int D, int WR>
+static cudaError_t cached_go(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,
+                             __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int ns, void *partials,
+                             DeviceStatus *st, cudaStream_t stream)
+{
+    const int R = d.T * (d.Hq / d.Hk), row_blocks = (R + 16 * WR - 1) / (16 * WR);
+    const int64_t rows = (int64_t)d.B * d.T * d.Hq, grid = (int64_t)d.B * d.Hk * row_blocks * ns;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    float *part_o = static_cast<float *>(partials), *part_ml = part_o + (size_t)ns * rows * D;
+    const size_t smem = sizeof(CachedSmem<D>);
+    cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    cached_kernel<D, WR><<<(unsigned)grid, kCThreads, smem, stream>>>(q, c, tree, scale, o, lse, part_o, part_ml, d.T,
+                                                                      d.Hq, d.Hk, row_blocks, ns, st);
+    err = cudaGetLastError();
+    if (err != cudaSuccess || ns == 1)
+        return err;
+    combine_kernel<D><<<(unsigned)rows, 128, 0, stream>>>(part_o, part_ml, c, scale, o, lse, d.T, d.Hq, d.Hk, ns);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,
-                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int, void *,
+                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int splits, void *partials,
                                DeviceStatus *st, cudaStream_t stream)
 {
-    const int64_t total = (int64_t)d.B * d.T * d.Hq;
-    const unsigned grid = (unsigned)((total + 3) / 4);
-    if (d.d == 64)
-        attn_cached_kernel<64><<<grid, 128, 0, stream>>>(q, c, tree, scale, o, lse, d.T, d.Hq, d.Hk, total, st);
-    else
-        attn_cached_kernel<128><<<grid, 128, 0, stream>>>(q, c, tree, scale, o, lse, d.T, d.Hq, d.Hk, total, st);
-    return cudaGetLastError();
+    const int mr = cached_rows(d);
+#define BDLA_GO(D_, W_) return cached_go<D_, W_>(q, c, tree, scale, o, lse, d, splits, partials, st, stream)
+    if (d.d == 64) {
+        if (mr == 16)
+            BDLA_GO(64, 1);
+        if (mr == 32)
+            BDLA_GO(64, 2);
+        BDLA_GO(64, 4);
+    }
+    if (mr == 16)
+        BDLA_GO(128, 1);
+    if (mr == 32)
+        BDLA_GO(128, 2);
+    BDLA_GO(128, 4);
+#undef BDLA_GO
 }
 
 }  // namespace bdla

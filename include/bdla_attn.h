@@ -126,8 +126,8 @@ bdla_status bdla_cache_append(const void *k, const void *v, bdla_cache c, const 
  * NULL means the tokens j <= i (T = 1: plain decoding).  A token that sees
  * nothing gets o = 0 and lse = -inf.
  *   q, o   bf16 [B, T, Hq, d];   lse  fp32 [B, T, Hq]
- * What lies in the cache outside the visible positions is not read into the
- * result, whatever its bits.  Positions past the page table, pages outside
+ * What lies in the cache outside the positions that a sequence's new tokens
+ * see is not read, whatever its bits.  Positions past the page table, pages outside
  * the cache and negative lens are recorded as BDLA_ERR_DEVICE and not seen.
  */
 bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, float scale, void *o, float *lse,
