@@ -591,13 +591,28 @@ def bwd_delta(q, k, v, a, beta, dO, b: float = -5.0, h0=None, dhT=None, cu_seqle
 
 
 # ---------------------------------------------------------------- softmax layer
-def _on(t: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
-    """A contiguous CUDA tensor of this type and shape, on the device of `like`."""
+# A decode step makes these calls once a layer, and their kernels run for a few
+# microseconds: every check below is one comparison on the good path.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _on(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape on `device` (a CUDA device)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return t.data_ptr()
     _check(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _new(shapes, dtypes, device, stream):
@@ -608,29 +623,34 @@ def _new(shapes, dtypes, device, stream):
         return [torch.empty(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
 
 
-def _attn_ws(op, d: AttnDims, n_docs, max_keys, ws, device, stream) -> Workspace:
-    need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
-    if need == 0:
-        raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_attn")
-    if ws is not None and need <= ws.nbytes:
-        return ws
-    if stream is None:
-        return Workspace(need, device) if ws is None else ws.ensure(need)
-    with torch.cuda.stream(stream):
-        return Workspace(need, device) if ws is None else ws.ensure(need)
+def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call):
+    """Makes the call with the caller's workspace; one that is missing or too
+    small is made or grown first, as the library's answer says."""
+    st = ERR_WORKSPACE if ws is None else call(ws.buf.data_ptr(), ws.nbytes)
+    if st == ERR_WORKSPACE:
+        need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
+        if need == 0:
+            raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_attn")
+        if stream is None:
+            ws = Workspace(need, device) if ws is None else ws.ensure(need)
+        else:
+            with torch.cuda.stream(stream):
+                ws = Workspace(need, device) if ws is None else ws.ensure(need)
+        st = call(ws.buf.data_ptr(), ws.nbytes)
+    if st:
+        raise BdlaError(st, where)
 
 
-def _documents(cu_seqlens, B, like):
+def _documents(cu_seqlens, B, device):
+    """(pointer, count) of packed documents, (None, 0) for fixed-length rows."""
     if cu_seqlens is None:
-        return 0
-    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    if cu_seqlens.device != like.device:
-        raise ValueError("cu_seqlens is on another device")
+        return None, 0
+    p = _on(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), device)
     if B != 1:
         raise ValueError("packed documents need B = 1")
     if cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens needs at least two offsets")
-    return cu_seqlens.numel() - 1
+    return p, cu_seqlens.numel() - 1
 
 
 def _strided(t: torch.Tensor, name: str):
@@ -657,20 +677,18 @@ def _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, e
     qt, qh = _strided(q, "q")
     kt, kh = _strided(k, "k")
     B, T, Hq, d = q.shape
-    if k.shape[0] != B or k.shape[1] != T or k.shape[3] != d:
+    Bk, Tk, Hk, dk = k.shape
+    if Bk != B or Tk != T or dk != d:
         raise ValueError("q and k shapes disagree")
-    if k.device != q.device:
+    device = q.device
+    if k.device != device:
         raise ValueError("q and k are on different devices")
-    _on(wq, "wq", torch.float32, (d,), q)
-    _on(wk, "wk", torch.float32, (d,), q)
-    n_docs = _documents(cu_seqlens, B, q)
-    if positions is not None:
-        _on(positions, "positions", torch.int32, (B, T), q)
-    a = QkNormArgs(q.data_ptr(), k.data_ptr(), qt, qh, kt, kh, wq.data_ptr(), wk.data_ptr(),
-                   None if positions is None else positions.data_ptr(),
-                   None if cu_seqlens is None else cu_seqlens.data_ptr(), base, eps,
-                   d if rotary is None else rotary, int(interleaved), n_docs)
-    return a, AttnDims(B, T, Hq, k.shape[2], d)
+    cu, n_docs = _documents(cu_seqlens, B, device)
+    a = QkNormArgs(q.data_ptr(), k.data_ptr(), qt, qh, kt, kh, _on(wq, "wq", torch.float32, (d,), device),
+                   _on(wk, "wk", torch.float32, (d,), device),
+                   None if positions is None else _on(positions, "positions", torch.int32, (B, T), device), cu, base,
+                   eps, d if rotary is None else rotary, int(interleaved), n_docs)
+    return a, AttnDims(B, T, Hq, Hk, d)
 
 
 def qk_norm(q, k, wq, wk, rotary: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
@@ -683,7 +701,7 @@ def qk_norm(q, k, wq, wk, rotary: Optional[int] = None, base: float = 10000.0, i
     than their own are the caller's to keep alive, as for every call here."""
     a, d = _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
     qn, kn = _new((q.shape, k.shape), (q.dtype, q.dtype), q.device, stream)
-    st = lib().bdla_qk_norm(a, _p(qn), _p(kn), d, _stream_handle(stream))
+    st = lib().bdla_qk_norm(a, qn.data_ptr(), kn.data_ptr(), d, _stream_of(q, stream))
     if st:
         raise BdlaError(st, "bdla_qk_norm")
     return qn, kn
@@ -696,26 +714,25 @@ def qk_norm_bwd(q, k, wq, wk, dqn, dkn, rotary: Optional[int] = None, base: floa
     Returns (dq, dk, dwq, dwk): bf16, bf16 and fp32 [d]."""
     a, d = _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
     code = _dtype_code(dqn.dtype)
-    _on(dqn, "dqn", dqn.dtype, q.shape, q)
-    _on(dkn, "dkn", dqn.dtype, k.shape, q)
+    gq = _on(dqn, "dqn", dqn.dtype, q.shape, q.device)
+    gk = _on(dkn, "dkn", dqn.dtype, k.shape, q.device)
     bf, f32 = torch.bfloat16, torch.float32
     dq, dk, dwq, dwk = _new((q.shape, k.shape, wq.shape, wk.shape), (bf, bf, f32, f32), q.device, stream)
-    ws = _attn_ws(ATTN_NORM_BWD, d, a.n_docs, 0, ws, q.device, stream)
-    st = lib().bdla_qk_norm_bwd(a, _p(dqn), _p(dkn), code, _p(dq), _p(dk), _p(dwq), _p(dwk), d, ws.ptr, ws.nbytes,
-                                _stream_handle(stream))
-    if st:
-        raise BdlaError(st, "bdla_qk_norm_bwd")
+    s = _stream_of(q, stream)
+    _with_ws("bdla_qk_norm_bwd", ATTN_NORM_BWD, d, a.n_docs, 0, ws, q.device, stream,
+             lambda p, n: lib().bdla_qk_norm_bwd(a, gq, gk, code, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(),
+                                                 dwk.data_ptr(), d, p, n, s))
     return dq, dk, dwq, dwk
 
 
-def _attn_dims(q, k, v):
+def _attn_args(q, k, v):
     _check(q, "q", torch.bfloat16, 4)
     B, T, Hq, d = q.shape
     _check(k, "k", torch.bfloat16, 4)
-    Hk = k.shape[2]
-    _on(k, "k", torch.bfloat16, (B, T, Hk, d), q)
-    _on(v, "v", torch.bfloat16, (B, T, Hk, d), q)
-    return AttnDims(B, T, Hq, Hk, d)
+    Hk, device = k.shape[2], q.device
+    shape = (B, T, Hk, d)
+    return (AttnDims(B, T, Hq, Hk, d), q.data_ptr(), _on(k, "k", torch.bfloat16, shape, device),
+            _on(v, "v", torch.bfloat16, shape, device))
 
 
 def attn_fwd(q, k, v, scale: Optional[float] = None, cu_seqlens=None, ws: Optional[Workspace] = None, stream=None):
@@ -723,14 +740,13 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, cu_seqlens=None, ws: Option
     [B, T, Hk, d] bf16, Hq a multiple of Hk; packed documents with B = 1 and
     cu_seqlens.  scale is 1/sqrt(d) unless given.  Returns (o, lse): o like q,
     lse fp32 [Hq, B*T]."""
-    d = _attn_dims(q, k, v)
-    n_docs = _documents(cu_seqlens, d.B, q)
+    d, pq, pk, pv = _attn_args(q, k, v)
+    cu, n_docs = _documents(cu_seqlens, d.B, q.device)
     o, lse = _new((q.shape, (d.Hq, d.B * d.T)), (q.dtype, torch.float32), q.device, stream)
-    ws = _attn_ws(ATTN_FWD, d, n_docs, 0, ws, q.device, stream)
-    st = lib().bdla_attn_fwd(_p(q), _p(k), _p(v), _p(cu_seqlens), n_docs, d.d ** -0.5 if scale is None else scale,
-                             _p(o), _p(lse), d, ws.ptr, ws.nbytes, _stream_handle(stream))
-    if st:
-        raise BdlaError(st, "bdla_attn_fwd")
+    scale = d.d ** -0.5 if scale is None else scale
+    s = _stream_of(q, stream)
+    _with_ws("bdla_attn_fwd", ATTN_FWD, d, n_docs, 0, ws, q.device, stream,
+             lambda p, n: lib().bdla_attn_fwd(pq, pk, pv, cu, n_docs, scale, o.data_ptr(), lse.data_ptr(), d, p, n, s))
     return o, lse
 
 
@@ -738,31 +754,27 @@ def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None
              stream=None):
     """Gradient of attn_fwd from its inputs, its (o, lse) and dO like o.
     Returns (dq, dk, dv), bf16.  The same inputs give the same bits."""
-    d = _attn_dims(q, k, v)
-    _on(o, "o", torch.bfloat16, q.shape, q)
-    _on(dO, "dO", torch.bfloat16, q.shape, q)
-    _on(lse, "lse", torch.float32, (d.Hq, d.B * d.T), q)
-    n_docs = _documents(cu_seqlens, d.B, q)
+    d, pq, pk, pv = _attn_args(q, k, v)
+    po = _on(o, "o", torch.bfloat16, q.shape, q.device)
+    pg = _on(dO, "dO", torch.bfloat16, q.shape, q.device)
+    pl = _on(lse, "lse", torch.float32, (d.Hq, d.B * d.T), q.device)
+    cu, n_docs = _documents(cu_seqlens, d.B, q.device)
     dq, dk, dv = _new((q.shape, k.shape, v.shape), (q.dtype,) * 3, q.device, stream)
-    ws = _attn_ws(ATTN_BWD, d, n_docs, 0, ws, q.device, stream)
-    st = lib().bdla_attn_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(dO), _p(cu_seqlens), n_docs,
-                             d.d ** -0.5 if scale is None else scale, _p(dq), _p(dk), _p(dv), d, ws.ptr, ws.nbytes,
-                             _stream_handle(stream))
-    if st:
-        raise BdlaError(st, "bdla_attn_bwd")
+    scale = d.d ** -0.5 if scale is None else scale
+    s = _stream_of(q, stream)
+    _with_ws("bdla_attn_bwd", ATTN_BWD, d, n_docs, 0, ws, q.device, stream,
+             lambda p, n: lib().bdla_attn_bwd(pq, pk, pv, po, pl, pg, cu, n_docs, scale, dq.data_ptr(), dk.data_ptr(),
+                                              dv.data_ptr(), d, p, n, s))
     return dq, dk, dv
 
 
-def _cache_args(kcache, vcache, pages, lens, B, like):
+def _cache_args(kcache, vcache, pages, lens, B, device):
     _check(kcache, "kcache", torch.bfloat16, 4)
-    _on(vcache, "vcache", torch.bfloat16, kcache.shape, like)
     _check(pages, "pages", torch.int32, 2)
-    _on(pages, "pages", torch.int32, (B, pages.shape[1]), like)
-    _on(lens, "lens", torch.int32, (B,), like)
-    if kcache.device != like.device:
-        raise ValueError("kcache is on another device")
-    return CacheArgs(kcache.data_ptr(), vcache.data_ptr(), pages.data_ptr(), lens.data_ptr(), kcache.shape[0],
-                     kcache.shape[1], pages.shape[1])
+    return CacheArgs(_on(kcache, "kcache", torch.bfloat16, kcache.shape, device),
+                     _on(vcache, "vcache", torch.bfloat16, kcache.shape, device),
+                     _on(pages, "pages", torch.int32, (B, pages.shape[1]), device),
+                     _on(lens, "lens", torch.int32, (B,), device), kcache.shape[0], kcache.shape[1], pages.shape[1])
 
 
 def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: Optional[Workspace] = None,
@@ -774,20 +786,17 @@ def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: 
     int32 page table [B, max_pages]; lens is left as it is."""
     _check(k, "k", torch.bfloat16, 4)
     B, T, Hk, d = k.shape
-    _on(v, "v", torch.bfloat16, k.shape, k)
-    c = _cache_args(kcache, vcache, pages, lens, B, k)
-    if tuple(kcache.shape[2:]) != (Hk, d):
+    device = k.device
+    pv = _on(v, "v", torch.bfloat16, k.shape, device)
+    c = _cache_args(kcache, vcache, pages, lens, B, device)
+    if kcache.shape[2:] != (Hk, d):
         raise ValueError("kcache must be [n_pages, page, Hk, d] with the heads of k")
-    if rows is not None:
-        _on(rows, "rows", torch.int32, (B, T), k)
-    if counts is not None:
-        _on(counts, "counts", torch.int32, (B,), k)
+    pr = None if rows is None else _on(rows, "rows", torch.int32, (B, T), device)
+    pc = None if counts is None else _on(counts, "counts", torch.int32, (B,), device)
     dims = AttnDims(B, T, Hk, Hk, d)
-    ws = _attn_ws(ATTN_APPEND, dims, 0, 0, ws, k.device, stream)
-    st = lib().bdla_cache_append(_p(k), _p(v), c, _p(rows), _p(counts), dims, ws.ptr, ws.nbytes,
-                                 _stream_handle(stream))
-    if st:
-        raise BdlaError(st, "bdla_cache_append")
+    pk, s = k.data_ptr(), _stream_of(k, stream)
+    _with_ws("bdla_cache_append", ATTN_APPEND, dims, 0, 0, ws, device, stream,
+             lambda p, n: lib().bdla_cache_append(pk, pv, c, pr, pc, dims, p, n, s))
 
 
 def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float] = None,
@@ -799,17 +808,15 @@ def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float
     (o like q, lse fp32 [B, T, Hq]); a token that sees nothing gets 0 and -inf."""
     _check(q, "q", torch.bfloat16, 4)
     B, T, Hq, d = q.shape
-    c = _cache_args(kcache, vcache, pages, lens, B, q)
-    Hk = kcache.shape[2]
+    device = q.device
+    c = _cache_args(kcache, vcache, pages, lens, B, device)
     if kcache.shape[3] != d:
         raise ValueError("kcache and q have different widths")
-    if tree is not None:
-        _on(tree, "tree", torch.int64, (B, T), q)
-    dims = AttnDims(B, T, Hq, Hk, d)
-    o, lse = _new((q.shape, (B, T, Hq)), (q.dtype, torch.float32), q.device, stream)
-    ws = _attn_ws(ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, q.device, stream)
-    st = lib().bdla_attn_cached(_p(q), c, _p(tree), d ** -0.5 if scale is None else scale, _p(o), _p(lse), dims,
-                                ws.ptr, ws.nbytes, _stream_handle(stream))
-    if st:
-        raise BdlaError(st, "bdla_attn_cached")
+    pt = None if tree is None else _on(tree, "tree", torch.int64, (B, T), device)
+    dims = AttnDims(B, T, Hq, kcache.shape[2], d)
+    o, lse = _new((q.shape, (B, T, Hq)), (q.dtype, torch.float32), device, stream)
+    scale = d ** -0.5 if scale is None else scale
+    pq, s = q.data_ptr(), _stream_of(q, stream)
+    _with_ws("bdla_attn_cached", ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, device, stream,
+             lambda p, n: lib().bdla_attn_cached(pq, c, pt, scale, o.data_ptr(), lse.data_ptr(), dims, p, n, s))
     return o, lse

@@ -6,12 +6,13 @@
 //   dx = r (h - n mean(h o n)),   dw = sum over tokens and heads of dy' o n
 //
 // Both directions are one pass over the tensors (4 bytes an element forward,
-// 6 backward) and bound by HBM.  A head of 64 or 128 features is 8 or 16
-// lanes of 16 bytes, so one head is one coalesced 128- or 256-byte access and
-// its mean a 3- or 4-step shuffle.  Such a group of lanes keeps one token and
-// walks a chunk of its heads, because the sines and cosines (8 per lane)
-// belong to the token: they are formed once per chunk, and four heads' loads
-// are in flight at a time.
+// 6 backward) and bound by HBM.  A head of 64 or 128 features belongs to 8 or
+// 16 lanes, each with two groups of four features that hold both halves of its
+// pairs, so the rotation stays in the lane, the mean is a 3- or 4-step shuffle
+// and the accesses of the lanes together cover whole lines.  Such a group of
+// lanes keeps one token and walks a chunk of its query or key heads: the four
+// angles of a lane belong to the token, and the products of weights and sines
+// are formed once per chunk; several heads' loads are in flight at a time.
 //
 // Angles.  pos * f with f = base^(-2i/rotary) loses its fraction of a turn in
 // fp32 for far positions.  f / (2 pi) is therefore kept as a 64-bit binary
@@ -42,7 +43,7 @@ struct NormParams {
     int64_t token[2], head[2];      // element strides
     const float *w[2];
     const int32_t *positions, *cu;
-    int n_docs, T, tokens, Hq, Hk, rotary, chunk, n_chunks;
+    int n_docs, T, tokens, heads[2], rotary, chunk, q_chunks, n_chunks;
     float eps;
 };
 
@@ -65,52 +66,52 @@ __device__ __forceinline__ int token_position(const NormParams &p, int t)
     return t - p.cu[lo];
 }
 
-// Sines and cosines of a lane's eight features.  Pairs at a distance: feature
-// e rotates with pair e mod rotary/2, and `sn` carries the sign of its role
-// (first of the pair: a cos - b sin).  Interleaved: entry 2m holds pair m of
-// the lane.  Features past `rotary` get (1, 0).
-template <bool INTER>
-__device__ __forceinline__ void lane_angles(const Turns &tu, int rotary, int e0, int pos, float (&cs)[8],
-                                            float (&sn)[8])
-{
-    const bool live = e0 < rotary;
-    const int half = rotary >> 1;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        cs[j] = 1.0f;
-        sn[j] = 0.0f;
-        if (!live || (INTER && (j & 1)))
-            continue;
-        const int i = INTER ? (e0 + j) >> 1 : (e0 < half ? e0 + j : e0 - half + j);
-        const uint64_t turns = (uint64_t)(int64_t)pos * tu.f[i];
-        sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[j], &cs[j]);   // 2^-31: half turns
-        if (!INTER && e0 < half)
-            sn[j] = -sn[j];
+// What a group of lanes works on: one token and a chunk of its query (s = 0)
+// or key (s = 1) heads.  The lane's eight features are f0 .. f0 + 3 and
+// f1 .. f1 + 3.  Pairs at a distance: feature f0 + j turns with f1 + j, and
+// lanes past the rotated features hold eight in a row.  Interleaved: eight in
+// a row, features 2m and 2m + 1 turn together.
+template <int D, bool INTER> struct Group {
+    static constexpr int kLanes = D / 8;
+    static constexpr int kPerBlock = kThreads / kLanes;
+    int f0, f1, t, s, h0, h1;
+    bool turns;
+    __device__ __forceinline__ explicit Group(const NormParams &p)
+    {
+        const int lane = threadIdx.x % kLanes;
+        turns = 8 * lane < p.rotary;
+        f0 = turns && !INTER ? 4 * lane : 8 * lane;
+        f1 = turns && !INTER ? (p.rotary >> 1) + 4 * lane : 8 * lane + 4;
     }
-}
-
-// y -> rotated y (or, with `back`, the transpose).  All lanes of the warp
-// take part; `partner` is the lane that holds the other halves of the pairs.
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&y)[8], const float (&cs)[8], const float (&sn)[8], int partner,
-                                       bool back)
-{
-    if (INTER) {
+    // A group past the end has no heads, and follows along: shuffles need whole warps.
+    __device__ __forceinline__ void take(const NormParams &p, int64_t item)
+    {
+        const bool any = item < (int64_t)p.tokens * p.n_chunks;
+        t = any ? (int)(item / p.n_chunks) : 0;
+        const int c = any ? (int)(item - (int64_t)t * p.n_chunks) : 0;
+        s = c >= p.q_chunks;
+        h0 = (s ? c - p.q_chunks : c) * p.chunk;
+        h1 = any ? min(h0 + p.chunk, p.heads[s]) : h0;
+    }
+    // Cosine and sine of the lane's four pairs.
+    __device__ __forceinline__ void angles(const NormParams &p, const Turns &tu, float (&cs)[4], float (&sn)[4]) const
+    {
+        const int pos = turns ? token_position(p, t) : 0;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float s = back ? -sn[j] : sn[j];
-            const float a = y[j], b = y[j + 1];
-            y[j] = a * cs[j] - b * s;
-            y[j + 1] = b * cs[j] + a * s;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float o = __shfl_sync(0xffffffffu, y[j], partner);
-            y[j] = y[j] * cs[j] + (back ? -sn[j] : sn[j]) * o;
+        for (int j = 0; j < 4; ++j) {
+            cs[j] = 1.0f;
+            sn[j] = 0.0f;
+            if (turns) {
+                const uint64_t u = (uint64_t)(int64_t)pos * tu.f[(INTER ? f0 >> 1 : f0) + j];
+                // the top 32 bits, signed, are 2^-31 half turns
+                sincospif((float)(int32_t)(u >> 32) * 4.656612873077393e-10f, &sn[j], &cs[j]);
+            }
         }
     }
-}
+    // Features of pair j in the lane's eight.
+    static __device__ __forceinline__ constexpr int a_of(int j) { return INTER ? 2 * j : j; }
+    static __device__ __forceinline__ constexpr int b_of(int j) { return INTER ? 2 * j + 1 : j + 4; }
+};
 
 template <int LANES> __device__ __forceinline__ float group_sum(float v)
 {
@@ -120,9 +121,9 @@ template <int LANES> __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])
+__device__ __forceinline__ void unpack8(const uint2 &u, const uint2 &v, float (&x)[8])
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = bf16_lo(w[i]);
@@ -130,66 +131,64 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+__device__ __forceinline__ uint2 load4(const __nv_bfloat16 *p) { return __ldcs(reinterpret_cast<const uint2 *>(p)); }
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int f0, int f1, const float (&x)[8])
 {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    __stcs(reinterpret_cast<uint2 *>(row + f0), make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])));
+    __stcs(reinterpret_cast<uint2 *>(row + f1), make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
 }
 
-// What a group of lanes works on: item -> (token, first head of its chunk).
-template <int D> struct Group {
-    static constexpr int kLanes = D / 8;
-    static constexpr int kPerBlock = kThreads / kLanes;
-    int lane, e0, partner;
-    __device__ __forceinline__ explicit Group(int rotary)
-    {
-        lane = threadIdx.x % kLanes;
-        e0 = 8 * lane;
-        const int step = rotary / 16;   // lanes between the two halves of a pair
-        const int other = e0 < rotary / 2 ? lane + step : (e0 < rotary ? lane - step : lane);
-        partner = (int)(threadIdx.x & 31) - lane + other;
-    }
-};
+__device__ __forceinline__ void load_weights(const float *w, int f0, int f1, float (&x)[8])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(w + f0), b = *reinterpret_cast<const float4 *>(w + f1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads)
 qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu, __nv_bfloat16 *__restrict__ qn,
                __nv_bfloat16 *__restrict__ kn)
 {
-    using G = Group<D>;
-    const G g(p.rotary);
-    const int64_t item = (int64_t)blockIdx.x * G::kPerBlock + threadIdx.x / G::kLanes;
-    // a group past the end follows along (shuffles need whole warps) and loads and stores nothing
-    const bool any = item < (int64_t)p.tokens * p.n_chunks;
-    const int t = any ? (int)(item / p.n_chunks) : 0;
-    const int h0 = any ? (int)(item % p.n_chunks) * p.chunk : 0;
-    const int heads = p.Hq + p.Hk;
-    const int h1 = any ? min(h0 + p.chunk, heads) : 0;
-    float w[2][8];
+    using G = Group<D, INTER>;
+    G g(p);
+    g.take(p, (int64_t)blockIdx.x * G::kPerBlock + threadIdx.x / G::kLanes);
+    const __nv_bfloat16 *src = p.x[g.s] + g.t * p.token[g.s];
+    const int64_t step = p.head[g.s];
+    __nv_bfloat16 *dst = (g.s ? kn : qn) + (int64_t)g.t * p.heads[g.s] * D;
+    // rotated feature = n_own * own + n_other * other, weights and signs included
+    float own[8], other[8];
+    {
+        float w[8], cs[4], sn[4];
+        load_weights(p.w[g.s], g.f0, g.f1, w);
+        g.angles(p, tu, cs, sn);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[s][j] = p.w[s][g.e0 + j];
-    float cs[8], sn[8];
-    lane_angles<INTER>(tu, p.rotary, g.e0, any ? token_position(p, t) : 0, cs, sn);
+        for (int j = 0; j < 4; ++j) {
+            const int a = G::a_of(j), b = G::b_of(j);
+            own[a] = w[a] * cs[j];
+            other[a] = -w[b] * sn[j];
+            own[b] = w[b] * cs[j];
+            other[b] = w[a] * sn[j];
+        }
+    }
     for (int b = 0; b < p.chunk; b += kBatch) {
-        uint4 in[kBatch];
+        uint2 in[kBatch][2];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int h = h0 + b + u;
-            if (b + u < p.chunk && h < h1) {
-                const int s = h >= p.Hq;
-                in[u] = *reinterpret_cast<const uint4 *>(p.x[s] + t * p.token[s] + (s ? h - p.Hq : h) * p.head[s] + g.e0);
+            const int h = g.h0 + b + u;
+            if (h < g.h1) {
+                in[u][0] = load4(src + h * step + g.f0);
+                in[u][1] = load4(src + h * step + g.f1);
             } else {
-                in[u] = make_uint4(0, 0, 0, 0);
+                in[u][0] = in[u][1] = make_uint2(0, 0);
             }
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int h = h0 + b + u;
-            const bool key = h >= p.Hq;
-            float x[8];
-            unpack8(in[u], x);
+            const int h = g.h0 + b + u;
+            float x[8], y[8];
+            unpack8(in[u][0], in[u][1], x);
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -197,27 +196,30 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
             const float r = rsqrtf(group_sum<G::kLanes>(ss) * (1.0f / D) + p.eps);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[j] = x[j] * r * (key ? w[1][j] : w[0][j]);
-            if (p.rotary > 0)
-                rotate<INTER>(x, cs, sn, g.partner, false);
-            if (b + u < p.chunk && h < h1) {
-                __nv_bfloat16 *dst = key ? kn + ((int64_t)t * p.Hk + h - p.Hq) * D : qn + ((int64_t)t * p.Hq + h) * D;
-                *reinterpret_cast<uint4 *>(dst + g.e0) = pack8(x);
+                x[j] *= r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int a = G::a_of(j), c = G::b_of(j);
+                y[a] = fmaf(x[c], other[a], x[a] * own[a]);
+                y[c] = fmaf(x[a], other[c], x[c] * own[c]);
             }
+            if (h < g.h1)
+                store8(dst + h * D, g.f0, g.f1, y);
         }
     }
 }
 
 template <bool GF32>
-__device__ __forceinline__ void load_grad(const void *base, int64_t off, float (&x)[8])
+__device__ __forceinline__ void load_grad(const void *base, int64_t off, int f0, int f1, float (&x)[8])
 {
     if (GF32) {
-        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-        const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off + 4);
+        const float *g = static_cast<const float *>(base) + off;
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(g + f0)), b = __ldcs(reinterpret_cast<const float4 *>(g + f1));
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     } else {
-        unpack8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + off), x);
+        const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(base) + off;
+        unpack8(load4(g + f0), load4(g + f1), x);
     }
 }
 
@@ -227,41 +229,40 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
                    const void *__restrict__ dqn, const void *__restrict__ dkn, __nv_bfloat16 *__restrict__ dq,
                    __nv_bfloat16 *__restrict__ dk, float *__restrict__ part)
 {
-    using G = Group<D>;
+    using G = Group<D, INTER>;
     constexpr int kB = 2;   // heads in flight: two tensors are read
     __shared__ float red[G::kPerBlock][2 * D];
-    const G g(p.rotary);
+    G g(p);
     const int gi = threadIdx.x / G::kLanes;
-    float w[2][8], dw[2][8];
+    float dw[2][8];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[s][j] = p.w[s][g.e0 + j];
+        for (int j = 0; j < 8; ++j)
             dw[s][j] = 0.0f;
-        }
-    const int heads = p.Hq + p.Hk;
     const int64_t items = (int64_t)p.tokens * p.n_chunks;
     const int64_t stride = (int64_t)gridDim.x * G::kPerBlock;
     // the block's groups stay together, so that whole warps reach the shuffles
     for (int64_t base = (int64_t)blockIdx.x * G::kPerBlock; base < items; base += stride) {
-        const int64_t item = base + gi;
-        const bool any = item < items;
-        const int t = any ? (int)(item / p.n_chunks) : 0;
-        const int h0 = any ? (int)(item % p.n_chunks) * p.chunk : 0;
-        const int h1 = any ? min(h0 + p.chunk, heads) : 0;
-        float cs[8], sn[8];
-        lane_angles<INTER>(tu, p.rotary, g.e0, any ? token_position(p, t) : 0, cs, sn);
+        g.take(p, base + gi);
+        const __nv_bfloat16 *src = p.x[g.s] + g.t * p.token[g.s];
+        const int64_t step = p.head[g.s], row = (int64_t)g.t * p.heads[g.s] * D;
+        const void *grad = g.s ? dkn : dqn;
+        __nv_bfloat16 *dst = (g.s ? dk : dq) + row;
+        float w[8], cs[4], sn[4], add[8];
+        load_weights(p.w[g.s], g.f0, g.f1, w);
+        g.angles(p, tu, cs, sn);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            add[j] = 0.0f;
         for (int b = 0; b < p.chunk; b += kB) {
             float x[kB][8], y[kB][8];
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int h = h0 + b + u;
-                if (b + u < p.chunk && h < h1) {
-                    const int s = h >= p.Hq;
-                    const int hh = s ? h - p.Hq : h;
-                    unpack8(*reinterpret_cast<const uint4 *>(p.x[s] + t * p.token[s] + hh * p.head[s] + g.e0), x[u]);
-                    load_grad<GF32>(s ? dkn : dqn, ((int64_t)t * (s ? p.Hk : p.Hq) + hh) * D + g.e0, y[u]);
+                const int h = g.h0 + b + u;
+                if (h < g.h1) {
+                    unpack8(load4(src + h * step + g.f0), load4(src + h * step + g.f1), x[u]);
+                    load_grad<GF32>(grad, row + (int64_t)h * D, g.f0, g.f1, y[u]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -270,45 +271,47 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int h = h0 + b + u;
-                const bool live = b + u < p.chunk && h < h1;
-                const bool key = h >= p.Hq;
+                const int h = g.h0 + b + u;
                 float ss = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     ss = fmaf(x[u][j], x[u][j], ss);
-                const float r = live ? rsqrtf(group_sum<G::kLanes>(ss) * (1.0f / D) + p.eps)
-                                     : (group_sum<G::kLanes>(ss), 0.0f);
-                if (p.rotary > 0)
-                    rotate<INTER>(y[u], cs, sn, g.partner, true);
+                ss = group_sum<G::kLanes>(ss);
+                const float r = h < g.h1 ? rsqrtf(ss * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
                 float hn = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int a = G::a_of(j), c = G::b_of(j);
+                    const float ya = y[u][a], yc = y[u][c];
+                    y[u][a] = fmaf(yc, sn[j], ya * cs[j]);
+                    y[u][c] = fmaf(-ya, sn[j], yc * cs[j]);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     x[u][j] *= r;   // n
-                    const float d = y[u][j] * x[u][j];
-                    if (live) {
-                        dw[0][j] += key ? 0.0f : d;
-                        dw[1][j] += key ? d : 0.0f;
-                    }
-                    y[u][j] *= key ? w[1][j] : w[0][j];   // h
+                    add[j] = fmaf(y[u][j], x[u][j], add[j]);
+                    y[u][j] *= w[j];   // h
                     hn = fmaf(y[u][j], x[u][j], hn);
                 }
                 const float m = group_sum<G::kLanes>(hn) * (1.0f / D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    y[u][j] = r * (y[u][j] - x[u][j] * m);
-                if (live) {
-                    __nv_bfloat16 *dst = key ? dk + ((int64_t)t * p.Hk + h - p.Hq) * D : dq + ((int64_t)t * p.Hq + h) * D;
-                    *reinterpret_cast<uint4 *>(dst + g.e0) = pack8(y[u]);
-                }
+                    y[u][j] = r * fmaf(-x[u][j], m, y[u][j]);
+                if (h < g.h1)
+                    store8(dst + h * D, g.f0, g.f1, y[u]);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dw[0][j] += g.s ? 0.0f : add[j];
+            dw[1][j] += g.s ? add[j] : 0.0f;
         }
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            red[gi][s * D + g.e0 + j] = dw[s][j];
+            red[gi][s * D + (j < 4 ? g.f0 + j : g.f1 + j - 4)] = dw[s][j];
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
         float v = 0.0f;
@@ -318,35 +321,40 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
     }
 }
 
-// Sums the blocks' partial weight gradients, 32 columns a CTA, in the order of
-// the blocks: the same sizes give the same bits.
-__global__ void __launch_bounds__(256)
+// Sums the blocks' partial weight gradients, 8 columns a CTA, each of 128
+// threads a column every 128th block, then the threads in order: the same
+// sizes give the same bits.
+__global__ void __launch_bounds__(1024)
 norm_dw_kernel(const float *__restrict__ part, int n_part, int D, float *__restrict__ dwq, float *__restrict__ dwk)
 {
-    __shared__ float red[8][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    __shared__ float red[128][9];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
     float v = 0.0f;
-    for (int i = y; i < n_part; i += 8)
+#pragma unroll 4
+    for (int i = y; i < n_part; i += 128)
         v += part[(size_t)i * 2 * D + c];
-    red[y][threadIdx.x & 31] = v;
+    red[y][x] = v;
     __syncthreads();
-    if (y == 0) {
-        float s = 0.0f;
-        for (int i = 0; i < 8; ++i)
-            s += red[i][threadIdx.x];
-        (c < D ? dwq : dwk)[c < D ? c : c - D] = s;
+    for (int w = 64; w > 0; w >>= 1) {
+        if (y < w)
+            red[y][x] += red[y + w][x];
+        __syncthreads();
     }
+    if (y == 0)
+        (c < D ? dwq : dwk)[c < D ? c : c - D] = red[0][x];
 }
 
 // Heads per group of lanes: as few as keep the GPU's lanes busy when tokens
-// are few, up to 16 when the angles' cost is worth sharing.
+// are few, up to 8 when the angles' cost is worth sharing.
 int head_chunk(const bdla_attn_dims &d)
 {
     const int64_t vecs = (int64_t)d.B * d.T * (d.Hq + d.Hk);
     const int64_t want = vecs / ((int64_t)sm_count() * 256);
-    const int c = want < 1 ? 1 : (want > 16 ? 16 : (int)want);
-    return c > d.Hq + d.Hk ? d.Hq + d.Hk : c;
+    const int c = want < 1 ? 1 : (want > 8 ? 8 : (int)want);
+    return c > d.Hq ? d.Hq : c;
 }
+
+int chunks_of(const bdla_attn_dims &d, int chunk) { return (d.Hq + chunk - 1) / chunk + (d.Hk + chunk - 1) / chunk; }
 
 NormParams norm_params(const bdla_qk_norm_args &a, const bdla_attn_dims &d)
 {
@@ -364,25 +372,34 @@ NormParams norm_params(const bdla_qk_norm_args &a, const bdla_attn_dims &d)
     p.n_docs = a.n_docs;
     p.T = d.T;
     p.tokens = d.B * d.T;
-    p.Hq = d.Hq;
-    p.Hk = d.Hk;
+    p.heads[0] = d.Hq;
+    p.heads[1] = d.Hk;
     p.rotary = a.rotary;
     p.chunk = head_chunk(d);
-    p.n_chunks = (d.Hq + d.Hk + p.chunk - 1) / p.chunk;
+    p.q_chunks = (d.Hq + p.chunk - 1) / p.chunk;
+    p.n_chunks = chunks_of(d, p.chunk);
     p.eps = a.eps;
     return p;
 }
 
-Turns turns_of(const bdla_qk_norm_args &a)
+// The pairs' frequencies, formed once per thread and (base, rotary): 64 calls
+// of pow are as long as the kernel of a decode step.
+const Turns &turns_of(const bdla_qk_norm_args &a)
 {
-    Turns t;
-    for (int i = 0; i < 64; ++i) {
-        t.f[i] = 0;
-        if (2 * i < a.rotary) {
-            // turns per position, at most 1 / (2 pi); scaled by 2^64 without passing 2^63
-            const double f = pow(a.base, -2.0 * i / a.rotary) / (2.0 * 3.14159265358979323846);
-            t.f[i] = (uint64_t)ldexp(f, 64);
+    thread_local Turns t{};
+    thread_local double base = 0.0;   // no valid base
+    thread_local int rotary = -1;
+    if (base != a.base || rotary != a.rotary) {
+        for (int i = 0; i < 64; ++i) {
+            t.f[i] = 0;
+            if (2 * i < a.rotary) {
+                // turns per position, at most 1 / (2 pi); scaled by 2^64 without passing 2^63
+                const double f = pow(a.base, -2.0 * i / a.rotary) / (2.0 * 3.14159265358979323846);
+                t.f[i] = (uint64_t)ldexp(f, 64);
+            }
         }
+        base = a.base;
+        rotary = a.rotary;
     }
     return t;
 }
@@ -395,7 +412,7 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
     if (d.T == 0)
         return cudaSuccess;
     const NormParams p = norm_params(a, d);
-    const Turns tu = turns_of(a);
+    const Turns &tu = turns_of(a);
     const int64_t items = (int64_t)p.tokens * p.n_chunks;
     const int per = kThreads / (d.d / 8);
     const unsigned grid = (unsigned)((items + per - 1) / per);
@@ -416,9 +433,9 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
 int norm_bwd_blocks(const bdla_attn_dims &d)
 {
     const int chunk = head_chunk(d);
-    const int64_t items = (int64_t)d.B * d.T * ((d.Hq + d.Hk + chunk - 1) / chunk);
+    const int64_t items = (int64_t)d.B * d.T * chunks_of(d, chunk);
     const int per = kThreads / (d.d / 8);
-    const int64_t need = (items + per - 1) / per, most = (int64_t)sm_count() * 4;
+    const int64_t need = (items + per - 1) / per, most = (int64_t)sm_count() * 16;
     return (int)(need < most ? need : most);
 }
 
@@ -429,7 +446,7 @@ cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, cons
     const int blocks = norm_bwd_blocks(d);
     if (blocks > 0) {
         const NormParams p = norm_params(a, d);
-        const Turns tu = turns_of(a);
+        const Turns &tu = turns_of(a);
 #define BDLA_NORM_GO(D_, I_, G_)                                                                                    \
     qk_norm_bwd_kernel<D_, I_, G_><<<blocks, kThreads, 0, stream>>>(p, tu, dqn, dkn, dq, dk, part)
 #define BDLA_NORM_D(D_)                                                                                             \
@@ -456,7 +473,7 @@ cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, cons
         if (err != cudaSuccess)
             return err;
     }
-    norm_dw_kernel<<<2 * d.d / 32, 256, 0, stream>>>(part, blocks, d.d, dwq, dwk);
+    norm_dw_kernel<<<2 * d.d / 8, 1024, 0, stream>>>(part, blocks, d.d, dwq, dwk);
     return cudaGetLastError();
 }
 
