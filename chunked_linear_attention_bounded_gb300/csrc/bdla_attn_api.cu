@@ -126,7 +126,7 @@ size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t m
     case BDLA_ATTN_BWD:
         return head + round_up((size_t)d.B * d.T * d.Hq * sizeof(float));
     case BDLA_ATTN_NORM_BWD:
-        return head + round_up((size_t)norm_bwd_blocks(d) * 2 * d.d * sizeof(float));
+        return head + round_up((size_t)norm_bwd_blocks(d) * d.d * sizeof(float));
     case BDLA_ATTN_CACHED:
         if (max_keys < 0 || d.T > 64)
             return 0;

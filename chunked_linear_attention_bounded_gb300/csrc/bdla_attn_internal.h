@@ -23,7 +23,7 @@ int sm_count();   // of the current device
 // Norm and rotation.  `tokens` = B * T; T > 0 gives fixed-length rows when cu is null.
 cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_bfloat16 *kn,
                            const bdla_attn_dims &d, cudaStream_t stream);
-// `part`: norm_bwd_blocks() partial sums of 2 d floats.
+// `part`: norm_bwd_blocks() partial sums of d floats.
 int norm_bwd_blocks(const bdla_attn_dims &d);
 cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, const void *dkn, int g_f32,
                                __nv_bfloat16 *dq, __nv_bfloat16 *dk, float *dwq, float *dwk, float *part,

@@ -93,6 +93,16 @@ template <int D, bool INTER> struct Group {
         h0 = (s ? c - p.q_chunks : c) * p.chunk;
         h1 = any ? min(h0 + p.chunk, p.heads[s]) : h0;
     }
+    // The same over the chunks of queries or of keys alone.
+    __device__ __forceinline__ void take_of(const NormParams &p, int which, int64_t item)
+    {
+        const int n = which ? p.n_chunks - p.q_chunks : p.q_chunks;
+        const bool any = item < (int64_t)p.tokens * n;
+        t = any ? (int)(item / n) : 0;
+        s = which;
+        h0 = any ? (int)(item - (int64_t)t * n) * p.chunk : 0;
+        h1 = any ? min(h0 + p.chunk, p.heads[s]) : h0;
+    }
     // Cosine and sine of the lane's four pairs.
     __device__ __forceinline__ void angles(const NormParams &p, const Turns &tu, float (&cs)[4], float (&sn)[4]) const
     {
@@ -209,130 +219,140 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
     }
 }
 
-template <bool GF32>
-__device__ __forceinline__ void load_grad(const void *base, int64_t off, int f0, int f1, float (&x)[8])
-{
-    if (GF32) {
+// Four features twice, as they lie in memory.
+template <bool GF32> struct Grad8;
+template <> struct Grad8<false> {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const void *base, int64_t off, int f0, int f1)
+    {
+        const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(base) + off;
+        a = load4(g + f0);
+        b = load4(g + f1);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(a, b, x); }
+};
+template <> struct Grad8<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void *base, int64_t off, int f0, int f1)
+    {
         const float *g = static_cast<const float *>(base) + off;
-        const float4 a = __ldcs(reinterpret_cast<const float4 *>(g + f0)), b = __ldcs(reinterpret_cast<const float4 *>(g + f1));
+        a = __ldcs(reinterpret_cast<const float4 *>(g + f0));
+        b = __ldcs(reinterpret_cast<const float4 *>(g + f1));
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(base) + off;
-        unpack8(load4(g + f0), load4(g + f1), x);
     }
-}
+};
 
+// The first q_blocks CTAs take the query heads, the others the key heads, so
+// that a thread sums one weight gradient; CTA i leaves its sums in part[i].
 template <int D, bool INTER, bool GF32>
-__global__ void __launch_bounds__(kThreads)
-qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu,
+__global__ void __launch_bounds__(kThreads, 3)
+qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu, int q_blocks,
                    const void *__restrict__ dqn, const void *__restrict__ dkn, __nv_bfloat16 *__restrict__ dq,
                    __nv_bfloat16 *__restrict__ dk, float *__restrict__ part)
 {
     using G = Group<D, INTER>;
     constexpr int kB = 2;   // heads in flight: two tensors are read
-    __shared__ float red[G::kPerBlock][2 * D];
+    __shared__ float red[G::kPerBlock][D];
     G g(p);
     const int gi = threadIdx.x / G::kLanes;
-    float dw[2][8];
+    const int s = (int)blockIdx.x >= q_blocks;
+    const int block = (int)blockIdx.x - (s ? q_blocks : 0), blocks = s ? (int)gridDim.x - q_blocks : q_blocks;
+    float w[8], dw[8];
+    load_weights(p.w[s], g.f0, g.f1, w);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dw[s][j] = 0.0f;
-    const int64_t items = (int64_t)p.tokens * p.n_chunks;
-    const int64_t stride = (int64_t)gridDim.x * G::kPerBlock;
+    for (int j = 0; j < 8; ++j)
+        dw[j] = 0.0f;
+    const int64_t items = (int64_t)p.tokens * (s ? p.n_chunks - p.q_chunks : p.q_chunks);
+    const int64_t stride = (int64_t)blocks * G::kPerBlock, step = p.head[s];
+    const void *grad = s ? dkn : dqn;
     // the block's groups stay together, so that whole warps reach the shuffles
-    for (int64_t base = (int64_t)blockIdx.x * G::kPerBlock; base < items; base += stride) {
-        g.take(p, base + gi);
-        const __nv_bfloat16 *src = p.x[g.s] + g.t * p.token[g.s];
-        const int64_t step = p.head[g.s], row = (int64_t)g.t * p.heads[g.s] * D;
-        const void *grad = g.s ? dkn : dqn;
-        __nv_bfloat16 *dst = (g.s ? dk : dq) + row;
-        float w[8], cs[4], sn[4], add[8];
-        load_weights(p.w[g.s], g.f0, g.f1, w);
+    for (int64_t base = (int64_t)block * G::kPerBlock; base < items; base += stride) {
+        g.take_of(p, s, base + gi);
+        const __nv_bfloat16 *src = p.x[s] + g.t * p.token[s];
+        const int64_t row = (int64_t)g.t * p.heads[s] * D;
+        __nv_bfloat16 *dst = (s ? dk : dq) + row;
+        float cs[4], sn[4];
         g.angles(p, tu, cs, sn);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            add[j] = 0.0f;
-        for (int b = 0; b < p.chunk; b += kB) {
-            float x[kB][8], y[kB][8];
+        for (int h = g.h0; h < g.h0 + p.chunk; h += kB) {
+            uint2 xa[kB], xb[kB];
+            Grad8<GF32> gr[kB];
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int h = g.h0 + b + u;
-                if (h < g.h1) {
-                    unpack8(load4(src + h * step + g.f0), load4(src + h * step + g.f1), x[u]);
-                    load_grad<GF32>(grad, row + (int64_t)h * D, g.f0, g.f1, y[u]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[u][j] = y[u][j] = 0.0f;
+                xa[u] = xb[u] = make_uint2(0, 0);
+                gr[u] = Grad8<GF32>{};
+                if (h + u < g.h1) {
+                    xa[u] = load4(src + (h + u) * step + g.f0);
+                    xb[u] = load4(src + (h + u) * step + g.f1);
+                    gr[u].load(grad, row + (int64_t)(h + u) * D, g.f0, g.f1);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int h = g.h0 + b + u;
+                float x[8], y[8];
+                unpack8(xa[u], xb[u], x);
+                gr[u].get(y);
                 float ss = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    ss = fmaf(x[u][j], x[u][j], ss);
+                    ss = fmaf(x[j], x[j], ss);
                 ss = group_sum<G::kLanes>(ss);
-                const float r = h < g.h1 ? rsqrtf(ss * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
-                float hn = 0.0f;
+                const float r = h + u < g.h1 ? rsqrtf(ss * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int a = G::a_of(j), c = G::b_of(j);
-                    const float ya = y[u][a], yc = y[u][c];
-                    y[u][a] = fmaf(yc, sn[j], ya * cs[j]);
-                    y[u][c] = fmaf(-ya, sn[j], yc * cs[j]);
+                    const float ya = y[a], yc = y[c];
+                    y[a] = fmaf(yc, sn[j], ya * cs[j]);
+                    y[c] = fmaf(-ya, sn[j], yc * cs[j]);
                 }
+                float hn = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    x[u][j] *= r;   // n
-                    add[j] = fmaf(y[u][j], x[u][j], add[j]);
-                    y[u][j] *= w[j];   // h
-                    hn = fmaf(y[u][j], x[u][j], hn);
+                    x[j] *= r;   // n
+                    dw[j] = fmaf(y[j], x[j], dw[j]);
+                    y[j] *= w[j];   // h
+                    hn = fmaf(y[j], x[j], hn);
                 }
                 const float m = group_sum<G::kLanes>(hn) * (1.0f / D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    y[u][j] = r * fmaf(-x[u][j], m, y[u][j]);
-                if (h < g.h1)
-                    store8(dst + h * D, g.f0, g.f1, y[u]);
+                    y[j] = r * fmaf(-x[j], m, y[j]);
+                if (h + u < g.h1)
+                    store8(dst + (h + u) * D, g.f0, g.f1, y);
             }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dw[0][j] += g.s ? 0.0f : add[j];
-            dw[1][j] += g.s ? add[j] : 0.0f;
         }
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            red[gi][s * D + (j < 4 ? g.f0 + j : g.f1 + j - 4)] = dw[s][j];
+    for (int j = 0; j < 8; ++j)
+        red[gi][j < 4 ? g.f0 + j : g.f1 + j - 4] = dw[j];
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+    for (int c = threadIdx.x; c < D; c += kThreads) {
         float v = 0.0f;
+#pragma unroll
         for (int i = 0; i < G::kPerBlock; ++i)
             v += red[i][c];
-        part[(size_t)blockIdx.x * 2 * D + c] = v;
+        part[(size_t)blockIdx.x * D + c] = v;
     }
 }
 
-// Sums the blocks' partial weight gradients, 8 columns a CTA, each of 128
-// threads a column every 128th block, then the threads in order: the same
+// Sums the CTAs' partial weight gradients, 8 columns a CTA, each of 128
+// threads a column every 128th partial, then the threads in order: the same
 // sizes give the same bits.
 __global__ void __launch_bounds__(1024)
-norm_dw_kernel(const float *__restrict__ part, int n_part, int D, float *__restrict__ dwq, float *__restrict__ dwk)
+norm_dw_kernel(const float *__restrict__ part, int q_blocks, int blocks, int D, float *__restrict__ dwq,
+               float *__restrict__ dwk)
 {
     __shared__ float red[128][9];
-    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, per = D / 8;
+    const int s = (int)blockIdx.x >= per, c = ((int)blockIdx.x - s * per) * 8 + x;
+    const int first = s ? q_blocks : 0, last = s ? blocks : q_blocks;
     float v = 0.0f;
 #pragma unroll 4
-    for (int i = y; i < n_part; i += 128)
-        v += part[(size_t)i * 2 * D + c];
+    for (int i = first + y; i < last; i += 128)
+        v += part[(size_t)i * D + c];
     red[y][x] = v;
     __syncthreads();
     for (int w = 64; w > 0; w >>= 1) {
@@ -341,7 +361,7 @@ norm_dw_kernel(const float *__restrict__ part, int n_part, int D, float *__restr
         __syncthreads();
     }
     if (y == 0)
-        (c < D ? dwq : dwk)[c < D ? c : c - D] = red[0][x];
+        (s ? dwk : dwq)[c] = red[0][x];
 }
 
 // Heads per group of lanes: as few as keep the GPU's lanes busy when tokens
@@ -430,25 +450,40 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
     return cudaGetLastError();
 }
 
+// CTAs for the query and for the key heads, in proportion to their work.
+static int norm_q_blocks(const bdla_attn_dims &d, int *total)
+{
+    const int chunk = head_chunk(d), per = kThreads / (d.d / 8);
+    const int64_t most = (int64_t)sm_count() * 12, tokens = (int64_t)d.B * d.T;
+    int64_t n[2];
+    for (int s = 0; s < 2; ++s) {
+        const int heads = s ? d.Hk : d.Hq;
+        const int64_t items = tokens * ((heads + chunk - 1) / chunk), need = (items + per - 1) / per;
+        const int64_t share = most * heads / (d.Hq + d.Hk) + 1;
+        n[s] = need < share ? need : share;
+    }
+    *total = (int)(n[0] + n[1]);
+    return (int)n[0];
+}
+
 int norm_bwd_blocks(const bdla_attn_dims &d)
 {
-    const int chunk = head_chunk(d);
-    const int64_t items = (int64_t)d.B * d.T * chunks_of(d, chunk);
-    const int per = kThreads / (d.d / 8);
-    const int64_t need = (items + per - 1) / per, most = (int64_t)sm_count() * 16;
-    return (int)(need < most ? need : most);
+    int total;
+    norm_q_blocks(d, &total);
+    return total;
 }
 
 cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, const void *dkn, int g_f32,
                                __nv_bfloat16 *dq, __nv_bfloat16 *dk, float *dwq, float *dwk, float *part,
                                const bdla_attn_dims &d, cudaStream_t stream)
 {
-    const int blocks = norm_bwd_blocks(d);
+    int blocks;
+    const int q_blocks = norm_q_blocks(d, &blocks);
     if (blocks > 0) {
         const NormParams p = norm_params(a, d);
         const Turns &tu = turns_of(a);
 #define BDLA_NORM_GO(D_, I_, G_)                                                                                    \
-    qk_norm_bwd_kernel<D_, I_, G_><<<blocks, kThreads, 0, stream>>>(p, tu, dqn, dkn, dq, dk, part)
+    qk_norm_bwd_kernel<D_, I_, G_><<<blocks, kThreads, 0, stream>>>(p, tu, q_blocks, dqn, dkn, dq, dk, part)
 #define BDLA_NORM_D(D_)                                                                                             \
     do {                                                                                                            \
         if (a.interleaved) {                                                                                        \
@@ -473,7 +508,7 @@ cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, cons
         if (err != cudaSuccess)
             return err;
     }
-    norm_dw_kernel<<<2 * d.d / 8, 1024, 0, stream>>>(part, blocks, d.d, dwq, dwk);
+    norm_dw_kernel<<<2 * d.d / 8, 1024, 0, stream>>>(part, q_blocks, blocks, d.d, dwq, dwk);
     return cudaGetLastError();
 }
 
