@@ -70,7 +70,8 @@ bdla_status check_cache(const bdla_cache &c)
         return BDLA_ERR_SHAPE;
     if (c.page > 65536)
         return BDLA_ERR_UNSUPPORTED;
-    if ((int64_t)c.max_pages * c.page > INT32_MAX - 65536)   // positions are 32-bit
+    // positions and rows of the cache are 32-bit (2^31 rows are more than the GPU's memory holds)
+    if ((int64_t)c.max_pages * c.page > INT32_MAX - 65536 || (int64_t)c.n_pages * c.page > INT32_MAX)
         return BDLA_ERR_TOO_LARGE;
     if (!c.lens || (c.max_pages > 0 && !c.pages) || (c.n_pages > 0 && (!c.k || !c.v)))
         return BDLA_ERR_NULL;
@@ -238,7 +239,7 @@ bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, 
         return BDLA_ERR_ALIGN;
     const int64_t max_keys = (int64_t)c.max_pages * c.page;
     BDLA_TRY(check_ws(ws, ws_bytes, bdla_workspace_bytes_attn(BDLA_ATTN_CACHED, d, 0, max_keys)));
-    BDLA_CUDA(launch_attn_cached(cb(q), c, tree, scale, mb(o), lse, d, cached_splits(d, max_keys),
+    BDLA_CUDA(launch_attn_cached(cb(q), c, tree, scale, mb(o), lse, d, max_keys,
                                  static_cast<char *>(ws) + round_up(kStatusBytes), static_cast<DeviceStatus *>(ws),
                                  static_cast<cudaStream_t>(stream)));
     return BDLA_OK;

@@ -46,7 +46,7 @@ cudaError_t launch_cache_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v, 
 int cached_splits(const bdla_attn_dims &d, int64_t max_keys);
 size_t cached_partial_bytes(const bdla_attn_dims &d, int splits);
 cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,
-                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int splits, void *partials,
+                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int64_t max_keys, void *partials,
                                DeviceStatus *st, cudaStream_t stream);
 
 }  // namespace bdla

@@ -1,11 +1,13 @@
 // The paged cache: writing rows into its pages, and attention of a sequence's
 // newest tokens over it.
-#include "bdla_attn_internal.h"
+#include "bdla_cache.cuh"
 #include "bdla_sm100.cuh"
 
 namespace bdla {
 
 namespace {
+
+using namespace cache;
 
 // Row of position t of a sequence in the cache's [n_pages * page] rows, or -1
 // where the table or the page does not reach.
@@ -77,18 +79,20 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 //   s = scale q . k over the visible positions,  o = (sum_t e^{s_t - m} v_t) / sum_t e^{s_t - m}
 //
 // A key head's cache is read once for all rows that use it: the new tokens of a
-// sequence times the query heads of the group, in blocks of 16, 32 or 64 rows
-// (the smallest that holds them).  With few rows the pass is bound by HBM: 16
-// rows of weights cost nothing beside 512 bytes of keys and values a position,
-// so the products run as warp MMAs (m16n8k16) straight from the tiles that
-// cp.async brings in, three tiles of 64 positions in flight.  A CTA's four
-// warps split the rows first and the positions of the tile with what is left,
-// and join through shared memory at the end.
+// sequence times the query heads of the group.  With up to 32 rows the pass is
+// bound by HBM: their products cost nothing beside 512 bytes of keys and values
+// a position, so they run as warp MMAs (m16n8k16, 16 or 32 rows) straight from
+// the tiles that cp.async brings in, three tiles of 64 positions in flight.  A
+// CTA's four warps split the rows first and the positions of the tile with what
+// is left, and join through shared memory at the end.  Warp MMAs run at an
+// eighth of the tensor cores' rate here: with 64 rows they took longer than the
+// keys' way from HBM (244 rows a key head: 100 us for 96 MB), so more rows go to
+// the tensor-memory kernel of bdla_cache_wide.cu.
 //
 // The long axis is split: every sequence into at most `ns` pieces of equal
-// length, at least kMinSplit positions each, as the lengths on the device say.
-// A sequence of one piece is finished by its CTA; the others leave an fp32 sum
-// per row and piece, which combine_kernel joins in the order of the pieces.
+// length, as the lengths on the device say.  A sequence of one piece is
+// finished by its CTA; the others leave an fp32 sum per row and piece, which
+// combine_kernel joins in the order of the pieces.
 //
 // Positions are looked up in the page table two tiles ahead of their load, by
 // 64 threads into shared memory, so any page size works and no tile has to end
@@ -97,20 +101,12 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 constexpr int kKeys = 64;         // positions of a tile
 constexpr int kCStages = 3;
 constexpr int kCThreads = 128;
-constexpr int kMinSplit = 128;
 
 template <int D> struct CachedSmem {
     alignas(128) unsigned char kv[kCStages][2][kKeys * D * 2];
-    int64_t row[4][kKeys];        // cache row of a tile's positions, -1: not seen
+    int row[4][kKeys];            // cache row of a tile's positions, -1: not seen
     uint32_t valid[4][2];
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -135,36 +131,9 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// How a sequence's positions are cut.
-struct Cut {
-    int len, end;   // committed positions; all positions inside the table
-    int size, used; // positions a piece, pieces
-};
-__device__ __forceinline__ Cut cut_of(const bdla_cache &c, int b, int T, int ns)
-{
-    Cut k;
-    k.len = c.lens[b];
-    const int64_t cap = (int64_t)c.max_pages * c.page, all = (int64_t)k.len + T;
-    k.end = k.len < 0 ? 0 : (int)(all < cap ? all : cap);
-    const int even = (int)(((int64_t)k.end + ns - 1) / ns);
-    k.size = even < kMinSplit ? kMinSplit : (even + kKeys - 1) / kKeys * kKeys;
-    k.used = k.end > 0 ? (k.end + k.size - 1) / k.size : 1;
-    return k;
-}
-
-// New tokens that token i sees (bit j: token j).
-__device__ __forceinline__ uint64_t sees(const uint64_t *tree, int64_t b, int T, int i)
-{
-    const uint64_t m = tree != nullptr ? tree[b * T + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-    return T < 64 ? m & ((1ull << T) - 1) : m;
-}
-
 template <int D, int WR>
 __global__ void __launch_bounds__(kCThreads)
-cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_cache c,
-              const uint64_t *__restrict__ tree, float scale, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
-              float *__restrict__ part_o, float *__restrict__ part_ml, int T, int Hq, int Hk, int row_blocks, int ns,
-              DeviceStatus *st)
+cached_kernel(const __grid_constant__ Call a, int row_blocks)
 {
     constexpr int WK = 4 / WR;          // warps along the positions
     constexpr int KW = kKeys / WK;      // positions of a warp
@@ -174,6 +143,8 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
     CachedSmem<D> &sm = *reinterpret_cast<CachedSmem<D> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wr = warp % WR, wk = warp / WR;
+    const bdla_cache &c = a.c;
+    const int T = a.T, Hq = a.Hq, Hk = a.Hk, ns = a.pieces.ns;
     // heads of one position lie next to each other in the cache: keep them together in time
     int idx = blockIdx.x;
     const int rb = idx % row_blocks;
@@ -181,33 +152,27 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
     const int kh = idx % Hk;
     idx /= Hk;
     const int piece = idx % ns, b = idx / ns;
-    const Cut cut = cut_of(c, b, T, ns);
+    const Cut cut = cut_of(c, b, T, a.pieces);
     if (piece >= cut.used)
         return;
-    if (piece == 0 && kh == 0 && rb == 0 && tid == 0 && (cut.len < 0 || (int64_t)cut.len + T > (int64_t)c.max_pages * c.page))
-        set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
+    if (piece == 0 && kh == 0 && rb == 0 && tid == 0 && cut_is_short(c, cut, T))
+        set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
     const int G = Hq / Hk, R = T * G;
     const int k0 = piece * cut.size, k1 = min(cut.end, k0 + cut.size);
     const int nt = (k1 - k0 + kKeys - 1) / kKeys;
     const int32_t *table = c.pages + (int64_t)b * c.max_pages;
     const bool drafts = k1 > cut.len;   // the piece holds new tokens
-    uint64_t seen = 0;                  // new tokens that any of the sequence's sees
-    if (drafts) {
-        for (int i = lane; i < T; i += 32)
-            seen |= sees(tree, b, T, i);
-        for (int w = 16; w > 0; w >>= 1)
-            seen |= __shfl_xor_sync(0xffffffffu, seen, w);
-    }
+    const uint64_t seen = drafts ? sees_any(a.tree, b, T, lane) : 0;
 
     // page table entry of position t (a tile's 64 positions, by the first 64 threads)
     auto lookup = [&](int t) { return t < k1 ? table[t / c.page] : -1; };
     auto place = [&](int n, int t, int pg) {
         bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
         if (live && (pg < 0 || pg >= c.n_pages)) {
-            set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
+            set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
             live = false;
         }
-        sm.row[n & 3][tid] = live ? (int64_t)pg * c.page + t % c.page : -1;
+        sm.row[n & 3][tid] = live ? pg * c.page + t % c.page : -1;
         const uint32_t m = __ballot_sync(0xffffffffu, live);
         if (lane == 0)
             sm.valid[n & 3][tid >> 5] = m;
@@ -218,8 +183,8 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
 #pragma unroll
             for (int u = 0; u < kKeys * kChunks / kCThreads; ++u) {
                 const int e = tid + u * kCThreads, r = e / kChunks, ch = e % kChunks;
-                const int64_t row = sm.row[n & 3][r];
-                const int64_t off = ((row < 0 ? 0 : row) * Hk + kh) * D + 8 * ch;
+                const int row = sm.row[n & 3][r];
+                const int64_t off = ((int64_t)(row < 0 ? 0 : row) * Hk + kh) * D + 8 * ch;
                 const uint32_t to = dst + (r * kChunks + (ch ^ (r & 7))) * 16;
                 cp16(to, static_cast<const __nv_bfloat16 *>(c.k) + off, row >= 0);
                 cp16(to + kKeys * D * 2, static_cast<const __nv_bfloat16 *>(c.v) + off, row >= 0);
@@ -239,8 +204,8 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
     // query fragments: rows lane/4 and lane/4 + 8 of the warp's 16
     const int r0 = rb * MR + 16 * wr + (lane >> 2), r1 = r0 + 8;
     const int i0 = min(r0, R - 1) / G, i1 = min(r1, R - 1) / G;
-    const __nv_bfloat16 *qa = q + (((int64_t)b * T + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
-    const __nv_bfloat16 *qb = q + (((int64_t)b * T + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qa = a.q + (((int64_t)b * T + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qb = a.q + (((int64_t)b * T + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
     uint32_t fq[D / 16][4];
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -249,8 +214,8 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
         fq[ks][2] = *reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8);
         fq[ks][3] = *reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8);
     }
-    const uint64_t see0 = drafts ? sees(tree, b, T, i0) : 0, see1 = drafts ? sees(tree, b, T, i1) : 0;
-    const float cs = scale * 1.4426950408889634f;
+    const uint64_t see0 = drafts ? sees(a.tree, b, T, i0) : 0, see1 = drafts ? sees(a.tree, b, T, i1) : 0;
+    const float cs = a.scale * 1.4426950408889634f;
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -360,11 +325,11 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
     }
     {
         const int ra = 16 * wr + (lane >> 2);
-        float *a = jo + (wk * MR + ra) * D + 2 * (lane & 3), *e = a + 8 * D;
+        float *x = jo + (wk * MR + ra) * D + 2 * (lane & 3), *y = x + 8 * D;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-            *reinterpret_cast<float2 *>(a + 8 * i) = make_float2(acc[i][0], acc[i][1]);
-            *reinterpret_cast<float2 *>(e + 8 * i) = make_float2(acc[i][2], acc[i][3]);
+            *reinterpret_cast<float2 *>(x + 8 * i) = make_float2(acc[i][0], acc[i][1]);
+            *reinterpret_cast<float2 *>(y + 8 * i) = make_float2(acc[i][2], acc[i][3]);
         }
         if ((lane & 3) == 0) {
             *reinterpret_cast<float2 *>(jm + 2 * (wk * MR + ra)) = make_float2(m0, l0);
@@ -394,73 +359,103 @@ cached_kernel(const __nv_bfloat16 *__restrict__ q, const __grid_constant__ bdla_
         }
         if (cut.used > 1) {
             const int64_t at = (((int64_t)b * Hk + kh) * ns + piece) * R + row;
-            *reinterpret_cast<float4 *>(part_o + at * D + d4) = v;
+            *reinterpret_cast<float4 *>(a.part_o + at * D + d4) = v;
             if (d4 == 0)
-                *reinterpret_cast<float2 *>(part_ml + 2 * at) = make_float2(m, l);
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m, l);
         } else {
             const int64_t at = ((int64_t)b * T + row / G) * Hq + kh * G + row % G;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            *reinterpret_cast<uint2 *>(o + at * D + d4) =
+            *reinterpret_cast<uint2 *>(a.o + at * D + d4) =
                 make_uint2(sm100::pack_bf16(v.x * inv, v.y * inv), sm100::pack_bf16(v.z * inv, v.w * inv));
             if (d4 == 0)
-                lse[at] = l == 0.0f ? -INFINITY : fmaf(m, scale, logf(l));
+                a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
         }
     }
 }
 
-// Joins the pieces of one row: one CTA a row, four warps over the pieces.
-template <int D>
-__global__ void __launch_bounds__(128)
-combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ml, const __grid_constant__ bdla_cache c,
-               float scale, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int T, int Hq, int Hk, int ns)
+// Joins the pieces of a row, W warps a row: each sums every W-th piece, and the
+// warps' sums are added in order.  W follows the most pieces of a sequence (one
+// warp for up to 8, so that a CTA joins four rows, 4 for up to 32, 16 beyond).
+template <int D, int W>
+__global__ void __launch_bounds__(W < 4 ? 128 : 32 * W)
+combine_kernel(const __grid_constant__ Call a, int64_t rows)
 {
-    constexpr int E = D / 32;
-    __shared__ float red_m[4], red_l[4], red_o[4][D];
-    const int64_t at = blockIdx.x;
-    const int h = (int)(at % Hq), i = (int)(at / Hq % T), b = (int)(at / Hq / T);
-    const Cut cut = cut_of(c, b, T, ns);
-    if (cut.used < 2)
-        return;   // finished by its own CTA
-    const int G = Hq / Hk, kh = h / G, R = T * G, row = i * G + h % G;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t base = ((int64_t)b * Hk + kh) * ns;
-    const float cs = scale * 1.4426950408889634f;
+    constexpr int E = D / 32, kRows = W < 4 ? 4 / W : 1;
+    __shared__ float red_l[kRows][W], red_m[kRows][W];
+    __shared__ __align__(16) float red_o[kRows][W][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / W, w = warp % W;
+    const int64_t at = (int64_t)blockIdx.x * kRows + mine;
+    const int T = a.T, Hq = a.Hq, G = Hq / a.Hk;
+    const bool any = at < rows;
+    const int h = any ? (int)(at % Hq) : 0, i = any ? (int)(at / Hq % T) : 0, b = any ? (int)(at / Hq / T) : 0;
+    Cut cut = cut_of(a.c, b, T, a.pieces);
+    const bool live = any && cut.used > 1;   // one piece: finished by its own CTA
+    if (W > 1 && !live)
+        return;   // the whole CTA
+    if (!live)
+        cut.used = 0;
+    const int64_t first = ((int64_t)b * a.Hk + h / G) * a.pieces.ns;
+    const int R = T * G, row = i * G + h % G;
+    const float cs = a.scale * 1.4426950408889634f;
     float m = -INFINITY;
-    for (int s = threadIdx.x; s < cut.used; s += 128)
-        m = fmaxf(m, part_ml[2 * ((base + s) * R + row)]);
-    for (int w = 16; w > 0; w >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    if (lane == 0)
-        red_m[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
+    for (int s = w * 32 + lane; s < cut.used; s += 32 * W)
+        m = fmaxf(m, a.part_ml[2 * ((first + s) * R + row)]);
+    for (int x = 16; x > 0; x >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if (W > 1) {
+        if (lane == 0)
+            red_m[mine][w] = m;
+        __syncthreads();
+        for (int x = 0; x < W; ++x)
+            m = fmaxf(m, red_m[mine][x]);
+    }
     float l = 0.0f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         v[e] = 0.0f;
 #pragma unroll 4
-    for (int s = warp; s < cut.used; s += 4) {
-        const int64_t p = (base + s) * R + row;
-        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + 2 * p);
+    for (int s = w; s < cut.used; s += W) {
+        const int64_t p = (first + s) * R + row;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * p);
         const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * cs);
         l = fmaf(ml.y, f, l);
+        const float *y = a.part_o + p * D + E * lane;
+        if (E == 4) {
+            const float4 z = *reinterpret_cast<const float4 *>(y);
+            v[0] = fmaf(z.x, f, v[0]);
+            v[1] = fmaf(z.y, f, v[1]);
+            v[E - 2] = fmaf(z.z, f, v[E - 2]);
+            v[E - 1] = fmaf(z.w, f, v[E - 1]);
+        } else {
+            const float2 z = *reinterpret_cast<const float2 *>(y);
+            v[0] = fmaf(z.x, f, v[0]);
+            v[1] = fmaf(z.y, f, v[1]);
+        }
+    }
+    if (W > 1) {
+        if (lane == 0)
+            red_l[mine][w] = l;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            v[e] = fmaf(part_o[p * D + lane + 32 * e], f, v[e]);
-    }
-    if (lane == 0)
-        red_l[warp] = l;
+            red_o[mine][w][E * lane + e] = v[e];
+        __syncthreads();
+        if (w != 0)
+            return;
+        for (int x = 1; x < W; ++x) {
+            l += red_l[mine][x];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        red_o[warp][lane + 32 * e] = v[e];
-    __syncthreads();
-    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+            for (int e = 0; e < E; ++e)
+                v[e] += red_o[mine][x][E * lane + e];
+        }
+    }
+    if (!live)
+        return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (threadIdx.x < D)
-        o[at * D + threadIdx.x] = __float2bfloat16_rn(((red_o[0][threadIdx.x] + red_o[1][threadIdx.x]) +
-                                                       (red_o[2][threadIdx.x] + red_o[3][threadIdx.x])) * inv);
-    if (threadIdx.x == 0)
-        lse[at] = l == 0.0f ? -INFINITY : fmaf(m, scale, logf(l));
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(a.o + at * D + E * lane + e) = sm100::pack_bf16(v[e] * inv, v[e + 1] * inv);
+    if (lane == 0)
+        a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
 }
 
 }  // namespace
@@ -479,30 +474,39 @@ cudaError_t launch_cache_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v, 
     return cudaGetLastError();
 }
 
-// Rows of a CTA: the smallest block that holds a key head's rows, at most 64.
+// Rows of a CTA: the smallest block that holds a key head's rows.
 static int cached_rows(const bdla_attn_dims &d)
 {
     const int R = d.T * (d.Hq / d.Hk);
-    return R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    return R <= 16 ? 16 : R <= 32 ? 32 : kWideRows;
 }
 
-// Pieces of a sequence: enough for eight CTAs an SM, and pieces of at most 2048
-// positions so that long and short sequences end together; no more than there
-// are kMinSplit positions, than 256 MB of partial sums, or than keep the grid
-// within 2^17 CTAs (more only where the sequences alone are more).
-int cached_splits(const bdla_attn_dims &d, int64_t max_keys)
+// Pieces of a sequence.  Few sequences: enough pieces for eight CTAs an SM (one
+// of the wide kernel, of which one is resident), of at least 128 positions.
+// Many: pieces of about 2048 positions, so that long and short sequences end
+// together, and of at least 1024, so that a CTA's start-up (length, page table,
+// first tile) stays small beside its keys.  No more than 256 MB of partial sums,
+// or a grid of 2^17 CTAs (more only where the sequences alone are more).
+static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
 {
     const int mr = cached_rows(d), R = d.T * (d.Hq / d.Hk);
-    const int64_t units = (int64_t)d.B * d.Hk * ((R + mr - 1) / mr);
-    int64_t ns = ((int64_t)sm_count() * 8 + units - 1) / units;
+    const bool wide = mr == kWideRows;
+    const int64_t units = (int64_t)d.B * d.Hk * ((R + mr - 1) / mr), sms = sm_count();
+    Pieces p;
+    p.unit = wide ? 128 : kKeys;
+    p.least = units >= 4 * sms ? 1024 : units >= sms ? 512 : units >= sms / 4 ? 256 : 128;
+    int64_t ns = (sms * (wide ? 1 : 8) + units - 1) / units;
     const int64_t even = (max_keys + 2047) / 2048;
     ns = ns > even ? ns : even;
-    const int64_t most[3] = {(max_keys + kMinSplit - 1) / kMinSplit,
+    const int64_t most[3] = {(max_keys + p.least - 1) / p.least,
                              ((int64_t)256 << 20) / ((int64_t)d.B * d.T * d.Hq * (d.d + 2) * 4), (1 << 17) / units};
     for (int i = 0; i < 3; ++i)
         ns = ns < most[i] ? ns : most[i];
-    return ns < 1 ? 1 : (int)ns;
+    p.ns = ns < 1 ? 1 : (int)ns;
+    return p;
 }
+
+int cached_splits(const bdla_attn_dims &d, int64_t max_keys) { return cached_pieces(d, max_keys).ns; }
 
 size_t cached_partial_bytes(const bdla_attn_dims &d, int splits)
 {
@@ -510,47 +514,61 @@ size_t cached_partial_bytes(const bdla_attn_dims &d, int splits)
 }
 
 template <int D, int WR>
-static cudaError_t cached_go(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,
-                             __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int ns, void *partials,
-                             DeviceStatus *st, cudaStream_t stream)
+static cudaError_t cached_go(const Call &a, const bdla_attn_dims &d, cudaStream_t stream)
 {
     const int R = d.T * (d.Hq / d.Hk), row_blocks = (R + 16 * WR - 1) / (16 * WR);
-    const int64_t rows = (int64_t)d.B * d.T * d.Hq, grid = (int64_t)d.B * d.Hk * row_blocks * ns;
-    if (grid > INT32_MAX)
-        return cudaErrorInvalidValue;
-    float *part_o = static_cast<float *>(partials), *part_ml = part_o + (size_t)ns * rows * D;
+    const int64_t grid = (int64_t)d.B * d.Hk * row_blocks * a.pieces.ns;
     const size_t smem = sizeof(CachedSmem<D>);
-    cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
-    cached_kernel<D, WR><<<(unsigned)grid, kCThreads, smem, stream>>>(q, c, tree, scale, o, lse, part_o, part_ml, d.T,
-                                                                      d.Hq, d.Hk, row_blocks, ns, st);
-    err = cudaGetLastError();
-    if (err != cudaSuccess || ns == 1)
-        return err;
-    combine_kernel<D><<<(unsigned)rows, 128, 0, stream>>>(part_o, part_ml, c, scale, o, lse, d.T, d.Hq, d.Hk, ns);
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    cached_kernel<D, WR><<<(unsigned)grid, kCThreads, smem, stream>>>(a, row_blocks);
+    return cudaGetLastError();
+}
+
+template <int D> static cudaError_t combine_go(const Call &a, int64_t rows, cudaStream_t stream)
+{
+    if (a.pieces.ns > 32)
+        combine_kernel<D, 16><<<(unsigned)rows, 512, 0, stream>>>(a, rows);
+    else if (a.pieces.ns > 8)
+        combine_kernel<D, 4><<<(unsigned)rows, 128, 0, stream>>>(a, rows);
+    else
+        combine_kernel<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a, rows);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,
-                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int splits, void *partials,
+                               __nv_bfloat16 *o, float *lse, const bdla_attn_dims &d, int64_t max_keys, void *partials,
                                DeviceStatus *st, cudaStream_t stream)
 {
     const int mr = cached_rows(d);
-#define BDLA_GO(D_, W_) return cached_go<D_, W_>(q, c, tree, scale, o, lse, d, splits, partials, st, stream)
-    if (d.d == 64) {
-        if (mr == 16)
-            BDLA_GO(64, 1);
-        if (mr == 32)
-            BDLA_GO(64, 2);
-        BDLA_GO(64, 4);
-    }
-    if (mr == 16)
-        BDLA_GO(128, 1);
-    if (mr == 32)
-        BDLA_GO(128, 2);
-    BDLA_GO(128, 4);
-#undef BDLA_GO
+    const int64_t rows = (int64_t)d.B * d.T * d.Hq;
+    Call a;
+    a.q = q;
+    a.c = c;
+    a.tree = tree;
+    a.scale = scale;
+    a.o = o;
+    a.lse = lse;
+    a.T = d.T;
+    a.Hq = d.Hq;
+    a.Hk = d.Hk;
+    a.pieces = cached_pieces(d, max_keys);
+    a.st = st;
+    a.part_o = static_cast<float *>(partials);
+    a.part_ml = a.part_o + (size_t)a.pieces.ns * rows * d.d;
+    cudaError_t err;
+    if (mr == kWideRows)
+        err = launch_cached_wide(a, d, stream);
+    else if (d.d == 64)
+        err = mr == 16 ? cached_go<64, 1>(a, d, stream) : cached_go<64, 2>(a, d, stream);
+    else
+        err = mr == 16 ? cached_go<128, 1>(a, d, stream) : cached_go<128, 2>(a, d, stream);
+    if (err != cudaSuccess || a.pieces.ns == 1)
+        return err;
+    return d.d == 64 ? combine_go<64>(a, rows, stream) : combine_go<128>(a, rows, stream);
 }
 
 }  // namespace bdla
