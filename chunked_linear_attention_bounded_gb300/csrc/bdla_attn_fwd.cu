@@ -45,7 +45,6 @@ using namespace attn;
 
 constexpr int kPairBlocks = 2;                   // query tiles of a CTA
 constexpr int kThreads = 64 + kPairBlocks * BT;  // loader, MMA issuer, softmax
-constexpr float kSlack = 8.0f;                   // log2 of how far weights may exceed 1
 
 template <int D> struct FwdSmem {
     static constexpr int kPanels = D / 64;
@@ -53,7 +52,8 @@ template <int D> struct FwdSmem {
     static constexpr int kStages = D == 128 ? 5 : 8;
     alignas(1024) unsigned char q[kPairBlocks][kTile];   // queries, then the output's staging
     alignas(1024) unsigned char ring[kStages][kTile];    // K_0 V_0 K_1 V_1 ...
-    uint64_t full_q, full[kStages], empty[kStages], s_full[kPairBlocks], p_ready[kPairBlocks], o_done[kPairBlocks];
+    uint64_t full_q, full[kStages], empty[kStages], s_full[kPairBlocks], o_done[kPairBlocks];
+    uint64_t p_ready[kPairBlocks][2];   // weights of the first and of the last 64 keys of a tile
     uint64_t drain, never;
     uint64_t wait_ns;
     uint32_t tmem_base;
@@ -105,7 +105,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
         for (int w = 0; w < kPairBlocks; ++w) {
             mbar_init(&sm.s_full[w], 1);
-            mbar_init(&sm.p_ready[w], BT);
+            mbar_init(&sm.p_ready[w][0], BT);
+            mbar_init(&sm.p_ready[w][1], BT);
             mbar_init(&sm.o_done[w], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -191,15 +192,23 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     const int it = 2 * j + 1;
                     const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
                     ok = !*abort_flag &&
-                         mbar_wait_lim(hook ? &sm.never : &sm.p_ready[w], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns) &&
+                         mbar_wait_lim(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns) &&
                          mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns);
                     if (!ok)
                         break;
                     tc_fence_after();
                     const uint32_t b = smem_u32(sm.ring[it % NS]);
-                    for (int ks = 0; ks < BT / 16; ++ks)
+                    for (int ks = 0; ks < BT / 16; ++ks) {
+                        if (ks == BT / 32) {
+                            if (!(ok = mbar_wait_lim(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns)))
+                                break;
+                            tc_fence_after();
+                        }
                         umma_bf16_ts(tmem + 2 * BT + BT * w, tmem + BT * w + ks * 8,
                                      sdesc_sw128(b + ks * 2048, kPanel, 1024), id_pv, j > 0 || ks > 0);
+                    }
+                    if (!ok)
+                        break;
                     if (w == 1 || j >= n_kv[1])
                         umma_commit(&sm.empty[it % NS]);
                     if (j + 1 < n_kv[w])
@@ -226,7 +235,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         const int n = n_kv[w];
         const int valid = (int)(span.len - w * BT);   // rows of the tile inside the document (may exceed 128)
         const float c = scale * kLog2e;
-        float m = -INFINITY, mc = -INFINITY, l = 0.0f;   // reference, times c; sum of the weights
+        RowSoftmax row;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
@@ -246,50 +255,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     for (int i = 0; i < 32; ++i)
                         x[k][i] = 32 * k + i > r ? 0xff800000u : x[k][i];
             }
-            float mx[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                mx[k] = __uint_as_float(x[k][0]);
-#pragma unroll
-                for (int i = 1; i < 32; ++i)
-                    mx[k] = fmaxf(mx[k], __uint_as_float(x[k][i]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool move = (top - m) * c > kSlack;
-            if (__any_sync(0xffffffffu, move)) {
-                const float f = move ? ex2(mc - top * c) : 1.0f;
-                if (move) {
-                    m = top;
-                    mc = top * c;
-                }
-                l *= f;
-                if (j > 0) {
-#pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t y[32];
-                        tmem_ld32(t_o + 32 * k, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                        tmem_st32(t_o + 32 * k, y);
-                    }
-                }
-            }
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t u[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = ex2(fmaf(__uint_as_float(x[k][2 * i]), c, -mc));
-                    const float b = ex2(fmaf(__uint_as_float(x[k][2 * i + 1]), c, -mc));
-                    sum[i & 3] += a + b;
-                    u[i] = pack_bf16(a, b);
-                }
-                tmem_st16(t_s + 16 * k, u);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (j == n - 1 && valid < BT) {
                 // this tile alone reads the document's last values: clear the rows past the end
                 const int it = 2 * j + 1;
@@ -299,9 +264,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 clear_rows(sm.ring[it % NS], NP, valid, r, BT);
                 fence_proxy_async_smem();
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sm.p_ready[w]);
+            row_weights<D>(x, c, t_s, t_o, j == 0, row, [&](int half) { mbar_arrive(&sm.p_ready[w][half]); });
         }
         if (ok && n > 0)
             ok = warp_wait(&sm.o_done[w], 0, &sm.wait_ns, abort_flag);
@@ -309,8 +272,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tc_fence_after();
             const int64_t t0 = span.start + w * BT;
             if (r < valid)
-                lse[(int64_t)h * tokens + t0 + r] = (mc + log2f(l)) * kLn2;
-            const float inv = 1.0f / l;
+                lse[(int64_t)h * tokens + t0 + r] = (row.mc + log2f(row.l)) * kLn2;
+            const float inv = 1.0f / row.l;
             // the tile's queries have been read: a warp stages its own 32 rows of 128 bytes there
 #pragma unroll
             for (int p = 0; p < NP; ++p)

@@ -25,6 +25,113 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Two fp32 values in one 64-bit register, and the operations that take both at
+// the cost of one.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Softmax of one row in one pass: reference m, the reference times the factor
+// c of the scores in base 2 (0 until something has been seen), and the sum of
+// the weights e^{(s - m)} so far.
+struct RowSoftmax {
+    float m = -INFINITY, mc = 0.0f, l = 0.0f;
+};
+
+constexpr float kSlack = 8.0f;   // log2 of how far weights may exceed 1
+
+// One thread's 128 scores x (masked ones -inf) into bf16 weights over them in
+// tensor memory (t_s), 64 at a time, each half handed over by half_done(0 / 1).
+// The reference moves only when a score exceeds it by more than kSlack; the
+// output so far (t_o, D columns, none if `first`) is then rescaled there.
+template <int D, typename Half>
+__device__ __forceinline__ void row_weights(uint32_t (&x)[4][32], float c, uint32_t t_s, uint32_t t_o, bool first,
+                                            RowSoftmax &s, Half half_done)
+{
+    float mx[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        mx[k] = fmaxf(__uint_as_float(x[k][0]), __uint_as_float(x[k][1]));
+#pragma unroll
+        for (int i = 2; i < 32; i += 2)
+            mx[k] = max3(mx[k], __uint_as_float(x[k][i]), __uint_as_float(x[k][i + 1]));
+    }
+    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+    const bool move = (top - s.m) * c > kSlack;
+    if (__any_sync(0xffffffffu, move)) {
+        const float f = !move ? 1.0f : s.m == -INFINITY ? 0.0f : ex2(s.mc - top * c);
+        if (move) {
+            s.m = top;
+            s.mc = top * c;
+        }
+        s.l *= f;
+        if (!first) {
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t y[16];
+                sm100::tmem_ld16(t_o + 16 * k, y);
+                sm100::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                sm100::tmem_st16(t_o + 16 * k, y);
+            }
+        }
+    }
+    const uint64_t c2 = pair(c, c), b2 = pair(-s.mc, -s.mc);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpair(fma2(pair(__uint_as_float(x[k][2 * i]), __uint_as_float(x[k][2 * i + 1])), c2, b2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[i & 1] = add2(sum[i & 1], pair(a, b));
+            u[i] = sm100::pack_bf16(a, b);
+        }
+        sm100::tmem_st16(t_s + 16 * k, u);
+        if (k & 1) {
+            sm100::tmem_st_wait();
+            sm100::tc_fence_before();
+            half_done(k >> 1);
+        }
+    }
+    float a, b;
+    unpair(add2(sum[0], sum[1]), a, b);
+    s.l += a + b;
+}
+
 // Packed offsets: cu[0] = 0, non-decreasing, cu[n_docs] = tokens; the first
 // bad document is recorded.  Run by the threads of one CTA.
 __device__ __forceinline__ void check_offsets(const int32_t *cu, int n_docs, int64_t tokens, DeviceStatus *st)
