@@ -138,28 +138,6 @@ __device__ __forceinline__ void run_loader(Smem &sm, int n, int stall_it, Device
     }
 }
 
-// D[acc] = A B^T of two tiles whose rows are the operands' rows (features summed).
-template <int D> __device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b)
-{
-    constexpr uint32_t id = idesc_bf16_f32(BT, BT, false, false);
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
-        umma_bf16(acc, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id, ks > 0);
-    }
-}
-
-// D[acc] += A B: A bf16 [128 x 128] in tensor memory (the first and second 64
-// columns' pairs at `a` and `a + 64`), B a tile whose rows are summed over.
-template <int D> __device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t a, uint32_t b, bool accumulate)
-{
-    constexpr uint32_t id = idesc_bf16_f32(BT, D, false, true);
-#pragma unroll
-    for (int ks = 0; ks < BT / 16; ++ks)
-        umma_bf16_ts(acc, a + (ks >> 2) * 64 + (ks & 3) * 8, sdesc_sw128(b + ks * 2048, kPanel, 1024), id,
-                     accumulate || ks > 0);
-}
-
 // ---------------------------------------------------------------- dq
 // Tensor memory: scores of even and odd key tiles (ds over them), dp, dq.  While
 // the weights of tile j are formed, the tensor cores run S of j + 1, dp of j + 1
@@ -213,14 +191,14 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t q = smem_u32(sm.own[0]), g = smem_u32(sm.own[1]);
+            const uint64_t q = rows_desc(smem_u32(sm.own[0])), g = rows_desc(smem_u32(sm.own[1]));
             auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
             auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
             auto issue_s = [&](int j) {
                 if (!landed(2 * j))
                     return false;
                 tc_fence_after();
-                mma_rows<D>(tmem + BT * (j & 1), q, tile(2 * j));
+                mma_rows<D>(tmem + BT * (j & 1), q, rows_desc(tile(2 * j)));
                 umma_commit(&sm.s_full[j & 1]);
                 return true;
             };
@@ -228,7 +206,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 if (!landed(2 * j + 1))
                     return false;
                 tc_fence_after();
-                mma_rows<D>(t_dp, g, tile(2 * j + 1));
+                mma_rows<D>(t_dp, g, rows_desc(tile(2 * j + 1)));
                 umma_commit(&sm.dp_full);
                 umma_commit(&sm.empty[(2 * j + 1) % NS]);
                 return true;
@@ -243,7 +221,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma_sum<D>(t_dq, tmem + BT * (j & 1), tile(2 * j), j > 0);
+                mma_sum<D, 64>(t_dq, tmem + BT * (j & 1), sum_desc(tile(2 * j)), j > 0);
                 umma_commit(&sm.empty[(2 * j) % NS]);
             }
             if (ok) {
@@ -401,14 +379,14 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t k = smem_u32(sm.own[0]), v = smem_u32(sm.own[1]);
+            const uint64_t k = rows_desc(smem_u32(sm.own[0])), v = rows_desc(smem_u32(sm.own[1]));
             auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
             auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
             auto issue_s = [&](int t) {
                 if (!landed(2 * t))
                     return false;
                 tc_fence_after();
-                mma_rows<D>(tmem, k, tile(2 * t));
+                mma_rows<D>(tmem, k, rows_desc(tile(2 * t)));
                 umma_commit(&sm.s_full[0]);
                 return true;
             };
@@ -416,7 +394,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!landed(2 * t + 1))
                     return false;
                 tc_fence_after();
-                mma_rows<D>(t_dp, v, tile(2 * t + 1));
+                mma_rows<D>(t_dp, v, rows_desc(tile(2 * t + 1)));
                 umma_commit(&sm.dp_full);
                 return true;
             };
@@ -428,14 +406,14 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma_sum<D>(t_dv, tmem, tile(2 * t + 1), t > 0);
+                mma_sum<D, 64>(t_dv, tmem, sum_desc(tile(2 * t + 1)), t > 0);
                 umma_commit(&sm.empty[(2 * t + 1) % NS]);
                 if (t + 1 < n && !(ok = issue_s(t + 1)))
                     break;
                 if (!(ok = mbar_wait_lim(&sm.ready[1], t & 1, &sm.wait_ns)))
                     break;
                 tc_fence_after();
-                mma_sum<D>(t_dk, t_dp, tile(2 * t), t > 0);
+                mma_sum<D, 64>(t_dk, t_dp, sum_desc(tile(2 * t)), t > 0);
                 umma_commit(&sm.empty[(2 * t) % NS]);
                 if (t + 1 < n)
                     ok = issue_dp(t + 1);

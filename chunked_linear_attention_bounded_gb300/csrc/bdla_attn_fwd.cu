@@ -162,8 +162,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (lane == 0) {
-            const uint32_t id_qk = idesc_bf16_f32(BT, BT, false, false);
-            const uint32_t id_pv = idesc_bf16_f32(BT, D, false, true);
+            const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
             bool ok = mbar_wait_lim(&sm.full_q, 0, &sm.wait_ns);
             // S_w = Q_w K_j^T over the scores (and weights) of tile j - 1
             auto issue_qk = [&](int w, int j) {
@@ -171,12 +170,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 if (!mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns))
                     return false;
                 tc_fence_after();
-                const uint32_t a = smem_u32(sm.q[w]), b = smem_u32(sm.ring[it % NS]);
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
-                    umma_bf16(tmem + BT * w, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id_qk,
-                              ks > 0);
-                }
+                mma_rows<D>(tmem + BT * w, q[w], rows_desc(smem_u32(sm.ring[it % NS])));
                 umma_commit(&sm.s_full[w]);
                 if (w == 1 || j >= n_kv[1])   // the last reader of this key tile
                     umma_commit(&sm.empty[it % NS]);
@@ -197,18 +191,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t b = smem_u32(sm.ring[it % NS]);
-                    for (int ks = 0; ks < BT / 16; ++ks) {
-                        if (ks == BT / 32) {
-                            if (!(ok = mbar_wait_lim(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns)))
-                                break;
-                            tc_fence_after();
-                        }
-                        umma_bf16_ts(tmem + 2 * BT + BT * w, tmem + BT * w + ks * 8,
-                                     sdesc_sw128(b + ks * 2048, kPanel, 1024), id_pv, j > 0 || ks > 0);
-                    }
-                    if (!ok)
+                    const uint64_t b = sum_desc(smem_u32(sm.ring[it % NS]));
+                    const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
+                    mma_sum<D, 32, 0, BT / 32>(acc, wt, b, j > 0);
+                    if (!(ok = mbar_wait_lim(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns)))
                         break;
+                    tc_fence_after();
+                    mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, b, true);
                     if (w == 1 || j >= n_kv[1])
                         umma_commit(&sm.empty[it % NS]);
                     if (j + 1 < n_kv[w])

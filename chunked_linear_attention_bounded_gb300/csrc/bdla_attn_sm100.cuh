@@ -141,6 +141,35 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int n_docs, int
             set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
 }
 
+// Products of two 128-row tiles, issued by one thread.  A K step of 16 takes the
+// tensor cores 64 cycles, so its descriptors are a constant added to the tile's
+// (the address field holds all of shared memory: no carry leaves it).
+__device__ __forceinline__ uint64_t rows_desc(uint32_t tile) { return sm100::sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t sum_desc(uint32_t tile) { return sm100::sdesc_sw128(tile, kPanel, 1024); }
+
+// D[acc] = A B^T: rows of both tiles are the operands' rows, features summed.
+template <int D> __device__ __forceinline__ void mma_rows(uint32_t acc, uint64_t a, uint64_t b)
+{
+    constexpr uint32_t id = sm100::idesc_bf16_f32(BT, BT, false, false);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
+        sm100::umma_bf16(acc, a + off, b + off, id, ks > 0);
+    }
+}
+
+// D[acc] (+)= A B: K steps [First, Last) of A, bf16 [128 x 128] in tensor memory
+// with its 64 left columns' pairs at `a` and the others at `a + Right`, and B a
+// tile whose rows are summed over.
+template <int D, int Right, int First = 0, int Last = BT / 16>
+__device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t a, uint64_t b, bool accumulate)
+{
+    constexpr uint32_t id = sm100::idesc_bf16_f32(BT, D, false, true);
+#pragma unroll
+    for (int ks = First; ks < Last; ++ks)
+        sm100::umma_bf16_ts(acc, a + (ks >> 2) * Right + (ks & 3) * 8, b + ks * (2048 >> 4), id, accumulate || ks > 0);
+}
+
 // All lanes' waits, as one answer for the warp (the tensor-memory accesses
 // that follow need whole warps).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const uint64_t *limit, volatile int *abort_flag)
