@@ -190,49 +190,58 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             });
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint64_t q = rows_desc(smem_u32(sm.own[0])), g = rows_desc(smem_u32(sm.own[1]));
-            auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
-            auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
-            auto issue_s = [&](int j) {
-                if (!landed(2 * j))
-                    return false;
-                tc_fence_after();
+        const uint64_t q = rows_desc(smem_u32(sm.own[0])), g = rows_desc(smem_u32(sm.own[1]));
+        auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
+        auto landed = [&](int it) { return warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag); };
+        auto issue_s = [&](int j) {
+            if (!landed(2 * j))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_rows<D>(tmem + BT * (j & 1), q, rows_desc(tile(2 * j)));
                 umma_commit(&sm.s_full[j & 1]);
-                return true;
-            };
-            auto issue_dp = [&](int j) {
-                if (!landed(2 * j + 1))
-                    return false;
-                tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_dp = [&](int j) {
+            if (!landed(2 * j + 1))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_rows<D>(t_dp, g, rows_desc(tile(2 * j + 1)));
                 umma_commit(&sm.dp_full);
                 umma_commit(&sm.empty[(2 * j + 1) % NS]);
-                return true;
-            };
-            bool ok = mbar_wait_lim(&sm.full_own, 0, &sm.wait_ns) && issue_s(0) && issue_dp(0);
-            for (int j = 0; ok && j < n; ++j) {
-                const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
-                if (j + 1 < n)
-                    ok = issue_s(j + 1) && mbar_wait_lim(&sm.dp_free, j & 1, &sm.wait_ns) && issue_dp(j + 1);
-                ok = ok && !*abort_flag &&
-                     mbar_wait_lim(hook ? &sm.never : &sm.ready[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns);
-                if (!ok)
-                    break;
-                tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = warp_wait(&sm.full_own, 0, &sm.wait_ns, abort_flag) && issue_s(0) && issue_dp(0);
+        for (int j = 0; ok && j < n; ++j) {
+            const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
+            if (j + 1 < n)
+                ok = issue_s(j + 1) && warp_wait(&sm.dp_free, j & 1, &sm.wait_ns, abort_flag) && issue_dp(j + 1);
+            ok = ok && warp_wait(hook ? &sm.never : &sm.ready[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns, abort_flag);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_sum<D, 64>(t_dq, tmem + BT * (j & 1), sum_desc(tile(2 * j)), j > 0);
                 umma_commit(&sm.empty[(2 * j) % NS]);
+                if (j == n - 1)
+                    umma_commit(&sm.done);
             }
-            if (ok) {
-                umma_commit(&sm.done);
-            } else {
-                *abort_flag = 1;
-                set_status(st, BDLA_ERR_TIMEOUT, 0x21u);
-            }
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, kDrainNs);
+            __syncwarp();
         }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x21u);
+        }
+        if (elect_one())
+            umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
     } else {
         const int half = (warp - 2) >> 2, q4 = warp & 3, r = 32 * q4 + lane, e = 128 * half + r;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
@@ -378,55 +387,67 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             });
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint64_t k = rows_desc(smem_u32(sm.own[0])), v = rows_desc(smem_u32(sm.own[1]));
-            auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
-            auto landed = [&](int it) { return mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns); };
-            auto issue_s = [&](int t) {
-                if (!landed(2 * t))
-                    return false;
-                tc_fence_after();
+        const uint64_t k = rows_desc(smem_u32(sm.own[0])), v = rows_desc(smem_u32(sm.own[1]));
+        auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
+        auto landed = [&](int it) { return warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag); };
+        auto issue_s = [&](int t) {
+            if (!landed(2 * t))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_rows<D>(tmem, k, rows_desc(tile(2 * t)));
                 umma_commit(&sm.s_full[0]);
-                return true;
-            };
-            auto issue_dp = [&](int t) {
-                if (!landed(2 * t + 1))
-                    return false;
-                tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_dp = [&](int t) {
+            if (!landed(2 * t + 1))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_rows<D>(t_dp, v, rows_desc(tile(2 * t + 1)));
                 umma_commit(&sm.dp_full);
-                return true;
-            };
-            bool ok = mbar_wait_lim(&sm.full_own, 0, &sm.wait_ns) && issue_s(0) && issue_dp(0);
-            for (int t = 0; ok && t < n; ++t) {
-                const bool hook = stall == BDLA_STALL_MMA && t == stall_at;
-                ok = !*abort_flag &&
-                     mbar_wait_lim(hook ? &sm.never : &sm.ready[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns);
-                if (!ok)
-                    break;
-                tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = warp_wait(&sm.full_own, 0, &sm.wait_ns, abort_flag) && issue_s(0) && issue_dp(0);
+        for (int t = 0; ok && t < n; ++t) {
+            const bool hook = stall == BDLA_STALL_MMA && t == stall_at;
+            ok = warp_wait(hook ? &sm.never : &sm.ready[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns, abort_flag);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_sum<D, 64>(t_dv, tmem, sum_desc(tile(2 * t + 1)), t > 0);
                 umma_commit(&sm.empty[(2 * t + 1) % NS]);
-                if (t + 1 < n && !(ok = issue_s(t + 1)))
-                    break;
-                if (!(ok = mbar_wait_lim(&sm.ready[1], t & 1, &sm.wait_ns)))
-                    break;
-                tc_fence_after();
+            }
+            __syncwarp();
+            if (t + 1 < n && !(ok = issue_s(t + 1)))
+                break;
+            if (!(ok = warp_wait(&sm.ready[1], t & 1, &sm.wait_ns, abort_flag)))
+                break;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_sum<D, 64>(t_dk, t_dp, sum_desc(tile(2 * t)), t > 0);
                 umma_commit(&sm.empty[(2 * t) % NS]);
-                if (t + 1 < n)
-                    ok = issue_dp(t + 1);
+                if (t == n - 1)
+                    umma_commit(&sm.done);
             }
-            if (ok) {
-                umma_commit(&sm.done);
-            } else {
-                *abort_flag = 1;
-                set_status(st, BDLA_ERR_TIMEOUT, 0x23u);
-            }
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, kDrainNs);
+            __syncwarp();
+            if (t + 1 < n)
+                ok = issue_dp(t + 1);
         }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x23u);
+        }
+        if (elect_one())
+            umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
     } else {
         const int half = (warp - 2) >> 2, q4 = warp & 3, r = 32 * q4 + lane, e = 128 * half + r;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;

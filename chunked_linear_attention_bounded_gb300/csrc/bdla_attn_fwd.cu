@@ -161,59 +161,70 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
-            bool ok = mbar_wait_lim(&sm.full_q, 0, &sm.wait_ns);
-            // S_w = Q_w K_j^T over the scores (and weights) of tile j - 1
-            auto issue_qk = [&](int w, int j) {
-                const int it = 2 * j;
-                if (!mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns))
-                    return false;
-                tc_fence_after();
-                mma_rows<D>(tmem + BT * w, q[w], rows_desc(smem_u32(sm.ring[it % NS])));
+        const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
+        bool ok = warp_wait(&sm.full_q, 0, &sm.wait_ns, abort_flag);
+        // S_w = Q_w K_j^T over the scores (and weights) of tile j - 1
+        auto issue_qk = [&](int w, int j) {
+            const int it = 2 * j;
+            if (!warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag))
+                return false;
+            tc_fence_after();
+            const uint64_t k = rows_desc(smem_u32(sm.ring[it % NS]));
+            if (elect_one()) {
+                mma_rows<D>(tmem + BT * w, q[w], k);
                 umma_commit(&sm.s_full[w]);
                 if (w == 1 || j >= n_kv[1])   // the last reader of this key tile
                     umma_commit(&sm.empty[it % NS]);
-                return true;
-            };
-            for (int w = 0; ok && w < 2; ++w)
-                if (n_kv[w] > 0)
-                    ok = issue_qk(w, 0);
-            for (int j = 0; ok && j < n_max; ++j) {
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (j >= n_kv[w])
-                        continue;
-                    const int it = 2 * j + 1;
-                    const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
-                    ok = !*abort_flag &&
-                         mbar_wait_lim(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns) &&
-                         mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint64_t b = sum_desc(smem_u32(sm.ring[it % NS]));
-                    const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
-                    mma_sum<D, 32, 0, BT / 32>(acc, wt, b, j > 0);
-                    if (!(ok = mbar_wait_lim(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns)))
-                        break;
-                    tc_fence_after();
-                    mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, b, true);
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int w = 0; ok && w < 2; ++w)
+            if (n_kv[w] > 0)
+                ok = issue_qk(w, 0);
+        for (int j = 0; ok && j < n_max; ++j) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!ok || j >= n_kv[w])
+                    continue;
+                const int it = 2 * j + 1;
+                const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
+                ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag) &&
+                     warp_wait(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    continue;
+                tc_fence_after();
+                const uint64_t v = sum_desc(smem_u32(sm.ring[it % NS]));
+                const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
+                if (elect_one())
+                    mma_sum<D, 32, 0, BT / 32>(acc, wt, v, j > 0);
+                __syncwarp();
+                ok = warp_wait(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    continue;
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, v, true);
                     if (w == 1 || j >= n_kv[1])
                         umma_commit(&sm.empty[it % NS]);
-                    if (j + 1 < n_kv[w])
-                        ok = issue_qk(w, j + 1);
-                    else
+                    if (j + 1 >= n_kv[w])
                         umma_commit(&sm.o_done[w]);
                 }
+                __syncwarp();
+                if (j + 1 < n_kv[w])
+                    ok = issue_qk(w, j + 1);
             }
-            if (!ok) {
-                *abort_flag = 1;
-                set_status(st, BDLA_ERR_TIMEOUT, 0x11u);
-            }
-            // every MMA issued above has completed before TMEM is released
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, kDrainNs);
         }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(st, BDLA_ERR_TIMEOUT, 0x11u);
+        }
+        // every MMA issued above has completed before TMEM is released
+        if (elect_one())
+            umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
     } else {
         // ---------------------------------------------------------------- softmax
         const int w = (warp - 2) >> 2;

@@ -141,9 +141,25 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int n_docs, int
             set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
 }
 
-// Products of two 128-row tiles, issued by one thread.  A K step of 16 takes the
-// tensor cores 64 cycles, so its descriptors are a constant added to the tile's
-// (the address field holds all of shared memory: no carry leaves it).
+// One lane of a whole warp, the same one each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// Products of two 128-row tiles.  A K step of 16 takes the tensor cores 64
+// cycles, so issuing it must take less: the whole warp walks the tiles, so that
+// descriptors are warp-uniform values, and one elected lane issues a product's
+// steps (one lane of a diverged warp took 85 to 120 cycles a step, which left
+// the tensor cores at half of their time).  A step's descriptors are a constant
+// added to the tile's (the address field holds all of shared memory: no carry
+// leaves it).
 __device__ __forceinline__ uint64_t rows_desc(uint32_t tile) { return sm100::sdesc_sw128(tile, 16, 1024); }
 __device__ __forceinline__ uint64_t sum_desc(uint32_t tile) { return sm100::sdesc_sw128(tile, kPanel, 1024); }
 
@@ -171,9 +187,13 @@ __device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t a, uint64_t b, bo
 }
 
 // All lanes' waits, as one answer for the warp (the tensor-memory accesses
-// that follow need whole warps).
+// that follow need whole warps).  The abort flag is read only after a wait that
+// was not over at once: the read cost the MMA warp a few hundred cycles each
+// time, a quarter of the forward's time.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const uint64_t *limit, volatile int *abort_flag)
 {
+    if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity)))
+        return true;
     const bool ok = sm100::mbar_wait_lim(bar, parity, limit) && !*abort_flag;
     return __all_sync(0xffffffffu, ok);
 }
