@@ -46,10 +46,15 @@ constexpr int kThreads = 64 + kEpi;    // + loader and MMA issuer
 template <int D> struct BwdSmem {
     static constexpr int kPanels = D / 64;
     static constexpr int kTile = kPanels * kPanel;
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    // Tiles of K and V (of Q and dO) in a ring each.  K (Q) is held from the scores to the last product of its tile,
+    // V (dO) for less long, so K's ring is the longer: in one ring of five, V waited for K, and a load's latency stood
+    // in every tile's time.
+    static constexpr int kA = D == 128 ? 3 : 4, kB = D == 128 ? 2 : 4, kStages = kA + kB;
     alignas(1024) unsigned char own[2][kTile];          // Q, dO of the query tile, or K, V of the key tile
-    alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 ..., or Q_0 dO_0 Q_1 ...
-    float col[2][2][BT];   // key tiles: lse * log2 e and delta of a query tile; query tiles: [0] halves of delta
+    alignas(1024) unsigned char ring[kStages][kTile];   // kA tiles of K (Q), kB of V (dO)
+    static __host__ __device__ constexpr int slot(int it) { return it & 1 ? kA + (it >> 1) % kB : (it >> 1) % kA; }
+    static __host__ __device__ constexpr int turn(int it) { return it & 1 ? (it >> 1) / kB : (it >> 1) / kA; }
+    float col[2][2][BT];   // key tiles: -lse * log2 e and -delta of a query tile; query tiles: [0] halves of delta
     uint64_t full_own, full[kStages], empty[kStages], s_full[2], ready[2], dp_full, dp_free, done;
     uint64_t drain, never;
     uint64_t wait_ns;
@@ -108,20 +113,20 @@ __device__ __forceinline__ void setup(Smem &sm, int tid, uint64_t wait_ns)
     tc_fence_after();
 }
 
-// The loader's ring: `n` tiles, tile `it` fetched by load(it, slot).  Lets its
-// copies land before it returns from a wait that ran out.
+// The loader's rings: `n` tiles, K_0 V_0 K_1 V_1 ..., tile `it` fetched by
+// load(it, slot).  Lets its copies land before it returns from a wait that ran
+// out.
 template <typename Smem, typename Load>
 __device__ __forceinline__ void run_loader(Smem &sm, int n, int stall_it, DeviceStatus *st, Load load)
 {
-    constexpr int NS = Smem::kStages;
     volatile int *abort_flag = &sm.abort_flag;
     int issued = 0;
     bool ok = true;
     for (int it = 0; it < n; ++it) {
-        const int s = it % NS;
+        const int s = Smem::slot(it), turn = Smem::turn(it);
         const bool hook = it == stall_it;
-        if (*abort_flag || ((it >= NS || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
-                                                                 hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns))) {
+        if (*abort_flag || ((turn > 0 || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
+                                                                 hook ? 0u : (uint32_t)((turn - 1) & 1), &sm.wait_ns))) {
             ok = false;
             break;
         }
@@ -133,8 +138,10 @@ __device__ __forceinline__ void run_loader(Smem &sm, int n, int stall_it, Device
         *abort_flag = 1;
         set_status(st, BDLA_ERR_TIMEOUT, 0x20u);
         mbar_wait(&sm.full_own, 0, kDrainNs);
-        for (int it = issued > NS ? issued - NS : 0; it < issued; ++it)
-            mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
+        // the last tile of every slot
+        for (int it = issued > 2 * Smem::kStages ? issued - 2 * Smem::kStages : 0; it < issued; ++it)
+            if (it + 2 * (it & 1 ? Smem::kB : Smem::kA) >= issued)
+                mbar_wait(&sm.full[Smem::slot(it)], Smem::turn(it) & 1, kDrainNs);
     }
 }
 
@@ -152,7 +159,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                uint64_t wait_ns, int stall)
 {
     using Smem = BwdSmem<D>;
-    constexpr int NS = Smem::kStages, NP = Smem::kPanels;
+    constexpr int NP = Smem::kPanels;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -191,8 +198,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         }
     } else if (warp == 1) {
         const uint64_t q = rows_desc(smem_u32(sm.own[0])), g = rows_desc(smem_u32(sm.own[1]));
-        auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
-        auto landed = [&](int it) { return warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag); };
+        auto tile = [&](int it) { return smem_u32(sm.ring[Smem::slot(it)]); };
+        auto landed = [&](int it) { return warp_wait(&sm.full[Smem::slot(it)], Smem::turn(it) & 1, &sm.wait_ns, abort_flag); };
         auto issue_s = [&](int j) {
             if (!landed(2 * j))
                 return false;
@@ -211,7 +218,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (elect_one()) {
                 mma_rows<D>(t_dp, g, rows_desc(tile(2 * j + 1)));
                 umma_commit(&sm.dp_full);
-                umma_commit(&sm.empty[(2 * j + 1) % NS]);
+                umma_commit(&sm.empty[Smem::slot(2 * j + 1)]);
             }
             __syncwarp();
             return true;
@@ -227,7 +234,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             tc_fence_after();
             if (elect_one()) {
                 mma_sum<D, 64>(t_dq, tmem + BT * (j & 1), sum_desc(tile(2 * j)), j > 0);
-                umma_commit(&sm.empty[(2 * j) % NS]);
+                umma_commit(&sm.empty[Smem::slot(2 * j)]);
                 if (j == n - 1)
                     umma_commit(&sm.done);
             }
@@ -267,6 +274,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         if (half == 0 && r < valid)
             delta[(int64_t)h * tokens + t] = dl;
         const float c = scale * kLog2e;
+        const uint64_t c2 = pair(c, c), nl2 = pair(-l2, -l2), nd2 = pair(-dl, -dl);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
@@ -290,25 +298,29 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const bool diag = j == n - 1;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int m = 0; m < 32; m += 2) {
+                    float a, b;
+                    unpair(fma2(pair(__uint_as_float(x[k][m]), __uint_as_float(x[k][m + 1])), c2, nl2), a, b);
+                    const uint64_t d = add2(pair(__uint_as_float(y[k][m]), __uint_as_float(y[k][m + 1])), nd2);
+                    unpair(mul2(pair(ex2(a), ex2(b)), d), a, b);
+                    y[k][m] = __float_as_uint(a);
+                    y[k][m + 1] = __float_as_uint(b);
+                }
+                if (diag) {
+#pragma unroll
+                    for (int m = 0; m < 32; ++m)
+                        y[k][m] = 64 * half + 32 * k + m > r ? 0u : y[k][m];
+                }
                 uint32_t u[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float ds[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int m = 2 * i + b;
-                        const float p = ex2(fmaf(__uint_as_float(x[k][m]), c, -l2));
-                        ds[b] = p * (__uint_as_float(y[k][m]) - dl);
-                        if (diag && 64 * half + 32 * k + m > r)
-                            ds[b] = 0.0f;
-                    }
-                    u[i] = pack_bf16(ds[0], ds[1]);
-                }
+                for (int i = 0; i < 16; ++i)
+                    u[i] = pack_bf16(__uint_as_float(y[k][2 * i]), __uint_as_float(y[k][2 * i + 1]));
                 tmem_st16(t_s + 16 * k, u);
             }
             if (diag && valid < BT) {
                 // this product sums over the diagonal tile's keys: clear those past the end (S has read them)
-                clear_rows(sm.ring[(2 * j) % NS], NP, valid, e, kEpi);
+                clear_rows(sm.ring[Smem::slot(2 * j)], NP, valid, e, kEpi);
                 fence_proxy_async_smem();
             }
             tmem_st_wait();
@@ -350,7 +362,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 __nv_bfloat16 *__restrict__ dv, DeviceStatus *st, uint64_t wait_ns, int stall)
 {
     using Smem = BwdSmem<D>;
-    constexpr int NS = Smem::kStages, NP = Smem::kPanels;
+    constexpr int NP = Smem::kPanels;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -388,8 +400,8 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
     } else if (warp == 1) {
         const uint64_t k = rows_desc(smem_u32(sm.own[0])), v = rows_desc(smem_u32(sm.own[1]));
-        auto tile = [&](int it) { return smem_u32(sm.ring[it % NS]); };
-        auto landed = [&](int it) { return warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag); };
+        auto tile = [&](int it) { return smem_u32(sm.ring[Smem::slot(it)]); };
+        auto landed = [&](int it) { return warp_wait(&sm.full[Smem::slot(it)], Smem::turn(it) & 1, &sm.wait_ns, abort_flag); };
         auto issue_s = [&](int t) {
             if (!landed(2 * t))
                 return false;
@@ -421,7 +433,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tc_fence_after();
             if (elect_one()) {
                 mma_sum<D, 64>(t_dv, tmem, sum_desc(tile(2 * t + 1)), t > 0);
-                umma_commit(&sm.empty[(2 * t + 1) % NS]);
+                umma_commit(&sm.empty[Smem::slot(2 * t + 1)]);
             }
             __syncwarp();
             if (t + 1 < n && !(ok = issue_s(t + 1)))
@@ -431,7 +443,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tc_fence_after();
             if (elect_one()) {
                 mma_sum<D, 64>(t_dk, t_dp, sum_desc(tile(2 * t)), t > 0);
-                umma_commit(&sm.empty[(2 * t) % NS]);
+                umma_commit(&sm.empty[Smem::slot(2 * t)]);
                 if (t == n - 1)
                     umma_commit(&sm.done);
             }
@@ -453,6 +465,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         const uint32_t t_s = tmem + lane_off + 64 * half, t_d = t_dp + lane_off + 64 * half;
         const float c = scale * kLog2e;
+        const uint64_t c2 = pair(c, c);
         // this thread's entry of a query tile's lse (half 0) or delta (half 1), fetched one tile ahead
         const float *src = half ? delta : lse;
         auto fetch = [&](int t) {
@@ -461,7 +474,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (row >= doc_len)
                 return 0.0f;
             const float x = src[(int64_t)(kh * group + g) * tokens + span.doc_start + row];
-            return half ? x : x * kLog2e;
+            return half ? -x : x * -kLog2e;
         };
         float next = fetch(0);
         bool ok = true;
@@ -486,12 +499,16 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 tmem_ld32(t_s + 32, x[1]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int m4 = 0; m4 < 16; ++m4) {
-                    const float4 l4 = *reinterpret_cast<const float4 *>(&sm.col[t & 1][0][64 * half + 4 * m4]);
-                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        p[4 * m4 + b] = ex2(fmaf(__uint_as_float(x[m4 >> 3][(4 * m4 + b) & 31]), c, -lv[b]));
+                for (int m = 0; m < 64; m += 4) {
+                    const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(&sm.col[t & 1][0][64 * half + m]);
+                    const uint32_t *z = &x[m >> 5][m & 31];
+                    float a, b;
+                    unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), c2, l4.x), a, b);
+                    p[m] = ex2(a);
+                    p[m + 1] = ex2(b);
+                    unpair(fma2(pair(__uint_as_float(z[2]), __uint_as_float(z[3])), c2, l4.y), a, b);
+                    p[m + 2] = ex2(a);
+                    p[m + 3] = ex2(b);
                 }
                 if (i_tile == 0 || valid < BT) {   // the diagonal, or queries past the end
 #pragma unroll
@@ -513,8 +530,8 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                     // dv and dk sum over this tile's queries: clear those past the end once S and dp have read them
                     ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
                     if (ok) {
-                        clear_rows(sm.ring[(2 * t) % NS], NP, valid, e, kEpi);
-                        clear_rows(sm.ring[(2 * t + 1) % NS], NP, valid, e, kEpi);
+                        clear_rows(sm.ring[Smem::slot(2 * t)], NP, valid, e, kEpi);
+                        clear_rows(sm.ring[Smem::slot(2 * t + 1)], NP, valid, e, kEpi);
                         fence_proxy_async_smem();
                     }
                 }
@@ -537,25 +554,30 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const bool mask = i_tile == 0 || valid < BT;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int m = 0; m < 32; m += 4) {
+                    const ulonglong2 d4 = *reinterpret_cast<const ulonglong2 *>(&sm.col[t & 1][1][64 * half + 32 * k + m]);
+                    float a, b;
+                    unpair(mul2(pair(p[32 * k + m], p[32 * k + m + 1]),
+                                add2(pair(__uint_as_float(y[k][m]), __uint_as_float(y[k][m + 1])), d4.x)), a, b);
+                    y[k][m] = __float_as_uint(a);
+                    y[k][m + 1] = __float_as_uint(b);
+                    unpair(mul2(pair(p[32 * k + m + 2], p[32 * k + m + 3]),
+                                add2(pair(__uint_as_float(y[k][m + 2]), __uint_as_float(y[k][m + 3])), d4.y)), a, b);
+                    y[k][m + 2] = __float_as_uint(a);
+                    y[k][m + 3] = __float_as_uint(b);
+                }
+                if (mask) {   // 0 times another document's NaN
+#pragma unroll
+                    for (int m = 0; m < 32; ++m) {
+                        const int q = 64 * half + 32 * k + m;
+                        y[k][m] = (i_tile == 0 && q < r) || q >= valid ? 0u : y[k][m];
+                    }
+                }
                 uint32_t u[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float4 d4 = *reinterpret_cast<const float4 *>(&sm.col[t & 1][1][64 * half + 32 * k + 2 * i]);
-                    const float dv4[4] = {d4.x, d4.y, d4.z, d4.w};
-                    float ds[4];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int m = 32 * k + 2 * i + b;
-                        ds[b] = p[m] * (__uint_as_float(y[k][2 * i + b]) - dv4[b]);
-                        if (mask) {   // 0 times another document's NaN
-                            const int q = 64 * half + m;
-                            if ((i_tile == 0 && q < r) || q >= valid)
-                                ds[b] = 0.0f;
-                        }
-                    }
-                    u[i] = pack_bf16(ds[0], ds[1]);
-                    u[i + 1] = pack_bf16(ds[2], ds[3]);
-                }
+                for (int i = 0; i < 16; ++i)
+                    u[i] = pack_bf16(__uint_as_float(y[k][2 * i]), __uint_as_float(y[k][2 * i + 1]));
                 tmem_st16(t_d + 16 * k, u);
             }
             tmem_st_wait();
