@@ -125,8 +125,8 @@ __device__ __forceinline__ void run_loader(Smem &sm, int n, int stall_it, Device
     for (int it = 0; it < n; ++it) {
         const int s = Smem::slot(it), turn = Smem::turn(it);
         const bool hook = it == stall_it;
-        if (*abort_flag || ((turn > 0 || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
-                                                                 hook ? 0u : (uint32_t)((turn - 1) & 1), &sm.wait_ns))) {
+        if ((turn > 0 || hook) && !lane_wait(hook ? &sm.never : &sm.empty[s], hook ? 0u : (uint32_t)((turn - 1) & 1),
+                                             &sm.wait_ns, abort_flag)) {
             ok = false;
             break;
         }

@@ -138,9 +138,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             for (int it = 0; it < 2 * n_max; ++it) {
                 const int s = it % NS;
                 const bool hook = stall == BDLA_STALL_PRODUCER && it == 2 * stall_at;
-                if (*abort_flag ||
-                    ((it >= NS || hook) && !mbar_wait_lim(hook ? &sm.never : &sm.empty[s],
-                                                          hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns))) {
+                if ((it >= NS || hook) && !lane_wait(hook ? &sm.never : &sm.empty[s],
+                                                     hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns, abort_flag)) {
                     ok = false;
                     break;
                 }

@@ -198,6 +198,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, ok);
 }
 
+// The same for threads on their own.
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, const uint64_t *limit, volatile int *abort_flag)
+{
+    return sm100::mbar_try_wait(bar, parity) || (sm100::mbar_wait_lim(bar, parity, limit) && !*abort_flag);
+}
+
 // Zeroes rows [first, 128) of a tile of `panels` panels; `i` of `n` threads.
 // Whole rows, so the swizzle does not matter.
 __device__ __forceinline__ void clear_rows(unsigned char *tile, int panels, int first, int i, int n)

@@ -27,7 +27,6 @@ using namespace cache;
 
 constexpr int kFetch = 96;                  // fetching threads
 constexpr int kThreads = 32 + kFetch + 256;
-constexpr float kSlack = 8.0f;              // log2 of how far weights may exceed 1
 constexpr int kAhead = 3;                   // tiles in flight per thread
 
 template <int D> struct WideSmem {
@@ -40,7 +39,8 @@ template <int D> struct WideSmem {
     alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 V_1 ...
     int row[kSlots][BT];     // cache row of a tile's positions, -1: not seen
     uint32_t valid[kSlots][4];
-    uint64_t q_ready, full[kStages], empty[kStages], s_full[2], p_ready[2], o_done[2], drain;
+    uint64_t q_ready, full[kStages], empty[kStages], s_full[2], o_done[2], drain;
+    uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
     uint64_t wait_ns;
     uint32_t tmem_base;
     int abort_flag;
@@ -92,7 +92,8 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&sm.s_full[w], 1);
-            mbar_init(&sm.p_ready[w], BT);
+            mbar_init(&sm.p_ready[w][0], BT);
+            mbar_init(&sm.p_ready[w][1], BT);
             mbar_init(&sm.o_done[w], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -108,55 +109,67 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
 
     if (warp == 0) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t id_qk = idesc_bf16_f32(BT, BT, false, false);
-            const uint32_t id_pv = idesc_bf16_f32(BT, D, false, true);
-            bool ok = mbar_wait_lim(&sm.q_ready, 0, &sm.wait_ns);
-            auto issue_qk = [&](int w, int j) {
-                const int it = 2 * j;
-                if (!mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns))
-                    return false;
-                tc_fence_after();
-                const uint32_t x = smem_u32(sm.q[w]), y = smem_u32(sm.ring[it % NS]);
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kPanel + (ks & 3) * 32;
-                    umma_bf16(tmem + BT * w, sdesc_sw128(x + off, 16, 1024), sdesc_sw128(y + off, 16, 1024), id_qk, ks > 0);
-                }
+        const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
+        bool ok = warp_wait(&sm.q_ready, 0, &sm.wait_ns, abort_flag);
+        auto issue_qk = [&](int w, int j) {
+            const int it = 2 * j;
+            if (!warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag))
+                return false;
+            tc_fence_after();
+            const uint64_t k = rows_desc(smem_u32(sm.ring[it % NS]));
+            if (elect_one()) {
+                mma_rows<D>(tmem + BT * w, q[w], k);
                 umma_commit(&sm.s_full[w]);
                 if (w == tiles - 1)   // the last reader of this key tile
                     umma_commit(&sm.empty[it % NS]);
-                return true;
-            };
-            for (int w = 0; ok && nt > 0 && w < tiles; ++w)
-                ok = issue_qk(w, 0);
-            for (int j = 0; ok && j < nt; ++j) {
-                for (int w = 0; ok && w < tiles; ++w) {
-                    const int it = 2 * j + 1;
-                    ok = !*abort_flag && mbar_wait_lim(&sm.p_ready[w], (uint32_t)(j & 1), &sm.wait_ns) &&
-                         mbar_wait_lim(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t y = smem_u32(sm.ring[it % NS]);
-                    for (int ks = 0; ks < BT / 16; ++ks)
-                        umma_bf16_ts(tmem + 2 * BT + BT * w, tmem + BT * w + ks * 8, sdesc_sw128(y + ks * 2048, kPanel, 1024),
-                                     id_pv, j > 0 || ks > 0);
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int w = 0; ok && nt > 0 && w < tiles; ++w)
+            ok = issue_qk(w, 0);
+        for (int j = 0; ok && j < nt; ++j) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!ok || w >= tiles)
+                    continue;
+                const int it = 2 * j + 1;
+                ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag) &&
+                     warp_wait(&sm.p_ready[w][0], (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    continue;
+                tc_fence_after();
+                const uint64_t v = sum_desc(smem_u32(sm.ring[it % NS]));
+                const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
+                if (elect_one())
+                    mma_sum<D, 32, 0, BT / 32>(acc, wt, v, j > 0);
+                __syncwarp();
+                ok = warp_wait(&sm.p_ready[w][1], (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    continue;
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, v, true);
                     if (w == tiles - 1)
                         umma_commit(&sm.empty[it % NS]);
-                    if (j + 1 < nt)
-                        ok = issue_qk(w, j + 1);
-                    else
+                    if (j + 1 == nt)
                         umma_commit(&sm.o_done[w]);
                 }
+                __syncwarp();
+                if (j + 1 < nt)
+                    ok = issue_qk(w, j + 1);
             }
-            if (!ok) {
-                *abort_flag = 1;
-                set_status(a.st, BDLA_ERR_TIMEOUT, 0x30u);
-            }
-            // every MMA issued above has completed before TMEM is released
-            umma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, kDrainNs);
         }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(a.st, BDLA_ERR_TIMEOUT, 0x30u);
+        }
+        // every MMA issued above has completed before TMEM is released
+        if (elect_one())
+            umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
     } else if (warp < 4) {
         // ---------------------------------------------------------------- fetching
         const int ft = tid - 32, fw = warp - 1;
@@ -212,7 +225,7 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
                 const int it = 2 * j + v;
                 // a wait that ran out: the tile is not fetched, and the consumers' waits run out as well
                 if (ok && it >= NS)
-                    ok = mbar_wait_lim(&sm.empty[it % NS], (uint32_t)((it / NS - 1) & 1), &sm.wait_ns) && !*abort_flag;
+                    ok = lane_wait(&sm.empty[it % NS], (uint32_t)((it / NS - 1) & 1), &sm.wait_ns, abort_flag);
                 if (ok) {
                     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(v ? c.v : c.k);
                     const uint32_t dst = smem_u32(sm.ring[it % NS]) + (ch >> 3) * kPanel;
@@ -261,7 +274,7 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         }
         const uint64_t see = k1 > cut.len ? sees(a.tree, b, T, i) : 0;
         const float cs = a.scale * kLog2e;
-        float m = -INFINITY, mc = 0.0f, l = 0.0f;   // reference; times cs (0 while nothing has been seen); sum
+        RowSoftmax row;
         bool ok = true;
         const int n = w < tiles ? nt : 0;
         for (int j = 0; j < n; ++j) {
@@ -293,53 +306,7 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
                         x[k][e] = (mask >> e) & 1 ? x[k][e] : 0xff800000u;
                 }
             }
-            float mx[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                mx[k] = __uint_as_float(x[k][0]);
-#pragma unroll
-                for (int e = 1; e < 32; ++e)
-                    mx[k] = fmaxf(mx[k], __uint_as_float(x[k][e]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool move = (top - m) * cs > kSlack;
-            if (__any_sync(0xffffffffu, move)) {
-                const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : ex2(mc - top * cs);
-                if (move) {
-                    m = top;
-                    mc = top * cs;
-                }
-                l *= f;
-                if (j > 0) {
-#pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t y[32];
-                        tmem_ld32(t_o + 32 * k, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                        tmem_st32(t_o + 32 * k, y);
-                    }
-                }
-            }
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t u[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float p0 = ex2(fmaf(__uint_as_float(x[k][2 * e]), cs, -mc));
-                    const float p1 = ex2(fmaf(__uint_as_float(x[k][2 * e + 1]), cs, -mc));
-                    sum[e & 3] += p0 + p1;
-                    u[e] = pack_bf16(p0, p1);
-                }
-                tmem_st16(t_s + 16 * k, u);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sm.p_ready[w]);
+            row_weights<D>(x, cs, t_s, t_o, j == 0, row, [&](int half) { mbar_arrive(&sm.p_ready[w][half]); });
         }
         if (ok && n > 0)
             ok = warp_wait(&sm.o_done[w], 0, &sm.wait_ns, abort_flag);
@@ -347,7 +314,7 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
             tc_fence_after();
             const bool part = cut.used > 1;
             const int64_t pt = (((int64_t)b * Hk + kh) * ns + piece) * R + rr;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t y[32];
@@ -379,9 +346,9 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
                 }
             }
             if (live_row && part)
-                *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(m, l);
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
             else if (live_row)
-                a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
+                a.lse[at] = row.l == 0.0f ? -INFINITY : fmaf(row.m, a.scale, logf(row.l));
         }
         if (!ok) {
             *abort_flag = 1;
