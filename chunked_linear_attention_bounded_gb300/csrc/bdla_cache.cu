@@ -483,8 +483,8 @@ static int cached_rows(const bdla_attn_dims &d)
 
 // Pieces of a sequence.  Few sequences: enough pieces for eight CTAs an SM (one
 // of the wide kernel, of which one is resident), of at least 128 positions.
-// Many: pieces of about 2048 positions, so that long and short sequences end
-// together, and of at least 1024, so that a CTA's start-up (length, page table,
+// Many: pieces of about 2048 positions (8192 of the wide kernel), so that long
+// and short sequences end together, and of at least 1024, so that a CTA's start-up (length, page table,
 // first tile) stays small beside its keys.  No more than 256 MB of partial sums,
 // or a grid of 2^17 CTAs (more only where the sequences alone are more).
 static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
@@ -496,7 +496,7 @@ static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
     p.unit = wide ? 128 : kKeys;
     p.least = units >= 4 * sms ? 1024 : units >= sms ? 512 : units >= sms / 4 ? 256 : 128;
     int64_t ns = (sms * (wide ? 1 : 8) + units - 1) / units;
-    const int64_t even = (max_keys + 2047) / 2048;
+    const int64_t even = wide ? (max_keys + 8191) / 8192 : (max_keys + 2047) / 2048;
     ns = ns > even ? ns : even;
     const int64_t most[3] = {(max_keys + p.least - 1) / p.least,
                              ((int64_t)256 << 20) / ((int64_t)d.B * d.T * d.Hq * (d.d + 2) * 4), (1 << 17) / units};

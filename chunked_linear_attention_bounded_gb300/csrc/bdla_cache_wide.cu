@@ -6,14 +6,18 @@
 // tiles of 128 that take turns between the tensor cores and their softmax
 // warps, scores and outputs in tensor memory, weights read from there by the
 // P V product, a reference maximum that moves only when a score passes it by
-// 2^8.  What differs is where the keys come from: positions are looked up in
-// the page table, so three warps fetch tiles of 128 positions row by row with
-// cp.async into the swizzled layout that the MMAs read, two or three tiles
-// ahead.  256 rows need 1024 tensor cycles for 64 KB of keys and values, which
-// take 2800 cycles of an SM's share of HBM: the pass is bound by the latter.
+// 2^8.  What differs is where the keys come from: three warps take the tiles of
+// 128 positions in turn, look the positions up in the page table (two tiles of
+// the other warps pass between a lookup and its use) and fetch.  Where 16 or
+// more consecutive positions always share a page, a tile that is wholly visible
+// comes by TMA, one box for each such run, and only a tile with something to
+// leave out (the last of a sequence, a bad page) row by row with cp.async, which
+// writes zeros for a row.  Other page sizes take cp.async throughout.
 //
 // Warp 0 issues the MMAs, warps 1-3 fetch, warps 4-7 and 8-11 are the softmax
 // of the two tiles, one thread a row.
+#include <cudaTypedefs.h>
+
 #include "bdla_attn_sm100.cuh"
 #include "bdla_cache.cuh"
 
@@ -25,21 +29,21 @@ using namespace sm100;
 using namespace attn;
 using namespace cache;
 
-constexpr int kFetch = 96;                  // fetching threads
-constexpr int kThreads = 32 + kFetch + 256;
-constexpr int kAhead = 3;                   // tiles in flight per thread
+constexpr int kFetchWarps = 3;
+constexpr int kThreads = 32 + 32 * kFetchWarps + 256;
 
 template <int D> struct WideSmem {
     static constexpr int kPanels = D / 64;
     static constexpr int kTile = kPanels * kPanel;
     static constexpr int kStages = D == 128 ? 5 : 8;
-    // A tile's slot is written again once the fetching warps are kStages tiles further: by then its softmax is done.
-    static constexpr int kSlots = D == 128 ? 4 : 8;
+    // `valid` of a tile is written again by the tile eight later, which is looked up when at most six tiles (the ring
+    // and the warps' own) lie between it and the softmax.
+    static constexpr int kSlots = 8;
     alignas(1024) unsigned char q[2][kTile];
     alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 V_1 ...
-    int row[kSlots][BT];     // cache row of a tile's positions, -1: not seen
-    uint32_t valid[kSlots][4];
-    uint64_t q_ready, full[kStages], empty[kStages], s_full[2], o_done[2], drain;
+    int row[kFetchWarps][BT];    // cache row of the positions of a warp's tile, -1: not seen
+    uint32_t valid[kSlots][4];   // positions of a tile that may be seen
+    uint64_t full[kStages], empty[kStages], s_full[2], o_done[2], drain;
     uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
     uint64_t wait_ns;
     uint32_t tmem_base;
@@ -47,14 +51,24 @@ template <int D> struct WideSmem {
 };
 static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxSmem, "shared memory of a CTA");
 
-__device__ __forceinline__ void fetch_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
 
+// `run`: consecutive positions that always share a page (a power of two, 16 ..
+// 128; the maps' boxes have that many rows), or 0: no TMA.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait_ns)
+cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, int run,
+                   const __grid_constant__ Call a, int row_blocks, uint64_t wait_ns)
 {
     using Smem = WideSmem<D>;
-    constexpr int NS = Smem::kStages, SL = Smem::kSlots, kChunks = D / 8;
+    constexpr int NS = Smem::kStages, SL = Smem::kSlots, NP = Smem::kPanels, kChunks = D / 8;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -85,9 +99,8 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         tmem_relinquish();
     }
     if (tid == 32) {
-        mbar_init(&sm.q_ready, 256);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sm.full[s], kFetch);
+            mbar_init(&sm.full[s], 32);
             mbar_init(&sm.empty[s], 1);
         }
         for (int w = 0; w < 2; ++w) {
@@ -101,6 +114,37 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         sm.wait_ns = wait_ns;
         mbar_fence_init();
     }
+    // softmax threads: tile, row of the tile, row of the key head, row of q, o and lse
+    const int w = warp >= 8, q4 = warp & 3, r = 32 * q4 + lane;
+    const int rr = rb * kWideRows + w * BT + r;
+    const bool live_row = warp >= 4 && rr < R;
+    const int i = live_row ? rr / G : 0;
+    const int64_t at = ((int64_t)b * T + i) * Hq + kh * G + (live_row ? rr - i * G : 0);
+    if (warp >= 4) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D);
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch)
+            *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) =
+                live_row ? src[ch] : make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    // fetching warps: pages of the lane's four positions of a tile
+    const int fw = warp - 1;
+    const int32_t *table = c.pages + (int64_t)b * c.max_pages;
+    auto lookup = [&](int j, int (&pg)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int t = k0 + j * BT + 4 * lane + u;
+            pg[u] = j < nt && t < k1 ? table[t / c.page] : -1;
+        }
+    };
+    int pg[4];
+    uint64_t seen = 0;
+    if (warp >= 1 && warp < 4) {
+        lookup(fw, pg);
+        if (k1 > cut.len)
+            seen = sees_any(a.tree, b, T, lane);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -110,7 +154,7 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
     if (warp == 0) {
         // ---------------------------------------------------------------- MMA issuer
         const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
-        bool ok = warp_wait(&sm.q_ready, 0, &sm.wait_ns, abort_flag);
+        bool ok = true;
         auto issue_qk = [&](int w, int j) {
             const int it = 2 * j;
             if (!warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag))
@@ -172,106 +216,93 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         mbar_wait(&sm.drain, 0, kDrainNs);
     } else if (warp < 4) {
         // ---------------------------------------------------------------- fetching
-        const int ft = tid - 32, fw = warp - 1;
-        const int32_t *table = c.pages + (int64_t)b * c.max_pages;
-        const uint64_t seen = k1 > cut.len ? sees_any(a.tree, b, T, lane) : 0;
-        // the page of this lane's positions of a tile (groups of 32: fw and, for the first warp, 3)
-        auto lookup = [&](int j, int g) {
-            const int t = k0 + j * BT + 32 * g + lane;
-            return t < k1 ? table[t / c.page] : -1;
-        };
-        auto place = [&](int j, int g, int pg) {
-            const int t = k0 + j * BT + 32 * g + lane;
-            bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
-            if (live && (pg < 0 || pg >= c.n_pages)) {
-                set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
-                live = false;
-            }
-            sm.row[j % SL][32 * g + lane] = live ? pg * c.page + t % c.page : -1;
-            const uint32_t m = __ballot_sync(0xffffffffu, live);
-            if (lane == 0)
-                sm.valid[j % SL][g] = m;
-        };
-        auto arrive = [&](int it) {
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.full[it % NS]);
-        };
-        // this thread's 16-byte chunk of every kRowStep-th row
-        constexpr int kRowStep = kFetch / kChunks, kRows = (BT + kRowStep - 1) / kRowStep;
-        const int ch = ft % kChunks, r0 = ft / kChunks;
-        int pg0 = nt > 0 ? lookup(0, fw) : -1, pg3 = nt > 0 && fw == 0 ? lookup(0, 3) : -1;
         bool ok = true;
-        int done = 0;   // tiles handed over
-        for (int j = 0; j < nt; ++j) {
-            place(j, fw, pg0);
-            if (fw == 0)
-                place(j, 3, pg3);
-            if (j + 1 < nt) {
-                pg0 = lookup(j + 1, fw);
-                if (fw == 0)
-                    pg3 = lookup(j + 1, 3);
-            }
-            fetch_sync();
-            // the rows' offsets serve keys and values
-            int64_t off[kRows];
+        int issued = -1;   // this warp's last tile asked of TMA
+        for (int j = fw; ok && j < nt; j += kFetchWarps) {
+            int row[4];
+            uint32_t bits = 0;
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int r = r0 + u * kRowStep;
-                const int row = r < BT ? sm.row[j % SL][r] : -1;
-                off[u] = row < 0 ? -1 : ((int64_t)row * Hk + kh) * D + 8 * ch;
-            }
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int it = 2 * j + v;
-                // a wait that ran out: the tile is not fetched, and the consumers' waits run out as well
-                if (ok && it >= NS)
-                    ok = lane_wait(&sm.empty[it % NS], (uint32_t)((it / NS - 1) & 1), &sm.wait_ns, abort_flag);
-                if (ok) {
-                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(v ? c.v : c.k);
-                    const uint32_t dst = smem_u32(sm.ring[it % NS]) + (ch >> 3) * kPanel;
-#pragma unroll
-                    for (int u = 0; u < kRows; ++u) {
-                        const int r = r0 + u * kRowStep;
-                        if (r < BT)
-                            cp16(dst + sw128_offset(r, ch & 7), src + (off[u] < 0 ? 0 : off[u]), off[u] >= 0);
-                    }
+            for (int u = 0; u < 4; ++u) {
+                const int t = k0 + j * BT + 4 * lane + u;
+                bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
+                if (live && (pg[u] < 0 || pg[u] >= c.n_pages)) {
+                    set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
+                    live = false;
                 }
-                cp_commit();
-                if (it >= kAhead - 1) {
-                    cp_wait<kAhead - 1>();
-                    if (ok)
-                        arrive(done);
-                    ++done;
+                row[u] = live ? pg[u] * c.page + t % c.page : -1;
+                bits |= (live ? 1u : 0u) << u;
+            }
+            const bool whole = run > 0 && __all_sync(0xffffffffu, bits == 15u);
+            bits <<= 4 * (lane & 7);
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1)
+                bits |= __shfl_xor_sync(0xffffffffu, bits, x);
+            if ((lane & 7) == 0)
+                sm.valid[j % SL][lane >> 3] = bits;
+            if (!whole) {
+                *reinterpret_cast<int4 *>(&sm.row[fw][4 * lane]) = make_int4(row[0], row[1], row[2], row[3]);
+                __syncwarp();
+            }
+            lookup(j + kFetchWarps, pg);
+#pragma unroll 1
+            for (int v = 0; ok && v < 2; ++v) {
+                const int it = 2 * j + v, s = it % NS;
+                if (it >= NS)
+                    ok = warp_wait(&sm.empty[s], (uint32_t)((it / NS - 1) & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    break;
+                if (whole) {
+                    if (elect_one())
+                        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)Smem::kTile);
+                    else
+                        mbar_arrive(&sm.full[s]);
+                    __syncwarp();
+                    for (int x = 0; x < BT; x += run) {
+                        const int first = __shfl_sync(0xffffffffu, row[0], x >> 2);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int p = 0; p < NP; ++p)
+                                tma_load_2d(sm.ring[s] + p * kPanel + x * 128, v ? &tv : &tk, &sm.full[s], kh * D + 64 * p,
+                                            first);
+                        }
+                        __syncwarp();
+                    }
+                    issued = it;
+                } else {
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(v ? c.v : c.k) + (int64_t)kh * D;
+                    const int ch = lane % kChunks;
+                    const uint32_t dst = smem_u32(sm.ring[s]) + (ch >> 3) * kPanel;
+#pragma unroll 8
+                    for (int x = lane / kChunks; x < BT; x += 32 / kChunks) {
+                        const int at_row = sm.row[fw][x];
+                        cp16(dst + sw128_offset(x, ch & 7), src + (int64_t)max(at_row, 0) * Hk * D + 8 * ch, at_row >= 0);
+                    }
+                    cp_commit();
+                    if (v == 1) {   // keys first, while the values are on their way
+                        cp_wait<1>();
+                        fence_proxy_async_smem();
+                        mbar_arrive(&sm.full[(it - 1) % NS]);
+                        cp_wait<0>();
+                        fence_proxy_async_smem();
+                        mbar_arrive(&sm.full[s]);
+                    }
                 }
             }
         }
-        cp_wait<0>();
-        if (ok) {
-            for (; done < 2 * nt; ++done)
-                arrive(done);
-        } else {
+        if (!ok) {
             *abort_flag = 1;
             if (lane == 0)
                 set_status(a.st, BDLA_ERR_TIMEOUT, 0x31u);
+            // this warp's copies in flight land before the CTA exits
+            cp_wait<0>();
+            for (int it = issued - 1; issued >= 0 && it <= issued; ++it)
+                if (it >= 0)
+                    mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        const int w = (warp - 4) >> 2, q4 = warp & 3, r = 32 * q4 + lane;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         const uint32_t t_s = tmem + BT * w + lane_off, t_o = tmem + 2 * BT + BT * w + lane_off;
-        const int rr = rb * kWideRows + w * BT + r;   // row of the key head
-        const bool live_row = rr < R;
-        const int i = live_row ? rr / G : 0, h = kh * G + (live_row ? rr - i * G : 0);
-        const int64_t at = ((int64_t)b * T + i) * Hq + h;   // row of q, o, lse
-        {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D);
-#pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch)
-                *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) =
-                    live_row ? src[ch] : make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.q_ready);
-        }
         const uint64_t see = k1 > cut.len ? sees(a.tree, b, T, i) : 0;
         const float cs = a.scale * kLog2e;
         RowSoftmax row;
@@ -315,35 +346,52 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
             const bool part = cut.used > 1;
             const int64_t pt = (((int64_t)b * Hk + kh) * ns + piece) * R + rr;
             const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
+            // 32 rows of 128 bytes at a time through the warp's own part of its query tile (read by now), so that whole
+            // lines leave: 32 fp32 columns of a piece, or 64 bf16 columns of an output
+            uint4 *stage = reinterpret_cast<uint4 *>(sm.q[w] + q4 * 4096);
 #pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
+            for (int k = 0; k < D / 32; k += part ? 1 : 2) {
                 uint32_t y[32];
-                if (n > 0) {
-                    tmem_ld32(t_o + 32 * k, y);
-                    tmem_ld_wait();
-                } else {
+                for (int u = 0; u < (part ? 1 : 2); ++u) {
+                    if (n > 0) {
+                        tmem_ld32(t_o + 32 * (k + u), y);
+                        tmem_ld_wait();
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        y[e] = 0u;
-                }
-                if (!live_row)
-                    continue;
-                if (part) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + pt * D + 32 * k);
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = 0u;
+                    }
+                    if (part) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.o + at * D + 32 * k);
+                        for (int e = 0; e < 8; ++e)
+                            stage[lane * 8 + (e ^ (lane & 7))] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t v[4];
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t z[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            v[u] = pack_bf16(__uint_as_float(y[8 * e + 2 * u]) * inv, __uint_as_float(y[8 * e + 2 * u + 1]) * inv);
-                        dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+                            for (int f = 0; f < 4; ++f)
+                                z[f] = pack_bf16(__uint_as_float(y[8 * e + 2 * f]) * inv, __uint_as_float(y[8 * e + 2 * f + 1]) * inv);
+                            stage[lane * 8 + ((4 * u + e) ^ (lane & 7))] = make_uint4(z[0], z[1], z[2], z[3]);
+                        }
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int x = 4 * u + (lane >> 3), row_x = rr - lane + x;   // row of the warp, of the key head
+                    const uint4 z = stage[x * 8 + ((lane & 7) ^ (x & 7))];
+                    if (row_x >= R)
+                        continue;
+                    if (part) {
+                        *reinterpret_cast<uint4 *>(a.part_o + (pt - lane + x) * D + 32 * k + 4 * (lane & 7)) = z;
+                    } else {
+                        const int i_x = row_x / G;
+                        *reinterpret_cast<uint4 *>(a.o + (((int64_t)b * T + i_x) * Hq + kh * G + row_x - i_x * G) * D + 32 * k +
+                                                   8 * (lane & 7)) = z;
+                    }
+                }
+                __syncwarp();
             }
             if (live_row && part)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
@@ -363,6 +411,29 @@ cached_wide_kernel(const __grid_constant__ Call a, int row_blocks, uint64_t wait
         tmem_dealloc(tmem, 512);
 }
 
+// 2-D map over the cache's rows [n_pages * page][Hk * d]: box = 64 features x
+// `run` rows, 128-byte swizzle.
+bool make_rows_map(CUtensorMap *map, const void *ptr, int64_t width, int64_t rows, int run)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (fn == nullptr)
+        return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)width * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)run};
+    cuuint32_t es[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D> cudaError_t go(const Call &a, const bdla_attn_dims &d, cudaStream_t stream)
 {
     const int R = d.T * (d.Hq / d.Hk), row_blocks = (R + kWideRows - 1) / kWideRows;
@@ -371,9 +442,17 @@ template <int D> cudaError_t go(const Call &a, const bdla_attn_dims &d, cudaStre
     const cudaError_t err = cudaFuncSetAttribute(cached_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
+    int run = a.c.page & -a.c.page;   // the largest power of two in the page
+    run = run > BT ? BT : run;
+    CUtensorMap tk{}, tv{};
+    const int64_t rows = (int64_t)a.c.n_pages * a.c.page, width = (int64_t)d.Hk * D;
+    if (run < 16 || rows == 0)
+        run = 0;
+    else if (!make_rows_map(&tk, a.c.k, width, rows, run) || !make_rows_map(&tv, a.c.v, width, rows, run))
+        return cudaErrorInvalidValue;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
-    cached_wide_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(a, row_blocks, g_wait_ns.load());
+    cached_wide_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(tk, tv, run, a, row_blocks, g_wait_ns.load());
     return cudaGetLastError();
 }
 
