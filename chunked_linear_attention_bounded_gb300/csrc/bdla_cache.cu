@@ -374,8 +374,8 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
 }
 
 // Joins the pieces of a row, W warps a row: each sums every W-th piece, and the
-// warps' sums are added in order.  W follows the most pieces of a sequence (one
-// warp for up to 8, so that a CTA joins four rows, 4 for up to 32, 16 beyond).
+// warps' sums are added in order.  W follows the most pieces of a sequence: one
+// warp for up to 16, so that a CTA joins four rows, 16 beyond.
 template <int D, int W>
 __global__ void __launch_bounds__(W < 4 ? 128 : 32 * W)
 combine_kernel(const __grid_constant__ Call a, int64_t rows)
@@ -413,7 +413,7 @@ combine_kernel(const __grid_constant__ Call a, int64_t rows)
 #pragma unroll
     for (int e = 0; e < E; ++e)
         v[e] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = w; s < cut.used; s += W) {
         const int64_t p = (first + s) * R + row;
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * p);
@@ -530,10 +530,8 @@ static cudaError_t cached_go(const Call &a, const bdla_attn_dims &d, cudaStream_
 
 template <int D> static cudaError_t combine_go(const Call &a, int64_t rows, cudaStream_t stream)
 {
-    if (a.pieces.ns > 32)
+    if (a.pieces.ns > 16)
         combine_kernel<D, 16><<<(unsigned)rows, 512, 0, stream>>>(a, rows);
-    else if (a.pieces.ns > 8)
-        combine_kernel<D, 4><<<(unsigned)rows, 128, 0, stream>>>(a, rows);
     else
         combine_kernel<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a, rows);
     return cudaGetLastError();
