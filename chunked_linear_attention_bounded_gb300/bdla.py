@@ -615,12 +615,12 @@ def _on(t, name: str, dtype, shape, device):
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _new(shapes, dtypes, device, stream):
-    """Outputs that belong to the stream the call runs on."""
+def _new(device, stream, *outs):
+    """Outputs, (shape, dtype) each, that belong to the stream the call runs on."""
     if stream is None:
-        return [torch.empty(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
+        return [torch.empty(s, dtype=t, device=device) for s, t in outs]
     with torch.cuda.stream(stream):
-        return [torch.empty(s, dtype=t, device=device) for s, t in zip(shapes, dtypes)]
+        return [torch.empty(s, dtype=t, device=device) for s, t in outs]
 
 
 def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call):
@@ -700,7 +700,7 @@ def qk_norm(q, k, wq, wk, rotary: Optional[int] = None, base: float = 10000.0, i
     document.  Returns (qn, kn), contiguous.  Inputs used on another stream
     than their own are the caller's to keep alive, as for every call here."""
     a, d = _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
-    qn, kn = _new((q.shape, k.shape), (q.dtype, q.dtype), q.device, stream)
+    qn, kn = _new(q.device, stream, (q.shape, q.dtype), (k.shape, q.dtype))
     st = lib().bdla_qk_norm(a, qn.data_ptr(), kn.data_ptr(), d, _stream_of(q, stream))
     if st:
         raise BdlaError(st, "bdla_qk_norm")
@@ -717,7 +717,7 @@ def qk_norm_bwd(q, k, wq, wk, dqn, dkn, rotary: Optional[int] = None, base: floa
     gq = _on(dqn, "dqn", dqn.dtype, q.shape, q.device)
     gk = _on(dkn, "dkn", dqn.dtype, k.shape, q.device)
     bf, f32 = torch.bfloat16, torch.float32
-    dq, dk, dwq, dwk = _new((q.shape, k.shape, wq.shape, wk.shape), (bf, bf, f32, f32), q.device, stream)
+    dq, dk, dwq, dwk = _new(q.device, stream, (q.shape, bf), (k.shape, bf), (wq.shape, f32), (wk.shape, f32))
     s = _stream_of(q, stream)
     _with_ws("bdla_qk_norm_bwd", ATTN_NORM_BWD, d, a.n_docs, 0, ws, q.device, stream,
              lambda p, n: lib().bdla_qk_norm_bwd(a, gq, gk, code, dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(),
@@ -742,7 +742,7 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, cu_seqlens=None, ws: Option
     lse fp32 [Hq, B*T]."""
     d, pq, pk, pv = _attn_args(q, k, v)
     cu, n_docs = _documents(cu_seqlens, d.B, q.device)
-    o, lse = _new((q.shape, (d.Hq, d.B * d.T)), (q.dtype, torch.float32), q.device, stream)
+    o, lse = _new(q.device, stream, (q.shape, q.dtype), ((d.Hq, d.B * d.T), torch.float32))
     scale = d.d ** -0.5 if scale is None else scale
     s = _stream_of(q, stream)
     _with_ws("bdla_attn_fwd", ATTN_FWD, d, n_docs, 0, ws, q.device, stream,
@@ -759,7 +759,7 @@ def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None
     pg = _on(dO, "dO", torch.bfloat16, q.shape, q.device)
     pl = _on(lse, "lse", torch.float32, (d.Hq, d.B * d.T), q.device)
     cu, n_docs = _documents(cu_seqlens, d.B, q.device)
-    dq, dk, dv = _new((q.shape, k.shape, v.shape), (q.dtype,) * 3, q.device, stream)
+    dq, dk, dv = _new(q.device, stream, (q.shape, q.dtype), (k.shape, q.dtype), (v.shape, q.dtype))
     scale = d.d ** -0.5 if scale is None else scale
     s = _stream_of(q, stream)
     _with_ws("bdla_attn_bwd", ATTN_BWD, d, n_docs, 0, ws, q.device, stream,
@@ -814,7 +814,7 @@ def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float
         raise ValueError("kcache and q have different widths")
     pt = None if tree is None else _on(tree, "tree", torch.int64, (B, T), device)
     dims = AttnDims(B, T, Hq, kcache.shape[2], d)
-    o, lse = _new((q.shape, (B, T, Hq)), (q.dtype, torch.float32), device, stream)
+    o, lse = _new(device, stream, (q.shape, q.dtype), ((B, T, Hq), torch.float32))
     scale = d ** -0.5 if scale is None else scale
     pq, s = q.data_ptr(), _stream_of(q, stream)
     _with_ws("bdla_attn_cached", ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, device, stream,

@@ -125,7 +125,8 @@ size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t m
     case BDLA_ATTN_APPEND:
         return head;
     case BDLA_ATTN_BWD:
-        return head + round_up((size_t)d.B * d.T * d.Hq * sizeof(float));
+        return head + round_up((size_t)d.B * d.T * d.Hq * sizeof(float)) +
+               round_up(attn_bwd_part_floats(d, n_docs > 0 ? n_docs : d.B) * sizeof(float));
     case BDLA_ATTN_NORM_BWD:
         return head + round_up((size_t)norm_bwd_blocks(d) * d.d * sizeof(float));
     case BDLA_ATTN_CACHED:
@@ -201,7 +202,10 @@ bdla_status bdla_attn_bwd(const void *q, const void *k, const void *v, const voi
     BDLA_TRY(check_ws(ws, ws_bytes, bdla_workspace_bytes_attn(BDLA_ATTN_BWD, d, packed ? n_docs : 0, 0)));
     const AttnProblem p = make_attn(d, cu_seqlens, n_docs, scale, ws, stream);
     float *delta = reinterpret_cast<float *>(static_cast<char *>(ws) + round_up(kStatusBytes));
-    BDLA_CUDA(launch_attn_bwd(p, cb(q), cb(k), cb(v), cb(o), lse, cb(dO), mb(dq), mb(dk), mb(dv), delta));
+    float *part = nullptr;
+    if (attn_bwd_part_floats(d, p.n_docs) != 0)
+        part = reinterpret_cast<float *>(reinterpret_cast<char *>(delta) + round_up((size_t)d.B * d.T * d.Hq * sizeof(float)));
+    BDLA_CUDA(launch_attn_bwd(p, cb(q), cb(k), cb(v), cb(o), lse, cb(dO), mb(dq), mb(dk), mb(dv), delta, part));
     return BDLA_OK;
 }
 

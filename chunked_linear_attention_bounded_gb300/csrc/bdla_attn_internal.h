@@ -33,11 +33,12 @@ cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, cons
 cudaError_t launch_doc_report(const AttnProblem &p);
 cudaError_t launch_attn_fwd(const AttnProblem &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                             const __nv_bfloat16 *v, __nv_bfloat16 *o, float *lse);
-// `delta`: [Hq][tokens] fp32 scratch.
+// `delta`: [Hq][tokens] fp32 scratch.  `part`: attn_bwd_part_floats() floats, or null where that is 0.
+size_t attn_bwd_part_floats(const bdla_attn_dims &d, int n_docs);
 cudaError_t launch_attn_bwd(const AttnProblem &p, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                             const __nv_bfloat16 *v, const __nv_bfloat16 *o, const float *lse,
                             const __nv_bfloat16 *dO, __nv_bfloat16 *dq, __nv_bfloat16 *dk, __nv_bfloat16 *dv,
-                            float *delta);
+                            float *delta, float *part);
 
 cudaError_t launch_cache_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v, const bdla_cache &c,
                                 const int32_t *rows, const int32_t *counts, const bdla_attn_dims &d,
