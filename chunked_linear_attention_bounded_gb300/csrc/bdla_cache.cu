@@ -165,14 +165,14 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     const uint64_t seen = drafts ? sees_any(a.tree, b, T, lane) : 0;
 
     // page table entry of position t (a tile's 64 positions, by the first 64 threads)
-    auto lookup = [&](int t) { return t < k1 ? table[t / c.page] : -1; };
+    auto lookup = [&](int t) { return t < k1 ? table[page_of(t, c.page, a.shift)] : -1; };
     auto place = [&](int n, int t, int pg) {
         bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
         if (live && (pg < 0 || pg >= c.n_pages)) {
             set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
             live = false;
         }
-        sm.row[n & 3][tid] = live ? pg * c.page + t % c.page : -1;
+        sm.row[n & 3][tid] = live ? pg * c.page + offset_of(t, c.page, a.shift) : -1;
         const uint32_t m = __ballot_sync(0xffffffffu, live);
         if (lane == 0)
             sm.valid[n & 3][tid >> 5] = m;
@@ -481,12 +481,14 @@ static int cached_rows(const bdla_attn_dims &d)
     return R <= 16 ? 16 : R <= 32 ? 32 : kWideRows;
 }
 
-// Pieces of a sequence.  Few sequences: enough pieces for eight CTAs an SM (one
-// of the wide kernel, of which one is resident), of at least 128 positions.
-// Many: pieces of about 2048 positions (8192 of the wide kernel), so that long
-// and short sequences end together, and of at least 1024, so that a CTA's start-up (length, page table,
-// first tile) stays small beside its keys.  No more than 256 MB of partial sums,
-// or a grid of 2^17 CTAs (more only where the sequences alone are more).
+// Pieces of a sequence.  Few sequences: enough pieces for eight CTAs an SM, of
+// at least 128 positions.  Many: pieces of about 2048 positions, so that long
+// and short sequences end together, and of at least 1024, so that a CTA's
+// start-up (length, page table, first tile) stays small beside its keys.  The
+// wide kernel holds an SM alone: as many pieces as fill the SMs a whole number
+// of times, with at most 8192 positions (160 CTAs for 152 SMs cost a second
+// round: 4 x 65536 positions, 186 us).  No more than 256 MB of partial sums, or
+// a grid of 2^17 CTAs (more only where the sequences alone are more).
 static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
 {
     const int mr = cached_rows(d), R = d.T * (d.Hq / d.Hk);
@@ -495,9 +497,15 @@ static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
     Pieces p;
     p.unit = wide ? 128 : kKeys;
     p.least = units >= 4 * sms ? 1024 : units >= sms ? 512 : units >= sms / 4 ? 256 : 128;
-    int64_t ns = (sms * (wide ? 1 : 8) + units - 1) / units;
-    const int64_t even = wide ? (max_keys + 8191) / 8192 : (max_keys + 2047) / 2048;
-    ns = ns > even ? ns : even;
+    int64_t ns;
+    if (wide) {
+        const int64_t rounds = (max_keys * units + 8192 * sms - 1) / (8192 * sms);
+        ns = (rounds < 1 ? 1 : rounds) * sms / units;
+    } else {
+        const int64_t even = (max_keys + 2047) / 2048;
+        ns = (sms * 8 + units - 1) / units;
+        ns = ns > even ? ns : even;
+    }
     const int64_t most[3] = {(max_keys + p.least - 1) / p.least,
                              ((int64_t)256 << 20) / ((int64_t)d.B * d.T * d.Hq * (d.d + 2) * 4), (1 << 17) / units};
     for (int i = 0; i < 3; ++i)
@@ -554,6 +562,7 @@ cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.Hq = d.Hq;
     a.Hk = d.Hk;
     a.pieces = cached_pieces(d, max_keys);
+    a.shift = (c.page & (c.page - 1)) == 0 ? __builtin_ctz(c.page) : -1;
     a.st = st;
     a.part_o = static_cast<float *>(partials);
     a.part_ml = a.part_o + (size_t)a.pieces.ns * rows * d.d;

@@ -53,6 +53,11 @@ __device__ __forceinline__ uint64_t sees_any(const uint64_t *tree, int64_t b, in
     return m;
 }
 
+// Entry of the page table and offset in the page of position t: a shift where
+// the page is a power of two (shift >= 0), else a division.
+__device__ __forceinline__ int page_of(int t, int page, int shift) { return shift >= 0 ? t >> shift : t / page; }
+__device__ __forceinline__ int offset_of(int t, int page, int shift) { return shift >= 0 ? t & (page - 1) : t % page; }
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
 {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -69,6 +74,7 @@ struct Call {
     float *lse;
     float *part_o, *part_ml;   // [B][Hk][ns][T * G] rows of D, and of (maximum, sum)
     int T, Hq, Hk;
+    int shift;                 // log2 of the page, or -1
     Pieces pieces;
     DeviceStatus *st;
 };

@@ -80,6 +80,17 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const int kh = idx % Hk;
     idx /= Hk;
     const int piece = idx % ns, b = idx / ns;
+    // softmax threads: tile, row of the tile, row of the key head, row of q, o and lse; their queries are asked for
+    // before the lengths, which the rest waits for
+    const int w = warp >= 8, q4 = warp & 3, r = 32 * q4 + lane;
+    const int rr = rb * kWideRows + w * BT + r;
+    const bool live_row = warp >= 4 && rr < R;
+    const int i = live_row ? rr / G : 0;
+    const int64_t at = ((int64_t)b * T + i) * Hq + kh * G + (live_row ? rr - i * G : 0);
+    uint4 qrow[kChunks];
+#pragma unroll
+    for (int ch = 0; ch < kChunks; ++ch)
+        qrow[ch] = live_row ? reinterpret_cast<const uint4 *>(a.q + at * D)[ch] : make_uint4(0, 0, 0, 0);
     const Cut cut = cut_of(c, b, T, a.pieces);
     if (piece >= cut.used)
         return;
@@ -94,40 +105,6 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const int nt = (k1 - k0 + BT - 1) / BT;
     const int tiles = R - rb * kWideRows > BT ? 2 : 1;   // row tiles of this CTA
 
-    if (warp == 0) {
-        tmem_alloc(&sm.tmem_base, 512);
-        tmem_relinquish();
-    }
-    if (tid == 32) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&sm.full[s], 32);
-            mbar_init(&sm.empty[s], 1);
-        }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(&sm.s_full[w], 1);
-            mbar_init(&sm.p_ready[w][0], BT);
-            mbar_init(&sm.p_ready[w][1], BT);
-            mbar_init(&sm.o_done[w], 1);
-        }
-        mbar_init(&sm.drain, 1);
-        sm.abort_flag = 0;
-        sm.wait_ns = wait_ns;
-        mbar_fence_init();
-    }
-    // softmax threads: tile, row of the tile, row of the key head, row of q, o and lse
-    const int w = warp >= 8, q4 = warp & 3, r = 32 * q4 + lane;
-    const int rr = rb * kWideRows + w * BT + r;
-    const bool live_row = warp >= 4 && rr < R;
-    const int i = live_row ? rr / G : 0;
-    const int64_t at = ((int64_t)b * T + i) * Hq + kh * G + (live_row ? rr - i * G : 0);
-    if (warp >= 4) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D);
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch)
-            *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) =
-                live_row ? src[ch] : make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-    }
     // fetching warps: pages of the lane's four positions of a tile
     const int fw = warp - 1;
     const int32_t *table = c.pages + (int64_t)b * c.max_pages;
@@ -135,20 +112,48 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int t = k0 + j * BT + 4 * lane + u;
-            pg[u] = j < nt && t < k1 ? table[t / c.page] : -1;
+            pg[u] = j < nt && t < k1 ? table[page_of(t, c.page, a.shift)] : -1;
         }
     };
     int pg[4];
     uint64_t seen = 0;
-    if (warp >= 1 && warp < 4) {
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    } else if (warp < 4) {
         lookup(fw, pg);
+        if (tid == 32) {
+            for (int s = 0; s < NS; ++s) {
+                mbar_init(&sm.full[s], 32);
+                mbar_init(&sm.empty[s], 1);
+            }
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&sm.s_full[x], 1);
+                mbar_init(&sm.p_ready[x][0], BT);
+                mbar_init(&sm.p_ready[x][1], BT);
+                mbar_init(&sm.o_done[x], 1);
+            }
+            mbar_init(&sm.drain, 1);
+            sm.abort_flag = 0;
+            sm.wait_ns = wait_ns;
+            mbar_fence_init();
+        }
         if (k1 > cut.len)
             seen = sees_any(a.tree, b, T, lane);
+        asm volatile("bar.sync 2, 96;" ::: "memory");   // the barriers are there: fetching starts
+    } else {
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch)
+            *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) = qrow[ch];
+        fence_proxy_async_smem();
     }
     tc_fence_before();
-    __syncthreads();
+    if (warp >= 1 && warp < 4)
+        asm volatile("bar.arrive 1, 384;" ::: "memory");
+    else
+        asm volatile("bar.sync 1, 384;" ::: "memory");
     tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    const uint32_t tmem = warp >= 1 && warp < 4 ? 0 : sm.tmem_base;   // (the fetching warps do not wait for it)
     volatile int *abort_flag = &sm.abort_flag;
 
     if (warp == 0) {
@@ -229,7 +234,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
                     live = false;
                 }
-                row[u] = live ? pg[u] * c.page + t % c.page : -1;
+                row[u] = live ? pg[u] * c.page + offset_of(t, c.page, a.shift) : -1;
                 bits |= (live ? 1u : 0u) << u;
             }
             const bool whole = run > 0 && __all_sync(0xffffffffu, bits == 15u);
