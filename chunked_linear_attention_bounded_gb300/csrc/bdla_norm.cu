@@ -6,11 +6,11 @@
 //   dx = r (h - n mean(h o n)),   dw = sum over tokens and heads of dy' o n
 //
 // Both directions are one pass over the tensors (4 bytes an element forward,
-// 6 backward) and bound by HBM.  A head of 64 or 128 features belongs to 8 or
-// 16 lanes, each with two groups of four features that hold both halves of its
-// pairs, so the rotation stays in the lane, the mean is a 3- or 4-step shuffle
+// 6 backward) and bound by HBM.  A head of 64 or 128 features belongs to 4 or 8
+// lanes, each with two groups of eight features that hold both halves of its
+// pairs, so the rotation stays in the lane, the mean is a 2- or 3-step shuffle
 // and the accesses of the lanes together cover whole lines.  Such a group of
-// lanes keeps one token and walks a chunk of its query or key heads: the four
+// lanes keeps one token and walks a chunk of its query or key heads: the eight
 // angles of a lane belong to the token, and the products of weights and sines
 // are formed once per chunk; several heads' loads are in flight at a time.
 //
@@ -67,21 +67,22 @@ __device__ __forceinline__ int token_position(const NormParams &p, int t)
 }
 
 // What a group of lanes works on: one token and a chunk of its query (s = 0)
-// or key (s = 1) heads.  The lane's eight features are f0 .. f0 + 3 and
-// f1 .. f1 + 3.  Pairs at a distance: feature f0 + j turns with f1 + j, and
-// lanes past the rotated features hold eight in a row.  Interleaved: eight in
-// a row, features 2m and 2m + 1 turn together.
+// or key (s = 1) heads.  The lane's sixteen features are f0 .. f0 + 7 and
+// f1 .. f1 + 7.  Pairs at a distance: feature f0 + j turns with f1 + j, and
+// lanes past the rotated features hold sixteen in a row.  Interleaved: sixteen
+// in a row, features 2m and 2m + 1 turn together.
+constexpr int kPairs = 8, kFeat = 2 * kPairs;   // of a lane
 template <int D, bool INTER> struct Group {
-    static constexpr int kLanes = D / 8;
+    static constexpr int kLanes = D / kFeat;
     static constexpr int kPerBlock = kThreads / kLanes;
     int f0, f1, t, s, h0, h1;
     bool turns;
     __device__ __forceinline__ explicit Group(const NormParams &p)
     {
         const int lane = threadIdx.x % kLanes;
-        turns = 8 * lane < p.rotary;
-        f0 = turns && !INTER ? 4 * lane : 8 * lane;
-        f1 = turns && !INTER ? (p.rotary >> 1) + 4 * lane : 8 * lane + 4;
+        turns = kFeat * lane < p.rotary;
+        f0 = turns && !INTER ? kPairs * lane : kFeat * lane;
+        f1 = turns && !INTER ? (p.rotary >> 1) + kPairs * lane : kFeat * lane + kPairs;
     }
     // A group past the end has no heads, and follows along: shuffles need whole warps.
     __device__ __forceinline__ void take(const NormParams &p, int64_t item)
@@ -103,12 +104,12 @@ template <int D, bool INTER> struct Group {
         h0 = any ? (int)(item - (int64_t)t * n) * p.chunk : 0;
         h1 = any ? min(h0 + p.chunk, p.heads[s]) : h0;
     }
-    // Cosine and sine of the lane's four pairs.
-    __device__ __forceinline__ void angles(const NormParams &p, const Turns &tu, float (&cs)[4], float (&sn)[4]) const
+    // Cosine and sine of the lane's pairs.
+    __device__ __forceinline__ void angles(const NormParams &p, const Turns &tu, float (&cs)[kPairs], float (&sn)[kPairs]) const
     {
         const int pos = turns ? token_position(p, t) : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
             cs[j] = 1.0f;
             sn[j] = 0.0f;
             if (turns) {
@@ -118,9 +119,9 @@ template <int D, bool INTER> struct Group {
             }
         }
     }
-    // Features of pair j in the lane's eight.
+    // Features of pair j in the lane's sixteen.
     static __device__ __forceinline__ constexpr int a_of(int j) { return INTER ? 2 * j : j; }
-    static __device__ __forceinline__ constexpr int b_of(int j) { return INTER ? 2 * j + 1 : j + 4; }
+    static __device__ __forceinline__ constexpr int b_of(int j) { return INTER ? 2 * j + 1 : j + kPairs; }
 };
 
 template <int LANES> __device__ __forceinline__ float group_sum(float v)
@@ -131,9 +132,9 @@ template <int LANES> __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint2 &u, const uint2 &v, float (&x)[8])
+__device__ __forceinline__ void unpack8(const uint4 &u, float *x)
 {
-    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = bf16_lo(w[i]);
@@ -141,23 +142,30 @@ __device__ __forceinline__ void unpack8(const uint2 &u, const uint2 &v, float (&
     }
 }
 
-__device__ __forceinline__ uint2 load4(const __nv_bfloat16 *p) { return __ldcs(reinterpret_cast<const uint2 *>(p)); }
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p) { return __ldcs(reinterpret_cast<const uint4 *>(p)); }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *row, int f0, int f1, const float (&x)[8])
+__device__ __forceinline__ void store16(__nv_bfloat16 *row, int f0, int f1, const float (&x)[kFeat])
 {
-    __stcs(reinterpret_cast<uint2 *>(row + f0), make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])));
-    __stcs(reinterpret_cast<uint2 *>(row + f1), make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
+    __stcs(reinterpret_cast<uint4 *>(row + f0),
+           make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
+    __stcs(reinterpret_cast<uint4 *>(row + f1),
+           make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15])));
 }
 
-__device__ __forceinline__ void load_weights(const float *w, int f0, int f1, float (&x)[8])
+__device__ __forceinline__ void load_weights(const float *w, int f0, int f1, float (&x)[kFeat])
 {
-    const float4 a = *reinterpret_cast<const float4 *>(w + f0), b = *reinterpret_cast<const float4 *>(w + f1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = *reinterpret_cast<const float4 *>(w + (i < 2 ? f0 : f1) + 4 * (i & 1));
+        x[4 * i] = a.x;
+        x[4 * i + 1] = a.y;
+        x[4 * i + 2] = a.z;
+        x[4 * i + 3] = a.w;
+    }
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu, __nv_bfloat16 *__restrict__ qn,
                __nv_bfloat16 *__restrict__ kn)
 {
@@ -168,13 +176,13 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
     const int64_t step = p.head[g.s];
     __nv_bfloat16 *dst = (g.s ? kn : qn) + (int64_t)g.t * p.heads[g.s] * D;
     // rotated feature = n_own * own + n_other * other, weights and signs included
-    float own[8], other[8];
+    float own[kFeat], other[kFeat];
     {
-        float w[8], cs[4], sn[4];
+        float w[kFeat], cs[kPairs], sn[kPairs];
         load_weights(p.w[g.s], g.f0, g.f1, w);
         g.angles(p, tu, cs, sn);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
             const int a = G::a_of(j), b = G::b_of(j);
             own[a] = w[a] * cs[j];
             other[a] = -w[b] * sn[j];
@@ -183,73 +191,83 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
         }
     }
     for (int b = 0; b < p.chunk; b += kBatch) {
-        uint2 in[kBatch][2];
+        uint4 in[kBatch][2];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = g.h0 + b + u;
+            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
             if (h < g.h1) {
-                in[u][0] = load4(src + h * step + g.f0);
-                in[u][1] = load4(src + h * step + g.f1);
-            } else {
-                in[u][0] = in[u][1] = make_uint2(0, 0);
+                in[u][0] = load8(src + h * step + g.f0);
+                in[u][1] = load8(src + h * step + g.f1);
             }
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = g.h0 + b + u;
-            float x[8], y[8];
-            unpack8(in[u][0], in[u][1], x);
-            float ss = 0.0f;
+            float x[kFeat], y[kFeat];
+            unpack8(in[u][0], x);
+            unpack8(in[u][1], x + 8);
+            float ss[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ss = fmaf(x[j], x[j], ss);
-            const float r = rsqrtf(group_sum<G::kLanes>(ss) * (1.0f / D) + p.eps);
+            for (int j = 0; j < kFeat; ++j)
+                ss[j & 1] = fmaf(x[j], x[j], ss[j & 1]);
+            const float r = rsqrtf(group_sum<G::kLanes>(ss[0] + ss[1]) * (1.0f / D) + p.eps);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < kFeat; ++j)
                 x[j] *= r;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kPairs; ++j) {
                 const int a = G::a_of(j), c = G::b_of(j);
                 y[a] = fmaf(x[c], other[a], x[a] * own[a]);
                 y[c] = fmaf(x[a], other[c], x[c] * own[c]);
             }
             if (h < g.h1)
-                store8(dst + h * D, g.f0, g.f1, y);
+                store16(dst + h * D, g.f0, g.f1, y);
         }
     }
 }
 
-// Four features twice, as they lie in memory.
-template <bool GF32> struct Grad8;
-template <> struct Grad8<false> {
-    uint2 a, b;
+// Eight features twice, as they lie in memory.
+template <bool GF32> struct Grad16;
+template <> struct Grad16<false> {
+    uint4 a, b;
     __device__ __forceinline__ void load(const void *base, int64_t off, int f0, int f1)
     {
         const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(base) + off;
-        a = load4(g + f0);
-        b = load4(g + f1);
+        a = load8(g + f0);
+        b = load8(g + f1);
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(a, b, x); }
+    __device__ __forceinline__ void get(float (&x)[kFeat]) const
+    {
+        unpack8(a, x);
+        unpack8(b, x + 8);
+    }
 };
-template <> struct Grad8<true> {
-    float4 a, b;
+template <> struct Grad16<true> {
+    float4 v[4];
     __device__ __forceinline__ void load(const void *base, int64_t off, int f0, int f1)
     {
         const float *g = static_cast<const float *>(base) + off;
-        a = __ldcs(reinterpret_cast<const float4 *>(g + f0));
-        b = __ldcs(reinterpret_cast<const float4 *>(g + f1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __ldcs(reinterpret_cast<const float4 *>(g + (i < 2 ? f0 : f1) + 4 * (i & 1)));
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const
+    __device__ __forceinline__ void get(float (&x)[kFeat]) const
     {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * i] = v[i].x;
+            x[4 * i + 1] = v[i].y;
+            x[4 * i + 2] = v[i].z;
+            x[4 * i + 3] = v[i].w;
+        }
     }
 };
 
 // The first q_blocks CTAs take the query heads, the others the key heads, so
 // that a thread sums one weight gradient; CTA i leaves its sums in part[i].
 template <int D, bool INTER, bool GF32>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu, int q_blocks,
                    const void *__restrict__ dqn, const void *__restrict__ dkn, __nv_bfloat16 *__restrict__ dq,
                    __nv_bfloat16 *__restrict__ dk, float *__restrict__ part)
@@ -261,10 +279,10 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
     const int gi = threadIdx.x / G::kLanes;
     const int s = (int)blockIdx.x >= q_blocks;
     const int block = (int)blockIdx.x - (s ? q_blocks : 0), blocks = s ? (int)gridDim.x - q_blocks : q_blocks;
-    float w[8], dw[8];
+    float w[kFeat], dw[kFeat];
     load_weights(p.w[s], g.f0, g.f1, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kFeat; ++j)
         dw[j] = 0.0f;
     const int64_t items = (int64_t)p.tokens * (s ? p.n_chunks - p.q_chunks : p.q_chunks);
     const int64_t stride = (int64_t)blocks * G::kPerBlock, step = p.head[s];
@@ -275,59 +293,60 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
         const __nv_bfloat16 *src = p.x[s] + g.t * p.token[s];
         const int64_t row = (int64_t)g.t * p.heads[s] * D;
         __nv_bfloat16 *dst = (s ? dk : dq) + row;
-        float cs[4], sn[4];
+        float cs[kPairs], sn[kPairs];
         g.angles(p, tu, cs, sn);
         for (int h = g.h0; h < g.h0 + p.chunk; h += kB) {
-            uint2 xa[kB], xb[kB];
-            Grad8<GF32> gr[kB];
+            uint4 xa[kB], xb[kB];
+            Grad16<GF32> gr[kB];
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                xa[u] = xb[u] = make_uint2(0, 0);
-                gr[u] = Grad8<GF32>{};
+                xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
+                gr[u] = Grad16<GF32>{};
                 if (h + u < g.h1) {
-                    xa[u] = load4(src + (h + u) * step + g.f0);
-                    xb[u] = load4(src + (h + u) * step + g.f1);
+                    xa[u] = load8(src + (h + u) * step + g.f0);
+                    xb[u] = load8(src + (h + u) * step + g.f1);
                     gr[u].load(grad, row + (int64_t)(h + u) * D, g.f0, g.f1);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                float x[8], y[8];
-                unpack8(xa[u], xb[u], x);
+                float x[kFeat], y[kFeat];
+                unpack8(xa[u], x);
+                unpack8(xb[u], x + 8);
                 gr[u].get(y);
-                float ss = 0.0f;
+                float ss[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ss = fmaf(x[j], x[j], ss);
-                ss = group_sum<G::kLanes>(ss);
-                const float r = h + u < g.h1 ? rsqrtf(ss * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
+                for (int j = 0; j < kFeat; ++j)
+                    ss[j & 1] = fmaf(x[j], x[j], ss[j & 1]);
+                const float sum = group_sum<G::kLanes>(ss[0] + ss[1]);
+                const float r = h + u < g.h1 ? rsqrtf(sum * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kPairs; ++j) {
                     const int a = G::a_of(j), c = G::b_of(j);
                     const float ya = y[a], yc = y[c];
                     y[a] = fmaf(yc, sn[j], ya * cs[j]);
                     y[c] = fmaf(-ya, sn[j], yc * cs[j]);
                 }
-                float hn = 0.0f;
+                float hn[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kFeat; ++j) {
                     x[j] *= r;   // n
                     dw[j] = fmaf(y[j], x[j], dw[j]);
                     y[j] *= w[j];   // h
-                    hn = fmaf(y[j], x[j], hn);
+                    hn[j & 1] = fmaf(y[j], x[j], hn[j & 1]);
                 }
-                const float m = group_sum<G::kLanes>(hn) * (1.0f / D);
+                const float m = group_sum<G::kLanes>(hn[0] + hn[1]) * (1.0f / D);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < kFeat; ++j)
                     y[j] = r * fmaf(-x[j], m, y[j]);
                 if (h + u < g.h1)
-                    store8(dst + (h + u) * D, g.f0, g.f1, y);
+                    store16(dst + (h + u) * D, g.f0, g.f1, y);
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        red[gi][j < 4 ? g.f0 + j : g.f1 + j - 4] = dw[j];
+    for (int j = 0; j < kFeat; ++j)
+        red[gi][j < kPairs ? g.f0 + j : g.f1 + j - kPairs] = dw[j];
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kThreads) {
         float v = 0.0f;
@@ -434,7 +453,7 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
     const NormParams p = norm_params(a, d);
     const Turns &tu = turns_of(a);
     const int64_t items = (int64_t)p.tokens * p.n_chunks;
-    const int per = kThreads / (d.d / 8);
+    const int per = kThreads / (d.d / kFeat);
     const unsigned grid = (unsigned)((items + per - 1) / per);
     if (d.d == 64) {
         if (a.interleaved)
@@ -453,7 +472,7 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
 // CTAs for the query and for the key heads, in proportion to their work.
 static int norm_q_blocks(const bdla_attn_dims &d, int *total)
 {
-    const int chunk = head_chunk(d), per = kThreads / (d.d / 8);
+    const int chunk = head_chunk(d), per = kThreads / (d.d / kFeat);
     const int64_t most = (int64_t)sm_count() * 12, tokens = (int64_t)d.B * d.T;
     int64_t n[2];
     for (int s = 0; s < 2; ++s) {
