@@ -17,22 +17,30 @@
 // Angles.  pos * f with f = base^(-2i/rotary) loses its fraction of a turn in
 // fp32 for far positions.  f / (2 pi) is therefore kept as a 64-bit binary
 // fraction of a turn; the product with the position modulo 2^64 drops whole
-// turns exactly, and its top 32 bits go to sincospif.
+// turns exactly.  Its top 32 bits, to the nearest quarter turn and the rest (at
+// most an eighth), give sine and cosine from their Taylor series to x^9 and
+// x^10 (remainders (pi/4)^11 / 11! = 2e-9 and (pi/4)^12 / 12! = 1e-10, below
+// half a step of fp32): with sincospif the angles were a third of the gradient's
+// instructions, which bound it.
 #include <math.h>
 
-#include "bdla_attn_internal.h"
-#include "bdla_sm100.cuh"
+#include "bdla_attn_sm100.cuh"
 
 namespace bdla {
 
 namespace {
 
+using attn::add2;
+using attn::fma2;
+using attn::mul2;
+using attn::pair;
+using attn::unpair;
 using sm100::bf16_hi;
 using sm100::bf16_lo;
 using sm100::pack_bf16;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;   // heads in flight per group of lanes
+constexpr int kBatch = 8;   // heads in flight per group of lanes (4: 249 us for 64K packed tokens, 8: 209)
 
 struct Turns {
     uint64_t f[64];   // turns per position of each pair, times 2^64
@@ -64,6 +72,20 @@ __device__ __forceinline__ int token_position(const NormParams &p, int t)
             hi = mid - 1;
     }
     return t - p.cu[lo];
+}
+
+// Cosine and sine of h / 2^32 turns.
+__device__ __forceinline__ void turn(uint32_t h, float &c, float &s)
+{
+    const uint32_t q = (h + 0x20000000u) >> 30;   // nearest quarter, 0 .. 3 (4 wraps to 0)
+    const float x = (float)(int32_t)(h - (q << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    const float z = x * x;
+    const float a = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
+    const float b =
+        fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+    const float sa = q & 1 ? b : a, ca = q & 1 ? a : b;
+    s = __uint_as_float(__float_as_uint(sa) ^ ((q & 2) << 30));
+    c = __uint_as_float(__float_as_uint(ca) ^ (((q + 1) & 2) << 30));
 }
 
 // What a group of lanes works on: one token and a chunk of its query (s = 0)
@@ -110,18 +132,10 @@ template <int D, bool INTER> struct Group {
         const int pos = turns ? token_position(p, t) : 0;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-            cs[j] = 1.0f;
-            sn[j] = 0.0f;
-            if (turns) {
-                const uint64_t u = (uint64_t)(int64_t)pos * tu.f[(INTER ? f0 >> 1 : f0) + j];
-                // the top 32 bits, signed, are 2^-31 half turns
-                sincospif((float)(int32_t)(u >> 32) * 4.656612873077393e-10f, &sn[j], &cs[j]);
-            }
+            const uint64_t u = turns ? (uint64_t)(int64_t)pos * tu.f[(INTER ? f0 >> 1 : f0) + j] : 0;
+            turn(static_cast<uint32_t>(u >> 32), cs[j], sn[j]);
         }
     }
-    // Features of pair j in the lane's sixteen.
-    static __device__ __forceinline__ constexpr int a_of(int j) { return INTER ? 2 * j : j; }
-    static __device__ __forceinline__ constexpr int b_of(int j) { return INTER ? 2 * j + 1 : j + kPairs; }
 };
 
 template <int LANES> __device__ __forceinline__ float group_sum(float v)
@@ -132,36 +146,83 @@ template <int LANES> __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float *x)
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A lane's sixteen features as eight pairs of neighbours.
+struct Pairs {
+    uint64_t v[kPairs];
+    __device__ __forceinline__ void unpack(const uint4 &a, const uint4 &b)
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
+        for (int i = 0; i < kPairs; ++i)
+            v[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+    }
+    __device__ __forceinline__ float sum_of_products(const Pairs &o) const
+    {
+        uint64_t s = 0;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            s = fma2(v[i], o.v[i], s);
+        float a, b;
+        unpair(s, a, b);
+        return a + b;
+    }
+    __device__ __forceinline__ void scale(uint64_t f)
+    {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            v[i] = mul2(v[i], f);
+    }
+};
+
+// What a feature is multiplied by: itself (own) and the other of its pair.
+// rotated = own o x + other o partner(x), the partner being the pair at a
+// distance, or the neighbour (INTER).
+template <bool INTER> __device__ __forceinline__ uint64_t partner(const Pairs &x, int i)
+{
+    if (!INTER)
+        return x.v[i ^ 4];
+    float a, b;
+    unpair(x.v[i], a, b);
+    return pair(b, a);
+}
+template <bool INTER>
+__device__ __forceinline__ void rotation(const float (&cs)[kPairs], const float (&sn)[kPairs], bool back, Pairs &own, Pairs &other)
+{
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        // the first of a pair takes -sin of the second, the second +sin of the first; the transpose the other way
+        const int m = INTER ? i : 2 * (i & 3), n = INTER ? i : m + 1;
+        const float f = INTER ? -1.0f : (i < 4 ? -1.0f : 1.0f), g = INTER ? 1.0f : f, d = back ? -1.0f : 1.0f;
+        own.v[i] = pair(cs[m], cs[n]);
+        other.v[i] = pair(d * f * sn[m], d * g * sn[n]);
     }
 }
 
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p) { return __ldcs(reinterpret_cast<const uint4 *>(p)); }
 
-__device__ __forceinline__ void store16(__nv_bfloat16 *row, int f0, int f1, const float (&x)[kFeat])
+__device__ __forceinline__ void store16(__nv_bfloat16 *row, int f0, int f1, const Pairs &x)
 {
-    __stcs(reinterpret_cast<uint4 *>(row + f0),
-           make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
-    __stcs(reinterpret_cast<uint4 *>(row + f1),
-           make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15])));
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        float a, b;
+        unpair(x.v[i], a, b);
+        w[i] = pack_bf16(a, b);
+    }
+    __stcs(reinterpret_cast<uint4 *>(row + f0), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(reinterpret_cast<uint4 *>(row + f1), make_uint4(w[4], w[5], w[6], w[7]));
 }
 
-__device__ __forceinline__ void load_weights(const float *w, int f0, int f1, float (&x)[kFeat])
+__device__ __forceinline__ Pairs load_weights(const float *w, int f0, int f1)
 {
+    Pairs x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float4 a = *reinterpret_cast<const float4 *>(w + (i < 2 ? f0 : f1) + 4 * (i & 1));
-        x[4 * i] = a.x;
-        x[4 * i + 1] = a.y;
-        x[4 * i + 2] = a.z;
-        x[4 * i + 3] = a.w;
+        x.v[2 * i] = pair(a.x, a.y);
+        x.v[2 * i + 1] = pair(a.z, a.w);
     }
+    return x;
 }
 
 template <int D, bool INTER>
@@ -175,19 +236,17 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
     const __nv_bfloat16 *src = p.x[g.s] + g.t * p.token[g.s];
     const int64_t step = p.head[g.s];
     __nv_bfloat16 *dst = (g.s ? kn : qn) + (int64_t)g.t * p.heads[g.s] * D;
-    // rotated feature = n_own * own + n_other * other, weights and signs included
-    float own[kFeat], other[kFeat];
+    // the weights' products with cosines and signed sines
+    Pairs own, other;
     {
-        float w[kFeat], cs[kPairs], sn[kPairs];
-        load_weights(p.w[g.s], g.f0, g.f1, w);
+        float cs[kPairs], sn[kPairs];
+        const Pairs w = load_weights(p.w[g.s], g.f0, g.f1);
         g.angles(p, tu, cs, sn);
+        rotation<INTER>(cs, sn, false, own, other);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-            const int a = G::a_of(j), b = G::b_of(j);
-            own[a] = w[a] * cs[j];
-            other[a] = -w[b] * sn[j];
-            own[b] = w[b] * cs[j];
-            other[b] = w[a] * sn[j];
+        for (int i = 0; i < kPairs; ++i) {
+            own.v[i] = mul2(own.v[i], w.v[i]);
+            other.v[i] = mul2(other.v[i], partner<INTER>(w, i));
         }
     }
     for (int b = 0; b < p.chunk; b += kBatch) {
@@ -204,23 +263,13 @@ qk_norm_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Tur
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = g.h0 + b + u;
-            float x[kFeat], y[kFeat];
-            unpack8(in[u][0], x);
-            unpack8(in[u][1], x + 8);
-            float ss[2] = {0.0f, 0.0f};
+            Pairs x, y;
+            x.unpack(in[u][0], in[u][1]);
+            const float r = rsqrtf(group_sum<G::kLanes>(x.sum_of_products(x)) * (1.0f / D) + p.eps);
+            x.scale(pair(r, r));
 #pragma unroll
-            for (int j = 0; j < kFeat; ++j)
-                ss[j & 1] = fmaf(x[j], x[j], ss[j & 1]);
-            const float r = rsqrtf(group_sum<G::kLanes>(ss[0] + ss[1]) * (1.0f / D) + p.eps);
-#pragma unroll
-            for (int j = 0; j < kFeat; ++j)
-                x[j] *= r;
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                const int a = G::a_of(j), c = G::b_of(j);
-                y[a] = fmaf(x[c], other[a], x[a] * own[a]);
-                y[c] = fmaf(x[a], other[c], x[c] * own[c]);
-            }
+            for (int i = 0; i < kPairs; ++i)
+                y.v[i] = fma2(partner<INTER>(x, i), other.v[i], mul2(x.v[i], own.v[i]));
             if (h < g.h1)
                 store16(dst + h * D, g.f0, g.f1, y);
         }
@@ -237,11 +286,7 @@ template <> struct Grad16<false> {
         a = load8(g + f0);
         b = load8(g + f1);
     }
-    __device__ __forceinline__ void get(float (&x)[kFeat]) const
-    {
-        unpack8(a, x);
-        unpack8(b, x + 8);
-    }
+    __device__ __forceinline__ void get(Pairs &x) const { x.unpack(a, b); }
 };
 template <> struct Grad16<true> {
     float4 v[4];
@@ -252,14 +297,12 @@ template <> struct Grad16<true> {
         for (int i = 0; i < 4; ++i)
             v[i] = __ldcs(reinterpret_cast<const float4 *>(g + (i < 2 ? f0 : f1) + 4 * (i & 1)));
     }
-    __device__ __forceinline__ void get(float (&x)[kFeat]) const
+    __device__ __forceinline__ void get(Pairs &x) const
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[4 * i] = v[i].x;
-            x[4 * i + 1] = v[i].y;
-            x[4 * i + 2] = v[i].z;
-            x[4 * i + 3] = v[i].w;
+            x.v[2 * i] = pair(v[i].x, v[i].y);
+            x.v[2 * i + 1] = pair(v[i].z, v[i].w);
         }
     }
 };
@@ -274,16 +317,16 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
 {
     using G = Group<D, INTER>;
     constexpr int kB = 2;   // heads in flight: two tensors are read
-    __shared__ float red[G::kPerBlock][D];
+    __shared__ __align__(8) float red[G::kPerBlock][D];
     G g(p);
     const int gi = threadIdx.x / G::kLanes;
     const int s = (int)blockIdx.x >= q_blocks;
     const int block = (int)blockIdx.x - (s ? q_blocks : 0), blocks = s ? (int)gridDim.x - q_blocks : q_blocks;
-    float w[kFeat], dw[kFeat];
-    load_weights(p.w[s], g.f0, g.f1, w);
+    const Pairs w = load_weights(p.w[s], g.f0, g.f1);
+    Pairs dw;
 #pragma unroll
-    for (int j = 0; j < kFeat; ++j)
-        dw[j] = 0.0f;
+    for (int i = 0; i < kPairs; ++i)
+        dw.v[i] = 0;
     const int64_t items = (int64_t)p.tokens * (s ? p.n_chunks - p.q_chunks : p.q_chunks);
     const int64_t stride = (int64_t)blocks * G::kPerBlock, step = p.head[s];
     const void *grad = s ? dkn : dqn;
@@ -293,8 +336,12 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
         const __nv_bfloat16 *src = p.x[s] + g.t * p.token[s];
         const int64_t row = (int64_t)g.t * p.heads[s] * D;
         __nv_bfloat16 *dst = (s ? dk : dq) + row;
-        float cs[kPairs], sn[kPairs];
-        g.angles(p, tu, cs, sn);
+        Pairs own, other;
+        {
+            float cs[kPairs], sn[kPairs];
+            g.angles(p, tu, cs, sn);
+            rotation<INTER>(cs, sn, true, own, other);
+        }
         for (int h = g.h0; h < g.h0 + p.chunk; h += kB) {
             uint4 xa[kB], xb[kB];
             Grad16<GF32> gr[kB];
@@ -310,43 +357,34 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                float x[kFeat], y[kFeat];
-                unpack8(xa[u], x);
-                unpack8(xb[u], x + 8);
-                gr[u].get(y);
-                float ss[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < kFeat; ++j)
-                    ss[j & 1] = fmaf(x[j], x[j], ss[j & 1]);
-                const float sum = group_sum<G::kLanes>(ss[0] + ss[1]);
+                Pairs x, y, z;
+                x.unpack(xa[u], xb[u]);
+                gr[u].get(z);
+                const float sum = group_sum<G::kLanes>(x.sum_of_products(x));
                 const float r = h + u < g.h1 ? rsqrtf(sum * (1.0f / D) + p.eps) : 0.0f;   // no head: 0, not 0 / 0
+                x.scale(pair(r, r));   // n
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) {
-                    const int a = G::a_of(j), c = G::b_of(j);
-                    const float ya = y[a], yc = y[c];
-                    y[a] = fmaf(yc, sn[j], ya * cs[j]);
-                    y[c] = fmaf(-ya, sn[j], yc * cs[j]);
+                for (int i = 0; i < kPairs; ++i) {
+                    y.v[i] = fma2(partner<INTER>(z, i), other.v[i], mul2(z.v[i], own.v[i]));
+                    dw.v[i] = fma2(y.v[i], x.v[i], dw.v[i]);
+                    y.v[i] = mul2(y.v[i], w.v[i]);   // h
                 }
-                float hn[2] = {0.0f, 0.0f};
+                const float m = group_sum<G::kLanes>(y.sum_of_products(x)) * (1.0f / D);
 #pragma unroll
-                for (int j = 0; j < kFeat; ++j) {
-                    x[j] *= r;   // n
-                    dw[j] = fmaf(y[j], x[j], dw[j]);
-                    y[j] *= w[j];   // h
-                    hn[j & 1] = fmaf(y[j], x[j], hn[j & 1]);
-                }
-                const float m = group_sum<G::kLanes>(hn[0] + hn[1]) * (1.0f / D);
-#pragma unroll
-                for (int j = 0; j < kFeat; ++j)
-                    y[j] = r * fmaf(-x[j], m, y[j]);
+                for (int i = 0; i < kPairs; ++i)
+                    y.v[i] = fma2(x.v[i], pair(-m, -m), y.v[i]);
+                y.scale(pair(r, r));
                 if (h + u < g.h1)
                     store16(dst + (h + u) * D, g.f0, g.f1, y);
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < kFeat; ++j)
-        red[gi][j < kPairs ? g.f0 + j : g.f1 + j - kPairs] = dw[j];
+    for (int i = 0; i < kPairs; ++i) {
+        float a, b;
+        unpair(dw.v[i], a, b);
+        *reinterpret_cast<float2 *>(&red[gi][i < 4 ? g.f0 + 2 * i : g.f1 + 2 * i - 8]) = make_float2(a, b);
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kThreads) {
         float v = 0.0f;
@@ -473,7 +511,7 @@ cudaError_t launch_qk_norm(const bdla_qk_norm_args &a, __nv_bfloat16 *qn, __nv_b
 static int norm_q_blocks(const bdla_attn_dims &d, int *total)
 {
     const int chunk = head_chunk(d), per = kThreads / (d.d / kFeat);
-    const int64_t most = (int64_t)sm_count() * 12, tokens = (int64_t)d.B * d.T;
+    const int64_t most = (int64_t)sm_count() * 24, tokens = (int64_t)d.B * d.T;
     int64_t n[2];
     for (int s = 0; s < 2; ++s) {
         const int heads = s ? d.Hk : d.Hq;
