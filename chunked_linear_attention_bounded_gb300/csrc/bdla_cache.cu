@@ -82,7 +82,10 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 // sequence times the query heads of the group.  With up to 32 rows the pass is
 // bound by HBM: their products cost nothing beside 512 bytes of keys and values
 // a position, so they run as warp MMAs (m16n8k16, 16 or 32 rows) straight from
-// the tiles that cp.async brings in, three tiles of 64 positions in flight.  A
+// the tiles that cp.async brings in.  Keys and values of 64 positions have two
+// buffers each, and a buffer is filled again as soon as its own product is done:
+// 64 KB a CTA, three CTAs an SM (three whole tiles a CTA, two CTAs an SM: 736 us
+// for 256 ragged sequences against 669).  A
 // CTA's four warps split the rows first and the positions of the tile with what
 // is left, and join through shared memory at the end.  Warp MMAs run at an
 // eighth of the tensor cores' rate here: with 64 rows they took longer than the
@@ -99,7 +102,7 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 // with a page.  A position that nobody may see is not loaded: its rows are
 // zeros.
 constexpr int kKeys = 64;         // positions of a tile
-constexpr int kCStages = 3;
+constexpr int kCStages = 2;       // of keys, and of values
 constexpr int kCThreads = 128;
 
 template <int D> struct CachedSmem {
@@ -132,7 +135,7 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 template <int D, int WR>
-__global__ void __launch_bounds__(kCThreads)
+__global__ void __launch_bounds__(kCThreads, D == 128 ? 3 : 4)
 cached_kernel(const __grid_constant__ Call a, int row_blocks)
 {
     constexpr int WK = 4 / WR;          // warps along the positions
@@ -165,29 +168,28 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     const uint64_t seen = drafts ? sees_any(a.tree, b, T, lane) : 0;
 
     // page table entry of position t (a tile's 64 positions, by the first 64 threads)
-    auto lookup = [&](int t) { return t < k1 ? table[page_of(t, c.page, a.shift)] : -1; };
+    auto lookup = [&](int t) { return t < k1 ? table[a.div.entry(t)] : -1; };
     auto place = [&](int n, int t, int pg) {
         bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
         if (live && (pg < 0 || pg >= c.n_pages)) {
             set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
             live = false;
         }
-        sm.row[n & 3][tid] = live ? pg * c.page + offset_of(t, c.page, a.shift) : -1;
+        sm.row[n & 3][tid] = live ? pg * c.page + a.div.offset(t) : -1;
         const uint32_t m = __ballot_sync(0xffffffffu, live);
         if (lane == 0)
             sm.valid[n & 3][tid >> 5] = m;
     };
-    auto load = [&](int n) {
+    // tile n of the keys (v = 0) or of the values (v = 1), one cp.async group
+    auto load = [&](int n, int v) {
         if (n < nt) {
-            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(sm.kv[n % kCStages][0]));
+            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(sm.kv[n % kCStages][v]));
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(v ? c.v : c.k) + (int64_t)kh * D;
 #pragma unroll
             for (int u = 0; u < kKeys * kChunks / kCThreads; ++u) {
                 const int e = tid + u * kCThreads, r = e / kChunks, ch = e % kChunks;
                 const int row = sm.row[n & 3][r];
-                const int64_t off = ((int64_t)(row < 0 ? 0 : row) * Hk + kh) * D + 8 * ch;
-                const uint32_t to = dst + (r * kChunks + (ch ^ (r & 7))) * 16;
-                cp16(to, static_cast<const __nv_bfloat16 *>(c.k) + off, row >= 0);
-                cp16(to + kKeys * D * 2, static_cast<const __nv_bfloat16 *>(c.v) + off, row >= 0);
+                cp16(dst + (r * kChunks + (ch ^ (r & 7))) * 16, src + (int64_t)max(row, 0) * Hk * D + 8 * ch, row >= 0);
             }
         }
         cp_commit();
@@ -198,8 +200,10 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
             place(n, t, lookup(t));
         }
     __syncthreads();
-    load(0);
-    load(1);
+    load(0, 0);
+    load(0, 1);
+    load(1, 0);
+    load(1, 1);
 
     // query fragments: rows lane/4 and lane/4 + 8 of the warp's 16
     const int r0 = rb * MR + 16 * wr + (lane >> 2), r1 = r0 + 8;
@@ -223,9 +227,14 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 
     for (int n = 0; n < nt; ++n) {
-        cp_wait<kCStages - 2>();
-        __syncthreads();   // tile n is here, tile n - 1 is done with, the rows of tile n + 2 are known
-        load(n + 2);
+        // in flight: V n, K n + 1, V n + 1 at most; one barrier says that K n is here and V n - 1 is done with
+        if (n == 0)
+            cp_wait<3>();
+        else
+            cp_wait<2>();
+        __syncthreads();
+        if (n > 0)
+            load(n + 1, 1);
         const int t3 = k0 + (n + 3) * kKeys + tid;
         const int pg3 = tid < kKeys ? lookup(t3) : -1;
         const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(sm.kv[n % kCStages][0]));
@@ -244,6 +253,10 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
                 mma16816(s[2 * nb], fq[ks], f[0], f[1]);
                 mma16816(s[2 * nb + 1], fq[ks], f[2], f[3]);
             }
+        // the same for V n and K n
+        cp_wait<2>();
+        __syncthreads();
+        load(n + 2, 0);
         const uint64_t ok = (uint64_t)sm.valid[n & 3][0] | ((uint64_t)sm.valid[n & 3][1] << 32);
         const int t0 = k0 + n * kKeys;
         if (ok != ~0ull || t0 + kKeys > cut.len) {
@@ -481,8 +494,9 @@ static int cached_rows(const bdla_attn_dims &d)
     return R <= 16 ? 16 : R <= 32 ? 32 : kWideRows;
 }
 
-// Pieces of a sequence.  Few sequences: enough pieces for eight CTAs an SM, of
-// at least 128 positions.  Many: pieces of about 2048 positions, so that long
+// Pieces of a sequence.  Few sequences: as many pieces as fill the SMs once, or
+// two or three times where they stay over 1024 positions (one sequence of
+// 262144 positions: 176 us in 3 rounds, 180 in 2.7), of at least 128.  Many: pieces of about 2048 positions, so that long
 // and short sequences end together, and of at least 1024, so that a CTA's
 // start-up (length, page table, first tile) stays small beside its keys.  The
 // wide kernel holds an SM alone: as many pieces as fill the SMs a whole number
@@ -503,7 +517,11 @@ static Pieces cached_pieces(const bdla_attn_dims &d, int64_t max_keys)
         ns = (rounds < 1 ? 1 : rounds) * sms / units;
     } else {
         const int64_t even = (max_keys + 2047) / 2048;
-        ns = (sms * 8 + units - 1) / units;
+        const int64_t held = sms * (d.d == 128 ? 3 : 4);   // CTAs at a time
+        int64_t rounds = 3;
+        while (rounds > 1 && max_keys * units < 1024 * rounds * held)
+            --rounds;
+        ns = rounds * held / units;
         ns = ns > even ? ns : even;
     }
     const int64_t most[3] = {(max_keys + p.least - 1) / p.least,
@@ -562,7 +580,7 @@ cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.Hq = d.Hq;
     a.Hk = d.Hk;
     a.pieces = cached_pieces(d, max_keys);
-    a.shift = (c.page & (c.page - 1)) == 0 ? __builtin_ctz(c.page) : -1;
+    a.div = PageDiv::of(c.page);
     a.st = st;
     a.part_o = static_cast<float *>(partials);
     a.part_ml = a.part_o + (size_t)a.pieces.ns * rows * d.d;

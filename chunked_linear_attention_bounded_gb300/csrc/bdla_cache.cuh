@@ -53,10 +53,23 @@ __device__ __forceinline__ uint64_t sees_any(const uint64_t *tree, int64_t b, in
     return m;
 }
 
-// Entry of the page table and offset in the page of position t: a shift where
-// the page is a power of two (shift >= 0), else a division.
-__device__ __forceinline__ int page_of(int t, int page, int shift) { return shift >= 0 ? t >> shift : t / page; }
-__device__ __forceinline__ int offset_of(int t, int page, int shift) { return shift >= 0 ? t & (page - 1) : t % page; }
+// Division of positions (31 bits) by the page without a division: with
+// s = ceil(log2 page) and mul = ceil(2^(31 + s) / page), which has 32 bits at
+// most, mul page exceeds 2^(31 + s) by less than 2^s, so t mul / 2^(31 + s)
+// exceeds t / page by less than 1 / page for t < 2^31.
+struct PageDiv {
+    uint32_t mul;
+    int shift, page;
+    static PageDiv of(int page)
+    {
+        int s = 0;
+        while ((1 << s) < page)
+            ++s;
+        return {(uint32_t)((((uint64_t)1 << (31 + s)) + page - 1) / page), 31 + s, page};
+    }
+    __device__ __forceinline__ int entry(int t) const { return (int)(((uint64_t)(uint32_t)t * mul) >> shift); }
+    __device__ __forceinline__ int offset(int t) const { return t - entry(t) * page; }
+};
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
 {
@@ -74,7 +87,7 @@ struct Call {
     float *lse;
     float *part_o, *part_ml;   // [B][Hk][ns][T * G] rows of D, and of (maximum, sum)
     int T, Hq, Hk;
-    int shift;                 // log2 of the page, or -1
+    PageDiv div;
     Pieces pieces;
     DeviceStatus *st;
 };

@@ -112,7 +112,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int t = k0 + j * BT + 4 * lane + u;
-            pg[u] = j < nt && t < k1 ? table[page_of(t, c.page, a.shift)] : -1;
+            pg[u] = j < nt && t < k1 ? table[a.div.entry(t)] : -1;
         }
     };
     int pg[4];
@@ -234,7 +234,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
                     live = false;
                 }
-                row[u] = live ? pg[u] * c.page + offset_of(t, c.page, a.shift) : -1;
+                row[u] = live ? pg[u] * c.page + a.div.offset(t) : -1;
                 bits |= (live ? 1u : 0u) << u;
             }
             const bool whole = run > 0 && __all_sync(0xffffffffu, bits == 15u);
