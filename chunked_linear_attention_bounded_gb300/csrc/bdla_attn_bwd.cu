@@ -58,7 +58,8 @@ template <int D> struct BwdSmem {
     static __host__ __device__ constexpr int slot(int it) { return it & 1 ? kA + (it >> 1) % kB : (it >> 1) % kA; }
     static __host__ __device__ constexpr int turn(int it) { return it & 1 ? (it >> 1) / kB : (it >> 1) / kA; }
     float col[2][2][BT];   // key tiles: -lse * log2 e and -delta of a query tile; query tiles: [0] halves of delta
-    uint64_t full_own, full[kStages], empty[kStages], s_full[2], ready[2], dp_full, dp_free, done;
+    uint64_t full_own, full[kStages], empty[kStages], s_full[2], dp_full, dp_free, done;
+    uint64_t ready[2][2];   // [tile, or p and ds][part]: weights whose first, last 32 columns of each warp's 64 are there
     uint64_t drain, never;
     uint64_t wait_ns;
     uint32_t tmem_base;
@@ -100,7 +101,8 @@ __device__ __forceinline__ void setup(Smem &sm, int tid, uint64_t wait_ns)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.s_full[b], 1);
-            mbar_init(&sm.ready[b], kEpi);
+            mbar_init(&sm.ready[b][0], kEpi);
+            mbar_init(&sm.ready[b][1], kEpi);
         }
         mbar_init(&sm.dp_full, 1);
         mbar_init(&sm.dp_free, kEpi);
@@ -231,12 +233,20 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
             if (j + 1 < n)
                 ok = issue_s(j + 1) && warp_wait(&sm.dp_free, j & 1, &sm.wait_ns, abort_flag) && issue_dp(j + 1);
-            ok = ok && warp_wait(hook ? &sm.never : &sm.ready[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns, abort_flag);
+            const uint32_t turn = (uint32_t)((j >> 1) & 1);
+            ok = ok && warp_wait(hook ? &sm.never : &sm.ready[j & 1][0], hook ? 0u : turn, &sm.wait_ns, abort_flag);
             if (!ok)
                 break;
             tc_fence_after();
+            const uint64_t k = sum_desc(tile(2 * j));
+            if (elect_one())
+                mma_sum_part<D, 0>(t_dq, tmem + BT * (j & 1), k, j > 0);
+            __syncwarp();
+            if (!(ok = warp_wait(&sm.ready[j & 1][1], turn, &sm.wait_ns, abort_flag)))
+                break;
+            tc_fence_after();
             if (elect_one()) {
-                mma_sum<D, 64>(t_dq, tmem + BT * (j & 1), sum_desc(tile(2 * j)), j > 0);
+                mma_sum_part<D, 1>(t_dq, tmem + BT * (j & 1), k, true);
                 umma_commit(&sm.empty[Smem::slot(2 * j)]);
                 if (j == n - 1)
                     umma_commit(&sm.done);
@@ -298,6 +308,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             tc_fence_before();
             mbar_arrive(&sm.dp_free);
             const bool diag = j == n - 1;
+            if (diag && valid < BT) {
+                // dq sums over the diagonal tile's keys: clear those past the end (S has read them)
+                clear_rows(sm.ring[Smem::slot(2 * j)], NP, valid, e, kEpi);
+                fence_proxy_async_smem();
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -330,15 +345,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 for (int i = 0; i < 16; ++i)
                     u[i] = pack_bf16(__uint_as_float(y[k][2 * i]), __uint_as_float(y[k][2 * i + 1]));
                 tmem_st16(t_s + 16 * k, u);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.ready[j & 1][k]);
             }
-            if (diag && valid < BT) {
-                // this product sums over the diagonal tile's keys: clear those past the end (S has read them)
-                clear_rows(sm.ring[Smem::slot(2 * j)], NP, valid, e, kEpi);
-                fence_proxy_async_smem();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sm.ready[j & 1]);
         }
         {
             float a, b;
@@ -449,22 +459,35 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         bool ok = warp_wait(&sm.full_own, 0, &sm.wait_ns, abort_flag) && issue_s(0) && issue_dp(0);
         for (int t = 0; ok && t < n; ++t) {
             const bool hook = stall == BDLA_STALL_MMA && t == stall_at;
-            ok = warp_wait(hook ? &sm.never : &sm.ready[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns, abort_flag);
+            ok = warp_wait(hook ? &sm.never : &sm.ready[0][0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns, abort_flag);
             if (!ok)
                 break;
             tc_fence_after();
+            const uint64_t g = sum_desc(tile(2 * t + 1)), q = sum_desc(tile(2 * t));
+            if (elect_one())
+                mma_sum_part<D, 0>(t_dv, tmem, g, t > 0);
+            __syncwarp();
+            if (!(ok = warp_wait(&sm.ready[0][1], t & 1, &sm.wait_ns, abort_flag)))
+                break;
+            tc_fence_after();
             if (elect_one()) {
-                mma_sum<D, 64>(t_dv, tmem, sum_desc(tile(2 * t + 1)), t > 0);
+                mma_sum_part<D, 1>(t_dv, tmem, g, true);
                 umma_commit(&sm.empty[Smem::slot(2 * t + 1)]);
             }
             __syncwarp();
             if (t + 1 < n && !(ok = issue_s(t + 1)))
                 break;
-            if (!(ok = warp_wait(&sm.ready[1], t & 1, &sm.wait_ns, abort_flag)))
+            if (!(ok = warp_wait(&sm.ready[1][0], t & 1, &sm.wait_ns, abort_flag)))
+                break;
+            tc_fence_after();
+            if (elect_one())
+                mma_sum_part<D, 0>(t_dk, t_dp, q, t > 0);
+            __syncwarp();
+            if (!(ok = warp_wait(&sm.ready[1][1], t & 1, &sm.wait_ns, abort_flag)))
                 break;
             tc_fence_after();
             if (elect_one()) {
-                mma_sum<D, 64>(t_dk, t_dp, sum_desc(tile(2 * t)), t > 0);
+                mma_sum_part<D, 1>(t_dk, t_dp, q, true);
                 umma_commit(&sm.empty[Smem::slot(2 * t)]);
                 if (t == n - 1)
                     umma_commit(&sm.done);
@@ -513,6 +536,16 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             if (t + 1 < n)
                 next = fetch(t + 1);
             ok = warp_wait(hook ? &sm.never : &sm.s_full[0], hook ? 0u : (uint32_t)(t & 1), &sm.wait_ns, abort_flag);
+            if (ok && valid < BT) {
+                // dv and dk sum over this tile's queries: clear those past the end once S and dp have read them
+                ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
+                if (ok) {
+                    clear_rows(sm.ring[Smem::slot(2 * t)], NP, valid, e, kEpi);
+                    clear_rows(sm.ring[Smem::slot(2 * t + 1)], NP, valid, e, kEpi);
+                    fence_proxy_async_smem();
+                }
+            }
+            const bool mask = i_tile == 0 || valid < BT;   // the diagonal, or queries past the end
             float p[64];
             if (ok) {
                 tc_fence_after();
@@ -521,46 +554,34 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 tmem_ld32(t_s + 32, x[1]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int m = 0; m < 64; m += 4) {
-                    const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(&sm.col[t & 1][0][64 * half + m]);
-                    const uint32_t *z = &x[m >> 5][m & 31];
-                    float a, b;
-                    unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), c2, l4.x), a, b);
-                    p[m] = ex2(a);
-                    p[m + 1] = ex2(b);
-                    unpair(fma2(pair(__uint_as_float(z[2]), __uint_as_float(z[3])), c2, l4.y), a, b);
-                    p[m + 2] = ex2(a);
-                    p[m + 3] = ex2(b);
-                }
-                if (i_tile == 0 || valid < BT) {   // the diagonal, or queries past the end
-#pragma unroll
-                    for (int m = 0; m < 64; ++m) {
-                        const int q = 64 * half + m;
-                        if ((i_tile == 0 && q < r) || q >= valid)
-                            p[m] = 0.0f;
-                    }
-                }
-#pragma unroll
                 for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int m = 0; m < 32; m += 4) {
+                        const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(&sm.col[t & 1][0][64 * half + 32 * k + m]);
+                        float a, b;
+                        unpair(fma2(pair(__uint_as_float(x[k][m]), __uint_as_float(x[k][m + 1])), c2, l4.x), a, b);
+                        p[32 * k + m] = ex2(a);
+                        p[32 * k + m + 1] = ex2(b);
+                        unpair(fma2(pair(__uint_as_float(x[k][m + 2]), __uint_as_float(x[k][m + 3])), c2, l4.y), a, b);
+                        p[32 * k + m + 2] = ex2(a);
+                        p[32 * k + m + 3] = ex2(b);
+                    }
+                    if (mask) {
+#pragma unroll
+                        for (int m = 32 * k; m < 32 * k + 32; ++m) {
+                            const int q = 64 * half + m;
+                            p[m] = (i_tile == 0 && q < r) || q >= valid ? 0.0f : p[m];
+                        }
+                    }
                     uint32_t u[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         u[i] = pack_bf16(p[32 * k + 2 * i], p[32 * k + 2 * i + 1]);
                     tmem_st16(t_s + 16 * k, u);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&sm.ready[0][k]);
                 }
-                if (valid < BT) {
-                    // dv and dk sum over this tile's queries: clear those past the end once S and dp have read them
-                    ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
-                    if (ok) {
-                        clear_rows(sm.ring[Smem::slot(2 * t)], NP, valid, e, kEpi);
-                        clear_rows(sm.ring[Smem::slot(2 * t + 1)], NP, valid, e, kEpi);
-                        fence_proxy_async_smem();
-                    }
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                if (ok)
-                    mbar_arrive(&sm.ready[0]);
             }
             if (ok)
                 ok = warp_wait(&sm.dp_full, t & 1, &sm.wait_ns, abort_flag);
@@ -573,7 +594,6 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             tmem_ld32(t_d, y[0]);
             tmem_ld32(t_d + 32, y[1]);
             tmem_ld_wait();
-            const bool mask = i_tile == 0 || valid < BT;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -601,10 +621,10 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                 for (int i = 0; i < 16; ++i)
                     u[i] = pack_bf16(__uint_as_float(y[k][2 * i]), __uint_as_float(y[k][2 * i + 1]));
                 tmem_st16(t_d + 16 * k, u);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.ready[1][k]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sm.ready[1]);
         }
         if (ok)
             ok = warp_wait(&sm.done, 0, &sm.wait_ns, abort_flag);

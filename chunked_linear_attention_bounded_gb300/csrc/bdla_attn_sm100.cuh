@@ -186,6 +186,18 @@ __device__ __forceinline__ void mma_sum(uint32_t acc, uint32_t a, uint64_t b, bo
         sm100::umma_bf16_ts(acc, a + (ks >> 2) * Right + (ks & 3) * 8, b + ks * (2048 >> 4), id, accumulate || ks > 0);
 }
 
+// The same in two parts with the weights laid out by two warps a row, 64 columns
+// each: Part 0 takes the first 32 of either's columns, Part 1 the others.
+template <int D, int Part> __device__ __forceinline__ void mma_sum_part(uint32_t acc, uint32_t a, uint64_t b, bool accumulate)
+{
+    constexpr uint32_t id = sm100::idesc_bf16_f32(BT, D, false, true);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int ks = (i >> 1) * 4 + 2 * Part + (i & 1);
+        sm100::umma_bf16_ts(acc, a + (ks >> 2) * 64 + (ks & 3) * 8, b + ks * (2048 >> 4), id, accumulate || Part > 0 || i > 0);
+    }
+}
+
 // All lanes' waits, as one answer for the warp (the tensor-memory accesses
 // that follow need whole warps).  The abort flag is read only after a wait that
 // was not over at once: the read cost the MMA warp a few hundred cycles each
