@@ -645,6 +645,8 @@ def _documents(cu_seqlens, B, device):
     """(pointer, count) of packed documents, (None, 0) for fixed-length rows."""
     if cu_seqlens is None:
         return None, 0
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     p = _on(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), device)
     if B != 1:
         raise ValueError("packed documents need B = 1")

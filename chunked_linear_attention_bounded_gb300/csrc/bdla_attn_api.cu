@@ -62,6 +62,13 @@ bdla_status check_norm(const bdla_qk_norm_args &a, const bdla_attn_dims &d)
     return BDLA_OK;
 }
 
+// Whole documents: a CTA for every (128 tokens of a document, head) is a grid extent.
+bdla_status check_grid(const bdla_attn_dims &d, int n_docs)
+{
+    const int64_t tiles = (int64_t)d.B * d.T / 128 + 1 + n_docs;
+    return tiles * d.Hq <= INT32_MAX ? BDLA_OK : BDLA_ERR_TOO_LARGE;
+}
+
 bdla_status check_scale(float s) { return isfinite(s) && s > 0.0f ? BDLA_OK : BDLA_ERR_RANGE; }
 
 bdla_status check_cache(const bdla_cache &c)
@@ -176,6 +183,7 @@ bdla_status bdla_attn_fwd(const void *q, const void *k, const void *v, const int
 {
     const bool packed = cu_seqlens != nullptr;
     BDLA_TRY(check_attn_dims(d, packed, n_docs));
+    BDLA_TRY(check_grid(d, packed ? n_docs : d.B));
     BDLA_TRY(check_scale(scale));
     if (d.T > 0 && (!q || !k || !v || !o || !lse))
         return BDLA_ERR_NULL;
@@ -193,6 +201,7 @@ bdla_status bdla_attn_bwd(const void *q, const void *k, const void *v, const voi
 {
     const bool packed = cu_seqlens != nullptr;
     BDLA_TRY(check_attn_dims(d, packed, n_docs));
+    BDLA_TRY(check_grid(d, packed ? n_docs : d.B));
     BDLA_TRY(check_scale(scale));
     if (d.T > 0 && (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv))
         return BDLA_ERR_NULL;

@@ -572,6 +572,8 @@ cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, cons
     Call a;
     a.q = q;
     a.c = c;
+    if ((int64_t)c.n_pages * c.page == 0)   // no rows: nothing is read, from an address that exists all the same
+        a.c.k = a.c.v = const_cast<__nv_bfloat16 *>(q);
     a.tree = tree;
     a.scale = scale;
     a.o = o;

@@ -94,7 +94,8 @@ bdla_status bdla_attn_bwd(const void *q, const void *k, const void *v, const voi
 /*
  * A paged cache of keys and values.  Page p holds the rows of `page`
  * consecutive positions; position t of sequence b is row t % page of page
- * pages[b][t / page].
+ * pages[b][t / page].  n_pages * page is at most 2^31 - 1, and so is (nearly)
+ * max_pages * page (BDLA_ERR_TOO_LARGE).
  */
 typedef struct {
     void *k, *v;            /* bf16 [n_pages, page, Hk, d] */
@@ -110,7 +111,9 @@ typedef struct {
  * NULL), position lens[b] + j of sequence b takes row rows[b][j] (row j where
  * rows is NULL) of k and v, bf16 [B, T, Hk, d].  With rows and counts this
  * also compacts a verified tree of drafts: the accepted drafts, in order, move
- * to the positions that follow the context.  lens is not changed.  A row whose
+ * to the positions that follow the context.  lens is not changed.  Sequences
+ * that share a page (after a fork) must not both write into it: copy it first.
+ * The source rows must not lie in the cache that is written.  A row whose
  * position lies past the page table, whose page lies outside the cache, or
  * whose source lies outside 0 .. T - 1 is not written and recorded as
  * BDLA_ERR_DEVICE, and so is a count outside 0 .. T.

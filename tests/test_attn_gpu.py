@@ -404,6 +404,21 @@ def test_cached_reports_pages_it_cannot_read():
         ref.check("lse " + what, lse, want_l)
 
 
+@pytest.mark.parametrize("T,Hq", [(1, 4), (20, 4)])
+def test_a_cache_without_pages_or_a_table_without_entries(T, Hq):
+    """Positions that no page holds: reported, seen by nobody; nothing at all in sequences of length 0 - T."""
+    q = _rn(_gen(15), 2, T, Hq, 64)
+    lens = torch.tensor([0, 7], dtype=torch.int32, device="cuda")
+    empty = torch.empty((0, 16, 2, 64), dtype=BF16, device="cuda")
+    some = torch.zeros((3, 16, 2, 64), dtype=BF16, device="cuda")
+    for cache, table in ((empty, torch.zeros((2, 3), dtype=torch.int32, device="cuda")),
+                         (some, torch.zeros((2, 0), dtype=torch.int32, device="cuda"))):
+        ws = bdla.Workspace(256, "cuda")
+        o, lse = bdla.attn_cached(q, cache, cache, table, lens, ws=ws)
+        assert ws.read_device_status() == bdla.ERR_DEVICE
+        assert float(o.float().abs().sum()) == 0.0 and bool((lse == -math.inf).all())
+
+
 def test_cache_offsets_past_32_bits():
     """Pages whose first element lies past 2^31 (and, in bytes, 2^32)."""
     page, Hk, d = 64, 4, 128

@@ -125,6 +125,7 @@ def test_attn_refusals(L):
         assert f(d=D(1, 4, 4, 2, 256)) == f(d=D(65536, 1, 4, 2, 64)) == E.ERR_UNSUPPORTED
         assert f(d=D(4, 1 << 29, 4, 2, 64)) == E.ERR_TOO_LARGE
         assert f(ws=None) == f(wsb=255) == E.ERR_WORKSPACE
+        assert f(d=D(1, 1 << 30, 512, 1, 64)) == E.ERR_TOO_LARGE      # (128 tokens, head) units are a grid extent
     assert L.bdla_workspace_bytes_attn(E.ATTN_BWD, D(1, 100, 4, 2, 64), 0, 0) >= 256 + 1600
     assert L.bdla_workspace_bytes_attn(E.ATTN_BWD, D(1, 100, 4, 3, 64), 0, 0) == 0
     assert L.bdla_workspace_bytes_attn(99, D(1, 100, 4, 2, 64), 0, 0) == 0
