@@ -42,7 +42,7 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_attn_cached", "bdla_workspace_bytes_attn")
 ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED = 0, 1, 2, 3, 4
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
-KERNEL_ATTN_FWD, KERNEL_ATTN_BWD = 5, 6
+KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED = 5, 6, 7
 STALL_NONE, STALL_PRODUCER, STALL_MMA, STALL_EPILOGUE = 0, 1, 2, 3
 
 

@@ -586,6 +586,7 @@ cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.st = st;
     a.part_o = static_cast<float *>(partials);
     a.part_ml = a.part_o + (size_t)a.pieces.ns * rows * d.d;
+    KernelMark mark_(BDLA_KERNEL_ATTN_CACHED, stream);
     cudaError_t err;
     if (mr == kWideRows)
         err = launch_cached_wide(a, d, stream);

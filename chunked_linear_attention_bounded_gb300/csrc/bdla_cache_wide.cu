@@ -43,7 +43,7 @@ template <int D> struct WideSmem {
     alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 V_1 ...
     int row[kFetchWarps][BT];    // cache row of the positions of a warp's tile, -1: not seen
     uint32_t valid[kSlots][4];   // positions of a tile that may be seen
-    uint64_t full[kStages], empty[kStages], s_full[2], o_done[2], drain;
+    uint64_t full[kStages], empty[kStages], s_full[2], o_done[2], drain, never;
     uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
     uint64_t wait_ns;
     uint32_t tmem_base;
@@ -65,7 +65,7 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, int run,
-                   const __grid_constant__ Call a, int row_blocks, uint64_t wait_ns)
+                   const __grid_constant__ Call a, int row_blocks, uint64_t wait_ns, int stall)
 {
     using Smem = WideSmem<D>;
     constexpr int NS = Smem::kStages, SL = Smem::kSlots, NP = Smem::kPanels, kChunks = D / 8;
@@ -134,6 +134,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 mbar_init(&sm.o_done[x], 1);
             }
             mbar_init(&sm.drain, 1);
+            mbar_init(&sm.never, 1);
             sm.abort_flag = 0;
             sm.wait_ns = wait_ns;
             mbar_fence_init();
@@ -155,6 +156,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = warp >= 1 && warp < 4 ? 0 : sm.tmem_base;   // (the fetching warps do not wait for it)
     volatile int *abort_flag = &sm.abort_flag;
+    const int stall_at = nt > 1 ? 1 : 0;   // test hook: the tile at which a role stalls
 
     if (warp == 0) {
         // ---------------------------------------------------------------- MMA issuer
@@ -183,8 +185,9 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 if (!ok || w >= tiles)
                     continue;
                 const int it = 2 * j + 1;
+                const bool hook = stall == BDLA_STALL_MMA && j == stall_at;
                 ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag) &&
-                     warp_wait(&sm.p_ready[w][0], (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+                     warp_wait(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
                 if (!ok)
                     continue;
                 tc_fence_after();
@@ -252,8 +255,10 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 #pragma unroll 1
             for (int v = 0; ok && v < 2; ++v) {
                 const int it = 2 * j + v, s = it % NS;
-                if (it >= NS)
-                    ok = warp_wait(&sm.empty[s], (uint32_t)((it / NS - 1) & 1), &sm.wait_ns, abort_flag);
+                const bool hook = stall == BDLA_STALL_PRODUCER && it == 2 * stall_at;
+                if (it >= NS || hook)
+                    ok = warp_wait(hook ? &sm.never : &sm.empty[s], hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns,
+                                   abort_flag);
                 if (!ok)
                     break;
                 if (whole) {
@@ -300,8 +305,8 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 set_status(a.st, BDLA_ERR_TIMEOUT, 0x31u);
             // this warp's copies in flight land before the CTA exits
             cp_wait<0>();
-            for (int it = issued - 1; issued >= 0 && it <= issued; ++it)
-                if (it >= 0)
+            for (int it = max(issued - NS + 1, 0); it <= issued; ++it)
+                if ((it >> 1) % kFetchWarps == fw)
                     mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
         }
     } else {
@@ -314,7 +319,8 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         bool ok = true;
         const int n = w < tiles ? nt : 0;
         for (int j = 0; j < n; ++j) {
-            ok = warp_wait(&sm.s_full[w], (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
+            const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
+            ok = warp_wait(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(j & 1), &sm.wait_ns, abort_flag);
             if (!ok)
                 break;
             tc_fence_after();
@@ -457,7 +463,8 @@ template <int D> cudaError_t go(const Call &a, const bdla_attn_dims &d, cudaStre
         return cudaErrorInvalidValue;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
-    cached_wide_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(tk, tv, run, a, row_blocks, g_wait_ns.load());
+    cached_wide_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(tk, tv, run, a, row_blocks, g_wait_ns.load(),
+                                                              g_test_stall[BDLA_KERNEL_ATTN_CACHED].load());
     return cudaGetLastError();
 }
 

@@ -79,7 +79,7 @@ inline const char *kernel_range_name(int kernel)
 {
     static const char *names[BDLA_KERNEL_COUNT] = {"bdla:decay", "bdla:fwd", "bdla:bwd",
                                                    "bdla:states", "bdla:seg", "bdla:attn_fwd",
-                                                   "bdla:attn_bwd"};
+                                                   "bdla:attn_bwd", "bdla:attn_cached"};
     return names[kernel];
 }
 // Bounded waits (bdla_set_wait_limit_ns, bdla_set_test_stall): the limit of
