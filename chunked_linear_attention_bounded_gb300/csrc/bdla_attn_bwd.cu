@@ -24,9 +24,13 @@
 // Rounding: scores, dp, delta and the accumulators are fp32; p and ds enter
 // their products as bf16 (half a step, 2^-8 of each); ds is formed from the
 // fp32 p.  delta is dO . o with the o that the forward rounded to bf16 for dq,
-// which needs it before it has seen a key; the same kernel sums p o dp in fp32
-// on its way, and the second takes that delta, free of o's rounding (dk's error
-// against 64 bits 2.8e-3 -> 2.4e-3 of its norm at 1537 tokens).
+// which needs it before it has seen every key; the same kernel sums p o dp in
+// fp32 on its way, and the second takes that delta, free of o's rounding (dk's
+// error against 64 bits 2.8e-3 -> 2.4e-3 of its norm at 1537 tokens).  A tile of
+// queries with one tile of keys, the first of every document, has all of its
+// weights at hand: it normalises them by their own sum and takes delta from them
+// before ds, so that short rows, where o's rounding weighs most, are as exact as
+// their weights, and a document's first token, whose ds is 0, gets 0.
 //
 // Rows past a document's end hold the next document.  Their p and ds are
 // zeroed by selection, and where such rows are the summed side of a product
@@ -288,7 +292,76 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const uint64_t c2 = pair(c, c), nl2 = pair(-l2, -l2), nd2 = pair(-dl, -dl);
         uint64_t sum2 = 0;   // of p dp, the row's own delta
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        if (n == 1) {
+            // Both barriers are for every warp, whether its waits ran out or not.
+            const uint32_t t_s = tmem + lane_off + 64 * half;
+            ok = warp_wait(stall == BDLA_STALL_EPILOGUE ? &sm.never : &sm.s_full[0], 0u, &sm.wait_ns, abort_flag) &&
+                 warp_wait(&sm.dp_full, 0u, &sm.wait_ns, abort_flag);
+            uint32_t x[2][32], y[2][32];
+            float sum = 0.0f;
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    tmem_ld32(t_s + 32 * k, x[k]);
+                    tmem_ld32(t_dp + lane_off + 64 * half + 32 * k, y[k]);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int m = 0; m < 32; ++m) {
+                        const bool out = 64 * half + 32 * k + m > r;
+                        const float p = out ? 0.0f : ex2(fmaf(__uint_as_float(x[k][m]), c, -l2));
+                        x[k][m] = __float_as_uint(p);
+                        y[k][m] = out ? 0u : y[k][m];
+                        sum += p;
+                    }
+                sm.col[1][half][r] = sum;
+                if (valid < BT) {
+                    clear_rows(sm.ring[Smem::slot(0)], NP, valid, e, kEpi);
+                    fence_proxy_async_smem();
+                }
+            }
+            ok = epi_all(ok);
+            float own = 0.0f;
+            if (ok) {
+                sum = sm.col[1][0][r] + sm.col[1][1][r];
+                const float inv = 1.0f / sum;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int m = 0; m < 32; ++m) {
+                        const float w = __uint_as_float(x[k][m]);
+                        const float p = w == sum ? 1.0f : w * inv;   // exactly 1 for a lone key
+                        x[k][m] = __float_as_uint(p);
+                        own = fmaf(p, __uint_as_float(y[k][m]), own);
+                    }
+                sm.col[0][half][r] = own;
+            }
+            ok = epi_all(ok);
+            if (ok) {
+                own = sm.col[0][0][r] + sm.col[0][1][r];
+                if (half == 0 && r < valid)
+                    delta[(int64_t)h * tokens + t] = own;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = __uint_as_float(x[k][2 * i]) * (__uint_as_float(y[k][2 * i]) - own);
+                        const float b = __uint_as_float(x[k][2 * i + 1]) * (__uint_as_float(y[k][2 * i + 1]) - own);
+                        u[i] = pack_bf16(64 * half + 32 * k + 2 * i > r ? 0.0f : a,
+                                         64 * half + 32 * k + 2 * i + 1 > r ? 0.0f : b);
+                    }
+                    tmem_st16(t_s + 16 * k, u);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&sm.ready[0][k]);
+                }
+            }
+        }
+        for (int j = 0; j < n && n > 1; ++j) {
             const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
             const uint32_t t_s = tmem + BT * (j & 1) + lane_off + 64 * half;
             ok = warp_wait(hook ? &sm.never : &sm.s_full[j & 1], hook ? 0u : (uint32_t)((j >> 1) & 1), &sm.wait_ns, abort_flag);
@@ -350,14 +423,14 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 mbar_arrive(&sm.ready[j & 1][k]);
             }
         }
-        {
+        if (n > 1) {
             float a, b;
             unpair(sum2, a, b);
             sm.col[1][half][r] = a + b;
+            // every warp comes here, after its last tile or a wait that ran out
+            if (epi_all(ok) && half == 0 && r < valid)
+                delta[(int64_t)h * tokens + t] = sm.col[1][0][r] + sm.col[1][1][r];
         }
-        // every warp comes here, after its last tile or a wait that ran out
-        if (epi_all(ok) && half == 0 && r < valid)
-            delta[(int64_t)h * tokens + t] = sm.col[1][0][r] + sm.col[1][1][r];
         if (ok)
             ok = warp_wait(&sm.done, 0, &sm.wait_ns, abort_flag);
         if (ok && half < NP) {

@@ -157,6 +157,22 @@ def test_attn_gradient_against_differences():
         assert abs(float((got[i].double() * u).sum() - diff)) <= float((2 * tol[n][1] * u.abs()).sum()) + 1e-5 * abs(float(diff))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_first_tokens_have_no_score_gradient(d):
+    """A token that sees itself alone has ds = p (dp - delta) = 0: its dq, and the dk of a document of one token, are
+    zero to the bit, as the difference of equal numbers is."""
+    lens = (1, 1, 3, 1, 200, 1, 129)
+    q, k, v, dO, cu = _attn_inputs((1, sum(lens), lens, 6, 2, d, 2), seed=6)
+    o, lse = bdla.attn_fwd(q, k, v, cu_seqlens=cu)
+    dq, dk, dv = bdla.attn_bwd(q, k, v, o, lse, dO, cu_seqlens=cu)
+    at = 0
+    for n in lens:
+        assert float(dq[0, at].abs().max()) == 0.0
+        if n == 1:
+            assert float(dk[0, at].abs().max()) == 0.0
+        at += n
+
+
 def test_attn_rows_whose_maximum_keeps_growing():
     """Scores that rise along the keys, so that every tile raises the running maximum, up to far beyond e^88."""
     T, d = 700, 64
