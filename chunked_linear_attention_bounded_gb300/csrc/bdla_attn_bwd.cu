@@ -172,6 +172,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    next_may_start();
     if (blockIdx.x == 0 && cu != nullptr)
         check_offsets(cu, n_docs, tokens, st);
     // late (long) query tiles first
@@ -461,7 +462,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                const float *__restrict__ lse, const float *__restrict__ delta, const int32_t *__restrict__ cu,
+                const float *lse, const float *delta, const int32_t *__restrict__ cu,
                 int n_docs, int T, int64_t tokens, int Hk, int group, float scale, __nv_bfloat16 *__restrict__ dk,
                 __nv_bfloat16 *__restrict__ dv, float *__restrict__ part, DeviceStatus *st, uint64_t wait_ns, int stall)
 {
@@ -474,10 +475,11 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const int units = part != nullptr ? Hk * group : Hk, unit = blockIdx.x % units;
     const int kh = part != nullptr ? unit / group : unit, h0 = part != nullptr ? unit : kh * group;
     const SegSpan span = seg_span(cu, T, tokens, n_docs, (int)(blockIdx.x / units), 1);
-    if (!span.valid || span.len <= 0)
-        return;
-    if ((smem_u32(smem_raw) & 1023u) != 0u) {
-        if (tid == 0)
+    const bool aligned = (smem_u32(smem_raw) & 1023u) == 0u;
+    next_may_start();
+    if (!span.valid || span.len <= 0 || !aligned) {
+        wait_for_previous();
+        if (tid == 0 && !aligned)
             set_status(st, BDLA_ERR_DEVICE, 0xA11u);
         return;
     }
@@ -486,6 +488,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const int n = part != nullptr ? nq : nq * group;                 // of every head of the group in turn
     const int stall_at = n > 1 ? 1 : 0;
     setup(sm, tid, wait_ns);
+    wait_for_previous();   // delta; ahead of every bounded wait, none of which is to count the first kernel's time
     const uint32_t tmem = sm.tmem_base, t_dp = tmem + BT, t_dv = tmem + 2 * BT, t_dk = tmem + 3 * BT;
     volatile int *abort_flag = &sm.abort_flag;
 
@@ -737,9 +740,10 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 // dv and dk of a key head from the fp32 sums of its query heads, in their order;
 // four features a thread.
 __global__ void __launch_bounds__(256)
-dkv_join_kernel(const float *__restrict__ part, int64_t n4, int d4, int group, float scale, __nv_bfloat16 *__restrict__ dv,
+dkv_join_kernel(const float *part, int64_t n4, int d4, int group, float scale, __nv_bfloat16 *__restrict__ dv,
                 __nv_bfloat16 *__restrict__ dk)
 {
+    wait_for_previous();
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;   // float4 of [tokens][Hk][d]
     if (e >= n4)
         return;
@@ -779,14 +783,13 @@ cudaError_t go(const AttnProblem &p, const CUtensorMap &mq, const CUtensorMap &m
     err = cudaGetLastError();
     if (err != cudaSuccess)
         return err;
-    attn_dkv_kernel<D><<<(unsigned)(n_slots * (part ? p.Hq : p.Hk)), kThreads, smem, p.stream>>>(
-        mq, mk, mv, mdo, lse, delta, p.cu, p.n_docs, p.T, p.tokens, p.Hk, group, p.scale, dk, dv, part, p.st, ns, stall);
-    err = cudaGetLastError();
+    err = launch_second(attn_dkv_kernel<D>, (unsigned)(n_slots * (part ? p.Hq : p.Hk)), kThreads, smem, p.stream, mq, mk, mv,
+                        mdo, lse, delta, p.cu, p.n_docs, p.T, p.tokens, p.Hk, group, p.scale, dk, dv, part, p.st, ns, stall);
     if (err != cudaSuccess || part == nullptr)
         return err;
     const int64_t n4 = p.tokens * p.Hk * D / 4;
-    dkv_join_kernel<<<dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, p.stream>>>(part, n4, D / 4, group, p.scale, dv, dk);
-    return cudaGetLastError();
+    return launch_second(dkv_join_kernel, dim3((unsigned)((n4 + 255) / 256), 2), 256, 0, p.stream, part, n4, D / 4, group,
+                         p.scale, dv, dk);
 }
 
 }  // namespace

@@ -142,6 +142,31 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int n_docs, int
 }
 
 // One lane of a whole warp, the same one each time.
+// Two kernels of one call, the second of which reads what the first wrote: the
+// first says at its start that the second's CTAs may take the places that its own
+// last ones leave, and the second waits, before it reads and before any CTA ends,
+// until the first is done and its writes are there.  That takes the launch, and
+// the second's set-up, out of the time between them (a kernel boundary otherwise
+// costs 3 to 4 us).  What the second reads of the first is not `__restrict__`:
+// such loads could move above the wait.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;

@@ -1,7 +1,7 @@
 // The paged cache: writing rows into its pages, and attention of a sequence's
 // newest tokens over it.
+#include "bdla_attn_sm100.cuh"
 #include "bdla_cache.cuh"
-#include "bdla_sm100.cuh"
 
 namespace bdla {
 
@@ -155,6 +155,7 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     const int kh = idx % Hk;
     idx /= Hk;
     const int piece = idx % ns, b = idx / ns;
+    attn::next_may_start();
     const Cut cut = cut_of(c, b, T, a.pieces);
     if (piece >= cut.used)
         return;
@@ -402,6 +403,7 @@ combine_kernel(const __grid_constant__ Call a, int64_t rows)
     const bool any = at < rows;
     const int h = any ? (int)(at % Hq) : 0, i = any ? (int)(at / Hq % T) : 0, b = any ? (int)(at / Hq / T) : 0;
     Cut cut = cut_of(a.c, b, T, a.pieces);
+    attn::wait_for_previous();
     const bool live = any && cut.used > 1;   // one piece: finished by its own CTA
     if (W > 1 && !live)
         return;   // the whole CTA
@@ -556,11 +558,8 @@ static cudaError_t cached_go(const Call &a, const bdla_attn_dims &d, cudaStream_
 
 template <int D> static cudaError_t combine_go(const Call &a, int64_t rows, cudaStream_t stream)
 {
-    if (a.pieces.ns > 16)
-        combine_kernel<D, 16><<<(unsigned)rows, 512, 0, stream>>>(a, rows);
-    else
-        combine_kernel<D, 1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a, rows);
-    return cudaGetLastError();
+    return a.pieces.ns > 16 ? attn::launch_second(combine_kernel<D, 16>, (unsigned)rows, 512, 0, stream, a, rows)
+                            : attn::launch_second(combine_kernel<D, 1>, (unsigned)((rows + 3) / 4), 128, 0, stream, a, rows);
 }
 
 cudaError_t launch_attn_cached(const __nv_bfloat16 *q, const bdla_cache &c, const uint64_t *tree, float scale,

@@ -80,6 +80,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const int kh = idx % Hk;
     idx /= Hk;
     const int piece = idx % ns, b = idx / ns;
+    next_may_start();
     // softmax threads: tile, row of the tile, row of the key head, row of q, o and lse; their queries are asked for
     // before the lengths, which the rest waits for
     const int w = warp >= 8, q4 = warp & 3, r = 32 * q4 + lane;

@@ -353,6 +353,7 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
     __shared__ __align__(8) float red[G::kPerBlock][D];
     G g(p), ahead(p);
     const R ring(ring_smem, g.f0, g.f1);
+    attn::next_may_start();
     const int gi = threadIdx.x / G::kLanes;
     const int s = (int)blockIdx.x >= q_blocks;
     const int block = (int)blockIdx.x - (s ? q_blocks : 0), blocks = s ? (int)gridDim.x - q_blocks : q_blocks;
@@ -452,7 +453,7 @@ qk_norm_bwd_kernel(const __grid_constant__ NormParams p, const __grid_constant__
 // threads a column every 128th partial, then the threads in order: the same
 // sizes give the same bits.
 __global__ void __launch_bounds__(1024)
-norm_dw_kernel(const float *__restrict__ part, int q_blocks, int blocks, int D, float *__restrict__ dwq,
+norm_dw_kernel(const float *part, int q_blocks, int blocks, int D, float *__restrict__ dwq,
                float *__restrict__ dwk)
 {
     __shared__ float red[128][9];
@@ -460,6 +461,7 @@ norm_dw_kernel(const float *__restrict__ part, int q_blocks, int blocks, int D, 
     const int s = (int)blockIdx.x >= per, c = ((int)blockIdx.x - s * per) * 8 + x;
     const int first = s ? q_blocks : 0, last = s ? blocks : q_blocks;
     float v = 0.0f;
+    attn::wait_for_previous();
 #pragma unroll 4
     for (int i = first + y; i < last; i += 128)
         v += part[(size_t)i * D + c];
@@ -629,8 +631,7 @@ cudaError_t launch_qk_norm_bwd(const bdla_qk_norm_args &a, const void *dqn, cons
         if (err != cudaSuccess)
             return err;
     }
-    norm_dw_kernel<<<2 * d.d / 8, 1024, 0, stream>>>(part, q_blocks, blocks, d.d, dwq, dwk);
-    return cudaGetLastError();
+    return attn::launch_second(norm_dw_kernel, 2 * d.d / 8, 1024, 0, stream, part, q_blocks, blocks, d.d, dwq, dwk);
 }
 
 }  // namespace bdla
