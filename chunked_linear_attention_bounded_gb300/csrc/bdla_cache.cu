@@ -25,7 +25,8 @@ __device__ __forceinline__ int64_t cache_row(const bdla_cache &c, const int32_t 
 constexpr int kAppendThreads = 256;
 
 // One warp writes one row of keys and values: Hk * d features, read and
-// written once, 16 bytes a lane, four loads of each in flight.
+// written once, 16 bytes a lane, four loads of each in flight.  Bound by HBM:
+// the accepted of 5 x 4093 rows of 8 heads of 128, 20 us (5.0 TB/s).
 __global__ void __launch_bounds__(kAppendThreads)
 cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, const __grid_constant__ bdla_cache c,
                     const int32_t *__restrict__ rows, const int32_t *__restrict__ counts, int T, int64_t total,
@@ -84,10 +85,11 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 // a position, so they run as warp MMAs (m16n8k16, 16 or 32 rows) straight from
 // the tiles that cp.async brings in.  Keys and values of 64 positions have two
 // buffers each, and a buffer is filled again as soon as its own product is done:
-// 64 KB a CTA, three CTAs an SM (three whole tiles a CTA, two CTAs an SM: 736 us
-// for 256 ragged sequences against 669).  A
-// CTA's four warps split the rows first and the positions of the tile with what
-// is left, and join through shared memory at the end.  Warp MMAs run at an
+// 64 KB a CTA, three CTAs an SM.  256 ragged sequences, 677 us (6.3 TB/s; three
+// whole tiles a CTA, two CTAs an SM: 736); one of 262144 positions, with the
+// join, 170 us (6.3 TB/s).  A CTA's four warps split the rows first and the
+// positions of the tile with what is left, and join through shared memory at the
+// end.  Warp MMAs run at an
 // eighth of the tensor cores' rate here: with 64 rows they took longer than the
 // keys' way from HBM (244 rows a key head: 100 us for 96 MB), so more rows go to
 // the tensor-memory kernel of bdla_cache_wide.cu.
@@ -127,12 +129,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+using attn::ex2;
 
 template <int D, int WR>
 __global__ void __launch_bounds__(kCThreads, D == 128 ? 3 : 4)
@@ -498,10 +495,10 @@ static int cached_rows(const bdla_attn_dims &d)
 
 // Pieces of a sequence.  Few sequences: as many pieces as fill the SMs once, or
 // two or three times where they stay over 1024 positions (one sequence of
-// 262144 positions: 176 us in 3 rounds, 180 in 2.7), of at least 128.  Many: pieces of about 2048 positions, so that long
-// and short sequences end together, and of at least 1024, so that a CTA's
-// start-up (length, page table, first tile) stays small beside its keys.  The
-// wide kernel holds an SM alone: as many pieces as fill the SMs a whole number
+// 262144 positions: 176 us in 3 rounds, 180 in 2.7), of at least 128.  Many:
+// pieces of about 2048 positions, so that long and short sequences end together,
+// and of at least 1024, so that a CTA's start-up (length, page table, first tile)
+// stays small beside its keys.  The wide kernel holds an SM alone: as many pieces as fill the SMs a whole number
 // of times, with at most 8192 positions (160 CTAs for 152 SMs cost a second
 // round: 4 x 65536 positions, 186 us).  No more than 256 MB of partial sums, or
 // a grid of 2^17 CTAs (more only where the sequences alone are more).
