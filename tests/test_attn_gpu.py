@@ -72,6 +72,35 @@ def test_norm_and_gradient(case):
         assert all(torch.equal(x, y) for x, y in zip((dq, dk, dwq, dwk), again))
 
 
+# more tokens than the gradient's lanes hold at a time, so that each walks several; heads that leave a turn half empty
+@pytest.mark.parametrize("case", [(1, 130000, (70001, 59999), 1, 1, 64, 32, True, 0), (2, 30011, None, 3, 3, 128, 128, False, 0)],
+                         ids=lambda c: "-".join(str(x) for x in c))
+def test_norm_gradient_of_many_tokens(case):
+    test_norm_and_gradient(case)
+
+
+def test_norm_gradient_on_another_stream_and_in_a_graph():
+    g = _gen(12)
+    q, k, dqn, dkn = _rn(g, 1, 5000, 4, 64), _rn(g, 1, 5000, 2, 64), _rn(g, 1, 5000, 4, 64), _rn(g, 1, 5000, 2, 64)
+    w = 1 + 0.3 * torch.randn(64, generator=g, device="cuda")
+    want = bdla.qk_norm_bwd(q, k, w, w, dqn, dkn)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = bdla.qk_norm_bwd(q, k, w, w, dqn, dkn, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    ws = bdla.Workspace(1 << 22, "cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bdla.qk_norm_bwd(q, k, w, w, dqn, dkn, ws=ws)
+    for x in got:
+        x.fill_(7)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_norm_of_no_tokens():
     q = torch.empty((1, 0, 4, 64), dtype=BF16, device="cuda")
     w = torch.ones(64, device="cuda")
