@@ -629,8 +629,8 @@ def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call)
     st = ERR_WORKSPACE if ws is None else call(ws.buf.data_ptr(), ws.nbytes)
     if st == ERR_WORKSPACE:
         need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
-        if need == 0:
-            raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_attn")
+        if need == 0:   # sizes that the call refuses, before it looks at the workspace or launches: with which status
+            raise BdlaError(call(None, 0), where)
         if stream is None:
             ws = Workspace(need, device) if ws is None else ws.ensure(need)
         else:

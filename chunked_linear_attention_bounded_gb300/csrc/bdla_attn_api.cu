@@ -137,7 +137,7 @@ size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t m
     case BDLA_ATTN_NORM_BWD:
         return head + round_up((size_t)norm_bwd_blocks(d) * d.d * sizeof(float));
     case BDLA_ATTN_CACHED:
-        if (max_keys < 0 || d.T > 64)
+        if (max_keys < 0 || d.T < 1 || d.T > 64)   // the sizes bdla_attn_cached refuses: no rows to cut pieces for
             return 0;
         return head + round_up(cached_partial_bytes(d, cached_splits(d, max_keys)));
     }

@@ -1,0 +1,47 @@
+"""The smallest and oddest arguments of the softmax layer's entry points, as far as they need no GPU."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from chunked_linear_attention_bounded_gb300 import bdla
+from chunked_linear_attention_bounded_gb300.build import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def L():
+    build()
+    return bdla.lib()
+
+
+def test_workspace_of_no_new_tokens_is_an_answer(L):
+    """0 bytes, as for all sizes that the call refuses, and not the end of the process (a child, so that such an end
+    would fail this test alone); the other operators take no tokens."""
+    code = ("from chunked_linear_attention_bounded_gb300 import bdla\n"
+            "size = bdla.lib().bdla_workspace_bytes_attn\n"
+            "print([size(op, bdla.AttnDims(B, 0, 8, 2, d), 0, keys) for op in range(5) for B in (1, 2) for d in (64, 128)"
+            " for keys in (0, 1024)])")
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert run.returncode == 0, (run.returncode, run.stderr)
+    sizes = eval(run.stdout)
+    assert all(n >= 256 for n in sizes[:32]) and sizes[32:] == [0] * 8
+
+
+def test_refused_sizes_raise_what_the_call_says(L):
+    """Where the workspace query has no answer the call is asked, without a workspace: it refuses before a launch."""
+    asked = []
+
+    def call(p, n):
+        asked.append((p, n))
+        return bdla.ERR_SHAPE
+
+    with pytest.raises(bdla.BdlaError) as e:
+        bdla._with_ws("bdla_attn_cached", bdla.ATTN_CACHED, bdla.AttnDims(2, 0, 8, 2, 128), 0, 1024, None, "cpu", None, call)
+    assert e.value.status == bdla.ERR_SHAPE and asked == [(None, 0)]
+    cache = bdla.CacheArgs(1 << 20, 1 << 20, 1 << 20, 1 << 20, 4, 16, 2)
+    for T, status in ((0, bdla.ERR_SHAPE), (65, bdla.ERR_UNSUPPORTED)):
+        assert L.bdla_attn_cached(1 << 20, cache, None, 0.1, 1 << 20, 1 << 20, bdla.AttnDims(2, T, 8, 2, 128), None, 0,
+                                  None) == status
