@@ -664,11 +664,18 @@ def _strided(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16 or t.dim() != 4:
         raise ValueError(f"{name} must be bf16 [B, T, H, d]")
-    B, T, H, d = t.shape
-    sb, st, sh, sd = t.stride()
+    return _token_strides(t.shape, t.stride(), name)
+
+
+def _token_strides(shape, strides, name: str):
+    """The strides that tell two tokens, or two heads, apart; where there are no two, what torch holds means nothing."""
+    B, T, H, d = shape
+    sb, st, sh, sd = strides
     if d > 1 and sd != 1:
         raise ValueError(f"{name}: features must be contiguous")
-    if T == 1:
+    if B * T <= 1:
+        st = H * d
+    elif T == 1:
         st = sb   # one token a row: the batch stride steps from token to token
     elif B > 1 and sb != T * st:
         raise ValueError(f"{name}: batch rows must follow each other (batch stride = T * token stride)")

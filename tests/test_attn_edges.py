@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from chunked_linear_attention_bounded_gb300 import bdla
 from chunked_linear_attention_bounded_gb300.build import build
@@ -45,3 +46,21 @@ def test_refused_sizes_raise_what_the_call_says(L):
     for T, status in ((0, bdla.ERR_SHAPE), (65, bdla.ERR_UNSUPPORTED)):
         assert L.bdla_attn_cached(1 << 20, cache, None, 0.1, 1 << 20, 1 << 20, bdla.AttnDims(2, T, 8, 2, 128), None, 0,
                                   None) == status
+
+
+def test_strides_of_a_projections_views():
+    """Token and head strides of [B, T, H, d]; a stride along an axis without a second entry says nothing."""
+    f = lambda shape, strides: bdla._token_strides(shape, strides, "q")
+    assert f((2, 5, 3, 64), (5 * 448, 448, 64, 1)) == (448, 64)
+    assert f((3, 1, 3, 64), (448, 7, 64, 1)) == (448, 64)        # one token a row
+    assert f((2, 5, 1, 64), (5 * 448, 448, 3, 1)) == (448, 64)   # one head
+    assert f((1, 5, 2, 64), (9, 448, 64, 1)) == (448, 64)        # one row
+    assert f((1, 1, 2, 64), (9, 5, 64, 1)) == (128, 64)          # one token
+    for B in (1, 2):                                             # no token: torch's own strides, and others
+        empty = torch.empty((B, 0, 4, 64))
+        assert f(tuple(empty.shape), empty.stride()) == (256, 64)
+        assert f((B, 0, 4, 64), (3, 5, 64, 1)) == (256, 64)
+    with pytest.raises(ValueError, match="batch rows"):
+        f((2, 5, 3, 64), (6 * 448, 448, 64, 1))
+    with pytest.raises(ValueError, match="features"):
+        f((2, 5, 3, 64), (5 * 448, 448, 1, 64))
