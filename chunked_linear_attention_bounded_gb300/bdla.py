@@ -8,6 +8,7 @@ fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -237,16 +238,33 @@ def n_slots(tokens: int, n_docs: int, stride: int) -> int:
     return (tokens + stride - 1) // stride + n_docs
 
 
+def _scope(stream):
+    """Allocations made in it belong to `stream` (None: the current stream)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class Workspace:
-    """Caller-owned device scratch for the library (status word first)."""
+    """Caller-owned device scratch for the library (status word first).  A call
+    that needs more grows it on the call's stream, and what the device has
+    recorded stays to be read.  Growing inside a graph's capture puts the new
+    buffer, and the clearing of its record, into the graph: size it before."""
 
     def __init__(self, nbytes: int, device):
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        self.held = []   # outgrown buffers whose record is read where it is
 
-    def ensure(self, nbytes: int):
+    def ensure(self, nbytes: int, stream=None):
         if nbytes > self.nbytes:
-            self.__init__(nbytes, self.buf.device)
+            with _scope(stream):
+                old, buf = self.buf, torch.zeros(int(nbytes), dtype=torch.uint8, device=self.buf.device)
+                if torch.cuda.is_current_stream_capturing():
+                    self.held.append(old)   # a captured copy would bring the old record back at every replay
+                else:
+                    buf[:256] = old[:256]
+                    if old.is_cuda:
+                        old.record_stream(torch.cuda.current_stream(old.device))
+            self.buf, self.nbytes = buf, int(nbytes)
         return self
 
     @property
@@ -254,7 +272,19 @@ class Workspace:
         return ctypes.c_void_p(self.buf.data_ptr())
 
     def read_device_status(self, stream=None) -> int:
-        return int(lib().bdla_read_device_status(self.ptr, _stream_handle(stream)))
+        """An error that the device has recorded since the last read (the first of each buffer is kept), OK if none;
+        waits for `stream`."""
+        handle = _stream_handle(stream)
+        read = [int(lib().bdla_read_device_status(ctypes.c_void_p(b.data_ptr()), handle)) for b in (*self.held, self.buf)]
+        return next((st for st in read if st != OK), OK)
+
+
+def _workspace(need: int, device, ws: Optional[Workspace], stream) -> Workspace:
+    """The caller's workspace, grown to `need` bytes, or a new one, made on the call's stream."""
+    if ws is not None:
+        return ws.ensure(need, stream)
+    with _scope(stream):
+        return Workspace(need, device)
 
 
 def workspace_bytes(op: int, q_shape, dv: int, n_docs: int = 0, mode: int = BOUNDED,
@@ -263,13 +293,11 @@ def workspace_bytes(op: int, q_shape, dv: int, n_docs: int = 0, mode: int = BOUN
     return int(lib().bdla_workspace_bytes(op, Dims(B, T, H, dk, dv), n_docs, mode, ckpt_stride))
 
 
-def _ws_for(op, q, v, n_docs, mode, ckpt_stride, ws: Optional[Workspace]) -> Workspace:
+def _ws_for(op, q, v, n_docs, mode, ckpt_stride, ws: Optional[Workspace], stream) -> Workspace:
     need = workspace_bytes(op, tuple(q.shape), v.shape[-1], n_docs, mode, ckpt_stride)
     if need == 0:
         raise BdlaError(ERR_SHAPE, "bdla_workspace_bytes")
-    if ws is None:
-        return Workspace(need, q.device)
-    return ws.ensure(need)
+    return _workspace(need, q.device, ws, stream)
 
 
 def decay(a: torch.Tensor, b: float = -5.0, cu_seqlens: Optional[torch.Tensor] = None,
@@ -283,7 +311,7 @@ def decay(a: torch.Tensor, b: float = -5.0, cu_seqlens: Optional[torch.Tensor] =
     if cu_seqlens is not None:
         _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
         n_docs = cu_seqlens.numel() - 1
-    ws = ws or Workspace(256, a.device)
+    ws = _workspace(256, a.device, ws, stream)
     st = lib().bdla_decay(_p(a), b, CHUNK, _p(cu_seqlens), n_docs, _p(gamma),
                           Dims(B, T, H, 64, 64), mode, ws.ptr, ws.nbytes, _stream_handle(stream))
     if st:
@@ -354,7 +382,7 @@ def fwd(q, k, v, a, b: float = -5.0, h0=None, cu_seqlens=None, mode: int = BOUND
     if ckpt is None and ckpt_stride:
         ckpt = torch.empty((H, n_slots(B * T, n_seq, ckpt_stride), dk, dv), dtype=ckpt_dtype,
                            device=dev)
-    ws = _ws_for(OP_FWD, q, v, n_docs, mode, 0, ws)
+    ws = _ws_for(OP_FWD, q, v, n_docs, mode, 0, ws, stream)
     odt = 1 if o.dtype == torch.float32 else 0
     ckdt = _dtype_code(ckpt.dtype) if ckpt is not None else 1
     args_tail = (_p(h0), _p(o), odt, _p(hT), _p(ckpt), int(ckpt_stride), ckdt, _dims(q, v), mode,
@@ -408,7 +436,7 @@ def bwd(q, k, v, a, dO, b: float = -5.0, h0=None, dhT=None, cu_seqlens=None, ckp
     dh0 = torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
     stride = int(ckpt_stride) if ckpt is not None else 0
     ws_stride = stride if (ckdt == 1 or dv <= 128) else 0
-    ws = _ws_for(OP_BWD, q, v, n_docs, mode, ws_stride, ws)
+    ws = _ws_for(OP_BWD, q, v, n_docs, mode, ws_stride, ws, stream)
     args_tail = (_p(h0), _p(dO), _p(dhT), _p(ckpt), stride, ckdt, _p(dq), _p(dkk), _p(dvv), _p(da),
                  _p(dh0), _dims(q, v), mode, ws.ptr, ws.nbytes, _stream_handle(stream))
     L = lib()
@@ -444,14 +472,12 @@ def _vec_checks(q, k, v, a, cu_seqlens, h0):
     return B, T, H, dk, dv, n_docs, n_seq
 
 
-def _ws_vec(op, q, v, n_docs, ws):
+def _ws_vec(op, q, v, n_docs, ws, stream):
     B, T, H, dk = q.shape
     need = int(lib().bdla_workspace_bytes_vec(op, Dims(B, T, H, dk, v.shape[-1]), n_docs))
     if need == 0:
         raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_vec")
-    if ws is None:
-        return Workspace(need, q.device)
-    return ws.ensure(need)
+    return _workspace(need, q.device, ws, stream)
 
 
 def tile_states(q, v, cu_seqlens=None):
@@ -475,7 +501,7 @@ def fwd_vec(q, k, v, a, b: float = -5.0, h0=None, cu_seqlens=None, mode: int = B
     B, T, H, dk, dv, n_docs, n_seq = _vec_checks(q, k, v, a, cu_seqlens, h0)
     o = torch.empty((B, T, H, dv), dtype=o_dtype, device=q.device)
     hT = torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=q.device)
-    ws = _ws_vec(OP_FWD, q, v, n_docs, ws)
+    ws = _ws_vec(OP_FWD, q, v, n_docs, ws, stream)
     st = lib().bdla_fwd_vec(_p(q), _p(k), _p(v), _p(a), b, CHUNK, _p(cu_seqlens), n_docs, _p(h0), _p(o),
                             _dtype_code(o.dtype), _p(hT), _p(states_out), _dims(q, v), mode, ws.ptr, ws.nbytes,
                             _stream_handle(stream))
@@ -502,7 +528,7 @@ def bwd_vec(q, k, v, a, dO, b: float = -5.0, h0=None, dhT=None, cu_seqlens=None,
                 torch.empty(a.shape, dtype=torch.float32, device=dev))
     dq, dk_, dv_, da = outs
     dh0 = torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
-    ws = _ws_vec(OP_BWD, q, v, n_docs, ws)
+    ws = _ws_vec(OP_BWD, q, v, n_docs, ws, stream)
     st = lib().bdla_bwd_vec(_p(q), _p(k), _p(v), _p(a), b, CHUNK, _p(cu_seqlens), n_docs, _p(h0), _p(dO),
                             _p(dhT), _p(states), _p(dq), _p(dk_), _p(dv_), _p(da), _p(dh0), _dims(q, v), mode,
                             ws.ptr, ws.nbytes, _stream_handle(stream))
@@ -534,14 +560,12 @@ def _delta_checks(q, k, v, a, beta, cu_seqlens, h0):
     return B, T, H, dk, dv, n_docs, n_seq
 
 
-def _ws_delta(op, q, v, n_docs, ws):
+def _ws_delta(op, q, v, n_docs, ws, stream):
     B, T, H, dk = q.shape
     need = int(lib().bdla_workspace_bytes_delta(op, Dims(B, T, H, dk, v.shape[-1]), n_docs))
     if need == 0:
         raise BdlaError(ERR_UNSUPPORTED, "bdla_workspace_bytes_delta")
-    if ws is None:
-        return Workspace(need, q.device)
-    return ws.ensure(need)
+    return _workspace(need, q.device, ws, stream)
 
 
 def fwd_delta(q, k, v, a, beta, b: float = -5.0, h0=None, cu_seqlens=None, mode: int = BOUNDED,
@@ -553,7 +577,7 @@ def fwd_delta(q, k, v, a, beta, b: float = -5.0, h0=None, cu_seqlens=None, mode:
     B, T, H, dk, dv, n_docs, n_seq = _delta_checks(q, k, v, a, beta, cu_seqlens, h0)
     o = out if out is not None else torch.empty((B, T, H, dv), dtype=o_dtype, device=q.device)
     hT = hT_out if hT_out is not None else torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=q.device)
-    ws = _ws_delta(OP_FWD, q, v, n_docs, ws)
+    ws = _ws_delta(OP_FWD, q, v, n_docs, ws, stream)
     st = lib().bdla_fwd_delta(_p(q), _p(k), _p(v), _p(a), _p(beta), b, CHUNK, _p(cu_seqlens), n_docs, _p(h0),
                               _p(o), _dtype_code(o.dtype), _p(hT), _p(states_out), _dims(q, v), mode, ws.ptr,
                               ws.nbytes, _stream_handle(stream))
@@ -581,7 +605,7 @@ def bwd_delta(q, k, v, a, beta, dO, b: float = -5.0, h0=None, dhT=None, cu_seqle
                 torch.empty(beta.shape, dtype=torch.float32, device=dev))
     dq, dk_, dv_, da, dbeta = outs
     dh0 = torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
-    ws = _ws_delta(OP_BWD, q, v, n_docs, ws)
+    ws = _ws_delta(OP_BWD, q, v, n_docs, ws, stream)
     st = lib().bdla_bwd_delta(_p(q), _p(k), _p(v), _p(a), _p(beta), b, CHUNK, _p(cu_seqlens), n_docs, _p(h0),
                               _p(dO), _p(dhT), _p(states), _p(dq), _p(dk_), _p(dv_), _p(da), _p(dbeta), _p(dh0),
                               _dims(q, v), mode, ws.ptr, ws.nbytes, _stream_handle(stream))
@@ -631,11 +655,7 @@ def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call)
         need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
         if need == 0:   # sizes that the call refuses, before it looks at the workspace or launches: with which status
             raise BdlaError(call(None, 0), where)
-        if stream is None:
-            ws = Workspace(need, device) if ws is None else ws.ensure(need)
-        else:
-            with torch.cuda.stream(stream):
-                ws = Workspace(need, device) if ws is None else ws.ensure(need)
+        ws = _workspace(need, device, ws, stream)
         st = call(ws.buf.data_ptr(), ws.nbytes)
     if st:
         raise BdlaError(st, where)

@@ -64,3 +64,30 @@ def test_strides_of_a_projections_views():
         f((2, 5, 3, 64), (6 * 448, 448, 64, 1))
     with pytest.raises(ValueError, match="features"):
         f((2, 5, 3, 64), (5 * 448, 448, 1, 64))
+
+
+def test_a_workspace_keeps_its_record_as_it_grows(monkeypatch):
+    """The status word survives growth (on any device), the scratch behind it starts at zero."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    ws = bdla.Workspace(256, "cpu")
+    ws.buf[:256] = torch.arange(256, dtype=torch.uint8)
+    assert ws.ensure(200) is ws and ws.nbytes == 256
+    ws.ensure(5000)
+    assert ws.nbytes == ws.buf.numel() == 5000 and not ws.held
+    assert torch.equal(ws.buf[:256], torch.arange(256, dtype=torch.uint8)) and not bool(ws.buf[256:].any())
+
+
+def test_growing_in_a_capture_leaves_the_record_where_it_is(monkeypatch):
+    """Nothing is copied, which the graph would repeat; the outgrown record is still read, and first."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    ws = bdla.Workspace(256, "cpu")
+    first = ws.buf
+    first[0] = 10
+    ws.ensure(1000)
+    assert not bool(ws.buf.any()) and ws.held == [first]
+    asked = []
+    monkeypatch.setattr(bdla, "_stream_handle", lambda s: None)
+    monkeypatch.setattr(bdla, "lib", lambda: type("L", (), {
+        "bdla_read_device_status": staticmethod(lambda p, s: asked.append(p.value) or (10 if p.value == first.data_ptr() else 0))}))
+    assert ws.read_device_status() == bdla.ERR_DEVICE
+    assert asked == [first.data_ptr(), ws.buf.data_ptr()]

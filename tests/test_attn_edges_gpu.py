@@ -39,3 +39,50 @@ def test_norm_of_one_token_whatever_its_token_stride_says():
     got = bdla.qk_norm(q, k, w, w)
     want = bdla.qk_norm(q.clone(memory_format=torch.contiguous_format), k.clone(memory_format=torch.contiguous_format), w, w)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def _cache(page=16, pages=4, Hk=2, d=64):
+    kc = torch.randn((pages, page, Hk, d), generator=torch.Generator("cuda").manual_seed(2), device="cuda").to(BF16)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    return kc, kc.clone(), table, torch.tensor([pages * page - 8], dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("on_side_stream", [False, True])
+def test_an_error_recorded_before_the_workspace_grows_is_still_read(on_side_stream):
+    """A bad page seen by an append, then attention that needs partial sums in the same workspace."""
+    kc, vc, table, lens = _cache(pages=400)
+    stream = torch.cuda.Stream() if on_side_stream else None
+    k, q = torch.zeros((1, 1, 2, 64), dtype=BF16, device="cuda"), torch.zeros((1, 1, 4, 64), dtype=BF16, device="cuda")
+    bad = table.clone()
+    bad[0, -1] = 400
+    ws = bdla.Workspace(256, "cuda")
+    torch.cuda.synchronize()
+    bdla.cache_append(k, k, kc, vc, bad, lens, ws=ws, stream=stream)
+    assert ws.nbytes == 256
+    bdla.attn_cached(q, kc, vc, table, lens, ws=ws, stream=stream)
+    assert ws.nbytes > 256   # it grew
+    assert ws.read_device_status(stream) == bdla.ERR_DEVICE
+    assert ws.read_device_status(stream) == bdla.OK
+
+
+def test_a_workspace_grows_on_the_stream_of_the_call():
+    """A call on an idle stream while the current one is busy: were the new buffer cleared on the busy one, the clearing
+    would come after the call and take what it recorded with it.  Linear attention and softmax attention."""
+    g = torch.Generator("cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    q, k, v, a = rn(1, 300, 2, 64).to(BF16), rn(1, 300, 2, 64).to(BF16), rn(1, 300, 2, 64).to(BF16), rn(1, 300, 2)
+    bad = torch.tensor([0, 200, 100, 300], dtype=torch.int32, device="cuda")   # reported, and left out
+    o, lse = torch.zeros_like(q), torch.zeros((2, 300), device="cuda")
+    busy = torch.ones((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    for call in (lambda ws: bdla.fwd(q, k, v, a, cu_seqlens=bad, ws=ws, stream=side),
+                 lambda ws: bdla.attn_bwd(q, k, v, o, lse, q, cu_seqlens=bad, ws=ws, stream=side)):
+        ws = bdla.Workspace(256, "cuda")
+        torch.cuda.synchronize()
+        for _ in range(20):
+            torch.mm(busy, busy)
+        kept = call(ws)   # its outputs live until everything is done
+        assert ws.nbytes > 256
+        torch.cuda.synchronize()
+        assert ws.read_device_status(side) == bdla.ERR_DEVICE
+        del kept
