@@ -252,20 +252,29 @@ class Workspace:
     def __init__(self, nbytes: int, device):
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
-        self.held = []   # outgrown buffers whose record is read where it is
+        self.in_graph = False   # a graph may hold the present buffer
+        self.held = []          # outgrown buffers that one may hold; their records are read where they are
 
     def ensure(self, nbytes: int, stream=None):
         if nbytes > self.nbytes:
             with _scope(stream):
                 old, buf = self.buf, torch.zeros(int(nbytes), dtype=torch.uint8, device=self.buf.device)
-                if torch.cuda.is_current_stream_capturing():
-                    self.held.append(old)   # a captured copy would bring the old record back at every replay
+                if self.in_graph or torch.cuda.is_current_stream_capturing():
+                    self.held.append(old)   # (and a captured copy would bring the old record back at every replay)
                 else:
                     buf[:256] = old[:256]
                     if old.is_cuda:
                         old.record_stream(torch.cuda.current_stream(old.device))
             self.buf, self.nbytes = buf, int(nbytes)
         return self
+
+    def note_capture(self, stream=None):
+        """To be told of every call that takes the buffer, before it is launched."""
+        if not self.in_graph:
+            self.in_graph = torch.cuda.is_current_stream_capturing()
+            if stream is not None and not self.in_graph:
+                with torch.cuda.stream(stream):
+                    self.in_graph = torch.cuda.is_current_stream_capturing()
 
     @property
     def ptr(self):
@@ -282,6 +291,7 @@ class Workspace:
 def _workspace(need: int, device, ws: Optional[Workspace], stream) -> Workspace:
     """The caller's workspace, grown to `need` bytes, or a new one, made on the call's stream."""
     if ws is not None:
+        ws.note_capture(stream)
         return ws.ensure(need, stream)
     with _scope(stream):
         return Workspace(need, device)
@@ -650,7 +660,10 @@ def _new(device, stream, *outs):
 def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call):
     """Makes the call with the caller's workspace; one that is missing or too
     small is made or grown first, as the library's answer says."""
-    st = ERR_WORKSPACE if ws is None else call(ws.buf.data_ptr(), ws.nbytes)
+    st = ERR_WORKSPACE
+    if ws is not None:
+        ws.note_capture(stream)
+        st = call(ws.buf.data_ptr(), ws.nbytes)
     if st == ERR_WORKSPACE:
         need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
         if need == 0:   # sizes that the call refuses, before it looks at the workspace or launches: with which status

@@ -91,3 +91,26 @@ def test_growing_in_a_capture_leaves_the_record_where_it_is(monkeypatch):
         "bdla_read_device_status": staticmethod(lambda p, s: asked.append(p.value) or (10 if p.value == first.data_ptr() else 0))}))
     assert ws.read_device_status() == bdla.ERR_DEVICE
     assert asked == [first.data_ptr(), ws.buf.data_ptr()]
+
+
+def test_buffers_that_a_graph_may_hold_outlive_growth(monkeypatch):
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    ws = bdla.Workspace(300, "cpu")
+    first = ws.buf
+    calls = []
+
+    def call(p, n):
+        calls.append(n)
+        return bdla.OK if n >= 300 else bdla.ERR_WORKSPACE
+
+    bdla._with_ws("x", bdla.ATTN_FWD, bdla.AttnDims(1, 4, 4, 2, 64), 0, 0, ws, torch.device("cpu"), None, call)   # captured
+    assert calls == [300] and ws.in_graph
+    capturing[0] = False
+    second = ws.ensure(1000).buf       # grown outside, twice
+    ws.ensure(2000)
+    assert [b.data_ptr() for b in ws.held] == [first.data_ptr(), second.data_ptr()]
+    ws = bdla.Workspace(300, "cpu")    # no capture: the old buffers go
+    bdla._with_ws("x", bdla.ATTN_FWD, bdla.AttnDims(1, 4, 4, 2, 64), 0, 0, ws, torch.device("cpu"), None, call)
+    ws.ensure(1000)
+    assert not ws.in_graph and not ws.held

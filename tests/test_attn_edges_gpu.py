@@ -86,3 +86,31 @@ def test_a_workspace_grows_on_the_stream_of_the_call():
         torch.cuda.synchronize()
         assert ws.read_device_status(side) == bdla.ERR_DEVICE
         del kept
+
+
+def test_a_graph_replays_on_its_buffer_after_the_workspace_has_grown():
+    """A decode step captured with a workspace that a larger call outgrows later: the replay's partial sums and record
+    go to the buffer that the graph knows, which nothing else has been given meanwhile."""
+    kc, vc, table, lens = _cache(pages=400)
+    q = torch.randn((1, 1, 4, 64), generator=torch.Generator("cuda").manual_seed(5), device="cuda").to(BF16)
+    want = bdla.attn_cached(q, kc, vc, table, lens)
+    need = bdla.lib().bdla_workspace_bytes_attn(bdla.ATTN_CACHED, bdla.AttnDims(1, 1, 4, 2, 64), 0, 6400)
+    ws = bdla.Workspace(need, "cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = bdla.attn_cached(q, kc, vc, table, lens, ws=ws)
+    assert ws.nbytes == need
+    ws.ensure(4 * need)
+    others = [torch.full((need,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]   # whoever asks for such a size
+    for x in got:
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert all(bool((x == 7).all()) for x in others)
+    assert ws.read_device_status() == bdla.OK
+    table[0, 0] = 400
+    graph.replay()
+    assert ws.read_device_status() == bdla.ERR_DEVICE   # the replay's own record
+    assert ws.read_device_status() == bdla.OK
