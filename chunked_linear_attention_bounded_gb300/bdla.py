@@ -215,11 +215,23 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _check(t: torch.Tensor, name: str, dtype, ndim: int):
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t, name: str):
+    """The library launches on the current device, whose streams and sizes it takes."""
+    if t.device.index != _current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}: "
+                         f"make the call within torch.cuda.device({t.device.index})")
+
+
+def _check(t: torch.Tensor, name: str, dtype, ndim: int, here: bool = True):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if here:
+        _here(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
@@ -268,8 +280,10 @@ class Workspace:
             self.buf, self.nbytes = buf, int(nbytes)
         return self
 
-    def note_capture(self, stream=None):
+    def note_call(self, device, stream=None):
         """To be told of every call that takes the buffer, before it is launched."""
+        if self.buf.device != device:
+            raise ValueError(f"ws is on {self.buf.device}, expected {device}")
         if not self.in_graph:
             self.in_graph = torch.cuda.is_current_stream_capturing()
             if stream is not None and not self.in_graph:
@@ -291,7 +305,7 @@ class Workspace:
 def _workspace(need: int, device, ws: Optional[Workspace], stream) -> Workspace:
     """The caller's workspace, grown to `need` bytes, or a new one, made on the call's stream."""
     if ws is not None:
-        ws.note_capture(stream)
+        ws.note_call(device, stream)
         return ws.ensure(need, stream)
     with _scope(stream):
         return Workspace(need, device)
@@ -643,7 +657,7 @@ def _on(t, name: str, dtype, shape, device):
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
             and t.is_contiguous():
         return t.data_ptr()
-    _check(t, name, dtype, len(shape))
+    _check(t, name, dtype, len(shape), here=False)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -662,7 +676,7 @@ def _with_ws(where, op, d: AttnDims, n_docs, max_keys, ws, device, stream, call)
     small is made or grown first, as the library's answer says."""
     st = ERR_WORKSPACE
     if ws is not None:
-        ws.note_capture(stream)
+        ws.note_call(device, stream)
         st = call(ws.buf.data_ptr(), ws.nbytes)
     if st == ERR_WORKSPACE:
         need = int(lib().bdla_workspace_bytes_attn(op, d, n_docs, max_keys))
@@ -725,6 +739,7 @@ def _norm_args(q, k, wq, wk, rotary, base, interleaved, positions, cu_seqlens, e
     device = q.device
     if k.device != device:
         raise ValueError("q and k are on different devices")
+    _here(q, "q")
     cu, n_docs = _documents(cu_seqlens, B, device)
     a = QkNormArgs(q.data_ptr(), k.data_ptr(), qt, qh, kt, kh, _on(wq, "wq", torch.float32, (d,), device),
                    _on(wk, "wk", torch.float32, (d,), device),
@@ -770,7 +785,7 @@ def qk_norm_bwd(q, k, wq, wk, dqn, dkn, rotary: Optional[int] = None, base: floa
 def _attn_args(q, k, v):
     _check(q, "q", torch.bfloat16, 4)
     B, T, Hq, d = q.shape
-    _check(k, "k", torch.bfloat16, 4)
+    _check(k, "k", torch.bfloat16, 4, here=False)   # (with q, below)
     Hk, device = k.shape[2], q.device
     shape = (B, T, Hk, d)
     return (AttnDims(B, T, Hq, Hk, d), q.data_ptr(), _on(k, "k", torch.bfloat16, shape, device),
@@ -811,8 +826,8 @@ def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None
 
 
 def _cache_args(kcache, vcache, pages, lens, B, device):
-    _check(kcache, "kcache", torch.bfloat16, 4)
-    _check(pages, "pages", torch.int32, 2)
+    _check(kcache, "kcache", torch.bfloat16, 4, here=False)
+    _check(pages, "pages", torch.int32, 2, here=False)
     return CacheArgs(_on(kcache, "kcache", torch.bfloat16, kcache.shape, device),
                      _on(vcache, "vcache", torch.bfloat16, kcache.shape, device),
                      _on(pages, "pages", torch.int32, (B, pages.shape[1]), device),

@@ -114,3 +114,23 @@ def test_buffers_that_a_graph_may_hold_outlive_growth(monkeypatch):
     bdla._with_ws("x", bdla.ATTN_FWD, bdla.AttnDims(1, 4, 4, 2, 64), 0, 0, ws, torch.device("cpu"), None, call)
     ws.ensure(1000)
     assert not ws.in_graph and not ws.held
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    class OnSecond:
+        device = torch.device("cuda", 1)
+
+    monkeypatch.setattr(bdla, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        bdla._here(OnSecond, "q")
+    monkeypatch.setattr(bdla, "_current_device", lambda: 1)
+    bdla._here(OnSecond, "q")
+
+
+def test_a_workspace_on_another_device_is_refused():
+    ws = bdla.Workspace(1000, "cpu")
+    launch = lambda p, n: pytest.fail("reached the library")
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        bdla._with_ws("x", bdla.ATTN_FWD, bdla.AttnDims(1, 4, 4, 2, 64), 0, 0, ws, torch.device("cuda", 0), None, launch)
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        bdla._workspace(256, torch.device("cuda", 0), ws, None)

@@ -114,3 +114,42 @@ def test_a_graph_replays_on_its_buffer_after_the_workspace_has_grown():
     graph.replay()
     assert ws.read_device_status() == bdla.ERR_DEVICE   # the replay's own record
     assert ws.read_device_status() == bdla.OK
+
+
+def _calls():
+    """Every public call with small right arguments, as (name, f(ws))."""
+    rn = lambda *s: torch.randn(s, generator=torch.Generator("cuda").manual_seed(7), device="cuda")
+    q, k, a = rn(1, 20, 4, 64).to(BF16), rn(1, 20, 2, 64).to(BF16), rn(1, 20, 4)
+    w, lse = torch.ones(64, device="cuda"), torch.zeros((4, 20), device="cuda")
+    kc, vc, table, lens = _cache()
+    lens = lens - 20
+    state, av, beta = torch.zeros((1, 4, 64, 64), device="cuda"), rn(1, 20, 4, 64), torch.sigmoid(a)
+    q1, a1 = q[:, 0].contiguous(), a[:, 0].contiguous()
+    return [("qk_norm", lambda ws: bdla.qk_norm(q, k, w, w)),
+            ("qk_norm_bwd", lambda ws: bdla.qk_norm_bwd(q, k, w, w, q, k, ws=ws)),
+            ("attn_fwd", lambda ws: bdla.attn_fwd(q, k, k, ws=ws)),
+            ("attn_bwd", lambda ws: bdla.attn_bwd(q, k, k, q, lse, q, ws=ws)),
+            ("cache_append", lambda ws: bdla.cache_append(k, k, kc, vc, table, lens, ws=ws)),
+            ("attn_cached", lambda ws: bdla.attn_cached(q, kc, vc, table, lens, ws=ws)),
+            ("fwd", lambda ws: bdla.fwd(q, q, q, a, ws=ws)),
+            ("bwd", lambda ws: bdla.bwd(q, q, q, a, q, ws=ws)),
+            ("decode", lambda ws: bdla.decode(q1, q1, q1, a1, state)),
+            ("decay", lambda ws: bdla.decay(a, ws=ws)),
+            ("fwd_vec", lambda ws: bdla.fwd_vec(q, q, q, av, ws=ws)),
+            ("fwd_delta", lambda ws: bdla.fwd_delta(q, q, q, a, beta, ws=ws))]
+
+
+def test_calls_off_the_current_device_or_with_a_workspace_from_elsewhere_are_refused(monkeypatch):
+    calls = _calls()
+    elsewhere = bdla.Workspace(1 << 20, "cpu")
+    for name, f in calls:
+        f(None)
+        f(bdla.Workspace(256, "cuda"))
+        if name not in ("qk_norm", "decode"):
+            with pytest.raises(ValueError, match="ws is on cpu"):
+                f(elsewhere)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(bdla, "_current_device", lambda: 1)
+    for name, f in calls:
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            f(None)
