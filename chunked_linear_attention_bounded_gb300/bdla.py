@@ -215,17 +215,19 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# the two questions that every call asks, without torch.cuda's checks of its own set-up (a tensor is there already)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _here(t, name: str):
     """The library launches on the current device, whose streams and sizes it takes."""
-    if t.device.index != _current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}: "
                          f"make the call within torch.cuda.device({t.device.index})")
 
 
-def _check(t: torch.Tensor, name: str, dtype, ndim: int, here: bool = True):
+def _check(t: torch.Tensor, name: str, dtype, ndim: int, here: bool = False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -258,37 +260,40 @@ def _scope(stream):
 class Workspace:
     """Caller-owned device scratch for the library (status word first).  A call
     that needs more grows it on the call's stream, and what the device has
-    recorded stays to be read.  Growing inside a graph's capture puts the new
-    buffer, and the clearing of its record, into the graph: size it before."""
+    recorded stays to be read.  A buffer that a captured graph uses lives as
+    long as the workspace, since replays write to it however the workspace has
+    grown.  Growing inside a capture puts the new buffer, and the clearing of
+    its record, into the graph: size it before."""
 
     def __init__(self, nbytes: int, device):
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        self.device = self.buf.device
         self.in_graph = False   # a graph may hold the present buffer
         self.held = []          # outgrown buffers that one may hold; their records are read where they are
 
     def ensure(self, nbytes: int, stream=None):
         if nbytes > self.nbytes:
             with _scope(stream):
-                old, buf = self.buf, torch.zeros(int(nbytes), dtype=torch.uint8, device=self.buf.device)
-                if self.in_graph or torch.cuda.is_current_stream_capturing():
+                old, buf = self.buf, torch.zeros(int(nbytes), dtype=torch.uint8, device=self.device)
+                if self.in_graph or _capturing():
                     self.held.append(old)   # (and a captured copy would bring the old record back at every replay)
                 else:
                     buf[:256] = old[:256]
                     if old.is_cuda:
-                        old.record_stream(torch.cuda.current_stream(old.device))
+                        old.record_stream(torch.cuda.current_stream(self.device))
             self.buf, self.nbytes = buf, int(nbytes)
         return self
 
     def note_call(self, device, stream=None):
         """To be told of every call that takes the buffer, before it is launched."""
-        if self.buf.device != device:
-            raise ValueError(f"ws is on {self.buf.device}, expected {device}")
+        if self.device != device:
+            raise ValueError(f"ws is on {self.device}, expected {device}")
         if not self.in_graph:
-            self.in_graph = torch.cuda.is_current_stream_capturing()
+            self.in_graph = _capturing()
             if stream is not None and not self.in_graph:
                 with torch.cuda.stream(stream):
-                    self.in_graph = torch.cuda.is_current_stream_capturing()
+                    self.in_graph = _capturing()
 
     @property
     def ptr(self):
@@ -328,7 +333,7 @@ def decay(a: torch.Tensor, b: float = -5.0, cu_seqlens: Optional[torch.Tensor] =
           mode: int = BOUNDED, ws: Optional[Workspace] = None, stream=None) -> torch.Tensor:
     """Tile-local inclusive cumsum Gamma of the log-decay, fp32 [H, B*T]
     (head-major)."""
-    _check(a, "a", torch.float32, 3)
+    _check(a, "a", torch.float32, 3, here=True)
     B, T, H = a.shape
     gamma = torch.empty((H, B * T), dtype=torch.float32, device=a.device)
     n_docs = 0
@@ -348,7 +353,7 @@ def decode(q, k, v, a, state, b: float = -5.0, mode: int = BOUNDED, o_dtype=torc
     """One recurrent step per sequence: q, k [B, H, dk], v [B, H, dv] bf16,
     a [B, H] fp32; `state` fp32 [B, H, dk, dv] is updated in place
     (S <- e^{lambda} S + k v^T).  Returns o = S^T q [B, H, dv]."""
-    _check(q, "q", torch.bfloat16, 3)
+    _check(q, "q", torch.bfloat16, 3, here=True)
     _check(k, "k", torch.bfloat16, 3)
     _check(v, "v", torch.bfloat16, 3)
     _check(a, "a", torch.float32, 2)
@@ -380,7 +385,7 @@ def fwd(q, k, v, a, b: float = -5.0, h0=None, cu_seqlens=None, mode: int = BOUND
     """Forward pass.  Returns (o, hT, ckpt); hT / ckpt are None when not asked
     for.  ckpt_stride > 0 also writes the state every ckpt_stride tokens
     ([H, n_slots, dk, dv], ckpt_dtype), which bwd() can reuse."""
-    _check(q, "q", torch.bfloat16, 4)
+    _check(q, "q", torch.bfloat16, 4, here=True)
     _check(k, "k", torch.bfloat16, 4)
     _check(v, "v", torch.bfloat16, 4)
     _check(a, "a", torch.float32, 3)
@@ -427,7 +432,7 @@ def bwd(q, k, v, a, dO, b: float = -5.0, h0=None, dhT=None, cu_seqlens=None, ckp
         ws: Optional[Workspace] = None, outs=None, stream=None):
     """Backward pass.  Returns (dq, dk, dv, da, dh0); dh0 is None unless asked for."""
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (dO, "dO")):
-        _check(t, n, torch.bfloat16, 4)
+        _check(t, n, torch.bfloat16, 4, here=t is q)
     _check(a, "a", torch.float32, 3)
     B, T, H, dk = q.shape
     dv = v.shape[-1]
@@ -476,7 +481,7 @@ def bwd(q, k, v, a, dO, b: float = -5.0, h0=None, dhT=None, cu_seqlens=None, ckp
 
 # ---------------------------------------------------------------- per-channel decay
 def _vec_checks(q, k, v, a, cu_seqlens, h0):
-    _check(q, "q", torch.bfloat16, 4)
+    _check(q, "q", torch.bfloat16, 4, here=True)
     _check(k, "k", torch.bfloat16, 4)
     _check(v, "v", torch.bfloat16, 4)
     _check(a, "a", torch.float32, 4)
@@ -563,7 +568,7 @@ def bwd_vec(q, k, v, a, dO, b: float = -5.0, h0=None, dhT=None, cu_seqlens=None,
 
 # ---------------------------------------------------------------- gated delta rule
 def _delta_checks(q, k, v, a, beta, cu_seqlens, h0):
-    _check(q, "q", torch.bfloat16, 4)
+    _check(q, "q", torch.bfloat16, 4, here=True)
     _check(k, "k", torch.bfloat16, 4)
     _check(v, "v", torch.bfloat16, 4)
     _check(a, "a", torch.float32, 3)
@@ -657,7 +662,7 @@ def _on(t, name: str, dtype, shape, device):
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
             and t.is_contiguous():
         return t.data_ptr()
-    _check(t, name, dtype, len(shape), here=False)
+    _check(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -783,9 +788,9 @@ def qk_norm_bwd(q, k, wq, wk, dqn, dkn, rotary: Optional[int] = None, base: floa
 
 
 def _attn_args(q, k, v):
-    _check(q, "q", torch.bfloat16, 4)
+    _check(q, "q", torch.bfloat16, 4, here=True)
     B, T, Hq, d = q.shape
-    _check(k, "k", torch.bfloat16, 4, here=False)   # (with q, below)
+    _check(k, "k", torch.bfloat16, 4)
     Hk, device = k.shape[2], q.device
     shape = (B, T, Hk, d)
     return (AttnDims(B, T, Hq, Hk, d), q.data_ptr(), _on(k, "k", torch.bfloat16, shape, device),
@@ -826,12 +831,14 @@ def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None
 
 
 def _cache_args(kcache, vcache, pages, lens, B, device):
-    _check(kcache, "kcache", torch.bfloat16, 4, here=False)
-    _check(pages, "pages", torch.int32, 2, here=False)
-    return CacheArgs(_on(kcache, "kcache", torch.bfloat16, kcache.shape, device),
-                     _on(vcache, "vcache", torch.bfloat16, kcache.shape, device),
-                     _on(pages, "pages", torch.int32, (B, pages.shape[1]), device),
-                     _on(lens, "lens", torch.int32, (B,), device), kcache.shape[0], kcache.shape[1], pages.shape[1])
+    _check(kcache, "kcache", torch.bfloat16, 4)
+    _check(pages, "pages", torch.int32, 2)
+    shape, width = kcache.shape, pages.shape[1]
+    if kcache.device != device or pages.device != device or pages.shape[0] != B:
+        _on(kcache, "kcache", torch.bfloat16, shape, device)
+        _on(pages, "pages", torch.int32, (B, width), device)   # one of the two says what is wrong
+    return CacheArgs(kcache.data_ptr(), _on(vcache, "vcache", torch.bfloat16, shape, device), pages.data_ptr(),
+                     _on(lens, "lens", torch.int32, (B,), device), shape[0], shape[1], width)
 
 
 def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: Optional[Workspace] = None,
@@ -841,7 +848,7 @@ def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: 
     0 .. T - 1, or the first counts[b] of rows[b] (int32 [B], [B, T]), which is
     how a verified tree's accepted drafts are made consecutive.  pages is the
     int32 page table [B, max_pages]; lens is left as it is."""
-    _check(k, "k", torch.bfloat16, 4)
+    _check(k, "k", torch.bfloat16, 4, here=True)
     B, T, Hk, d = k.shape
     device = k.device
     pv = _on(v, "v", torch.bfloat16, k.shape, device)
@@ -863,7 +870,7 @@ def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float
     positions lens[b] .. lens[b] + T - 1.  tree: int64 [B, T] bit masks of the
     new tokens each one sees (None: those up to and with itself).  Returns
     (o like q, lse fp32 [B, T, Hq]); a token that sees nothing gets 0 and -inf."""
-    _check(q, "q", torch.bfloat16, 4)
+    _check(q, "q", torch.bfloat16, 4, here=True)
     B, T, Hq, d = q.shape
     device = q.device
     c = _cache_args(kcache, vcache, pages, lens, B, device)

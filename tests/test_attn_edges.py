@@ -68,7 +68,7 @@ def test_strides_of_a_projections_views():
 
 def test_a_workspace_keeps_its_record_as_it_grows(monkeypatch):
     """The status word survives growth (on any device), the scratch behind it starts at zero."""
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(bdla, "_capturing", lambda: False)
     ws = bdla.Workspace(256, "cpu")
     ws.buf[:256] = torch.arange(256, dtype=torch.uint8)
     assert ws.ensure(200) is ws and ws.nbytes == 256
@@ -79,7 +79,7 @@ def test_a_workspace_keeps_its_record_as_it_grows(monkeypatch):
 
 def test_growing_in_a_capture_leaves_the_record_where_it_is(monkeypatch):
     """Nothing is copied, which the graph would repeat; the outgrown record is still read, and first."""
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(bdla, "_capturing", lambda: True)
     ws = bdla.Workspace(256, "cpu")
     first = ws.buf
     first[0] = 10
@@ -95,7 +95,7 @@ def test_growing_in_a_capture_leaves_the_record_where_it_is(monkeypatch):
 
 def test_buffers_that_a_graph_may_hold_outlive_growth(monkeypatch):
     capturing = [True]
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(bdla, "_capturing", lambda: capturing[0])
     ws = bdla.Workspace(300, "cpu")
     first = ws.buf
     calls = []
@@ -119,6 +119,7 @@ def test_buffers_that_a_graph_may_hold_outlive_growth(monkeypatch):
 def test_tensors_off_the_current_device_are_refused(monkeypatch):
     class OnSecond:
         device = torch.device("cuda", 1)
+        get_device = staticmethod(lambda: 1)
 
     monkeypatch.setattr(bdla, "_current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device is cuda:0"):

@@ -153,3 +153,18 @@ def test_calls_off_the_current_device_or_with_a_workspace_from_elsewhere_are_ref
     for name, f in calls:
         with pytest.raises(ValueError, match="current device is cuda:1"):
             f(None)
+
+
+def test_cache_arguments_are_refused_by_name():
+    kc, vc, table, lens = _cache()
+    q = torch.zeros((1, 1, 4, 64), dtype=BF16, device="cuda")
+    for change, message in ((dict(pages=table.repeat(2, 1)), "pages must be"), (dict(pages=table[0]), "pages must have 2"),
+                            (dict(pages=table.long()), "pages must be torch.int32"), (dict(lens=lens.repeat(2)), "lens must be"),
+                            (dict(vcache=vc[:2]), "vcache must be"), (dict(kcache=kc.float()), "kcache must be torch.bfloat16"),
+                            (dict(kcache=kc.transpose(0, 1)), "kcache must be contiguous"), (dict(pages=table.cpu()), "CUDA")):
+        args = dict(kcache=kc, vcache=vc, pages=table, lens=lens)
+        args.update(change)
+        with pytest.raises(ValueError, match=message):
+            bdla.attn_cached(q, **args)
+        with pytest.raises(ValueError, match=message):
+            bdla.cache_append(q[:, :, :2].contiguous(), q[:, :, :2].contiguous(), **args)
