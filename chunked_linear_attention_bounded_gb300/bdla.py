@@ -814,8 +814,10 @@ def attn_fwd(q, k, v, scale: Optional[float] = None, cu_seqlens=None, ws: Option
 
 def attn_bwd(q, k, v, o, lse, dO, scale: Optional[float] = None, cu_seqlens=None, ws: Optional[Workspace] = None,
              stream=None):
-    """Gradient of attn_fwd from its inputs, its (o, lse) and dO like o.
-    Returns (dq, dk, dv), bf16.  The same inputs give the same bits."""
+    """Gradient of attn_fwd from its inputs, its (o, lse) and dO like o; o and
+    lse may also have been joined with a sink's or other keys' (p = e^{s - lse},
+    delta = dO . o).  Returns (dq, dk, dv), bf16.  The same inputs give the same
+    bits."""
     d, pq, pk, pv = _attn_args(q, k, v)
     po = _on(o, "o", torch.bfloat16, q.shape, q.device)
     pg = _on(dO, "dO", torch.bfloat16, q.shape, q.device)

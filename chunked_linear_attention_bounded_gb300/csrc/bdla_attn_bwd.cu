@@ -32,6 +32,13 @@
 // before ds, so that short rows, where o's rounding weighs most, are as exact as
 // their weights, and a document's first token, whose ds is 0, gets 0.
 //
+// All of that stands in for the formula only while it cannot be told from it: the
+// sum of p o dp for dO . o within the rounding of o's entries, 2^-8 sum |dO o|, and
+// the weights over their sum for the weights where that sum is 1 within 2^-8, the
+// rounding of ds.  o and lse that were joined with other keys' (a sink, another
+// set of keys) are outside, and p = e^{s - lse} and delta = dO . o are then taken
+// as they are.
+//
 // Rows past a document's end hold the next document.  Their p and ds are
 // zeroed by selection, and where such rows are the summed side of a product
 // their operand rows are cleared in shared memory, so that another document's
@@ -54,6 +61,7 @@ using namespace attn;
 
 constexpr int kEpi = 256;              // weight threads
 constexpr int kThreads = 64 + kEpi;    // + loader and MMA issuer
+constexpr float kHalfStep = 0x1p-8f;   // of bf16, relative
 
 template <int D> struct BwdSmem {
     static constexpr int kPanels = D / 64;
@@ -66,7 +74,7 @@ template <int D> struct BwdSmem {
     alignas(1024) unsigned char ring[kStages][kTile];   // kA tiles of K (Q), kB of V (dO)
     static __host__ __device__ constexpr int slot(int it) { return it & 1 ? kA + (it >> 1) % kB : (it >> 1) % kA; }
     static __host__ __device__ constexpr int turn(int it) { return it & 1 ? (it >> 1) / kB : (it >> 1) / kA; }
-    float col[2][2][BT];   // key tiles: -lse * log2 e and -delta of a query tile; query tiles: [0] halves of delta
+    float col[2][2][BT];   // key tiles: -lse * log2 e and -delta of a query tile; query tiles: halves of dO . o, of sum |dO o|
     uint64_t full_own, full[kStages], empty[kStages], s_full[2], dp_full, dp_free, done;
     uint64_t ready[2][2];   // [tile, or p and ds][part]: weights whose first, last 32 columns of each warp's 64 are there
     uint64_t drain, never;
@@ -276,8 +284,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const int half = (warp - 2) >> 2, q4 = warp & 3, r = 32 * q4 + lane, e = 128 * half + r;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         const int64_t t = span.start + r;
-        // delta of the row, half the features each
-        float dl = 0.0f, l2 = 0.0f;
+        // delta of the row, and how far o's rounding may have moved it, half the features each
+        float dl = 0.0f, dev = 0.0f, l2 = 0.0f;
         if (r < valid) {
             const size_t off = ((size_t)t * Hq + h) * D + half * (D / 2);
 #pragma unroll
@@ -286,14 +294,25 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 const uint4 b = *reinterpret_cast<const uint4 *>(dO + off + 8 * i);
                 const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    dl = fmaf(bf16_hi(x[u]), bf16_hi(y[u]), fmaf(bf16_lo(x[u]), bf16_lo(y[u]), dl));
+                for (int u = 0; u < 4; ++u) {
+                    const float f = bf16_lo(x[u]) * bf16_lo(y[u]), g = bf16_hi(x[u]) * bf16_hi(y[u]);   // exact
+                    dl = g + (f + dl);
+                    dev += fabsf(f) + fabsf(g);
+                }
             }
             l2 = lse[(int64_t)h * tokens + t] * kLog2e;
         }
         sm.col[0][half][r] = dl;
+        sm.col[1][half][r] = dev;
         epi_sync();
         dl = sm.col[0][0][r] + sm.col[0][1][r];
+        // The row's own delta in dO . o's place, if o's rounding covers the difference.
+        auto chosen = [&](float own) {
+            const float given = sm.col[0][0][r] + sm.col[0][1][r];
+            return fabsf(own - given) <= kHalfStep * (sm.col[1][0][r] + sm.col[1][1][r]) ? own : given;
+        };
+        // The two halves' sums of a row, over dO's tile: written after the last dp has come from it.
+        float (*sums)[2][BT] = reinterpret_cast<float (*)[2][BT]>(sm.own[1]);
         const float c = scale * kLog2e;
         const uint64_t c2 = pair(c, c), nl2 = pair(-l2, -l2), nd2 = pair(-dl, -dl);
         uint64_t sum2 = 0;   // of p dp, the row's own delta
@@ -323,7 +342,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                         y[k][m] = out ? 0u : y[k][m];
                         sum += p;
                     }
-                sm.col[1][half][r] = sum;
+                sums[0][half][r] = sum;
                 if (valid < BT) {
                     clear_rows(sm.ring[Smem::slot(0)], NP, valid, e, kEpi);
                     fence_proxy_async_smem();
@@ -332,22 +351,23 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             ok = epi_all(ok);
             float own = 0.0f;
             if (ok) {
-                sum = sm.col[1][0][r] + sm.col[1][1][r];
-                const float inv = 1.0f / sum;
+                sum = sums[0][0][r] + sums[0][1][r];
+                const bool whole = fabsf(sum - 1.0f) <= kHalfStep;   // these keys are all that lse has seen
+                const float inv = whole ? 1.0f / sum : 1.0f;
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int m = 0; m < 32; ++m) {
                         const float w = __uint_as_float(x[k][m]);
-                        const float p = w == sum ? 1.0f : w * inv;   // exactly 1 for a lone key
+                        const float p = whole && w == sum ? 1.0f : w * inv;   // exactly 1 for a lone key
                         x[k][m] = __float_as_uint(p);
                         own = fmaf(p, __uint_as_float(y[k][m]), own);
                     }
-                sm.col[0][half][r] = own;
+                sums[1][half][r] = own;
             }
             ok = epi_all(ok);
             if (ok) {
-                own = sm.col[0][0][r] + sm.col[0][1][r];
+                own = chosen(sums[1][0][r] + sums[1][1][r]);
                 if (half == 0 && r < valid)
                     delta[(int64_t)h * tokens + t] = own;
 #pragma unroll
@@ -432,10 +452,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         if (n > 1) {
             float a, b;
             unpair(sum2, a, b);
-            sm.col[1][half][r] = a + b;
+            if (ok)
+                sums[1][half][r] = a + b;
             // every warp comes here, after its last tile or a wait that ran out
             if (epi_all(ok) && half == 0 && r < valid)
-                delta[(int64_t)h * tokens + t] = sm.col[1][0][r] + sm.col[1][1][r];
+                delta[(int64_t)h * tokens + t] = chosen(sums[1][0][r] + sums[1][1][r]);
         }
         if (ok)
             ok = warp_wait(&sm.done, 0, &sm.wait_ns, abort_flag);

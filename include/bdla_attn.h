@@ -79,10 +79,17 @@ bdla_status bdla_qk_norm_bwd(bdla_qk_norm_args a, const void *dqn, const void *d
  *   q, o, dO, dq   bf16 [B, T, Hq, d];   k, v, dk, dv  bf16 [B, T, Hk, d]
  *   lse            fp32 [Hq, B*T] (head-major)
  * Documents are the B rows, or packed (B = 1, device int32 cu_seqlens
- * [n_docs + 1] as in bdla.h).  scale > 0.  The gradient reads the forward's o
- * and lse; dk and dv are summed over the query heads of their key head in a
- * fixed order, so the same inputs give the same bits.  Infinities and NaN in
- * one document do not reach another.
+ * [n_docs + 1] as in bdla.h).  scale > 0.  The gradient is
+ *     delta_i = dO_i . o_i,   ds_ij = p_ij (dO_i . v_j - delta_i),
+ *     dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,   dv_j = sum_i p_ij dO_i
+ * at the o and lse that it is handed: the forward's, or those joined with what
+ * the call does not see (a sink in the denominator, other keys).  For delta it
+ * may take its own fp32 sum of p dO . v where that lies within the rounding of
+ * o, and weights over their sum where that sum is 1 within 2^-8.  dk and dv are
+ * summed over the query heads of their key head in a fixed order, so the same
+ * inputs give the same bits.  Infinities and NaN in one document do not reach
+ * another.  Within a document they reach what sees them and, since a masked
+ * weight is a factor of 0, may reach other rows of the same 128 queries or keys.
  */
 bdla_status bdla_attn_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int n_docs,
                           float scale, void *o, float *lse, bdla_attn_dims d, void *ws, size_t ws_bytes,
