@@ -1,5 +1,7 @@
-// What the softmax attention kernels share: tile sizes, the base-2
-// exponential, the check of packed offsets, and the store of 32 rows.
+// What the softmax attention kernels share: tile sizes, paired fp32 arithmetic
+// and the base-2 exponential, one row's softmax in tensor memory, the check of
+// packed offsets, the launch of a call's second kernel, products of 128-row
+// tiles, bounded waits of warps, and the stores of 32 rows.
 #pragma once
 
 #include "bdla_attn_internal.h"
@@ -141,7 +143,6 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int n_docs, int
             set_status(st, BDLA_ERR_DEVICE, (unsigned)n);
 }
 
-// One lane of a whole warp, the same one each time.
 // Two kernels of one call, the second of which reads what the first wrote: the
 // first says at its start that the second's CTAs may take the places that its own
 // last ones leave, and the second waits, before it reads and before any CTA ends,
@@ -167,6 +168,7 @@ cudaError_t launch_second(void (*kernel)(P...), dim3 grid, unsigned threads, siz
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// One lane of a whole warp, the same one each time.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t r;

@@ -85,9 +85,12 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 // a position, so they run as warp MMAs (m16n8k16, 16 or 32 rows) straight from
 // the tiles that cp.async brings in.  Keys and values of 64 positions have two
 // buffers each, and a buffer is filled again as soon as its own product is done:
-// 64 KB a CTA, three CTAs an SM.  256 ragged sequences, 677 us (6.3 TB/s; three
+// 64 KB a CTA, three CTAs an SM.  256 ragged sequences, 676 us (6.3 TB/s; three
 // whole tiles a CTA, two CTAs an SM: 736); one of 262144 positions, with the
-// join, 170 us (6.3 TB/s).  A CTA's four warps split the rows first and the
+// join, 170 us (6.3 TB/s).  With 32 rows 12 to 16 bytes of registers are spilled.
+// Pieces are counted from the table's width, so a table for 262144 positions over
+// sequences of up to 8192 launches CTAs that find nothing to do: 856 us for 688 (both
+// from cold).  A CTA's four warps split the rows first and the
 // positions of the tile with what is left, and join through shared memory at the
 // end.  Warp MMAs run at an
 // eighth of the tensor cores' rate here: with 64 rows they took longer than the

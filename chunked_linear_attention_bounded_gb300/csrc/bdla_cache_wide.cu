@@ -18,8 +18,9 @@
 // of the two tiles, one thread a row.
 //
 // Between HBM and the tensor cores (61% and 59% of their peaks): 4 sequences of
-// 65536 positions, 61 drafts, 16 heads on 4, d = 128: 113 us (4.8 TB/s); at a few
-// thousand positions the start-up, a CTA's first tiles and the join weigh more.
+// 65536 positions, 61 drafts, 16 heads on 4, d = 128: 113 us (4.8 TB/s), from cold
+// and with the join 123; at a few thousand positions the start-up, a CTA's first
+// tiles and the join weigh more.  168 registers a thread, 20 bytes spilled.
 #include <cudaTypedefs.h>
 
 #include "bdla_attn_sm100.cuh"

@@ -14,7 +14,10 @@
 // angles of a lane belong to the token, and the products of weights and sines
 // are formed once per chunk; several heads' loads are in flight at a time.
 // Measured for 65536 tokens, 32 + 8 heads of 128: forward 203 us (6.6 TB/s),
-// gradient 302 us (6.7 TB/s; loads through registers, two heads at a time, 364).
+// gradient 305 us (6.6 TB/s; loads through registers, two heads at a time, 364),
+// from fp32 gradients, 8 bytes an element, 393 us (6.8 TB/s).  Registers end at
+// the 128 of two CTAs an SM: the forward and two forms of the gradient spill 12 to
+// 16 bytes.
 //
 // Angles.  pos * f with f = base^(-2i/rotary) loses its fraction of a turn in
 // fp32 for far positions.  f / (2 pi) is therefore kept as a 64-bit binary
@@ -43,7 +46,7 @@ using sm100::bf16_lo;
 using sm100::pack_bf16;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;   // heads in flight per group of lanes (4: 249 us for 64K packed tokens, 8: 209)
+constexpr int kBatch = 8;   // heads in flight per group of lanes (64K packed tokens from cold: 258 us with 4, 213 with 8)
 
 struct Turns {
     uint64_t f[64];   // turns per position of each pair, times 2^64

@@ -41,7 +41,8 @@ typedef struct {
  * rotary is 0 (no rotation) or a multiple of 16 up to d.  The angle is taken
  * from an exact product of the position with a 64-bit binary fraction of a
  * turn, so far positions lose nothing.  An L2 norm (the keys of the linear
- * attention) is eps = 0 or tiny with w = 1/sqrt(d).
+ * attention) is eps = 0 or tiny with w = 1/sqrt(d); with eps = 0 a head of zeros
+ * gives NaN.  Squares are summed in fp32: a mean square above its range gives 0.
  *   q, k      bf16 [B, T, Hq | Hk, d] with strides: element strides of a
  *             token and of a head, multiples of 8 (so that they may be views
  *             of one fused projection); features contiguous; rows of a batch
@@ -137,8 +138,10 @@ bdla_status bdla_cache_append(const void *k, const void *v, bdla_cache c, const 
  * nothing gets o = 0 and lse = -inf.
  *   q, o   bf16 [B, T, Hq, d];   lse  fp32 [B, T, Hq]
  * What lies in the cache outside the positions that a sequence's new tokens
- * see is not read, whatever its bits.  Positions past the page table, pages outside
- * the cache and negative lens are recorded as BDLA_ERR_DEVICE and not seen.
+ * see is not read, whatever its bits; a value that one of them sees and that is
+ * not finite may reach the others, whose weight of 0 it is multiplied by.
+ * Positions past the page table, pages outside the cache and negative lens are
+ * recorded as BDLA_ERR_DEVICE and not seen.
  */
 bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, float scale, void *o, float *lse,
                              bdla_attn_dims d, void *ws, size_t ws_bytes, void *stream);
