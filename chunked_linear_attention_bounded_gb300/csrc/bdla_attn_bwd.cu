@@ -44,11 +44,11 @@
 // their operand rows are cleared in shared memory, so that another document's
 // infinity or NaN never enters a sum.
 //
-// Bound by the tensor cores' turns (60 and 65% of the cycles of the two) and the
+// Bound by the tensor cores' turns (62 and 69% of the cycles of the two) and the
 // chain from scores to weights between them.  Measured, d = 128: 4 documents of
 // 8192, 16 heads on 4, 2.78 ms, 0.99 PFLOP/s of the five products that a gradient
-// needs, 1.39 of the seven; one of 16384, 16 on 4, 2.54 ms, 1.08 and 1.51.  168
-// registers a thread; the first kernel spills 4 to 8 bytes.
+// needs, 1.39 of the seven; one of 16384, 16 on 4, 2.54 ms, 1.08 and 1.51.  Up to
+// 168 registers a thread; the first kernel spills 4 to 8 bytes.
 #include <cudaTypedefs.h>
 
 #include "bdla_attn_sm100.cuh"

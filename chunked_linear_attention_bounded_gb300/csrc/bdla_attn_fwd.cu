@@ -33,7 +33,7 @@
 // cleared in shared memory, so that 0 times another document's infinity or NaN
 // never enters a sum.
 //
-// Bound by the tensor cores' turns (67% of the cycles), then by the chain from a
+// Bound by the tensor cores' turns (69% of the cycles), then by the chain from a
 // tile's scores to its weights.  Measured, d = 128: 65536 tokens in 8 documents,
 // 32 heads on 8, 4.32 ms (1.46 PFLOP/s, under the power cap); one document of
 // 16384, 16 on 4, 0.68 ms (1.61 PFLOP/s, the GEMM's own rate being 1.91).  168
