@@ -40,7 +40,7 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_workspace_bytes_vec", "bdla_fwd_vec", "bdla_bwd_vec", "bdla_workspace_bytes_delta",
            "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes",
            "bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
-           "bdla_attn_cached", "bdla_workspace_bytes_attn")
+           "bdla_attn_cached", "bdla_workspace_bytes_attn", "bdla_decode_delta")
 ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED = 0, 1, 2, 3, 4
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
 KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED = 5, 6, 7
@@ -137,6 +137,8 @@ def lib():
         L.bdla_tile_states_bytes.argtypes = [Dims, ci]
         L.bdla_tile_states_bytes.restype = sz
         L.bdla_bwd_delta.restype = ci
+        L.bdla_decode_delta.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, ci, vp, vp, ci, Dims, ci, vp, sz, vp]
+        L.bdla_decode_delta.restype = ci
         L.bdla_qk_norm.argtypes = [QkNormArgs, vp, vp, AttnDims, vp]
         L.bdla_qk_norm_bwd.argtypes = [QkNormArgs, vp, vp, ci, vp, vp, vp, vp, AttnDims, vp, sz, vp]
         L.bdla_attn_fwd.argtypes = [vp, vp, vp, vp, ci, f32, vp, vp, AttnDims, vp, sz, vp]
@@ -641,6 +643,39 @@ def bwd_delta(q, k, v, a, beta, dO, b: float = -5.0, h0=None, dhT=None, cu_seqle
     if st:
         raise BdlaError(st, "bdla_bwd_delta")
     return dq, dk_, dv_, da, dbeta, dh0
+
+
+def decode_delta(q, k, v, a, beta, state, slots=None, counts=None, b: float = -5.0, mode: int = BOUNDED,
+                 o_dtype=torch.bfloat16, ws: Optional[Workspace] = None, out=None, stream=None) -> torch.Tensor:
+    """T recurrent steps of the gated delta rule per sequence (q, k [B, T, H, dk], v [B, T, H, dv] bf16, a and beta
+    [B, T, H] fp32) from resident states, fp32 [n, H, dk, dv], updated in place: sequence n's is slots[n] (int32 [B],
+    -1: an unused place of the batch, o = 0), or n without slots (n = B).  With counts (int32 [B]) the state that is
+    left is the one after the first counts[n] tokens; o is that of all T either way: verify drafts with zeros, then
+    keep the accepted.  Returns o [B, T, H, dv].  What the device refuses (a slot out of range or named twice, a bad
+    count) is recorded in `ws`."""
+    _check(q, "q", torch.bfloat16, 4, here=True)
+    _check(v, "v", torch.bfloat16, 4)
+    B, T, H, dk = q.shape
+    dv, device = v.shape[3], q.device
+    rows = (B, T, H)
+    pk, pv = _on(k, "k", torch.bfloat16, q.shape, device), _on(v, "v", torch.bfloat16, (B, T, H, dv), device)
+    pa, pb = _on(a, "a", torch.float32, rows, device), _on(beta, "beta", torch.float32, rows, device)
+    _check(state, "state", torch.float32, 4)
+    n = state.shape[0] if slots is not None else B
+    ps = _on(state, "state", torch.float32, (n, H, dk, dv), device)
+    pi = None if slots is None else _on(slots, "slots", torch.int32, (B,), device)
+    pc = None if counts is None else _on(counts, "counts", torch.int32, (B,), device)
+    if out is None:
+        out, = _new(device, stream, ((B, T, H, dv), o_dtype))
+    po = _on(out, "out", out.dtype, (B, T, H, dv), device)
+    if ws is not None or pi is not None or pc is not None:
+        ws = _workspace(256, device, ws, stream)
+    st = lib().bdla_decode_delta(q.data_ptr(), pk, pv, pa, pb, b, ps, pi, n, pc, po, _dtype_code(out.dtype),
+                                 Dims(B, T, H, dk, dv), mode, None if ws is None else ws.buf.data_ptr(),
+                                 0 if ws is None else ws.nbytes, _stream_of(q, stream))
+    if st:
+        raise BdlaError(st, "bdla_decode_delta")
+    return out
 
 
 # ---------------------------------------------------------------- softmax layer

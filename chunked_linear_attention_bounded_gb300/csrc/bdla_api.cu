@@ -697,6 +697,34 @@ bdla_status bdla_bwd_delta(const void *q, const void *k, const void *v, const fl
     return BDLA_OK;
 }
 
+bdla_status bdla_decode_delta(const void *q, const void *k, const void *v, const float *a, const float *beta, float b,
+                              float *state, const int32_t *slots, int n_slots, const int32_t *counts, void *o,
+                              bdla_dtype o_dtype, bdla_dims d, bdla_decay_mode mode, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    BDLA_TRY(check_vec(d, nullptr, 0));
+    if (d.T < 1 || (slots && n_slots < 0))
+        return BDLA_ERR_SHAPE;
+    BDLA_TRY(check_decay(b, kChunk, mode));
+    // warps are a grid extent, a quarter of it
+    if ((int64_t)d.B * d.T > INT32_MAX || (int64_t)d.B * d.H * (d.dv / 32) > INT32_MAX)
+        return BDLA_ERR_TOO_LARGE;
+    if (!q || !k || !v || !a || !beta || !o || (!state && !(slots && n_slots == 0)))
+        return BDLA_ERR_NULL;
+    const auto aligned4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(o) || !aligned16(a) ||
+        !aligned16(beta) || !aligned4(slots) || !aligned4(counts))
+        return BDLA_ERR_ALIGN;
+    if (o_dtype != BDLA_BF16 && o_dtype != BDLA_F32)
+        return BDLA_ERR_DTYPE;
+    if (slots || counts)
+        BDLA_TRY(check_ws(ws, ws_bytes, kStatusBytes));
+    BDLA_CUDA(launch_delta_step(d, static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
+                                static_cast<const __nv_bfloat16 *>(v), a, beta, b, mode, state, slots, n_slots, counts, o,
+                                o_dtype == BDLA_F32, static_cast<DeviceStatus *>(ws), static_cast<cudaStream_t>(stream)));
+    return BDLA_OK;
+}
+
 bdla_status bdla_set_wait_limit_ns(uint64_t ns)
 {
     g_wait_ns.store(ns == 0 ? kDefaultWaitNs : ns);

@@ -290,6 +290,34 @@ bdla_status bdla_bwd_delta(const void *q, const void *k, const void *v, const fl
                            bdla_dims d, bdla_decay_mode mode, void *ws, size_t ws_bytes,
                            void *stream);
 
+/*
+ * Recurrent steps of the gated delta rule: d.T new tokens per sequence (one in
+ * plain decoding, a few where drafts are verified) from resident states, which
+ * may be the hT of a chunked prefill.  For token t of sequence n and head h the
+ * rule above; o_t reads the state after token t.
+ *   q, k     bf16 [B, T, H, dk];  v bf16 [B, T, H, dv];  a, beta fp32 [B, T, H]
+ *   state    fp32 [n_slots, H, dk, dv], updated in place
+ *   slots    device int32 [B]: where in `state` sequence n lives, -1 for a place
+ *            of the batch that is not used (o = 0); NULL: sequence n in slot n
+ *   n_slots  states in the pool (not looked at where slots is NULL)
+ *   counts   device int32 [B]: the state that is left is the one after the
+ *            first counts[n] of the T tokens, 0 .. T (0 leaves it as it was); o
+ *            is that of all T tokens either way, so a first call with zeros
+ *            verifies drafts and a second keeps the accepted; NULL: all T
+ *   o        bf16 or fp32 [B, T, H, dv]
+ * T >= 1 (the tokens run one after the other: long prompts belong to
+ * bdla_fwd_delta).  dk in {64, 128}, dv in {64, 128}; same b / mode rules as
+ * bdla_fwd.  A slot below -1 or not in the pool, and one that an earlier
+ * sequence of the batch has named, are recorded as BDLA_ERR_DEVICE and treated
+ * as -1; a count outside 0 .. T is recorded and leaves the state as it was.
+ * Workspace: 256 bytes, the status word alone; NULL will do where slots and
+ * counts are.
+ */
+bdla_status bdla_decode_delta(const void *q, const void *k, const void *v, const float *a, const float *beta, float b,
+                              float *state, const int32_t *slots, int n_slots, const int32_t *counts, void *o,
+                              bdla_dtype o_dtype, bdla_dims d, bdla_decay_mode mode, void *ws, size_t ws_bytes,
+                              void *stream);
+
 /* Static English description of a status code. */
 const char *bdla_status_string(bdla_status s);
 
