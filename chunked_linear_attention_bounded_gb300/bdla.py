@@ -40,7 +40,8 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_workspace_bytes_vec", "bdla_fwd_vec", "bdla_bwd_vec", "bdla_workspace_bytes_delta",
            "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes",
            "bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
-           "bdla_attn_cached", "bdla_workspace_bytes_attn", "bdla_decode_delta")
+           "bdla_attn_cached", "bdla_workspace_bytes_attn", "bdla_decode_delta",
+           "bdla_qk_norm_append")
 ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED = 0, 1, 2, 3, 4
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
 KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED = 5, 6, 7
@@ -145,7 +146,9 @@ def lib():
         L.bdla_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, f32, vp, vp, vp, AttnDims, vp, sz, vp]
         L.bdla_cache_append.argtypes = [vp, vp, CacheArgs, vp, vp, AttnDims, vp, sz, vp]
         L.bdla_attn_cached.argtypes = [vp, CacheArgs, vp, f32, vp, vp, AttnDims, vp, sz, vp]
-        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
+        L.bdla_qk_norm_append.argtypes = [QkNormArgs, vp, ctypes.c_int64, ctypes.c_int64, CacheArgs, vp, vp, vp, AttnDims, vp,
+                                          sz, vp]
+        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_qk_norm_append", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
                      "bdla_attn_cached"):
             getattr(L, name).restype = ci
         L.bdla_workspace_bytes_attn.argtypes = [ci, AttnDims, ci, ctypes.c_int64]
@@ -898,6 +901,38 @@ def cache_append(k, v, kcache, vcache, pages, lens, rows=None, counts=None, ws: 
     pk, s = k.data_ptr(), _stream_of(k, stream)
     _with_ws("bdla_cache_append", ATTN_APPEND, dims, 0, 0, ws, device, stream,
              lambda p, n: lib().bdla_cache_append(pk, pv, c, pr, pc, dims, p, n, s))
+
+
+def qk_norm_append(q, k, v, wq, wk, kcache, vcache, pages, lens, rows=None, counts=None, rotary: Optional[int] = None,
+                   base: float = 10000.0, interleaved: bool = False, positions=None, cu_seqlens=None, eps: float = 1e-6,
+                   ws: Optional[Workspace] = None, stream=None):
+    """qk_norm and cache_append in one launch: queries normed and rotated (the result, like q), keys normed and rotated
+    and values as they are written into the paged cache behind each sequence's lens[b] tokens.  q [B, T, Hq, d], k and v
+    [B, T, Hk, d] may be views of one projection; q and wq None: keys and values alone (returns None).  A token's
+    position is its place in the cache unless `positions` says otherwise.  With cu_seqlens (B = 1) the new tokens of all
+    sequences (the rows of pages and lens) are packed.  rows and counts choose what is written, as for cache_append."""
+    some = k if q is None else q
+    a, d = _norm_args(some, k, wk if q is None else wq, wk, rotary, base, interleaved, positions, cu_seqlens, eps)
+    B, T, Hk, width = k.shape
+    device = k.device
+    vt, vh = _strided(v, "v")
+    if v.shape != k.shape or v.device != device:
+        raise ValueError(f"v must be {tuple(k.shape)} on {device}, got {tuple(v.shape)} on {v.device}")
+    c = _cache_args(kcache, vcache, pages, lens, a.n_docs if a.n_docs else B, device)
+    if kcache.shape[2:] != (Hk, width):
+        raise ValueError("kcache must be [n_pages, page, Hk, d] with the heads of k")
+    pr = None if rows is None else _on(rows, "rows", torch.int32, (B, T), device)
+    pc = None if counts is None else _on(counts, "counts", torch.int32, (B,), device)
+    qn, pq = None, None
+    if q is None:
+        a.q = a.wq = None
+    else:
+        qn, = _new(device, stream, (q.shape, q.dtype))
+        pq = qn.data_ptr()
+    pv, s = v.data_ptr(), _stream_of(k, stream)
+    _with_ws("bdla_qk_norm_append", ATTN_APPEND, d, a.n_docs, 0, ws, device, stream,
+             lambda p, n: lib().bdla_qk_norm_append(a, pv, vt, vh, c, pr, pc, pq, d, p, n, s))
+    return qn
 
 
 def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float] = None,

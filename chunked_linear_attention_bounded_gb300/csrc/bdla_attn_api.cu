@@ -233,6 +233,40 @@ bdla_status bdla_cache_append(const void *k, const void *v, bdla_cache c, const 
     return BDLA_OK;
 }
 
+bdla_status bdla_qk_norm_append(bdla_qk_norm_args a, const void *v, int64_t v_token, int64_t v_head, bdla_cache c,
+                                const int32_t *rows, const int32_t *counts, void *qn, bdla_attn_dims d, void *ws,
+                                size_t ws_bytes, void *stream)
+{
+    const bool packed = a.cu_seqlens != nullptr;
+    if (!a.q) {   // keys and values alone
+        d.Hq = d.Hk;
+        a.q_token = a.q_head = 0;
+    }
+    BDLA_TRY(check_attn_dims(d, packed, a.n_docs));
+    bdla_qk_norm_args both = a;
+    if (!a.q) {
+        both.q = a.k;
+        both.wq = a.wk;
+    }
+    BDLA_TRY(check_norm(both, d));
+    BDLA_TRY(check_cache(c));
+    if (packed && (rows || counts))
+        return BDLA_ERR_UNSUPPORTED;
+    if (d.T > 0 && (!v || (a.q && !qn)))
+        return BDLA_ERR_NULL;
+    if (v_token % 8 != 0 || v_head % 8 != 0 || !aligned16(v) || !aligned16(qn))
+        return BDLA_ERR_ALIGN;
+    BDLA_TRY(check_ws(ws, ws_bytes, bdla_workspace_bytes_attn(BDLA_ATTN_APPEND, d, packed ? a.n_docs : 0, 0)));
+    DeviceStatus *st = static_cast<DeviceStatus *>(ws);
+    if (d.T == 0) {
+        BDLA_CUDA(launch_doc_report(make_attn(d, a.cu_seqlens, a.n_docs, 1.0f, ws, stream)));
+        return BDLA_OK;
+    }
+    BDLA_CUDA(launch_qk_norm_append(a, cb(v), v_token, v_head, c, rows, counts, mb(qn), d, st,
+                                    static_cast<cudaStream_t>(stream)));
+    return BDLA_OK;
+}
+
 bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, float scale, void *o, float *lse,
                              bdla_attn_dims d, void *ws, size_t ws_bytes, void *stream)
 {

@@ -43,6 +43,10 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, const __nv_bfloat16 *q, const 
 cudaError_t launch_cache_append(const __nv_bfloat16 *k, const __nv_bfloat16 *v, const bdla_cache &c,
                                 const int32_t *rows, const int32_t *counts, const bdla_attn_dims &d,
                                 DeviceStatus *st, cudaStream_t stream);
+// Norm, rotation and append in one launch (T > 0).
+cudaError_t launch_qk_norm_append(const bdla_qk_norm_args &a, const __nv_bfloat16 *v, int64_t v_token, int64_t v_head,
+                                  const bdla_cache &c, const int32_t *rows, const int32_t *counts, __nv_bfloat16 *qn,
+                                  const bdla_attn_dims &d, DeviceStatus *st, cudaStream_t stream);
 // Key splits of one call and the bytes of their partial results.
 int cached_splits(const bdla_attn_dims &d, int64_t max_keys);
 size_t cached_partial_bytes(const bdla_attn_dims &d, int splits);

@@ -9,19 +9,6 @@ namespace {
 
 using namespace cache;
 
-// Row of position t of a sequence in the cache's [n_pages * page] rows, or -1
-// where the table or the page does not reach.
-__device__ __forceinline__ int64_t cache_row(const bdla_cache &c, const int32_t *table, int t)
-{
-    const int e = t / c.page;
-    if (t < 0 || e >= c.max_pages)
-        return -1;
-    const int pg = table[e];
-    if (pg < 0 || pg >= c.n_pages)
-        return -1;
-    return (int64_t)pg * c.page + (t - e * c.page);
-}
-
 constexpr int kAppendThreads = 256;
 
 // One warp writes one row of keys and values: Hk * d features, read and

@@ -1,0 +1,154 @@
+// New tokens into a paged cache in one launch: queries and keys normed and
+// rotated as in bdla_norm.cu, keys and values written to their rows of the
+// cache.  Saves the keys' way through memory (4 bytes an element) and a launch
+// against bdla_qk_norm followed by bdla_cache_append, whose bits it gives.
+//
+// A group of lanes takes one token and a chunk of its query, key or value heads;
+// value heads are copied and run through the norm's shuffles along with their
+// warp.  The first heads are asked for before the token's place is looked up
+// (length, page), so that the two chains overlap.
+#include "bdla_cache.cuh"
+#include "bdla_norm.cuh"
+
+namespace bdla {
+
+namespace {
+
+using namespace norm;
+
+struct AppendParams {
+    const __nv_bfloat16 *v;
+    int64_t v_token, v_head;   // element strides
+    bdla_cache c;
+    const int32_t *rows, *counts;
+    int kv_chunks;             // chunks of the key heads, and of the value heads
+    DeviceStatus *st;
+};
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2)
+norm_append_kernel(const __grid_constant__ NormParams p, const __grid_constant__ Turns tu,
+                   const __grid_constant__ AppendParams a, __nv_bfloat16 *__restrict__ qn)
+{
+    using G = Group<D, INTER>;
+    if (blockIdx.x == 0 && p.cu != nullptr)
+        attn::check_offsets(p.cu, p.n_docs, p.tokens, a.st);
+    G g(p);
+    const int64_t item = (int64_t)blockIdx.x * G::kPerBlock + threadIdx.x / G::kLanes;
+    const bool any = item < (int64_t)p.tokens * p.n_chunks;
+    const int t = any ? (int)(item / p.n_chunks) : 0;
+    int c = any ? (int)(item - (int64_t)t * p.n_chunks) : 0;
+    const int kind = c < p.q_chunks ? 0 : c < p.q_chunks + a.kv_chunks ? 1 : 2;   // queries, keys, values
+    c -= kind == 0 ? 0 : kind == 1 ? p.q_chunks : p.q_chunks + a.kv_chunks;
+    const int s = kind > 0, h0 = c * p.chunk;
+    int h1 = any ? min(h0 + p.chunk, p.heads[s]) : h0;
+
+    // the token's sequence, and its number among the sequence's new ones
+    int b, j;
+    bool good = true;
+    if (p.cu != nullptr) {
+        b = document_of(p, t);
+        j = t - p.cu[b];
+        good = j >= 0 && t < p.cu[b + 1];
+    } else {
+        b = t / p.T;
+        j = t - b * p.T;
+    }
+    // place j of the sequence is filled from this token
+    int src = t;
+    if (s && a.rows != nullptr) {
+        const int r = a.rows[t];
+        good &= r >= 0 && r < p.T;
+        src = b * p.T + (good ? r : 0);
+    }
+    const __nv_bfloat16 *x = kind == 2 ? a.v + src * a.v_token : p.x[s] + src * p.token[s];
+    const int64_t step = kind == 2 ? a.v_head : p.head[s];
+    uint4 in[kBatch][2];
+    const auto fetch = [&](int first) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = first + u;
+            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
+            if (h < h1) {
+                in[u][0] = load8(x + h * step + g.f0);
+                in[u][1] = load8(x + h * step + g.f1);
+            }
+        }
+    };
+    fetch(h0);
+
+    const int len = a.c.lens[b];
+    __nv_bfloat16 *dst = qn + (int64_t)t * p.heads[0] * D;
+    if (s) {
+        int n = p.T;
+        if (a.counts != nullptr) {
+            n = a.counts[b];
+            if (n < 0 || n > p.T) {
+                if (any)
+                    set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
+                n = n < 0 ? 0 : p.T;
+            }
+        }
+        const int64_t at = (int64_t)len + j;
+        const int64_t row = good && len >= 0 && at <= INT32_MAX ? cache::cache_row(a.c, a.c.pages + (int64_t)b * a.c.max_pages, (int)at) : -1;
+        if (j >= n) {
+            h1 = h0;
+        } else if (row < 0) {
+            if (any)
+                set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
+            h1 = h0;
+        }
+        dst = static_cast<__nv_bfloat16 *>(kind == 1 ? a.c.k : a.c.v) + (row < 0 ? 0 : row) * p.heads[1] * D;
+    }
+    Pairs own, other;
+    {
+        float cs[kPairs], sn[kPairs];
+        const Pairs w = load_weights(p.w[s], g.f0, g.f1);
+        const int pos = p.positions != nullptr ? p.positions[src] : (int)((uint32_t)len + (uint32_t)j);
+        g.angles_at(g.turns ? pos : 0, tu, cs, sn);
+        weighted_rotation<INTER>(w, cs, sn, own, other);
+    }
+    for (int first = h0; first < h0 + p.chunk; first += kBatch) {
+        if (first > h0)
+            fetch(first);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = first + u;
+            const Pairs y = normed<D, INTER>(in[u][0], in[u][1], p.eps, own, other);
+            if (h >= h1)
+                continue;
+            if (kind == 2) {
+                *reinterpret_cast<uint4 *>(dst + h * D + g.f0) = in[u][0];
+                *reinterpret_cast<uint4 *>(dst + h * D + g.f1) = in[u][1];
+            } else {
+                store16(dst + h * D, g.f0, g.f1, y);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_append(const bdla_qk_norm_args &a, const __nv_bfloat16 *v, int64_t v_token, int64_t v_head,
+                                  const bdla_cache &c, const int32_t *rows, const int32_t *counts, __nv_bfloat16 *qn,
+                                  const bdla_attn_dims &d, DeviceStatus *st, cudaStream_t stream)
+{
+    const int q_heads = a.q != nullptr ? d.Hq : 0;
+    NormParams p = norm_params(a, d, head_chunk(d, q_heads + 2 * d.Hk));
+    AppendParams ap = {v, v_token, v_head, c, rows, counts, (d.Hk + p.chunk - 1) / p.chunk, st};
+    p.heads[0] = q_heads;
+    p.q_chunks = (q_heads + p.chunk - 1) / p.chunk;
+    p.n_chunks = p.q_chunks + 2 * ap.kv_chunks;
+    const Turns &tu = turns_of(a);
+    const int64_t items = (int64_t)p.tokens * p.n_chunks;
+    const int per = kThreads / (d.d / kFeat);
+    const int64_t grid = (items + per - 1) / per;
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidValue;
+    auto *kern = d.d == 64 ? (a.interleaved ? norm_append_kernel<64, true> : norm_append_kernel<64, false>)
+                           : (a.interleaved ? norm_append_kernel<128, true> : norm_append_kernel<128, false>);
+    kern<<<(unsigned)grid, kThreads, 0, stream>>>(p, tu, ap, qn);
+    return cudaGetLastError();
+}
+
+}  // namespace bdla

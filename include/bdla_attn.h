@@ -2,8 +2,8 @@
  * bdla_attn.h — the softmax layer that stands beside the linear attention of
  * bdla.h in a hybrid stack: norm and rotation of queries and keys, causal
  * softmax attention with grouped heads over packed documents, the paged cache
- * of its keys and values, and attention of a sequence's newest tokens over
- * that cache.
+ * of its keys and values (norm, rotation and append also in one call), and
+ * attention of a sequence's newest tokens over that cache.
  *
  * Conventions are those of bdla.h: device pointers owned by the caller, no
  * allocation and no synchronisation inside a call, every call ordered on
@@ -128,6 +128,31 @@ typedef struct {
  */
 bdla_status bdla_cache_append(const void *k, const void *v, bdla_cache c, const int32_t *rows,
                               const int32_t *counts, bdla_attn_dims d, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * bdla_qk_norm and bdla_cache_append in one launch, with their bits: queries
+ * normed and rotated to qn, keys normed and rotated into the cache, values into
+ * the cache.  A token's position is its place in the cache (lens[b] + j for the
+ * j-th new token of sequence b) unless `a` gives positions.
+ *   a        as for bdla_qk_norm; q NULL: keys and values alone (wq and qn may
+ *            be NULL, d.Hq is not looked at).  With cu_seqlens (B = 1, n_docs
+ *            sequences) the tokens of all sequences are packed, as many of each
+ *            as there happen to be (prompts and single tokens in one call)
+ *   v        bf16 [B, T, Hk, d] with element strides of a token and of a head,
+ *            multiples of 8, as q and k
+ *   rows, counts   as for bdla_cache_append (NULL for packed tokens,
+ *            BDLA_ERR_UNSUPPORTED): place j takes the keys and values of row
+ *            rows[b][j], at that place's position, or at positions[b][rows[b][j]]
+ *            where positions are given.  They say nothing about queries: all T
+ *            are normed, row j at place j
+ *   qn       bf16 [B, T, Hq, d] contiguous
+ * lens is not changed; what bdla_cache_append records as BDLA_ERR_DEVICE and does
+ * not write is treated so here too, and so are malformed cu_seqlens and the
+ * tokens that they give to no sequence.  Neither q, k nor v may lie in the cache.
+ */
+bdla_status bdla_qk_norm_append(bdla_qk_norm_args a, const void *v, int64_t v_token, int64_t v_head, bdla_cache c,
+                                const int32_t *rows, const int32_t *counts, void *qn, bdla_attn_dims d, void *ws,
+                                size_t ws_bytes, void *stream);
 
 /*
  * Softmax attention of a sequence's T newest tokens (1 .. 64), whose keys and
