@@ -41,10 +41,10 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes",
            "bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
            "bdla_attn_cached", "bdla_workspace_bytes_attn", "bdla_decode_delta",
-           "bdla_qk_norm_append")
-ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED = 0, 1, 2, 3, 4
+           "bdla_qk_norm_append", "bdla_attn_shared")
+ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED, ATTN_SHARED = 0, 1, 2, 3, 4, 5
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
-KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED = 5, 6, 7
+KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED, KERNEL_ATTN_SHARED = 5, 6, 7, 8
 STALL_NONE, STALL_PRODUCER, STALL_MMA, STALL_EPILOGUE = 0, 1, 2, 3
 
 
@@ -148,7 +148,8 @@ def lib():
         L.bdla_attn_cached.argtypes = [vp, CacheArgs, vp, f32, vp, vp, AttnDims, vp, sz, vp]
         L.bdla_qk_norm_append.argtypes = [QkNormArgs, vp, ctypes.c_int64, ctypes.c_int64, CacheArgs, vp, vp, vp, AttnDims, vp,
                                           sz, vp]
-        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_qk_norm_append", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
+        L.bdla_attn_shared.argtypes = [vp, CacheArgs, vp, vp, ci, vp, f32, vp, vp, AttnDims, vp, sz, vp]
+        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_qk_norm_append", "bdla_attn_shared", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
                      "bdla_attn_cached"):
             getattr(L, name).restype = ci
         L.bdla_workspace_bytes_attn.argtypes = [ci, AttnDims, ci, ctypes.c_int64]
@@ -935,13 +936,8 @@ def qk_norm_append(q, k, v, wq, wk, kcache, vcache, pages, lens, rows=None, coun
     return qn
 
 
-def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float] = None,
-                ws: Optional[Workspace] = None, stream=None):
-    """Attention of each sequence's T newest tokens (q [B, T, Hq, d], T <= 64)
-    over the paged cache, their own keys and values already appended at
-    positions lens[b] .. lens[b] + T - 1.  tree: int64 [B, T] bit masks of the
-    new tokens each one sees (None: those up to and with itself).  Returns
-    (o like q, lse fp32 [B, T, Hq]); a token that sees nothing gets 0 and -inf."""
+def _newest(q, kcache, vcache, pages, lens, tree, scale, stream):
+    """The checked arguments of a call of each sequence's newest tokens over the cache, and its outputs."""
     _check(q, "q", torch.bfloat16, 4, here=True)
     B, T, Hq, d = q.shape
     device = q.device
@@ -951,8 +947,34 @@ def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float
     pt = None if tree is None else _on(tree, "tree", torch.int64, (B, T), device)
     dims = AttnDims(B, T, Hq, kcache.shape[2], d)
     o, lse = _new(device, stream, (q.shape, q.dtype), ((B, T, Hq), torch.float32))
-    scale = d ** -0.5 if scale is None else scale
+    return c, pt, dims, o, lse, d ** -0.5 if scale is None else scale
+
+
+def attn_cached(q, kcache, vcache, pages, lens, tree=None, scale: Optional[float] = None,
+                ws: Optional[Workspace] = None, stream=None):
+    """Attention of each sequence's T newest tokens (q [B, T, Hq, d], T <= 64)
+    over the paged cache, their own keys and values already appended at
+    positions lens[b] .. lens[b] + T - 1.  tree: int64 [B, T] bit masks of the
+    new tokens each one sees (None: those up to and with itself).  Returns
+    (o like q, lse fp32 [B, T, Hq]); a token that sees nothing gets 0 and -inf."""
+    c, pt, dims, o, lse, scale = _newest(q, kcache, vcache, pages, lens, tree, scale, stream)
     pq, s = q.data_ptr(), _stream_of(q, stream)
-    _with_ws("bdla_attn_cached", ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, device, stream,
+    _with_ws("bdla_attn_cached", ATTN_CACHED, dims, 0, c.max_pages * c.page, ws, q.device, stream,
              lambda p, n: lib().bdla_attn_cached(pq, c, pt, scale, o.data_ptr(), lse.data_ptr(), dims, p, n, s))
+    return o, lse
+
+
+def attn_shared(q, kcache, vcache, pages, lens, cu_groups, shared, tree=None, scale: Optional[float] = None,
+                ws: Optional[Workspace] = None, stream=None):
+    """attn_cached for a batch in which groups of consecutive sequences share the positions that they begin with: group g
+    is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [n_groups + 1]), whose tables name the same pages for
+    their first shared[g] positions (int32 [n_groups]).  Those are read once for the whole group.  Returns (o, lse) as
+    attn_cached does, up to rounding."""
+    c, pt, dims, o, lse, scale = _newest(q, kcache, vcache, pages, lens, tree, scale, stream)
+    n = shared.shape[0] if isinstance(shared, torch.Tensor) and shared.dim() == 1 else 0
+    ps = _on(shared, "shared", torch.int32, (n,), q.device)
+    pg = _on(cu_groups, "cu_groups", torch.int32, (n + 1,), q.device)
+    pq, s = q.data_ptr(), _stream_of(q, stream)
+    _with_ws("bdla_attn_shared", ATTN_SHARED, dims, n, c.max_pages * c.page, ws, q.device, stream,
+             lambda p, m: lib().bdla_attn_shared(pq, c, pg, ps, n, pt, scale, o.data_ptr(), lse.data_ptr(), dims, p, m, s))
     return o, lse

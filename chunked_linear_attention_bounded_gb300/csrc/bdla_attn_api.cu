@@ -118,12 +118,39 @@ AttnProblem make_attn(const bdla_attn_dims &d, const int32_t *cu, int n_docs, fl
 template <typename T> const __nv_bfloat16 *cb(const T *p) { return static_cast<const __nv_bfloat16 *>(p); }
 __nv_bfloat16 *mb(void *p) { return static_cast<__nv_bfloat16 *>(p); }
 
+// Calls of a sequence's newest tokens over the cache.
+bdla_status check_newest(const void *q, const bdla_cache &c, const uint64_t *tree, float scale, const void *o,
+                         const float *lse, const bdla_attn_dims &d)
+{
+    BDLA_TRY(check_attn_dims(d, false, 0));
+    if (d.T < 1)
+        return BDLA_ERR_SHAPE;
+    if (d.T > 64)
+        return BDLA_ERR_UNSUPPORTED;
+    if ((int64_t)d.B * d.T * d.Hq > INT32_MAX)   // rows are a grid extent
+        return BDLA_ERR_TOO_LARGE;
+    BDLA_TRY(check_scale(scale));
+    BDLA_TRY(check_cache(c));
+    if (!q || !o || !lse)
+        return BDLA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
+        return BDLA_ERR_ALIGN;
+    return BDLA_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t max_keys)
 {
+    if (op == BDLA_ATTN_SHARED) {   // n_docs: groups
+        if (check_attn_dims(d, false, 0) != BDLA_OK || max_keys < 0 || max_keys > INT32_MAX || d.T < 1 || d.T > 64 ||
+            n_docs < 1 || n_docs > 65535 || (int64_t)d.B * d.T * d.Hq > INT32_MAX || !shared_fits(d, n_docs, max_keys))
+            return 0;
+        return round_up(kStatusBytes) + shared_bytes(d, n_docs);
+    }
     if (check_attn_dims(d, n_docs > 0, n_docs) != BDLA_OK)
         return 0;
     const size_t head = round_up(kStatusBytes);
@@ -270,23 +297,33 @@ bdla_status bdla_qk_norm_append(bdla_qk_norm_args a, const void *v, int64_t v_to
 bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, float scale, void *o, float *lse,
                              bdla_attn_dims d, void *ws, size_t ws_bytes, void *stream)
 {
-    BDLA_TRY(check_attn_dims(d, false, 0));
-    if (d.T < 1)
-        return BDLA_ERR_SHAPE;
-    if (d.T > 64)
-        return BDLA_ERR_UNSUPPORTED;
-    if ((int64_t)d.B * d.T * d.Hq > INT32_MAX)   // rows are a grid extent
-        return BDLA_ERR_TOO_LARGE;
-    BDLA_TRY(check_scale(scale));
-    BDLA_TRY(check_cache(c));
-    if (!q || !o || !lse)
-        return BDLA_ERR_NULL;
-    if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
-        (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
-        return BDLA_ERR_ALIGN;
+    BDLA_TRY(check_newest(q, c, tree, scale, o, lse, d));
     const int64_t max_keys = (int64_t)c.max_pages * c.page;
     BDLA_TRY(check_ws(ws, ws_bytes, bdla_workspace_bytes_attn(BDLA_ATTN_CACHED, d, 0, max_keys)));
     BDLA_CUDA(launch_attn_cached(cb(q), c, tree, scale, mb(o), lse, d, max_keys,
+                                 static_cast<char *>(ws) + round_up(kStatusBytes), static_cast<DeviceStatus *>(ws),
+                                 static_cast<cudaStream_t>(stream)));
+    return BDLA_OK;
+}
+
+bdla_status bdla_attn_shared(const void *q, bdla_cache c, const int32_t *cu_groups, const int32_t *shared, int n_groups,
+                             const uint64_t *tree, float scale, void *o, float *lse, bdla_attn_dims d, void *ws,
+                             size_t ws_bytes, void *stream)
+{
+    BDLA_TRY(check_newest(q, c, tree, scale, o, lse, d));
+    if (n_groups < 1)
+        return BDLA_ERR_SHAPE;
+    if (n_groups > 65535)
+        return BDLA_ERR_UNSUPPORTED;
+    if (!cu_groups || !shared)
+        return BDLA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(cu_groups) & 3u) != 0 || (reinterpret_cast<uintptr_t>(shared) & 3u) != 0)
+        return BDLA_ERR_ALIGN;
+    const int64_t max_keys = (int64_t)c.max_pages * c.page;
+    if (!shared_fits(d, n_groups, max_keys))
+        return BDLA_ERR_TOO_LARGE;
+    BDLA_TRY(check_ws(ws, ws_bytes, bdla_workspace_bytes_attn(BDLA_ATTN_SHARED, d, n_groups, max_keys)));
+    BDLA_CUDA(launch_attn_shared(cb(q), c, cu_groups, shared, n_groups, tree, scale, mb(o), lse, d,
                                  static_cast<char *>(ws) + round_up(kStatusBytes), static_cast<DeviceStatus *>(ws),
                                  static_cast<cudaStream_t>(stream)));
     return BDLA_OK;

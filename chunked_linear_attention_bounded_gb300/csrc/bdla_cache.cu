@@ -121,7 +121,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 using attn::ex2;
 
-template <int D, int WR>
+// LIST: the pieces are those of a list on the device, which an earlier kernel of
+// the same call has made (bdla_cache_shared.cu).
+template <int D, int WR, bool LIST>
 __global__ void __launch_bounds__(kCThreads, D == 128 ? 3 : 4)
 cached_kernel(const __grid_constant__ Call a, int row_blocks)
 {
@@ -136,29 +138,55 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     const bdla_cache &c = a.c;
     const int T = a.T, Hq = a.Hq, Hk = a.Hk, ns = a.pieces.ns;
     // heads of one position lie next to each other in the cache: keep them together in time
-    int idx = blockIdx.x;
-    const int rb = idx % row_blocks;
-    idx /= row_blocks;
-    const int kh = idx % Hk;
-    idx /= Hk;
-    const int piece = idx % ns, b = idx / ns;
+    const int G = Hq / Hk;
+    int idx = blockIdx.x, kh, piece = 0, b;
+    int k0, k1, len, R, row0;   // positions, committed ones, rows of the key head and the CTA's first
+    int64_t tok0, part;         // the rows' first token, and the partial sums' first row (-1: none)
     attn::next_may_start();
-    const Cut cut = cut_of(c, b, T, a.pieces);
-    if (piece >= cut.used)
-        return;
-    if (piece == 0 && kh == 0 && rb == 0 && tid == 0 && cut_is_short(c, cut, T))
-        set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
-    const int G = Hq / Hk, R = T * G;
-    const int k0 = piece * cut.size, k1 = min(cut.end, k0 + cut.size);
+    if (LIST) {
+        attn::wait_for_previous();
+        kh = idx % Hk;
+        idx /= Hk;
+        if (idx >= *a.n_list)
+            return;
+        const Work w = a.list[idx];
+        b = w.b;
+        k0 = w.k0;
+        k1 = w.k1;
+        len = w.len;
+        R = w.R;
+        row0 = w.row0;
+        tok0 = w.tok0;
+        part = w.part < 0 ? -1 : (int64_t)w.part + (int64_t)kh * R;
+    } else {
+        const int rb = idx % row_blocks;
+        idx /= row_blocks;
+        kh = idx % Hk;
+        idx /= Hk;
+        piece = idx % ns;
+        b = idx / ns;
+        const Cut cut = cut_of(c, b, T, a.pieces);
+        if (piece >= cut.used)
+            return;
+        if (piece == 0 && kh == 0 && rb == 0 && tid == 0 && cut_is_short(c, cut, T))
+            set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
+        k0 = piece * cut.size;
+        k1 = min(cut.end, k0 + cut.size);
+        len = cut.len;
+        R = T * G;
+        row0 = rb * MR;
+        tok0 = (int64_t)b * T;
+        part = cut.used > 1 ? (((int64_t)b * Hk + kh) * ns + piece) * R : -1;
+    }
     const int nt = (k1 - k0 + kKeys - 1) / kKeys;
     const int32_t *table = c.pages + (int64_t)b * c.max_pages;
-    const bool drafts = k1 > cut.len;   // the piece holds new tokens
+    const bool drafts = k1 > len;   // the piece holds new tokens
     const uint64_t seen = drafts ? sees_any(a.tree, b, T, lane) : 0;
 
     // page table entry of position t (a tile's 64 positions, by the first 64 threads)
     auto lookup = [&](int t) { return t < k1 ? table[a.div.entry(t)] : -1; };
     auto place = [&](int n, int t, int pg) {
-        bool live = t < k1 && (t < cut.len || ((seen >> (t - cut.len)) & 1));
+        bool live = t < k1 && (t < len || ((seen >> (t - len)) & 1));
         if (live && (pg < 0 || pg >= c.n_pages)) {
             set_status(a.st, BDLA_ERR_DEVICE, (unsigned)b);
             live = false;
@@ -194,10 +222,10 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     load(1, 1);
 
     // query fragments: rows lane/4 and lane/4 + 8 of the warp's 16
-    const int r0 = rb * MR + 16 * wr + (lane >> 2), r1 = r0 + 8;
+    const int r0 = row0 + 16 * wr + (lane >> 2), r1 = r0 + 8;
     const int i0 = min(r0, R - 1) / G, i1 = min(r1, R - 1) / G;
-    const __nv_bfloat16 *qa = a.q + (((int64_t)b * T + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
-    const __nv_bfloat16 *qb = a.q + (((int64_t)b * T + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qa = a.q + ((tok0 + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qb = a.q + ((tok0 + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
     uint32_t fq[D / 16][4];
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -247,12 +275,12 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
         load(n + 2, 0);
         const uint64_t ok = (uint64_t)sm.valid[n & 3][0] | ((uint64_t)sm.valid[n & 3][1] << 32);
         const int t0 = k0 + n * kKeys;
-        if (ok != ~0ull || t0 + kKeys > cut.len) {
+        if (ok != ~0ull || t0 + kKeys > len) {
 #pragma unroll
             for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int kk = wk * KW + 8 * i + 2 * (lane & 3) + u, j = t0 + kk - cut.len;
+                    const int kk = wk * KW + 8 * i + 2 * (lane & 3) + u, j = t0 + kk - len;
                     const bool live = (ok >> kk) & 1;
                     if (!(live && (j < 0 || ((see0 >> j) & 1))))
                         s[i][u] = -INFINITY;
@@ -339,7 +367,7 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     }
     __syncthreads();
     for (int e = tid; e < MR * (D / 4); e += kCThreads) {
-        const int r = e / (D / 4), d4 = 4 * (e % (D / 4)), row = rb * MR + r;
+        const int r = e / (D / 4), d4 = 4 * (e % (D / 4)), row = row0 + r;
         if (row >= R)
             break;
         float m = -INFINITY, l = 0.0f;
@@ -358,13 +386,13 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
             v.z = fmaf(y.z, f, v.z);
             v.w = fmaf(y.w, f, v.w);
         }
-        if (cut.used > 1) {
-            const int64_t at = (((int64_t)b * Hk + kh) * ns + piece) * R + row;
+        if (part >= 0) {
+            const int64_t at = part + row;
             *reinterpret_cast<float4 *>(a.part_o + at * D + d4) = v;
             if (d4 == 0)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m, l);
         } else {
-            const int64_t at = ((int64_t)b * T + row / G) * Hq + kh * G + row % G;
+            const int64_t at = (tok0 + row / G) * Hq + kh * G + row % G;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             *reinterpret_cast<uint2 *>(a.o + at * D + d4) =
                 make_uint2(sm100::pack_bf16(v.x * inv, v.y * inv), sm100::pack_bf16(v.z * inv, v.w * inv));
@@ -534,13 +562,33 @@ static cudaError_t cached_go(const Call &a, const bdla_attn_dims &d, cudaStream_
     const int R = d.T * (d.Hq / d.Hk), row_blocks = (R + 16 * WR - 1) / (16 * WR);
     const int64_t grid = (int64_t)d.B * d.Hk * row_blocks * a.pieces.ns;
     const size_t smem = sizeof(CachedSmem<D>);
-    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
-    cached_kernel<D, WR><<<(unsigned)grid, kCThreads, smem, stream>>>(a, row_blocks);
+    cached_kernel<D, WR, false><<<(unsigned)grid, kCThreads, smem, stream>>>(a, row_blocks);
     return cudaGetLastError();
+}
+
+template <int D, int WR>
+static cudaError_t list_go(const Call &a, int most, cudaStream_t stream)
+{
+    const size_t smem = sizeof(CachedSmem<D>);
+    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    return attn::launch_second(cached_kernel<D, WR, true>, (unsigned)((int64_t)most * a.Hk), kCThreads, smem, stream, a, 1);
+}
+
+// The pieces of a list of at most `most`, with 16 `row_tiles` rows a CTA.
+cudaError_t launch_cached_list(const Call &a, int d, int row_tiles, int most, cudaStream_t stream)
+{
+    if ((int64_t)most * a.Hk > INT32_MAX)
+        return cudaErrorInvalidValue;
+    if (d == 64)
+        return row_tiles == 1 ? list_go<64, 1>(a, most, stream) : list_go<64, 2>(a, most, stream);
+    return row_tiles == 1 ? list_go<128, 1>(a, most, stream) : list_go<128, 2>(a, most, stream);
 }
 
 template <int D> static cudaError_t combine_go(const Call &a, int64_t rows, cudaStream_t stream)

@@ -2,6 +2,8 @@
 // cut into pieces, and what a new token sees.
 #pragma once
 
+#include <cuda.h>
+
 #include "bdla_attn_internal.h"
 
 namespace bdla {
@@ -91,6 +93,19 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// A piece of attention over the cache that a plan on the device hands to a CTA
+// of each key head: rows row0 .. of the R rows (tokens tok0 .. times query heads
+// of the group) that see positions k0 .. k1 - 1 of sequence b's page table, and
+// of those past `len` as new tokens what the masks say.  The results go to the
+// rows part + kh R + .. of the partial sums, or to the outputs where part < 0.
+struct Work {
+    int b, k0, k1, len;
+    int tok0, R, row0, part;
+};
+
+// Map over the cache's rows [n_pages * page][Hk * d]: boxes of 64 features x `run` rows.
+bool make_rows_map(CUtensorMap *map, const void *ptr, int64_t width, int64_t rows, int run);
+
 struct Call {
     const __nv_bfloat16 *q;
     bdla_cache c;
@@ -103,12 +118,15 @@ struct Call {
     PageDiv div;
     Pieces pieces;
     DeviceStatus *st;
+    const Work *list;     // of a planned call, n_list on the device
+    const int *n_list;
 };
 
 }  // namespace cache
 
 // More than 32 rows a key head: tensor-memory MMAs (bdla_cache_wide.cu).
 constexpr int kWideRows = 256;
+cudaError_t launch_cached_list(const cache::Call &call, int d, int row_tiles, int most, cudaStream_t stream);
 cudaError_t launch_cached_wide(const cache::Call &call, const bdla_attn_dims &d, cudaStream_t stream);
 
 }  // namespace bdla

@@ -1,0 +1,983 @@
+// Attention of the newest tokens over the paged cache where groups of sequences
+// share the pages that their tables begin with.
+//
+//   o = (sum_t e^{s_t - m} v_t) / sum_t e^{s_t - m}
+// over a sequence's positions is joined from sums over any parts of them, so the
+// shared positions of a group are taken once, with the rows of all its sequences
+// (new tokens times query heads of the key head) as one matrix, and each
+// sequence's own positions by themselves.  Four kernels in stream order, each
+// launched ahead of the end of the one before:
+//
+//   plan     one CTA reads offsets and lengths and cuts the work: how far each
+//            group shares, tiles for the wide kernel, pieces for the narrow one
+//   wide     groups (and trees of drafts) of more than 32 rows a key head, on
+//            the tensor cores: this file
+//   narrow   everything of up to 32 rows: the kernel of bdla_cache.cu over the
+//            plan's list; a sequence of one piece that shares nothing is
+//            finished there
+//   join     the sums of a row's pieces, in their order
+//
+// Everything that the cut depends on (group sizes, shared lengths, lengths) is on
+// the device and changes from step to step under a captured graph, so the grids
+// are sized from the tensors' shapes and the plan fills them.
+#include <cudaTypedefs.h>
+
+#include "bdla_attn_sm100.cuh"
+#include "bdla_cache.cuh"
+
+namespace bdla {
+
+namespace {
+
+using namespace sm100;
+using namespace attn;
+using namespace cache;
+
+constexpr int kNarrowRows = 32;   // rows a key head up to which warp MMAs take a group
+constexpr int kWideTile = 256;    // rows of a CTA of the wide kernel
+constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
+
+// What the wide kernel walks: positions first .. end - 1 of sequence b's table
+// for the R rows from token tok0 on, as blocks of 256 rows times key heads, each
+// of nt tiles of 128 positions.  `base`: tiles of the entries before it.
+struct WideEntry {
+    int64_t base;
+    int b, tok0, R, first, end, len, nt, part;
+};
+
+// Where an entry's partial sums are.  wide: pieces follow from the tiles' cut;
+// narrow: np pieces; np < 0: its rows are finished.
+struct Parts {
+    int64_t base;
+    int nt, R, part, np, tok0, pad;
+};
+
+struct Head {
+    int64_t tiles;   // of the wide kernel
+    int per_cta;     // tiles of a CTA
+    int n_list;      // pieces of the narrow kernel
+};
+
+// Entries are the groups, then the sequences.
+struct Plan {
+    Head *head;
+    WideEntry *wide;
+    Parts *parts;
+    Work *list;
+    int *first_entry;   // of each CTA of the wide kernel
+    int *group;         // of each sequence, -1: none
+    int *len;           // positions of each entry (scratch of the plan)
+    float *part_o, *part_ml;
+};
+
+struct Sizes {
+    int B, T, G, Hk, D, n_groups;
+    int ctas;            // of the wide kernel
+    bool wide, own_wide; // the wide kernel runs; it takes the sequences' own positions too
+    int narrow_tiles;    // rows of a narrow CTA, in 16
+    int slots;           // narrow CTAs that the GPU holds
+    int extra;           // pieces of the narrow list beyond one for every block of rows
+    int most;            // pieces of the narrow list
+    int64_t rows;        // of partial sums
+};
+
+// Bounds of the plan.  Narrow: a piece size of at least the (block-weighted)
+// positions over `extra` cuts at most `extra` pieces beyond the first of each
+// block; sequences have one block, groups of at most 32 rows one or two, and a
+// group that shares has two sequences or more.  Wide: a unit of nt tiles lies in
+// nt / per_cta + 2 CTAs at most; nt R <= 256 tiles of the blocks, and all tiles
+// are at most ctas x per_cta.
+Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
+{
+    Sizes s;
+    s.B = d.B;
+    s.T = d.T;
+    s.G = d.Hq / d.Hk;
+    s.Hk = d.Hk;
+    s.D = d.d;
+    s.n_groups = n_groups;
+    s.ctas = sm_count();
+    const int64_t R = (int64_t)d.T * s.G, all = R * d.B;
+    s.wide = all > kNarrowRows;
+    s.own_wide = R > kNarrowRows;
+    s.narrow_tiles = (s.wide ? R : all) <= 16 ? 1 : 2;
+    s.slots = s.ctas * (d.d == 128 ? 3 : 4);
+    s.extra = 4 * ((s.slots + d.Hk - 1) / d.Hk);
+    const int groups = n_groups < d.B / 2 ? n_groups : d.B / 2;
+    s.most = s.own_wide ? 0 : d.B + 2 * groups + s.extra;
+    s.rows = 0;
+    if (s.wide)
+        s.rows += 2 * all * d.Hk * (s.own_wide ? 2 : 1) + (int64_t)kWideTile * s.ctas;
+    if (!s.own_wide)
+        s.rows += (2 * all + (int64_t)kNarrowRows * s.extra) * d.Hk;
+    return s;
+}
+
+size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t carve(const Sizes &s, char *at, Plan *p)
+{
+    const size_t entries = (size_t)s.n_groups + s.B;
+    size_t off = 0;
+    const auto take = [&](auto *&ptr, size_t n) {
+        ptr = reinterpret_cast<std::remove_reference_t<decltype(ptr)>>(at + off);
+        off += aligned(n * sizeof(*ptr));
+    };
+    take(p->head, 1);
+    take(p->wide, entries);
+    take(p->parts, entries);
+    take(p->list, (size_t)s.most);
+    take(p->first_entry, (size_t)s.ctas);
+    take(p->group, (size_t)s.B);
+    take(p->len, entries);
+    take(p->part_o, (size_t)s.rows * s.D);
+    take(p->part_ml, (size_t)s.rows * 2);
+    return off;
+}
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanEntries = 8192;   // whose lengths fit into shared memory
+constexpr int kLeastShared = 64;     // shared positions that are worth a piece of their own
+constexpr int kLeastTiles = 2;       // tiles of a wide CTA
+constexpr int kSizes = 32;           // piece sizes that are weighed, one a warp
+
+// The narrow kernel's piece sizes, in tiles of 64: 2, 3, 4, 6, 8, 12 ..
+__device__ __forceinline__ int64_t narrow_size(int i) { return (int64_t)64 * ((i & 1 ? 3 : 2) << (i >> 1)); }
+
+struct Sums {
+    int64_t tiles, positions;
+    int rows, pieces, wides;
+    __device__ __forceinline__ void add(const Sums &o)
+    {
+        tiles += o.tiles;
+        positions += o.positions;
+        rows += o.rows;
+        pieces += o.pieces;
+        wides += o.wides;
+    }
+    __device__ __forceinline__ Sums shifted(int by) const
+    {
+        return {__shfl_up_sync(0xffffffffu, tiles, by), __shfl_up_sync(0xffffffffu, positions, by),
+                __shfl_up_sync(0xffffffffu, rows, by), __shfl_up_sync(0xffffffffu, pieces, by),
+                __shfl_up_sync(0xffffffffu, wides, by)};
+    }
+};
+
+// Sums over the threads before this one, and of all (every thread of the CTA).
+__device__ __forceinline__ Sums scan(const Sums &mine, Sums *of_warp, Sums &all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums s = mine;
+#pragma unroll
+    for (int by = 1; by < 32; by <<= 1) {
+        const Sums o = s.shifted(by);
+        if (lane >= by)
+            s.add(o);
+    }
+    __syncthreads();
+    if (lane == 31)
+        of_warp[warp] = s;
+    __syncthreads();
+    Sums before = {};
+    all = {};
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w == warp)
+            before = all;
+        all.add(of_warp[w]);
+    }
+    s.add(before);
+    s.tiles -= mine.tiles;
+    s.positions -= mine.positions;
+    s.rows -= mine.rows;
+    s.pieces -= mine.pieces;
+    s.wides -= mine.wides;
+    return s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu, const int32_t *shared, const __grid_constant__ Sizes z,
+            const __grid_constant__ Plan p, DeviceStatus *st)
+{
+    extern __shared__ int smem_len[];
+    __shared__ Sums of_warp[kPlanThreads / 32];
+    __shared__ int64_t cost[kSizes];
+    next_may_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int NG = z.n_groups, E = NG + z.B, rows_of = z.T * z.G;
+    int *len = E <= kPlanEntries ? smem_len : p.len;
+    const int cap = c.max_pages * c.page;
+
+    // groups: inside the batch and in order, or there are none
+    bool bad = false;
+    for (int g = tid; g < NG; g += kPlanThreads) {
+        const int n0 = cu[g], n1 = cu[g + 1], s = shared[g];
+        bad |= n0 < 0 || n1 < n0 || n1 > z.B;
+        if (s < 0)
+            set_status(st, BDLA_ERR_DEVICE, (unsigned)g);
+        len[g] = min(max(s, 0), cap);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0)
+        set_status(st, BDLA_ERR_DEVICE, 0u);
+    // a group shares what the shortest of its sequences has in the cache
+    for (int b = tid; b < z.B; b += kPlanThreads) {
+        int g = -1;
+        if (!bad) {
+            int lo = 0, hi = NG;   // the last offset at or before b
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cu[mid] <= b)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            g = lo < NG && cu[lo] <= b ? lo : -1;
+        }
+        if (g >= 0)
+            atomicMin(&len[g], max(c.lens[b], 0));
+        p.group[b] = g;
+    }
+    __syncthreads();
+    // one sequence reads nothing twice
+    for (int g = tid; g < NG; g += kPlanThreads)
+        if (bad || cu[g + 1] - cu[g] < 2 || len[g] < kLeastShared)
+            len[g] = 0;
+    __syncthreads();
+    for (int b = tid; b < z.B; b += kPlanThreads) {
+        const int l = c.lens[b], g = p.group[b];
+        const int64_t all = (int64_t)l + z.T;
+        if (l < 0 || all > cap)
+            set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
+        const int end = l < 0 ? 0 : (int)(all < cap ? all : cap);
+        len[NG + b] = end - (g >= 0 ? len[g] : 0);
+    }
+    __syncthreads();
+
+    // one entry: rows, first token, whether it is the wide kernel's, its blocks of rows
+    struct Entry {
+        int R, tok0, blocks;
+        bool wide;
+    };
+    const int mr = 16 * z.narrow_tiles;
+    const auto entry = [&](int e) {
+        Entry x;
+        x.R = rows_of;
+        x.tok0 = (e - NG) * z.T;
+        x.wide = z.own_wide;
+        if (e < NG) {
+            x.tok0 = len[e] > 0 ? cu[e] * z.T : 0;
+            x.R = len[e] > 0 ? (cu[e + 1] - cu[e]) * rows_of : 0;
+            x.wide = x.R > kNarrowRows;
+        }
+        x.blocks = x.wide ? (x.R + kWideTile - 1) / kWideTile : (x.R + mr - 1) / mr;
+        return x;
+    };
+    const auto tiles_of = [](int n) { return (n + BT - 1) / BT; };
+    Sums total = {}, mine = {};
+    for (int e = tid; e < E; e += kPlanThreads) {
+        const Entry x = entry(e);
+        if (x.wide)
+            mine.tiles += (int64_t)x.blocks * z.Hk * tiles_of(len[e]);
+        else
+            mine.positions += (int64_t)x.blocks * len[e];
+    }
+    scan(mine, of_warp, total);
+    const int64_t tiles = total.tiles;
+    int64_t even = (tiles + z.ctas - 1) / z.ctas;
+    const int per_cta = (int)(even < kLeastTiles ? kLeastTiles : even);
+    // The narrow pieces' size: their work (a piece costs its start-up, about 128
+    // positions) spread over the CTAs that the GPU holds, plus the last piece's
+    // own length, plus what the join reads of the longest entry's pieces.
+    const int64_t least = z.extra > 0 ? (total.positions + z.extra - 1) / z.extra : 0;
+    const auto size_of = [&](int i) {
+        const int64_t s = narrow_size(i);
+        return s >= least ? s : (least + 63) / 64 * 64;
+    };
+    int size = 64;   // (no narrow piece: not looked at)
+    if (z.most > 0) {
+        const int64_t s = size_of(warp);
+        int64_t pieces = 0, longest = 0;
+        for (int e = lane; e < E; e += 32) {
+            const Entry x = entry(e);
+            if (x.wide)
+                continue;
+            const int64_t n = ((int64_t)len[e] + s - 1) / s;
+            pieces += x.blocks * (e >= NG && n < 1 ? 1 : n);
+            longest = n > longest ? n : longest;
+        }
+        for (int w = 16; w > 0; w >>= 1) {
+            pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
+            const int64_t o = __shfl_xor_sync(0xffffffffu, longest, w);
+            longest = o > longest ? o : longest;
+        }
+        if (lane == 0)
+            cost[warp] = (total.positions + 128 * pieces) * z.Hk / z.slots + s + 4 * longest;
+        __syncthreads();
+        int best = 0;
+        for (int i = 1; i < kSizes; ++i)
+            best = cost[i] < cost[best] ? i : best;
+        const int64_t chosen = size_of(best);
+        size = (int)(chosen < INT32_MAX - 64 ? chosen : INT32_MAX - 64);
+    }
+
+    // places of everything, entries in order
+    Sums done = {};
+    for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
+        const int e = e0 + tid;
+        Sums m = {};
+        Entry x = {};
+        int n = 0, np = 0;
+        bool direct = false;
+        if (e < E) {
+            x = entry(e);
+            n = len[e];
+            if (x.wide) {
+                const int nt = tiles_of(n);
+                m.tiles = (int64_t)x.blocks * z.Hk * nt;
+                m.rows = nt > 0 ? ((nt + per_cta - 1) / per_cta + 1) * x.R * z.Hk : 0;
+                m.wides = nt > 0;
+            } else {
+                np = (int)(((int64_t)n + size - 1) / size);
+                if (e >= NG) {
+                    np = np < 1 ? 1 : np;
+                    const int g = p.group[e - NG];
+                    direct = np == 1 && (g < 0 || len[g] == 0);
+                }
+                m.pieces = x.blocks * np;
+                m.rows = direct ? 0 : np * x.R * z.Hk;
+            }
+        }
+        Sums all, at = scan(m, of_warp, all);
+        at.add(done);
+        done.add(all);
+        if (e >= E)
+            continue;
+        const int b = e < NG ? (n > 0 ? cu[e] : 0) : e - NG;
+        const int first = e < NG || p.group[b] < 0 ? 0 : len[p.group[b]];
+        const int seen = e < NG ? kSeen : max(c.lens[b], 0);
+        p.parts[e] = {at.tiles, x.wide ? tiles_of(n) : 0, x.R, at.rows, direct ? -1 : np, x.tok0, 0};
+        if (m.wides) {
+            p.wide[at.wides] = {at.tiles, b, x.tok0, x.R, first, first + n, seen, tiles_of(n), at.rows};
+            // the CTAs whose first tile is one of these
+            for (int64_t w = (at.tiles + per_cta - 1) / per_cta; w * per_cta < at.tiles + m.tiles; ++w)
+                p.first_entry[w] = at.wides;
+        }
+        for (int i = 0, u = at.pieces; i < np; ++i)
+            for (int rb = 0; rb < x.blocks; ++rb, ++u)
+                p.list[u] = {b, first + (int)min((int64_t)n, (int64_t)i * size), first + (int)min((int64_t)n, (int64_t)(i + 1) * size),
+                             seen, x.tok0, x.R, rb * mr, direct ? -1 : at.rows + i * z.Hk * x.R};
+    }
+    if (tid == 0)
+        *p.head = {tiles, per_cta, done.pieces};
+}
+
+// ---------------------------------------------------------------- wide
+constexpr int kFetchWarps = 3;
+constexpr int kThreads = 32 + 32 * kFetchWarps + 256;
+
+template <int D> struct WideSmem {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kTile = kPanels * kPanel;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    // `valid` of a tile is written again by the tile eight later, which is looked up when at most six tiles (the ring
+    // and the warps' own) lie between it and the softmax.
+    static constexpr int kSlots = 8;
+    alignas(1024) unsigned char q[2][kTile];
+    alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 V_1 ...
+    int row[kFetchWarps][BT];    // cache row of the positions of a warp's tile, -1: not seen
+    uint32_t valid[kSlots][4];   // positions of a tile that may be seen
+    uint64_t full[kStages], empty[kStages], q_full[2], s_full[2], o_done[2], drain, never;
+    uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
+    uint64_t wait_ns;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxSmem, "shared memory of a CTA");
+
+// One CTA's way through its share of all tiles: runs of consecutive tiles of one
+// (entry, block of rows, key head).  Every role walks it by itself.
+struct Walk {
+    const WideEntry *at;
+    WideEntry en;
+    int Hk, rb, kh, t0, n, piece, left;
+    __device__ __forceinline__ Walk(const Plan &p, int heads, int cta) : Hk(heads)
+    {
+        const Head h = *p.head;
+        const int64_t x = (int64_t)cta * h.per_cta;
+        left = x < h.tiles ? (int)(h.tiles - x < h.per_cta ? h.tiles - x : h.per_cta) : 0;
+        n = 0;
+        if (left == 0)
+            return;
+        at = p.wide + p.first_entry[cta];
+        en = *at;
+        const int64_t unit = (x - en.base) / en.nt, begin = en.base + unit * en.nt;
+        t0 = (int)(x - begin);
+        rb = (int)(unit / Hk);
+        kh = (int)(unit - (int64_t)rb * Hk);
+        piece = cta - (int)(begin / h.per_cta);
+        n = min(en.nt - t0, left);
+    }
+    // The next run; false: there is none.
+    __device__ __forceinline__ bool next()
+    {
+        left -= n;
+        if (left <= 0)
+            return false;
+        t0 = piece = 0;
+        if (++kh == Hk) {
+            kh = 0;
+            if (++rb * kWideTile >= en.R) {
+                rb = 0;
+                en = *++at;
+            }
+        }
+        n = min(en.nt, left);
+        return true;
+    }
+    __device__ __forceinline__ int row_tiles() const { return en.R - rb * kWideTile > BT ? 2 : 1; }
+};
+
+// The pipeline of the wide kernel of bdla_cache_wide.cu, kept running from one
+// run of tiles to the next: tiles, ring stages and barrier phases count on, keys
+// and values of the next run are fetched while the last of this one is worked
+// on, and only the rows (queries in, sums out) change hands.  All CTAs get the
+// same number of tiles.  `run` as there.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, int run,
+                   const __grid_constant__ Call a, const __grid_constant__ Plan plan, uint64_t wait_ns, int stall)
+{
+    using Smem = WideSmem<D>;
+    constexpr int NS = Smem::kStages, SL = Smem::kSlots, NP = Smem::kPanels, kChunks = D / 8;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bdla_cache &c = a.c;
+    const int T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
+    next_may_start();
+    if ((smem_u32(smem_raw) & 1023u) != 0u) {
+        if (tid == 0)
+            set_status(a.st, BDLA_ERR_DEVICE, 0xA11u);
+        wait_for_previous();
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    } else if (tid == 32) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sm.full[s], 32);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sm.q_full[x], BT);
+            mbar_init(&sm.s_full[x], 1);
+            mbar_init(&sm.p_ready[x][0], BT);
+            mbar_init(&sm.p_ready[x][1], BT);
+            mbar_init(&sm.o_done[x], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.never, 1);
+        sm.abort_flag = 0;
+        sm.wait_ns = wait_ns;
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    wait_for_previous();   // the plan is there
+    const uint32_t tmem = sm.tmem_base;
+    volatile int *abort_flag = &sm.abort_flag;
+    Walk walk(plan, Hk, blockIdx.x);
+    const int total = walk.left, stall_at = total > 1 ? 1 : 0;   // test hook: the tile at which a role stalls
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- MMA issuer
+        const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
+        bool ok = total > 0;
+        const bool any = ok;
+        int j0 = 0;                 // tiles before this run
+        int runs[2] = {0, 0};       // runs that a row tile has had
+        int had[2] = {0, 0};        // and tiles
+        while (ok) {
+            const int tiles = walk.row_tiles(), n = walk.n;
+            auto issue_qk = [&](int w, int j) {
+                const int it = 2 * j;
+                if (!warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag))
+                    return false;
+                tc_fence_after();
+                const uint64_t k = rows_desc(smem_u32(sm.ring[it % NS]));
+                if (elect_one()) {
+                    mma_rows<D>(tmem + BT * w, q[w], k);
+                    umma_commit(&sm.s_full[w]);
+                    if (w == tiles - 1)   // the last reader of this key tile
+                        umma_commit(&sm.empty[it % NS]);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int w = 0; ok && w < tiles; ++w) {
+                ok = warp_wait(&sm.q_full[w], (uint32_t)(runs[w]++ & 1), &sm.wait_ns, abort_flag);
+                tc_fence_after();
+                ok = ok && issue_qk(w, j0);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!ok || w >= tiles)
+                        continue;
+                    const int it = 2 * (j0 + j) + 1;
+                    const uint32_t phase = (uint32_t)(had[w] & 1);
+                    ++had[w];
+                    const bool hook = stall == BDLA_STALL_MMA && j0 + j == stall_at;
+                    ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag) &&
+                         warp_wait(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : phase, &sm.wait_ns, abort_flag);
+                    if (!ok)
+                        continue;
+                    tc_fence_after();
+                    const uint64_t v = sum_desc(smem_u32(sm.ring[it % NS]));
+                    const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
+                    if (elect_one())
+                        mma_sum<D, 32, 0, BT / 32>(acc, wt, v, j > 0);
+                    __syncwarp();
+                    ok = warp_wait(&sm.p_ready[w][1], phase, &sm.wait_ns, abort_flag);
+                    if (!ok)
+                        continue;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, v, true);
+                        if (w == tiles - 1)
+                            umma_commit(&sm.empty[it % NS]);
+                        if (j + 1 == n)
+                            umma_commit(&sm.o_done[w]);
+                    }
+                    __syncwarp();
+                    if (j + 1 < n)
+                        ok = issue_qk(w, j0 + j + 1);
+                }
+            }
+            j0 += n;
+            if (!walk.next())
+                break;
+        }
+        if (any && !ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(a.st, BDLA_ERR_TIMEOUT, 0x40u);
+        }
+        // every MMA issued above has completed before TMEM is released
+        if (elect_one())
+            umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
+    } else if (warp < 4) {
+        // ---------------------------------------------------------------- fetching
+        const int fw = warp - 1;
+        bool ok = true;
+        int issued = -1;   // this warp's last tile asked of TMA
+        int j1 = walk.n;   // tiles up to the end of this run
+        // a tile of this warp: its first position, where they end and which are committed, its heads and table
+        struct Tile {
+            int t, end, len, kh, b;
+        };
+        const auto tile_at = [&](int j) {   // j does not go back; j < total
+            while (j >= j1) {
+                walk.next();
+                j1 += walk.n;
+            }
+            return Tile{walk.en.first + (walk.t0 + j - (j1 - walk.n)) * BT, walk.en.end, walk.en.len, walk.kh, walk.en.b};
+        };
+        const auto lookup = [&](const Tile &x, int (&pg)[4]) {
+            const int32_t *table = c.pages + (int64_t)x.b * c.max_pages;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = x.t + 4 * lane + u;
+                pg[u] = t < x.end ? table[a.div.entry(t)] : -1;
+            }
+        };
+        Tile now{}, ahead{};
+        int pg[4];
+        if (fw < total) {
+            ahead = tile_at(fw);
+            lookup(ahead, pg);
+        }
+        for (int j = fw; ok && j < total; j += kFetchWarps) {
+            now = ahead;
+            const uint64_t seen = now.t + BT > now.len ? sees_any(a.tree, now.b, T, lane) : 0;
+            int row[4];
+            uint32_t bits = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = now.t + 4 * lane + u;
+                bool live = t < now.end && (t < now.len || ((seen >> (t - now.len)) & 1));
+                if (live && (pg[u] < 0 || pg[u] >= c.n_pages)) {
+                    set_status(a.st, BDLA_ERR_DEVICE, (unsigned)now.b);
+                    live = false;
+                }
+                row[u] = live ? pg[u] * c.page + a.div.offset(t) : -1;
+                bits |= (live ? 1u : 0u) << u;
+            }
+            const bool whole = run > 0 && now.t % run == 0 && __all_sync(0xffffffffu, bits == 15u);
+            bits <<= 4 * (lane & 7);
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1)
+                bits |= __shfl_xor_sync(0xffffffffu, bits, x);
+            if ((lane & 7) == 0)
+                sm.valid[j % SL][lane >> 3] = bits;
+            if (!whole) {
+                *reinterpret_cast<int4 *>(&sm.row[fw][4 * lane]) = make_int4(row[0], row[1], row[2], row[3]);
+                __syncwarp();
+            }
+            if (j + kFetchWarps < total) {
+                ahead = tile_at(j + kFetchWarps);
+                lookup(ahead, pg);
+            }
+#pragma unroll 1
+            for (int v = 0; ok && v < 2; ++v) {
+                const int it = 2 * j + v, s = it % NS;
+                const bool hook = stall == BDLA_STALL_PRODUCER && it == 2 * stall_at;
+                if (it >= NS || hook)
+                    ok = warp_wait(hook ? &sm.never : &sm.empty[s], hook ? 0u : (uint32_t)((it / NS - 1) & 1), &sm.wait_ns,
+                                   abort_flag);
+                if (!ok)
+                    break;
+                if (whole) {
+                    if (elect_one())
+                        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)Smem::kTile);
+                    else
+                        mbar_arrive(&sm.full[s]);
+                    __syncwarp();
+                    for (int x = 0; x < BT; x += run) {
+                        const int first = __shfl_sync(0xffffffffu, row[0], x >> 2);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int p = 0; p < NP; ++p)
+                                tma_load_2d(sm.ring[s] + p * kPanel + x * 128, v ? &tv : &tk, &sm.full[s], now.kh * D + 64 * p,
+                                            first);
+                        }
+                        __syncwarp();
+                    }
+                    issued = it;
+                } else {
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(v ? c.v : c.k) + (int64_t)now.kh * D;
+                    const int ch = lane % kChunks;
+                    const uint32_t dst = smem_u32(sm.ring[s]) + (ch >> 3) * kPanel;
+#pragma unroll 8
+                    for (int x = lane / kChunks; x < BT; x += 32 / kChunks) {
+                        const int at_row = sm.row[fw][x];
+                        cp16(dst + sw128_offset(x, ch & 7), src + (int64_t)max(at_row, 0) * Hk * D + 8 * ch, at_row >= 0);
+                    }
+                    cp_commit();
+                    if (v == 1) {   // keys first, while the values are on their way
+                        cp_wait<1>();
+                        fence_proxy_async_smem();
+                        mbar_arrive(&sm.full[(it - 1) % NS]);
+                        cp_wait<0>();
+                        fence_proxy_async_smem();
+                        mbar_arrive(&sm.full[s]);
+                    }
+                }
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(a.st, BDLA_ERR_TIMEOUT, 0x41u);
+            // this warp's copies in flight land before the CTA exits
+            cp_wait<0>();
+            for (int it = max(issued - NS + 1, 0); it <= issued; ++it)
+                if ((it >> 1) % kFetchWarps == fw)
+                    mbar_wait(&sm.full[it % NS], (it / NS) & 1, kDrainNs);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int w = warp >= 8, q4 = warp & 3, r = 32 * q4 + lane;
+        const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+        const uint32_t t_s = tmem + BT * w + lane_off, t_o = tmem + 2 * BT + BT * w + lane_off;
+        const float cs = a.scale * kLog2e;
+        bool ok = total > 0;
+        const bool any = ok;
+        int j = 0, had = 0, runs = 0;   // tiles of the CTA; tiles and runs of this row tile
+        while (ok) {
+            const int n = walk.n;
+            if (w >= walk.row_tiles()) {
+                j += n;
+                if (!walk.next())
+                    break;
+                continue;
+            }
+            const int rr = walk.rb * kWideTile + w * BT + r, R = walk.en.R;
+            const bool live_row = rr < R;
+            const int i = live_row ? rr / G : 0;
+            {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (((int64_t)walk.en.tok0 + i) * Hq + walk.kh * G + (live_row ? rr - i * G : 0)) * D);
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch)
+                    *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) =
+                        live_row ? src[ch] : make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                tc_fence_before();   // the sums of the run before have been read
+                mbar_arrive(&sm.q_full[w]);
+            }
+            const int len = walk.en.len;
+            int t0 = walk.en.first + walk.t0 * BT;
+            const uint64_t see = walk.en.end > len ? sees(a.tree, walk.en.b, T, i) : 0;
+            RowSoftmax row;
+            for (int x = 0; x < n; ++x, ++j, t0 += BT) {
+                const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
+                ok = warp_wait(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(had & 1), &sm.wait_ns, abort_flag);
+                ++had;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tmem_ld32(t_s + 32 * k, s[k]);
+                tmem_ld_wait();
+                uint32_t all = 0xffffffffu;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    all &= sm.valid[j % SL][k];
+                if (all != 0xffffffffu || t0 + BT > len) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // what this row sees of the 32 positions: the context, and its bits of the new tokens
+                        const int j0 = t0 + 32 * k - len;   // first of them as a new token
+                        uint32_t mask = j0 <= -32 ? 0xffffffffu
+                                                  : j0 < 0 ? ((1u << -j0) - 1) | (uint32_t)(see << -j0)
+                                                           : j0 < 64 ? (uint32_t)(see >> j0) : 0u;
+                        mask &= sm.valid[j % SL][k];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[k][e] = (mask >> e) & 1 ? s[k][e] : 0xff800000u;
+                    }
+                }
+                row_weights<D>(s, cs, t_s, t_o, x == 0, row, [&](int half) { mbar_arrive(&sm.p_ready[w][half]); });
+            }
+            if (ok)
+                ok = warp_wait(&sm.o_done[w], (uint32_t)(runs & 1), &sm.wait_ns, abort_flag);
+            ++runs;
+            if (!ok)
+                break;
+            tc_fence_after();
+            const int64_t pt = (int64_t)walk.en.part + ((int64_t)walk.piece * Hk + walk.kh) * R + rr;
+            // 32 rows of 128 bytes at a time through the warp's own rows of its query tile (read by now), so that whole
+            // lines leave
+            uint4 *stage = reinterpret_cast<uint4 *>(sm.q[w] + q4 * 4096);
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t y[32];
+                tmem_ld32(t_o + 32 * k, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    stage[lane * 8 + (e ^ (lane & 7))] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int x = 4 * u + (lane >> 3);   // row of the warp
+                    const uint4 z = stage[x * 8 + ((lane & 7) ^ (x & 7))];
+                    if (rr - lane + x < R)
+                        *reinterpret_cast<uint4 *>(a.part_o + (pt - lane + x) * D + 32 * k + 4 * (lane & 7)) = z;
+                }
+                __syncwarp();
+            }
+            if (live_row)
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
+            if (!walk.next())
+                break;
+        }
+        if (any && !ok) {
+            *abort_flag = 1;
+            if (lane == 0)
+                set_status(a.st, BDLA_ERR_TIMEOUT, 0x42u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- join
+// The pieces of a row: the group's, then the sequence's own, W warps a row (as
+// combine_kernel of bdla_cache.cu).
+template <int D, int W>
+__global__ void __launch_bounds__(W < 4 ? 128 : 32 * W)
+shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan plan, int n_groups, int64_t rows)
+{
+    constexpr int E = D / 32, kRows = W < 4 ? 4 / W : 1;
+    __shared__ float red_l[kRows][W], red_m[kRows][W];
+    __shared__ __align__(16) float red_o[kRows][W][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / W, w = warp % W;
+    const int64_t at = (int64_t)blockIdx.x * kRows + mine;
+    const int T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
+    const bool any = at < rows;
+    const int h = any ? (int)(at % Hq) : 0, i = any ? (int)(at / Hq % T) : 0, b = any ? (int)(at / Hq / T) : 0;
+    const int kh = h / G;
+    wait_for_previous();
+    const Head head = *plan.head;
+    const int g = plan.group[b];
+    // first row of the pieces' sums, the step from piece to piece, and how many there are
+    const auto pieces = [&](int e, int64_t &first, int64_t &step) {
+        const Parts x = plan.parts[e];
+        const int rr = (b * T + i - x.tok0) * G + h % G;
+        first = (int64_t)x.part + (int64_t)kh * x.R + rr;
+        step = (int64_t)Hk * x.R;
+        if (x.nt == 0)
+            return x.np;
+        const int64_t begin = x.base + ((int64_t)(rr / kWideTile) * Hk + kh) * x.nt;
+        return (int)((begin + x.nt - 1) / head.per_cta - begin / head.per_cta) + 1;
+    };
+    int64_t f0 = 0, s0 = 0, f1 = 0, s1 = 0;
+    const int n1 = pieces(n_groups + b, f1, s1);
+    const int n0 = g >= 0 && any ? pieces(g, f0, s0) : 0;
+    const bool live = any && n1 >= 0;   // else finished by its own CTA
+    if (W > 1 && !live)
+        return;   // the whole CTA
+    const int n = live ? n0 + n1 : 0;
+    const auto place = [&](int s) { return s < n0 ? f0 + s * s0 : f1 + (s - n0) * s1; };
+    const float cs = a.scale * kLog2e;
+    float m = -INFINITY;
+    for (int s = w * 32 + lane; s < n; s += 32 * W)
+        m = fmaxf(m, a.part_ml[2 * place(s)]);
+    for (int x = 16; x > 0; x >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if (W > 1) {
+        if (lane == 0)
+            red_m[mine][w] = m;
+        __syncthreads();
+        for (int x = 0; x < W; ++x)
+            m = fmaxf(m, red_m[mine][x]);
+    }
+    float l = 0.0f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        v[e] = 0.0f;
+#pragma unroll 8
+    for (int s = w; s < n; s += W) {
+        const int64_t p = place(s);
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * p);
+        const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * cs);
+        l = fmaf(ml.y, f, l);
+        const float *y = a.part_o + p * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 z = *reinterpret_cast<const float2 *>(y + e);
+            v[e] = fmaf(z.x, f, v[e]);
+            v[e + 1] = fmaf(z.y, f, v[e + 1]);
+        }
+    }
+    if (W > 1) {
+        if (lane == 0)
+            red_l[mine][w] = l;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            red_o[mine][w][E * lane + e] = v[e];
+        __syncthreads();
+        if (w != 0)
+            return;
+        for (int x = 1; x < W; ++x) {
+            l += red_l[mine][x];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                v[e] += red_o[mine][x][E * lane + e];
+        }
+    }
+    if (!live)
+        return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(a.o + at * D + E * lane + e) = pack_bf16(v[e] * inv, v[e + 1] * inv);
+    if (lane == 0)
+        a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
+}
+
+template <int D> cudaError_t wide_go(const Call &a, const Plan &p, const Sizes &z, cudaStream_t stream)
+{
+    const size_t smem = sizeof(WideSmem<D>);
+    const cudaError_t err = cudaFuncSetAttribute(shared_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    CUtensorMap tk{}, tv{};
+    int run = a.c.page & -a.c.page;   // the largest power of two in the page
+    run = run > BT ? BT : run;
+    const int64_t rows = (int64_t)a.c.n_pages * a.c.page, width = (int64_t)a.Hk * D;
+    if (run < 16 || rows == 0)
+        run = 0;
+    else if (!make_rows_map(&tk, a.c.k, width, rows, run) || !make_rows_map(&tv, a.c.v, width, rows, run))
+        return cudaErrorInvalidValue;
+    return launch_second(shared_wide_kernel<D>, (unsigned)z.ctas, kThreads, smem, stream, tk, tv, run, a, p, g_wait_ns.load(),
+                         g_test_stall[BDLA_KERNEL_ATTN_SHARED].load());
+}
+
+template <int D> cudaError_t join_go(const Call &a, const Plan &p, const Sizes &z, int64_t rows, cudaStream_t stream)
+{
+    // few rows have many pieces, and leave the SMs idle with a warp each
+    return rows <= 16 * (int64_t)z.ctas
+               ? launch_second(shared_join_kernel<D, 4>, (unsigned)rows, 128, 0, stream, a, p, z.n_groups, rows)
+               : launch_second(shared_join_kernel<D, 1>, (unsigned)((rows + 3) / 4), 128, 0, stream, a, p, z.n_groups, rows);
+}
+
+}  // namespace
+
+size_t shared_bytes(const bdla_attn_dims &d, int n_groups)
+{
+    Plan p;
+    return carve(sizes_of(d, n_groups), nullptr, &p);
+}
+
+// Tiles of a CTA and rows of the partial sums are 32-bit.
+bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
+{
+    const Sizes z = sizes_of(d, n_groups);
+    const int64_t blocks = ((int64_t)d.B * d.T * (d.Hq / d.Hk) / kWideTile + n_groups + 2 * (int64_t)d.B) * d.Hk;
+    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1) / z.ctas <= INT32_MAX / 4;
+}
+
+cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, const int32_t *cu_groups, const int32_t *shared,
+                               int n_groups, const uint64_t *tree, float scale, __nv_bfloat16 *o, float *lse,
+                               const bdla_attn_dims &d, void *scratch, DeviceStatus *st, cudaStream_t stream)
+{
+    const Sizes z = sizes_of(d, n_groups);
+    Plan p;
+    carve(z, static_cast<char *>(scratch), &p);
+    Call a;
+    a.q = q;
+    a.c = c;
+    if ((int64_t)c.n_pages * c.page == 0)   // no rows: nothing is read, from an address that exists all the same
+        a.c.k = a.c.v = const_cast<__nv_bfloat16 *>(q);
+    a.tree = tree;
+    a.scale = scale;
+    a.o = o;
+    a.lse = lse;
+    a.part_o = p.part_o;
+    a.part_ml = p.part_ml;
+    a.T = d.T;
+    a.Hq = d.Hq;
+    a.Hk = d.Hk;
+    a.div = PageDiv::of(c.page);
+    a.pieces = {1, 1, 1};
+    a.st = st;
+    a.list = p.list;
+    a.n_list = &p.head->n_list;
+    KernelMark mark_(BDLA_KERNEL_ATTN_SHARED, stream);
+    const int entries = n_groups + d.B;
+    plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? entries * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
+    cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess && z.wide)
+        err = d.d == 64 ? wide_go<64>(a, p, z, stream) : wide_go<128>(a, p, z, stream);
+    if (err == cudaSuccess && z.most > 0)
+        err = launch_cached_list(a, d.d, z.narrow_tiles, z.most, stream);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t rows = (int64_t)d.B * d.T * d.Hq;
+    return d.d == 64 ? join_go<64>(a, p, z, rows, stream) : join_go<128>(a, p, z, rows, stream);
+}
+
+}  // namespace bdla

@@ -171,9 +171,35 @@ bdla_status bdla_qk_norm_append(bdla_qk_norm_args a, const void *v, int64_t v_to
 bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, float scale, void *o, float *lse,
                              bdla_attn_dims d, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * bdla_attn_cached for a batch in which groups of sequences share the positions
+ * that they begin with (a system prompt, several samples of one prompt): what a
+ * group shares is read once for all of its sequences.  The result is that of
+ * bdla_attn_cached up to rounding.
+ *   cu_groups  device int32 [n_groups + 1], 0 <= cu[0] <= cu[1] .. <= B: group g
+ *              is the sequences cu[g] .. cu[g + 1] - 1 (sequences outside all
+ *              groups share nothing; groups may be empty)
+ *   shared     device int32 [n_groups]: positions that the group's sequences share.
+ *              The first shared[g] positions of all of them lie in the same
+ *              pages: those positions are taken from the table of the group's
+ *              first sequence, and the other tables are not read there.  What
+ *              goes beyond the shortest committed context of a group's sequences
+ *              (lens) is not counted as shared
+ * n_groups is 1 .. 65535, T 1 .. 64.  Both arrays may change between replays of a
+ * captured call, as lens and the tables may.  Malformed cu_groups (then no
+ * sequence shares anything) and negative shared[g] are recorded as
+ * BDLA_ERR_DEVICE, and so is what bdla_attn_cached records.  Sizes whose counts
+ * pass 32 bits are BDLA_ERR_TOO_LARGE.
+ */
+bdla_status bdla_attn_shared(const void *q, bdla_cache c, const int32_t *cu_groups, const int32_t *shared, int n_groups,
+                             const uint64_t *tree, float scale, void *o, float *lse, bdla_attn_dims d, void *ws,
+                             size_t ws_bytes, void *stream);
+
 /* Bytes of workspace of the calls above (0 on invalid sizes).  n_docs as for
- * bdla_workspace_bytes; max_keys is max_pages * page of a BDLA_ATTN_CACHED. */
-enum { BDLA_ATTN_FWD = 0, BDLA_ATTN_BWD = 1, BDLA_ATTN_NORM_BWD = 2, BDLA_ATTN_APPEND = 3, BDLA_ATTN_CACHED = 4 };
+ * bdla_workspace_bytes, the groups of a BDLA_ATTN_SHARED; max_keys is max_pages *
+ * page of a BDLA_ATTN_CACHED or BDLA_ATTN_SHARED. */
+enum { BDLA_ATTN_FWD = 0, BDLA_ATTN_BWD = 1, BDLA_ATTN_NORM_BWD = 2, BDLA_ATTN_APPEND = 3, BDLA_ATTN_CACHED = 4,
+       BDLA_ATTN_SHARED = 5 };
 size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t max_keys);
 
 #ifdef __cplusplus

@@ -49,7 +49,7 @@ bdla_status bdla_set_seq_split(int blocks);
  */
 enum { BDLA_KERNEL_DECAY = 0, BDLA_KERNEL_FWD = 1, BDLA_KERNEL_BWD = 2, BDLA_KERNEL_STATES = 3,
        BDLA_KERNEL_SEG = 4, BDLA_KERNEL_ATTN_FWD = 5, BDLA_KERNEL_ATTN_BWD = 6, BDLA_KERNEL_ATTN_CACHED = 7,
-       BDLA_KERNEL_COUNT = 8 };
+       BDLA_KERNEL_ATTN_SHARED = 8, BDLA_KERNEL_COUNT = 9 };
 bdla_status bdla_set_kernel_events(int kernel, void *start_event, void *stop_event);
 
 /*
@@ -66,8 +66,8 @@ bdla_status bdla_set_kernel_events(int kernel, void *start_event, void *stop_eve
  *
  * bdla_set_test_stall: until called again with role 0, every later launch
  * of kernel `kernel` (BDLA_KERNEL_FWD, _BWD, _STATES, _SEG, _ATTN_FWD,
- * _ATTN_BWD, or _ATTN_CACHED with more than 32 rows a key head) makes the
- * warp(s) of one role wait, at their second block (their first if there is
+ * _ATTN_BWD, _ATTN_CACHED with more than 32 rows a key head, or _ATTN_SHARED
+ * where a group or a sequence has as many) makes the warp(s) of one role wait, at their second block (their first if there is
  * one block), on a barrier that nothing arrives at; the wait runs out after
  * the limit above.  Returns BDLA_ERR_SHAPE for an unknown kernel or role.
  * Off by default; not for production use.

@@ -1,0 +1,218 @@
+"""The plan of attention over shared pages, restated: that every row meets every position that it has to meet exactly once,
+that the join finds the sums where the pieces put them, and that lists and partial sums stay inside what the sizes alone
+give them."""
+import random
+
+import pytest
+
+SMS, TILE, WIDE, NARROW = 152, 128, 256, 32
+LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2, 32
+
+
+def up(a, b):
+    return -(-a // b)
+
+
+class Sizes:
+    def __init__(s, B, T, G, Hk, d, n_groups):
+        s.B, s.T, s.G, s.Hk, s.n_groups = B, T, G, Hk, n_groups
+        R, every = T * G, T * G * B
+        s.wide, s.own_wide = every > NARROW, R > NARROW
+        s.mr = 16 * (1 if (R if s.wide else every) <= 16 else 2)
+        s.slots = SMS * (3 if d == 128 else 4)
+        s.extra = 4 * up(s.slots, Hk)
+        s.most = 0 if s.own_wide else B + 2 * min(n_groups, B // 2) + s.extra
+        s.rows = 0
+        if s.wide:
+            s.rows += 2 * every * Hk * (2 if s.own_wide else 1) + WIDE * SMS
+        if not s.own_wide:
+            s.rows += (2 * every + NARROW * s.extra) * Hk
+
+
+def plan(z, cu, shared, lens, cap):
+    NG, E = z.n_groups, z.n_groups + z.B
+    n = [min(max(x, 0), cap) for x in shared]
+    bad = any(cu[g] < 0 or cu[g + 1] < cu[g] or cu[g + 1] > z.B for g in range(NG))
+    group = [-1] * z.B
+    for b in range(z.B):
+        if not bad:
+            lo, hi = 0, NG
+            while lo < hi:
+                mid = (lo + hi + 1) // 2
+                lo, hi = (mid, hi) if cu[mid] <= b else (lo, mid - 1)
+            group[b] = lo if lo < NG and cu[lo] <= b else -1
+        if group[b] >= 0:
+            n[group[b]] = min(n[group[b]], max(lens[b], 0))
+    n = [0 if bad or cu[g + 1] - cu[g] < 2 or n[g] < LEAST_SHARED else n[g] for g in range(NG)]
+    for b in range(z.B):
+        end = 0 if lens[b] < 0 else min(lens[b] + z.T, cap)
+        n.append(end - (n[group[b]] if group[b] >= 0 else 0))
+
+    def entry(e):
+        R, tok0, wide = z.T * z.G, (e - NG) * z.T, z.own_wide
+        if e < NG:
+            tok0, R = (cu[e] * z.T, (cu[e + 1] - cu[e]) * z.T * z.G) if n[e] > 0 else (0, 0)
+            wide = R > NARROW
+        return R, tok0, wide, up(R, WIDE if wide else z.mr)
+
+    entries = [entry(e) for e in range(E)]
+    tiles = sum(x[3] * z.Hk * up(n[e], TILE) for e, x in enumerate(entries) if x[2])
+    positions = sum(x[3] * n[e] for e, x in enumerate(entries) if not x[2])
+    per_cta = max(LEAST_TILES, up(tiles, SMS))
+    size = 64
+    if z.most > 0:
+        least, best = up(positions, z.extra), None
+        for i in range(N_SIZES):
+            s = 64 * ((3 if i & 1 else 2) << (i >> 1))
+            s = s if s >= least else up(least, 64) * 64
+            pieces = sum(x[3] * max(up(n[e], s), 1 if e >= NG else 0) for e, x in enumerate(entries) if not x[2])
+            longest = max([up(n[e], s) for e, x in enumerate(entries) if not x[2]], default=0)
+            cost = (positions + 128 * pieces) * z.Hk // z.slots + s + 4 * longest
+            if best is None or cost < best[0]:
+                best = (cost, s)
+        size = min(best[1], 2 ** 31 - 1 - 64)
+    parts, wides, work, base, rows, first_entry = [], [], [], 0, 0, {}
+    for e, (R, tok0, wide, blocks) in enumerate(entries):
+        g = group[e - NG] if e >= NG else -1
+        first = 0 if e < NG or g < 0 else n[g]
+        b = e - NG if e >= NG else (cu[e] if n[e] > 0 else 0)
+        np, direct, nt = 0, False, up(n[e], TILE) if wide else 0
+        w = blocks * z.Hk * nt
+        need = (up(nt, per_cta) + 1) * R * z.Hk if nt else 0
+        if not wide:
+            np = up(n[e], size)
+            if e >= NG:
+                np = max(np, 1)
+                direct = np == 1 and (g < 0 or n[g] == 0)
+            need = 0 if direct else np * R * z.Hk
+        parts.append((base, nt, R, rows, -1 if direct else np, tok0))
+        if nt:
+            c = up(base, per_cta)
+            while c * per_cta < base + w:
+                first_entry[c] = len(wides)
+                c += 1
+            wides.append((base, b, tok0, R, first, first + n[e], nt, rows))
+        for i in range(np):
+            for rb in range(blocks):
+                work.append((b, first + min(n[e], i * size), first + min(n[e], (i + 1) * size), tok0, R, rb * z.mr,
+                             -1 if direct else rows + i * z.Hk * R))
+        base, rows = base + w, rows + need
+    assert base == tiles
+    return group, parts, wides, work, rows, tiles, per_cta, first_entry
+
+
+def walk(z, wides, tiles, per_cta, first_entry, cta):
+    """(entry, block of rows, key head, first tile, tiles, piece) of each run of a CTA of the wide kernel."""
+    x = cta * per_cta
+    left = min(tiles - x, per_cta) if x < tiles else 0
+    if not left:
+        return
+    e = first_entry[cta]
+    base, nt = wides[e][0], wides[e][6]
+    unit = (x - base) // nt
+    begin = base + unit * nt
+    t0, rb, kh, piece = x - begin, unit // z.Hk, unit % z.Hk, cta - begin // per_cta
+    while True:
+        n = min(wides[e][6] - t0, left)
+        yield e, rb, kh, t0, n, piece
+        left -= n
+        if left <= 0:
+            return
+        t0 = piece = 0
+        kh += 1
+        if kh == z.Hk:
+            kh, rb = 0, rb + 1
+            if rb * WIDE >= wides[e][3]:
+                rb, e = 0, e + 1
+
+
+def check(B, T, G, Hk, d, cu, shared, lens, cap):
+    z = Sizes(B, T, G, Hk, d, len(shared))
+    group, parts, wides, work, rows, tiles, per_cta, first_entry = plan(z, cu, shared, lens, cap)
+    assert rows <= z.rows and len(work) <= z.most and tiles <= SMS * per_cta and all(0 <= c < SMS for c in first_entry)
+    # what each piece leaves, by its row of the partial sums: (token, query head) and positions
+    left, done = {}, {}
+
+    def put(at, token, head, a, e):
+        if at is None:
+            assert (token, head) not in done
+            done[token, head] = [(a, e)]
+        else:
+            assert 0 <= at < z.rows and at not in left, at
+            left[at] = (token, head, a, e)
+
+    for b, a, e, tok0, R, row0, part in work:
+        for kh in range(Hk):
+            for r in range(row0, min(R, row0 + z.mr)):
+                put(None if part < 0 else part + kh * R + r, tok0 + r // G, kh * G + r % G, a, e)
+    for cta in range(SMS):
+        for i, rb, kh, t0, n, piece in walk(z, wides, tiles, per_cta, first_entry, cta):
+            base, b, tok0, R, first, end, nt, part = wides[i]
+            for r in range(rb * WIDE, min(R, rb * WIDE + WIDE)):
+                put(part + (piece * Hk + kh) * R + r, tok0 + r // G, kh * G + r % G, first + t0 * TILE,
+                    min(end, first + (t0 + n) * TILE))
+
+    def pieces(e, b, i, h):
+        base, nt, R, part, np, tok0 = parts[e]
+        rr, kh = (b * T + i - tok0) * G + h % G, h // G
+        if nt:
+            begin = base + (rr // WIDE * Hk + kh) * nt
+            np = (begin + nt - 1) // per_cta - begin // per_cta + 1
+        return [part + kh * R + rr + s * Hk * R for s in range(max(np, 0))] if np >= 0 else None
+
+    used = set()
+    for b in range(B):
+        end = 0 if lens[b] < 0 else min(lens[b] + T, cap)
+        for i in range(T):
+            for h in range(G * Hk):
+                own = pieces(z.n_groups + b, b, i, h)
+                if own is None:
+                    spans = done[b * T + i, h]
+                else:
+                    at = (pieces(group[b], b, i, h) if group[b] >= 0 else []) + own
+                    used.update(at)
+                    assert all(left[x][:2] == (b * T + i, h) for x in at)
+                    spans = [left[x][2:] for x in at]
+                spans = [s for s in spans if s[0] < s[1]]
+                assert (spans[0][0] if spans else 0) == 0 and (spans[-1][1] if spans else 0) == end
+                assert all(x[1] == y[0] for x, y in zip(spans, spans[1:]))
+    assert used == set(left)   # nothing is summed that nobody joins
+
+
+def test_small_and_odd():
+    check(1, 1, 1, 1, 64, [0, 1], [100], [200], 1024)
+    check(2, 1, 1, 1, 64, [0, 2], [100], [200, 64], 1024)
+    check(2, 1, 4, 2, 128, [0, 2], [0], [0, 0], 0)
+    check(3, 2, 4, 2, 128, [0, 2], [500], [-1, 700, 9], 640)          # a bad length, one past the table
+    check(9, 5, 8, 1, 64, [0, 9], [4000], [4000] * 9, 8192)
+    check(4, 64, 8, 1, 128, [1, 3], [900], [900, 1000, 901, 5], 2048)  # trees of several blocks of rows
+    check(3, 1, 2, 2, 64, [2, 1], [5], [100, 100, 100], 1024)          # malformed: nobody shares
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_every_position_once(seed):
+    r = random.Random(seed)
+    B = r.choice([1, 2, 3, 8, 17, 40])
+    T, G, Hk = r.choice([1, 1, 2, 7, 20]), r.choice([1, 2, 4, 8]), r.choice([1, 2, 3, 8])
+    NG = r.randint(1, min(B, 5))
+    cu = sorted(r.randint(0, B) for _ in range(NG + 1))
+    top = r.choice([50, 1000, 20000])
+    lens = [r.randint(0, top) for _ in range(B)]
+    shared = [r.choice([0, 63, 64, r.randint(0, top), 10 ** 9]) for _ in range(NG)]
+    if r.random() < 0.6:   # contexts that are longer than what is shared
+        lens = [n + max(min(shared[g], top) for g in range(NG)) for n in lens]
+    check(B, T, G, Hk, r.choice([64, 128]), cu, shared, lens, max(lens) + r.choice([T, T + 77, 1]))
+
+
+def test_bounds_at_large_sizes():
+    """Lists and partial sums of batches too large to follow row by row."""
+    r = random.Random(1)
+    for B, T, G, Hk, NG, top in ((256, 1, 4, 8, 1, 131072), (256, 1, 4, 8, 128, 131072), (256, 1, 1, 1, 100, 1 << 21),
+                                 (600, 8, 4, 8, 3, 1 << 17), (5000, 1, 8, 1, 2500, 40000), (64, 64, 8, 8, 9, 1 << 16)):
+        z = Sizes(B, T, G, Hk, 128, NG)
+        cu = [B * g // NG for g in range(NG + 1)]
+        for kind in range(3):
+            shared = [r.randint(top // 2, top) if kind else top for _ in range(NG)]
+            lens = [top + (r.randint(0, top) if kind == 2 else 5) for _ in range(B)]
+            _, _, _, work, rows, tiles, per_cta, first = plan(z, cu, shared, lens, 1 << 30)
+            assert rows <= z.rows and len(work) <= z.most and tiles <= SMS * per_cta and all(c < SMS for c in first)
