@@ -98,7 +98,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 // of the group) that see positions k0 .. k1 - 1 of sequence b's page table, and
 // of those past `len` as new tokens what the masks say.  The results go to the
 // rows part + kh R + .. of the partial sums, or to the outputs where part < 0.
-struct Work {
+struct alignas(16) Work {
     int b, k0, k1, len;
     int tok0, R, row0, part;
 };

@@ -40,20 +40,18 @@ constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is
 // What the wide kernel walks: positions first .. end - 1 of sequence b's table
 // for the R rows from token tok0 on, as blocks of 256 rows times key heads, each
 // of nt tiles of 128 positions.  `base`: tiles of the entries before it.
-struct WideEntry {
-    int64_t base;
-    int b, tok0, R, first, end, len, nt, part;
+struct alignas(16) WideEntry {
+    int base, b, tok0, R, first, end, len, nt, part;
 };
 
 // Where an entry's partial sums are.  wide: pieces follow from the tiles' cut;
 // narrow: np pieces; np < 0: its rows are finished.
-struct Parts {
-    int64_t base;
-    int nt, R, part, np, tok0, pad;
+struct alignas(16) Parts {
+    int base, nt, R, part, np, tok0;
 };
 
 struct Head {
-    int64_t tiles;   // of the wide kernel
+    int tiles;       // of the wide kernel
     int per_cta;     // tiles of a CTA
     int n_list;      // pieces of the narrow kernel
 };
@@ -66,7 +64,7 @@ struct Plan {
     Work *list;
     int *first_entry;   // of each CTA of the wide kernel
     int *group;         // of each sequence, -1: none
-    int *len;           // positions of each entry (scratch of the plan)
+    int *scratch;       // of the plan, where shared memory is too small
     float *part_o, *part_ml;
 };
 
@@ -76,10 +74,15 @@ struct Sizes {
     bool wide, own_wide; // the wide kernel runs; it takes the sequences' own positions too
     int narrow_tiles;    // rows of a narrow CTA, in 16
     int slots;           // narrow CTAs that the GPU holds
+    float heads_per_slot;
     int extra;           // pieces of the narrow list beyond one for every block of rows
     int most;            // pieces of the narrow list
     int64_t rows;        // of partial sums
 };
+
+// Integers that the plan keeps: offsets and shared lengths of the groups,
+// lengths of all entries, the sequences' groups.
+constexpr size_t plan_ints(int n_groups, int B) { return 3 * (size_t)n_groups + 2 * (size_t)B + 1; }
 
 // Bounds of the plan.  Narrow: a piece size of at least the (block-weighted)
 // positions over `extra` cuts at most `extra` pieces beyond the first of each
@@ -102,6 +105,7 @@ Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
     s.own_wide = R > kNarrowRows;
     s.narrow_tiles = (s.wide ? R : all) <= 16 ? 1 : 2;
     s.slots = s.ctas * (d.d == 128 ? 3 : 4);
+    s.heads_per_slot = (float)d.Hk / (float)s.slots;
     s.extra = 4 * ((s.slots + d.Hk - 1) / d.Hk);
     const int groups = n_groups < d.B / 2 ? n_groups : d.B / 2;
     s.most = s.own_wide ? 0 : d.B + 2 * groups + s.extra;
@@ -129,99 +133,101 @@ size_t carve(const Sizes &s, char *at, Plan *p)
     take(p->list, (size_t)s.most);
     take(p->first_entry, (size_t)s.ctas);
     take(p->group, (size_t)s.B);
-    take(p->len, entries);
+    take(p->scratch, plan_ints(s.n_groups, s.B));
     take(p->part_o, (size_t)s.rows * s.D);
     take(p->part_ml, (size_t)s.rows * 2);
     return off;
 }
 
 // ---------------------------------------------------------------- plan
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanEntries = 8192;   // whose lengths fit into shared memory
+constexpr int kPlanThreads = 512;
+constexpr int kPlanEntries = 4000;   // whose offsets, groups and lengths fit into 48 KB of shared memory
 constexpr int kLeastShared = 64;     // shared positions that are worth a piece of their own
 constexpr int kLeastTiles = 2;       // tiles of a wide CTA
-constexpr int kSizes = 32;           // piece sizes that are weighed, one a warp
+constexpr int kFew = 4;               // pieces, or CTAs, of an entry that one lane writes
+constexpr int kSizes = 8;            // piece sizes of the narrow kernel that are weighed: 128, 256 .. 16384 positions
 
-// The narrow kernel's piece sizes, in tiles of 64: 2, 3, 4, 6, 8, 12 ..
-__device__ __forceinline__ int64_t narrow_size(int i) { return (int64_t)64 * ((i & 1 ? 3 : 2) << (i >> 1)); }
+__device__ __forceinline__ int tiles_of(int n) { return (int)(((uint32_t)n + BT - 1) / BT); }
+__device__ __forceinline__ int over(int n, int size) { return (int)(((uint32_t)n + (uint32_t)size - 1) / (uint32_t)size); }
 
+// What comes before an entry: tiles of the wide kernel, rows of partial sums,
+// pieces of the narrow list, entries of the wide one.
 struct Sums {
-    int64_t tiles, positions;
-    int rows, pieces, wides;
+    int tiles, rows, pieces, wides;
     __device__ __forceinline__ void add(const Sums &o)
     {
         tiles += o.tiles;
-        positions += o.positions;
         rows += o.rows;
         pieces += o.pieces;
         wides += o.wides;
     }
-    __device__ __forceinline__ Sums shifted(int by) const
+    // Sums over this and the lower lanes.
+    __device__ __forceinline__ Sums scanned() const
     {
-        return {__shfl_up_sync(0xffffffffu, tiles, by), __shfl_up_sync(0xffffffffu, positions, by),
-                __shfl_up_sync(0xffffffffu, rows, by), __shfl_up_sync(0xffffffffu, pieces, by),
-                __shfl_up_sync(0xffffffffu, wides, by)};
+        Sums s = *this;
+#pragma unroll
+        for (int by = 1; by < 32; by <<= 1) {
+            const Sums o = {__shfl_up_sync(0xffffffffu, s.tiles, by), __shfl_up_sync(0xffffffffu, s.rows, by),
+                            __shfl_up_sync(0xffffffffu, s.pieces, by), __shfl_up_sync(0xffffffffu, s.wides, by)};
+            if ((int)(threadIdx.x & 31) >= by)
+                s.add(o);
+        }
+        return s;
+    }
+    __device__ __forceinline__ Sums of_lane(int lane) const
+    {
+        return {__shfl_sync(0xffffffffu, tiles, lane), __shfl_sync(0xffffffffu, rows, lane),
+                __shfl_sync(0xffffffffu, pieces, lane), __shfl_sync(0xffffffffu, wides, lane)};
     }
 };
 
-// Sums over the threads before this one, and of all (every thread of the CTA).
-__device__ __forceinline__ Sums scan(const Sums &mine, Sums *of_warp, Sums &all)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums s = mine;
-#pragma unroll
-    for (int by = 1; by < 32; by <<= 1) {
-        const Sums o = s.shifted(by);
-        if (lane >= by)
-            s.add(o);
-    }
-    __syncthreads();
-    if (lane == 31)
-        of_warp[warp] = s;
-    __syncthreads();
-    Sums before = {};
-    all = {};
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w == warp)
-            before = all;
-        all.add(of_warp[w]);
-    }
-    s.add(before);
-    s.tiles -= mine.tiles;
-    s.positions -= mine.positions;
-    s.rows -= mine.rows;
-    s.pieces -= mine.pieces;
-    s.wides -= mine.wides;
-    return s;
-}
-
+// One CTA, a few microseconds of latencies one after the other: everything
+// between the loads and the stores stays in shared memory for up to kPlanEntries
+// entries, warps without entries pass the barriers only, and the code is kept
+// short, since each call runs it once, from cold.
 __global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu, const int32_t *shared, const __grid_constant__ Sizes z,
-            const __grid_constant__ Plan p, DeviceStatus *st)
+plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, const int32_t *shared,
+            const __grid_constant__ Sizes z, const __grid_constant__ Plan p, DeviceStatus *st)
 {
-    extern __shared__ int smem_len[];
-    __shared__ Sums of_warp[kPlanThreads / 32];
-    __shared__ int64_t cost[kSizes];
+    extern __shared__ int smem_ints[];
+    __shared__ int64_t s_positions;
+    __shared__ int s_tiles, s_pieces[kSizes], s_longest;
+    __shared__ Sums of_warp[32];
     next_may_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int NG = z.n_groups, E = NG + z.B, rows_of = z.T * z.G;
-    int *len = E <= kPlanEntries ? smem_len : p.len;
+    const int NG = z.n_groups, B = z.B, E = NG + B;
+    int *base = E <= kPlanEntries ? smem_ints : p.scratch;
+    int *cu = base, *most = cu + NG + 1, *len = most + NG, *group = len + E;   // most: before the short ones are dropped
     const int cap = c.max_pages * c.page;
 
     // groups: inside the batch and in order, or there are none
+    const int first_len = tid < B ? c.lens[tid] : 0;
     bool bad = false;
-    for (int g = tid; g < NG; g += kPlanThreads) {
-        const int n0 = cu[g], n1 = cu[g + 1], s = shared[g];
-        bad |= n0 < 0 || n1 < n0 || n1 > z.B;
+    for (int g = tid; g <= NG; g += kPlanThreads) {
+        const int n0 = cu_groups[g];
+        cu[g] = n0;
+        if (g == NG)
+            break;
+        const int n1 = cu_groups[g + 1], s = shared[g];
+        bad |= n0 < 0 || n1 < n0 || n1 > B;
         if (s < 0)
             set_status(st, BDLA_ERR_DEVICE, (unsigned)g);
-        len[g] = min(max(s, 0), cap);
+        most[g] = min(max(s, 0), cap);
+    }
+    if (tid < kSizes)
+        s_pieces[tid] = 0;
+    if (tid < 32)
+        of_warp[tid] = {};
+    if (tid == 0) {
+        s_tiles = s_longest = 0;
+        s_positions = 0;
     }
     bad = __syncthreads_or(bad);
     if (bad && tid == 0)
         set_status(st, BDLA_ERR_DEVICE, 0u);
     // a group shares what the shortest of its sequences has in the cache
-    for (int b = tid; b < z.B; b += kPlanThreads) {
+    for (int b = tid; b < B; b += kPlanThreads) {
+        const int l = b == tid ? first_len : c.lens[b];
         int g = -1;
         if (!bad) {
             int lo = 0, hi = NG;   // the last offset at or before b
@@ -235,138 +241,170 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu, const int32
             g = lo < NG && cu[lo] <= b ? lo : -1;
         }
         if (g >= 0)
-            atomicMin(&len[g], max(c.lens[b], 0));
+            atomicMin(&most[g], max(l, 0));
+        group[b] = g;
         p.group[b] = g;
-    }
-    __syncthreads();
-    // one sequence reads nothing twice
-    for (int g = tid; g < NG; g += kPlanThreads)
-        if (bad || cu[g + 1] - cu[g] < 2 || len[g] < kLeastShared)
-            len[g] = 0;
-    __syncthreads();
-    for (int b = tid; b < z.B; b += kPlanThreads) {
-        const int l = c.lens[b], g = p.group[b];
+        // what the sequence has all in all
         const int64_t all = (int64_t)l + z.T;
         if (l < 0 || all > cap)
             set_status(st, BDLA_ERR_DEVICE, (unsigned)b);
-        const int end = l < 0 ? 0 : (int)(all < cap ? all : cap);
-        len[NG + b] = end - (g >= 0 ? len[g] : 0);
+        len[NG + b] = l < 0 ? 0 : (int)(all < cap ? all : cap);
     }
     __syncthreads();
-
-    // one entry: rows, first token, whether it is the wide kernel's, its blocks of rows
-    struct Entry {
-        int R, tok0, blocks;
-        bool wide;
-    };
-    const int mr = 16 * z.narrow_tiles;
-    const auto entry = [&](int e) {
-        Entry x;
-        x.R = rows_of;
-        x.tok0 = (e - NG) * z.T;
-        x.wide = z.own_wide;
-        if (e < NG) {
-            x.tok0 = len[e] > 0 ? cu[e] * z.T : 0;
-            x.R = len[e] > 0 ? (cu[e + 1] - cu[e]) * rows_of : 0;
-            x.wide = x.R > kNarrowRows;
-        }
-        x.blocks = x.wide ? (x.R + kWideTile - 1) / kWideTile : (x.R + mr - 1) / mr;
-        return x;
-    };
-    const auto tiles_of = [](int n) { return (n + BT - 1) / BT; };
-    Sums total = {}, mine = {};
+    // one sequence reads nothing twice, and a short prefix is not worth the joining
+    const auto taken = [&](int g) { return g < 0 || bad || cu[g + 1] - cu[g] < 2 || most[g] < kLeastShared ? 0 : most[g]; };
+    const int rows_of = z.T * z.G, mr_log = z.narrow_tiles == 1 ? 4 : 5;
+    const auto rows = [&](int e, int n) { return e >= NG ? rows_of : n > 0 ? (cu[e + 1] - cu[e]) * rows_of : 0; };
+    const auto wide = [&](int e, int R) { return e >= NG ? z.own_wide : R > kNarrowRows; };
+    const auto blocks = [&](int R, bool w) { return w ? (R + kWideTile - 1) / kWideTile : (R + (1 << mr_log) - 1) >> mr_log; };
+    int tiles = 0;
+    int64_t positions = 0;
     for (int e = tid; e < E; e += kPlanThreads) {
-        const Entry x = entry(e);
-        if (x.wide)
-            mine.tiles += (int64_t)x.blocks * z.Hk * tiles_of(len[e]);
+        const int n = e < NG ? taken(e) : len[e] - taken(group[e - NG]), R = rows(e, n);
+        len[e] = n;
+        if (wide(e, R))
+            tiles += blocks(R, true) * z.Hk * tiles_of(n);
         else
-            mine.positions += (int64_t)x.blocks * len[e];
+            positions += (int64_t)blocks(R, false) * n;
     }
-    scan(mine, of_warp, total);
-    const int64_t tiles = total.tiles;
-    int64_t even = (tiles + z.ctas - 1) / z.ctas;
-    const int per_cta = (int)(even < kLeastTiles ? kLeastTiles : even);
+    if (warp * 32 < E) {
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1)
+            positions += __shfl_xor_sync(0xffffffffu, positions, w);
+        if (lane == 0) {
+            atomicAdd(&s_tiles, tiles);
+            atomicAdd(reinterpret_cast<unsigned long long *>(&s_positions), (unsigned long long)positions);
+        }
+    }
+    __syncthreads();
+    tiles = s_tiles;
+    positions = s_positions;
+    const int per_cta = max(kLeastTiles, over(tiles, z.ctas));
+
     // The narrow pieces' size: their work (a piece costs its start-up, about 128
     // positions) spread over the CTAs that the GPU holds, plus the last piece's
-    // own length, plus what the join reads of the longest entry's pieces.
-    const int64_t least = z.extra > 0 ? (total.positions + z.extra - 1) / z.extra : 0;
-    const auto size_of = [&](int i) {
-        const int64_t s = narrow_size(i);
-        return s >= least ? s : (least + 63) / 64 * 64;
-    };
-    int size = 64;   // (no narrow piece: not looked at)
-    if (z.most > 0) {
-        const int64_t s = size_of(warp);
-        int64_t pieces = 0, longest = 0;
-        for (int e = lane; e < E; e += 32) {
-            const Entry x = entry(e);
-            if (x.wide)
-                continue;
-            const int64_t n = ((int64_t)len[e] + s - 1) / s;
-            pieces += x.blocks * (e >= NG && n < 1 ? 1 : n);
-            longest = n > longest ? n : longest;
+    // own length, plus what the join reads of the longest entry's pieces.  At
+    // least the size that keeps the list inside its bounds.
+    const int64_t least64 = z.most > 0 ? (positions + z.extra - 1) / z.extra : 0;
+    int size = least64 > INT32_MAX - 128 ? INT32_MAX - 127 : ((int)least64 + 63) / 64 * 64;
+    if (z.most > 0 && size <= 128 << (kSizes - 1)) {
+        for (int e0 = warp * 32; e0 < E; e0 += kPlanThreads) {
+            const int e = e0 + lane, n = e < E ? len[e] : 0, R = e < E ? rows(e, n) : 0;
+            const bool mine = e < E && !wide(e, R);
+            const int x = mine ? blocks(R, false) : 0, some = mine && e >= NG ? 1 : 0;
+            const int longest = __reduce_max_sync(0xffffffffu, mine ? n : 0);
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < kSizes; ++i) {
+                const int all = __reduce_add_sync(0xffffffffu, max(x * ((n + (128 << i) - 1) >> (7 + i)), some));
+                sum = lane == i ? all : sum;
+            }
+            if (lane < kSizes)
+                atomicAdd(&s_pieces[lane], sum);
+            if (lane == kSizes)
+                atomicMax(&s_longest, longest);
         }
-        for (int w = 16; w > 0; w >>= 1) {
-            pieces += __shfl_xor_sync(0xffffffffu, pieces, w);
-            const int64_t o = __shfl_xor_sync(0xffffffffu, longest, w);
-            longest = o > longest ? o : longest;
-        }
-        if (lane == 0)
-            cost[warp] = (total.positions + 128 * pieces) * z.Hk / z.slots + s + 4 * longest;
         __syncthreads();
-        int best = 0;
-        for (int i = 1; i < kSizes; ++i)
-            best = cost[i] < cost[best] ? i : best;
-        const int64_t chosen = size_of(best);
-        size = (int)(chosen < INT32_MAX - 64 ? chosen : INT32_MAX - 64);
+        // one size a lane, the cheapest to all
+        const int i = lane % kSizes;
+        float cost = 128 << i < size ? INFINITY
+                                     : ((float)positions + 128.0f * (float)s_pieces[i]) * z.heads_per_slot + (float)(128 << i) +
+                                           4.0f * (float)((s_longest + (128 << i) - 1) >> (7 + i));
+        size = 128 << i;
+#pragma unroll
+        for (int w = 1; w < kSizes; w <<= 1) {
+            const float c2 = __shfl_xor_sync(0xffffffffu, cost, w);
+            const int s2 = __shfl_xor_sync(0xffffffffu, size, w);
+            if (c2 < cost || (c2 == cost && s2 < size)) {
+                cost = c2;
+                size = s2;
+            }
+        }
     }
+    size = max(size, 64);   // (no narrow piece: not looked at)
 
     // places of everything, entries in order
     Sums done = {};
     for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
         const int e = e0 + tid;
         Sums m = {};
-        Entry x = {};
-        int n = 0, np = 0;
-        bool direct = false;
+        int n = 0, R = 0, nb = 0, np = 0, nt = 0, first = 0;
+        bool direct = false;   // not even a group's sums are joined to one piece
         if (e < E) {
-            x = entry(e);
             n = len[e];
-            if (x.wide) {
-                const int nt = tiles_of(n);
-                m.tiles = (int64_t)x.blocks * z.Hk * nt;
-                m.rows = nt > 0 ? ((nt + per_cta - 1) / per_cta + 1) * x.R * z.Hk : 0;
+            R = rows(e, n);
+            const bool w = wide(e, R);
+            nb = blocks(R, w);
+            first = e < NG ? 0 : taken(group[e - NG]);
+            if (w) {
+                nt = tiles_of(n);
+                m.tiles = nb * z.Hk * nt;
+                m.rows = nt > 0 ? (over(nt, per_cta) + 1) * R * z.Hk : 0;
                 m.wides = nt > 0;
             } else {
-                np = (int)(((int64_t)n + size - 1) / size);
-                if (e >= NG) {
-                    np = np < 1 ? 1 : np;
-                    const int g = p.group[e - NG];
-                    direct = np == 1 && (g < 0 || len[g] == 0);
-                }
-                m.pieces = x.blocks * np;
-                m.rows = direct ? 0 : np * x.R * z.Hk;
+                np = n > 0 ? over(n, size) : e >= NG;
+                direct = first == 0 && np == 1 && e >= NG;
+                m.pieces = nb * np;
+                m.rows = direct ? 0 : np * R * z.Hk;
             }
         }
-        Sums all, at = scan(m, of_warp, all);
-        at.add(done);
-        done.add(all);
-        if (e >= E)
-            continue;
-        const int b = e < NG ? (n > 0 ? cu[e] : 0) : e - NG;
-        const int first = e < NG || p.group[b] < 0 ? 0 : len[p.group[b]];
-        const int seen = e < NG ? kSeen : max(c.lens[b], 0);
-        p.parts[e] = {at.tiles, x.wide ? tiles_of(n) : 0, x.R, at.rows, direct ? -1 : np, x.tok0, 0};
-        if (m.wides) {
-            p.wide[at.wides] = {at.tiles, b, x.tok0, x.R, first, first + n, seen, tiles_of(n), at.rows};
-            // the CTAs whose first tile is one of these
-            for (int64_t w = (at.tiles + per_cta - 1) / per_cta; w * per_cta < at.tiles + m.tiles; ++w)
-                p.first_entry[w] = at.wides;
+        const bool active = e0 + warp * 32 < E;
+        const Sums upto = active ? m.scanned() : m;
+        if (e0 > 0)
+            __syncthreads();   // the sums of the chunk before have been read
+        if (lane == 31)
+            of_warp[warp] = upto;
+        __syncthreads();
+        if (!active)
+            continue;   // (in the last chunk; `done` is read by warp 0, which always has entries)
+        const Sums warps = of_warp[lane].scanned(), before = warps.of_lane(max(warp - 1, 0));
+        Sums at = done;
+        if (warp > 0)
+            at.add(before);
+        done.add(warps.of_lane(31));
+        at.tiles += upto.tiles - m.tiles;
+        at.rows += upto.rows - m.rows;
+        at.pieces += upto.pieces - m.pieces;
+        at.wides += upto.wides - m.wides;
+        // A lane writes what its entry has few of, the warp together where there are many: the pieces of the narrow
+        // list, and the CTAs whose first tile lies in the entry.
+        int w0 = 0, w1 = 0;
+        Work piece = {};
+        if (e < E) {
+            const int b = e >= NG ? e - NG : n > 0 ? cu[e] : 0;
+            piece = {b, first, n, e < NG ? kSeen : max(c.lens[b], 0), b * z.T, R, nb, direct ? -1 : at.rows};
+            p.parts[e] = {at.tiles, nt, R, at.rows, direct ? -1 : np, piece.tok0};
+            if (nt > 0) {
+                p.wide[at.wides] = {at.tiles, b, piece.tok0, R, first, first + n, piece.len, nt, at.rows};
+                w0 = over(at.tiles, per_cta);
+                w1 = over(at.tiles + m.tiles, per_cta);
+            }
         }
-        for (int i = 0, u = at.pieces; i < np; ++i)
-            for (int rb = 0; rb < x.blocks; ++rb, ++u)
-                p.list[u] = {b, first + (int)min((int64_t)n, (int64_t)i * size), first + (int)min((int64_t)n, (int64_t)(i + 1) * size),
-                             seen, x.tok0, x.R, rb * mr, direct ? -1 : at.rows + i * z.Hk * x.R};
+        const auto write = [&](const Work &x, int pieces, int u, int i, int rb) {   // x: k1 positions, row0 blocks of rows
+            p.list[u] = {x.b, x.k0 + i * size, x.k0 + (i + 1 < pieces ? (i + 1) * size : x.k1), x.len, x.tok0, x.R, rb << mr_log,
+                         x.part < 0 ? -1 : x.part + i * z.Hk * x.R};
+        };
+        if (np <= kFew)
+            for (int i = 0, u = at.pieces; i < np; ++i)
+                for (int rb = 0; rb < nb; ++rb, ++u)
+                    write(piece, np, u, i, rb);
+        if (w1 - w0 <= kFew)
+            for (int w = w0; w < w1; ++w)
+                p.first_entry[w] = at.wides;
+        for (uint32_t left = __ballot_sync(0xffffffffu, np > kFew || w1 - w0 > kFew); left != 0; left &= left - 1) {
+            const int l = __ffs(left) - 1;
+            const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
+            const int pieces = of(np), to = of(w1), from = of(w0), which = of(at.wides), u0 = of(at.pieces);
+            const Work x = {of(piece.b), of(piece.k0), of(piece.k1), of(piece.len), of(piece.tok0), of(piece.R), of(piece.row0),
+                            of(piece.part)};
+            if (pieces > kFew)
+                for (int i = lane; i < pieces; i += 32)
+                    for (int rb = 0; rb < x.row0; ++rb)
+                        write(x, pieces, u0 + i * x.row0 + rb, i, rb);
+            for (int w = from + lane; w < to; w += 32)
+                p.first_entry[w] = which;
+        }
     }
     if (tid == 0)
         *p.head = {tiles, per_cta, done.pieces};
@@ -375,6 +413,56 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu, const int32
 // ---------------------------------------------------------------- wide
 constexpr int kFetchWarps = 3;
 constexpr int kThreads = 32 + 32 * kFetchWarps + 256;
+
+// One CTA's way through its share of all tiles: runs of consecutive tiles of one
+// (entry, block of rows, key head).  Every warp walks it by itself, in shared
+// memory: it is looked at between runs, and its registers are wanted within them.
+struct Walk {
+    WideEntry en;
+    const WideEntry *at;
+    int rb, kh, t0, n, piece, left;
+    // One lane; false: there is no tile.
+    __device__ __forceinline__ bool begin(const Plan &p, int Hk, int cta)
+    {
+        const Head h = *p.head;
+        const int x = cta * h.per_cta;
+        left = x < h.tiles ? min(h.tiles - x, h.per_cta) : 0;
+        n = 0;
+        if (left == 0)
+            return false;
+        at = p.wide + p.first_entry[cta];
+        en = *at;
+        const int unit = (x - en.base) / en.nt, from = en.base + unit * en.nt;
+        t0 = x - from;
+        rb = unit / Hk;
+        kh = unit - rb * Hk;
+        piece = cta - from / h.per_cta;
+        n = min(en.nt - t0, left);
+        return true;
+    }
+    // The next run, by the whole warp; false: there is none.
+    __device__ __forceinline__ bool next(int Hk)
+    {
+        __syncwarp();   // all have looked at the run before
+        if ((threadIdx.x & 31) == 0) {
+            left -= n;
+            if (left > 0) {
+                t0 = piece = 0;
+                if (++kh == Hk) {
+                    kh = 0;
+                    if (++rb * kWideTile >= en.R) {
+                        rb = 0;
+                        en = *++at;
+                    }
+                }
+                n = min(en.nt, left);
+            }
+        }
+        __syncwarp();
+        return left > 0;
+    }
+    __device__ __forceinline__ int row_tiles() const { return en.R - rb * kWideTile > BT ? 2 : 1; }
+};
 
 template <int D> struct WideSmem {
     static constexpr int kPanels = D / 64;
@@ -390,53 +478,11 @@ template <int D> struct WideSmem {
     uint64_t full[kStages], empty[kStages], q_full[2], s_full[2], o_done[2], drain, never;
     uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
     uint64_t wait_ns;
+    Walk walk[1 + kFetchWarps + 8];   // of each warp
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxSmem, "shared memory of a CTA");
-
-// One CTA's way through its share of all tiles: runs of consecutive tiles of one
-// (entry, block of rows, key head).  Every role walks it by itself.
-struct Walk {
-    const WideEntry *at;
-    WideEntry en;
-    int Hk, rb, kh, t0, n, piece, left;
-    __device__ __forceinline__ Walk(const Plan &p, int heads, int cta) : Hk(heads)
-    {
-        const Head h = *p.head;
-        const int64_t x = (int64_t)cta * h.per_cta;
-        left = x < h.tiles ? (int)(h.tiles - x < h.per_cta ? h.tiles - x : h.per_cta) : 0;
-        n = 0;
-        if (left == 0)
-            return;
-        at = p.wide + p.first_entry[cta];
-        en = *at;
-        const int64_t unit = (x - en.base) / en.nt, begin = en.base + unit * en.nt;
-        t0 = (int)(x - begin);
-        rb = (int)(unit / Hk);
-        kh = (int)(unit - (int64_t)rb * Hk);
-        piece = cta - (int)(begin / h.per_cta);
-        n = min(en.nt - t0, left);
-    }
-    // The next run; false: there is none.
-    __device__ __forceinline__ bool next()
-    {
-        left -= n;
-        if (left <= 0)
-            return false;
-        t0 = piece = 0;
-        if (++kh == Hk) {
-            kh = 0;
-            if (++rb * kWideTile >= en.R) {
-                rb = 0;
-                en = *++at;
-            }
-        }
-        n = min(en.nt, left);
-        return true;
-    }
-    __device__ __forceinline__ int row_tiles() const { return en.R - rb * kWideTile > BT ? 2 : 1; }
-};
 
 // The pipeline of the wide kernel of bdla_cache_wide.cu, kept running from one
 // run of tiles to the next: tiles, ring stages and barrier phases count on, keys
@@ -489,7 +535,10 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     wait_for_previous();   // the plan is there
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
-    Walk walk(plan, Hk, blockIdx.x);
+    Walk &walk = sm.walk[warp];
+    if (lane == 0)
+        walk.begin(plan, Hk, blockIdx.x);
+    __syncwarp();
     const int total = walk.left, stall_at = total > 1 ? 1 : 0;   // test hook: the tile at which a role stalls
 
     if (warp == 0) {
@@ -558,7 +607,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 }
             }
             j0 += n;
-            if (!walk.next())
+            if (!walk.next(Hk))
                 break;
         }
         if (any && !ok) {
@@ -583,7 +632,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         };
         const auto tile_at = [&](int j) {   // j does not go back; j < total
             while (j >= j1) {
-                walk.next();
+                walk.next(Hk);
                 j1 += walk.n;
             }
             return Tile{walk.en.first + (walk.t0 + j - (j1 - walk.n)) * BT, walk.en.end, walk.en.len, walk.kh, walk.en.b};
@@ -703,7 +752,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             const int n = walk.n;
             if (w >= walk.row_tiles()) {
                 j += n;
-                if (!walk.next())
+                if (!walk.next(Hk))
                     break;
                 continue;
             }
@@ -787,7 +836,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             }
             if (live_row)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
-            if (!walk.next())
+            if (!walk.next(Hk))
                 break;
         }
         if (any && !ok) {
@@ -804,8 +853,9 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 }
 
 // ---------------------------------------------------------------- join
-// The pieces of a row: the group's, then the sequence's own, W warps a row (as
-// combine_kernel of bdla_cache.cu).
+// The pieces of a row: the group's, then the sequence's own.  W warps a row, each
+// taking every W-th piece with a maximum of its own; their sums are added in
+// order.
 template <int D, int W>
 __global__ void __launch_bounds__(W < 4 ? 128 : 32 * W)
 shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan plan, int n_groups, int64_t rows)
@@ -830,8 +880,8 @@ shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan 
         step = (int64_t)Hk * x.R;
         if (x.nt == 0)
             return x.np;
-        const int64_t begin = x.base + ((int64_t)(rr / kWideTile) * Hk + kh) * x.nt;
-        return (int)((begin + x.nt - 1) / head.per_cta - begin / head.per_cta) + 1;
+        const int begin = x.base + ((rr / kWideTile) * Hk + kh) * x.nt;
+        return (begin + x.nt - 1) / head.per_cta - begin / head.per_cta + 1;
     };
     int64_t f0 = 0, s0 = 0, f1 = 0, s1 = 0;
     const int n1 = pieces(n_groups + b, f1, s1);
@@ -841,36 +891,67 @@ shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan 
         return;   // the whole CTA
     const int n = live ? n0 + n1 : 0;
     const auto place = [&](int s) { return s < n0 ? f0 + s * s0 : f1 + (s - n0) * s1; };
-    const float cs = a.scale * kLog2e;
-    float m = -INFINITY;
-    for (int s = w * 32 + lane; s < n; s += 32 * W)
-        m = fmaxf(m, a.part_ml[2 * place(s)]);
-    for (int x = 16; x > 0; x >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (W > 1) {
-        if (lane == 0)
-            red_m[mine][w] = m;
-        __syncthreads();
-        for (int x = 0; x < W; ++x)
-            m = fmaxf(m, red_m[mine][x]);
-    }
-    float l = 0.0f, v[E];
+    const float cs = a.scale * 1.4426950408889634f;
+    // rounds of 32 pieces of each warp, a lane's own piece's maximum and sum; sums of rows eight at a time, asked for
+    // before the maximum is known
+    float m = -INFINITY, l = 0.0f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         v[e] = 0.0f;
-#pragma unroll 8
-    for (int s = w; s < n; s += W) {
-        const int64_t p = place(s);
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * p);
-        const float f = ml.x == m ? 1.0f : ex2((ml.x - m) * cs);
-        l = fmaf(ml.y, f, l);
-        const float *y = a.part_o + p * D + E * lane;
+    for (int s0_ = 0; s0_ < n; s0_ += 32 * W) {
+        const int mine_s = s0_ + w + W * lane;
+        const float2 ml = mine_s < n ? *reinterpret_cast<const float2 *>(a.part_ml + 2 * place(mine_s)) : make_float2(-INFINITY, 0.0f);
+        float top = ml.x;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 z = *reinterpret_cast<const float2 *>(y + e);
-            v[e] = fmaf(z.x, f, v[e]);
-            v[e + 1] = fmaf(z.y, f, v[e + 1]);
+        for (int x = 16; x > 0; x >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, m);
+        const float old = m == top ? 1.0f : ex2((m - top) * cs);
+        m = top;
+        const float f = ml.x == top ? 1.0f : ex2((ml.x - top) * cs);
+        l *= old;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] *= old;
+        const int here = min(32, (n - s0_ - w + W - 1) / W);   // pieces of this warp
+        for (int u0 = 0; u0 < here; u0 += 8) {
+            float y[8][E];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float *src = a.part_o + place(s0_ + w + W * (u0 + u)) * D + E * lane;
+                const bool some = u0 + u < here;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 z = some ? *reinterpret_cast<const float2 *>(src + e) : make_float2(0.0f, 0.0f);
+                    y[u][e] = z.x;
+                    y[u][e + 1] = z.y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float fu = __shfl_sync(0xffffffffu, f, u0 + u), lu = __shfl_sync(0xffffffffu, ml.y, u0 + u);
+                if (u0 + u >= here)
+                    continue;
+                l = fmaf(lu, fu, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    v[e] = fmaf(y[u][e], fu, v[e]);
+            }
         }
+    }
+    if (W > 1) {   // the warps' sums to one maximum
+        if (lane == 0)
+            red_m[mine][w] = m;
+        __syncthreads();
+        float top = m;
+        for (int x = 0; x < W; ++x)
+            top = fmaxf(top, red_m[mine][x]);
+        const float f = m == top ? 1.0f : ex2((m - top) * cs);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] *= f;
     }
     if (W > 1) {
         if (lane == 0)
@@ -932,12 +1013,13 @@ size_t shared_bytes(const bdla_attn_dims &d, int n_groups)
     return carve(sizes_of(d, n_groups), nullptr, &p);
 }
 
-// Tiles of a CTA and rows of the partial sums are 32-bit.
+// Tiles (with a CTA's worth beyond them) and rows of the partial sums are 32-bit.
 bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
 {
     const Sizes z = sizes_of(d, n_groups);
-    const int64_t blocks = ((int64_t)d.B * d.T * (d.Hq / d.Hk) / kWideTile + n_groups + 2 * (int64_t)d.B) * d.Hk;
-    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1) / z.ctas <= INT32_MAX / 4;
+    const int64_t R = (int64_t)d.T * z.G, groups = z.wide ? R * d.B / kWideTile + (n_groups < d.B / 2 ? n_groups : d.B / 2) : 0;
+    const int64_t blocks = (groups + (z.own_wide ? (R + kWideTile - 1) / kWideTile * d.B : 0)) * d.Hk;
+    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1) <= INT32_MAX / 2;
 }
 
 cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, const int32_t *cu_groups, const int32_t *shared,
@@ -968,7 +1050,7 @@ cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.n_list = &p.head->n_list;
     KernelMark mark_(BDLA_KERNEL_ATTN_SHARED, stream);
     const int entries = n_groups + d.B;
-    plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? entries * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
+    plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? plan_ints(n_groups, d.B) * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
     cudaError_t err = cudaGetLastError();
     if (err == cudaSuccess && z.wide)
         err = d.d == 64 ? wide_go<64>(a, p, z, stream) : wide_go<128>(a, p, z, stream);

@@ -6,7 +6,7 @@ import random
 import pytest
 
 SMS, TILE, WIDE, NARROW = 152, 128, 256, 32
-LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2, 32
+LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2, 8
 
 
 def up(a, b):
@@ -59,18 +59,16 @@ def plan(z, cu, shared, lens, cap):
     tiles = sum(x[3] * z.Hk * up(n[e], TILE) for e, x in enumerate(entries) if x[2])
     positions = sum(x[3] * n[e] for e, x in enumerate(entries) if not x[2])
     per_cta = max(LEAST_TILES, up(tiles, SMS))
-    size = 64
-    if z.most > 0:
-        least, best = up(positions, z.extra), None
-        for i in range(N_SIZES):
-            s = 64 * ((3 if i & 1 else 2) << (i >> 1))
-            s = s if s >= least else up(least, 64) * 64
+    size = min(up(up(positions, z.extra), 64) * 64, 2 ** 31 - 128) if z.most > 0 else 64
+    if z.most > 0 and size <= 128 << (N_SIZES - 1):
+        best = None
+        for s in (128 << i for i in range(N_SIZES)):
             pieces = sum(x[3] * max(up(n[e], s), 1 if e >= NG else 0) for e, x in enumerate(entries) if not x[2])
             longest = max([up(n[e], s) for e, x in enumerate(entries) if not x[2]], default=0)
-            cost = (positions + 128 * pieces) * z.Hk // z.slots + s + 4 * longest
-            if best is None or cost < best[0]:
+            cost = (positions + 128 * pieces) * z.Hk / z.slots + s + 4 * longest
+            if s >= size and (best is None or cost < best[0]):
                 best = (cost, s)
-        size = min(best[1], 2 ** 31 - 1 - 64)
+        size = best[1]
     parts, wides, work, base, rows, first_entry = [], [], [], 0, 0, {}
     for e, (R, tok0, wide, blocks) in enumerate(entries):
         g = group[e - NG] if e >= NG else -1
