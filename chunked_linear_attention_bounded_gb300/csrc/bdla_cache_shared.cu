@@ -35,11 +35,13 @@ using namespace cache;
 
 constexpr int kNarrowRows = 32;   // rows a key head up to which warp MMAs take a group
 constexpr int kWideTile = 256;    // rows of a CTA of the wide kernel
+constexpr int kRunTiles = 3;      // what a change of rows costs the wide kernel, in tiles
 constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
 
 // What the wide kernel walks: positions first .. end - 1 of sequence b's table
 // for the R rows from token tok0 on, as blocks of 256 rows times key heads, each
-// of nt tiles of 128 positions.  `base`: tiles of the entries before it.
+// kRunTiles and then nt tiles of 128 positions on the line that the CTAs cut
+// evenly.  `base`: the line before it.
 struct alignas(16) WideEntry {
     int base, b, tok0, R, first, end, len, nt, part;
 };
@@ -51,8 +53,8 @@ struct alignas(16) Parts {
 };
 
 struct Head {
-    int tiles;       // of the wide kernel
-    int per_cta;     // tiles of a CTA
+    int tiles;       // of the wide kernel, its runs' costs among them
+    int per_cta;     // of a CTA
     int n_list;      // pieces of the narrow kernel
 };
 
@@ -87,7 +89,7 @@ constexpr size_t plan_ints(int n_groups, int B) { return 3 * (size_t)n_groups + 
 // Bounds of the plan.  Narrow: a piece size of at least the (block-weighted)
 // positions over `extra` cuts at most `extra` pieces beyond the first of each
 // block; sequences have one block, groups of at most 32 rows one or two, and a
-// group that shares has two sequences or more.  Wide: a unit of nt tiles lies in
+// group that shares has two sequences or more.  Wide: nt tiles in a row lie in
 // nt / per_cta + 2 CTAs at most; nt R <= 256 tiles of the blocks, and all tiles
 // are at most ctas x per_cta.
 Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
@@ -143,7 +145,7 @@ size_t carve(const Sizes &s, char *at, Plan *p)
 constexpr int kPlanThreads = 512;
 constexpr int kPlanEntries = 4000;   // whose offsets, groups and lengths fit into 48 KB of shared memory
 constexpr int kLeastShared = 64;     // shared positions that are worth a piece of their own
-constexpr int kLeastTiles = 2;       // tiles of a wide CTA
+constexpr int kLeastTiles = 2 + kRunTiles;   // of a wide CTA
 constexpr int kFew = 4;               // pieces, or CTAs, of an entry that one lane writes
 constexpr int kSizes = 8;            // piece sizes of the narrow kernel that are weighed: 128, 256 .. 16384 positions
 
@@ -263,7 +265,7 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
         const int n = e < NG ? taken(e) : len[e] - taken(group[e - NG]), R = rows(e, n);
         len[e] = n;
         if (wide(e, R))
-            tiles += blocks(R, true) * z.Hk * tiles_of(n);
+            tiles += n > 0 ? blocks(R, true) * z.Hk * (tiles_of(n) + kRunTiles) : 0;
         else
             positions += (int64_t)blocks(R, false) * n;
     }
@@ -339,7 +341,7 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
             first = e < NG ? 0 : taken(group[e - NG]);
             if (w) {
                 nt = tiles_of(n);
-                m.tiles = nb * z.Hk * nt;
+                m.tiles = nt > 0 ? nb * z.Hk * (nt + kRunTiles) : 0;
                 m.rows = nt > 0 ? (over(nt, per_cta) + 1) * R * z.Hk : 0;
                 m.wides = nt > 0;
             } else {
@@ -421,31 +423,32 @@ struct Walk {
     WideEntry en;
     const WideEntry *at;
     int rb, kh, t0, n, piece, left;
-    // One lane; false: there is no tile.
-    __device__ __forceinline__ bool begin(const Plan &p, int Hk, int cta)
+    // One lane.  n = 0: there is no tile.
+    __device__ __forceinline__ void begin(const Plan &p, int Hk, int cta)
     {
         const Head h = *p.head;
         const int x = cta * h.per_cta;
         left = x < h.tiles ? min(h.tiles - x, h.per_cta) : 0;
         n = 0;
         if (left == 0)
-            return false;
+            return;
         at = p.wide + p.first_entry[cta];
         en = *at;
-        const int unit = (x - en.base) / en.nt, from = en.base + unit * en.nt;
-        t0 = x - from;
+        const int whole = en.nt + kRunTiles, unit = (x - en.base) / whole, from = en.base + unit * whole + kRunTiles;
+        t0 = max(x - from, 0);
+        left -= from + t0 - x;   // (a run may be paid for by the CTA before)
         rb = unit / Hk;
         kh = unit - rb * Hk;
         piece = cta - from / h.per_cta;
-        n = min(en.nt - t0, left);
-        return true;
+        n = max(min(en.nt - t0, left), 0);
     }
     // The next run, by the whole warp; false: there is none.
     __device__ __forceinline__ bool next(int Hk)
     {
         __syncwarp();   // all have looked at the run before
         if ((threadIdx.x & 31) == 0) {
-            left -= n;
+            left -= n + kRunTiles;
+            n = 0;
             if (left > 0) {
                 t0 = piece = 0;
                 if (++kh == Hk) {
@@ -459,7 +462,7 @@ struct Walk {
             }
         }
         __syncwarp();
-        return left > 0;
+        return n > 0;
     }
     __device__ __forceinline__ int row_tiles() const { return en.R - rb * kWideTile > BT ? 2 : 1; }
 };
@@ -475,7 +478,7 @@ template <int D> struct WideSmem {
     alignas(1024) unsigned char ring[kStages][kTile];   // K_0 V_0 K_1 V_1 ...
     int row[kFetchWarps][BT];    // cache row of the positions of a warp's tile, -1: not seen
     uint32_t valid[kSlots][4];   // positions of a tile that may be seen
-    uint64_t full[kStages], empty[kStages], q_full[2], s_full[2], o_done[2], drain, never;
+    uint64_t full[kStages], empty[kStages], q_full[2], s_full[2], o_done[2], merge, merged, drain, never;
     uint64_t p_ready[2][2];   // weights of the first and of the last 64 positions of a tile
     uint64_t wait_ns;
     Walk walk[1 + kFetchWarps + 8];   // of each warp
@@ -488,7 +491,10 @@ static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxS
 // run of tiles to the next: tiles, ring stages and barrier phases count on, keys
 // and values of the next run are fetched while the last of this one is worked
 // on, and only the rows (queries in, sums out) change hands.  All CTAs get the
-// same number of tiles.  `run` as there.
+// same number of tiles.  Where a block has 128 rows or fewer there is no second
+// row tile to turn to: both softmax groups then take the same rows and every
+// second tile of positions, and the first reads the output of both out of tensor
+// memory at the run's end.  `run` as there.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, int run,
@@ -523,6 +529,8 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             mbar_init(&sm.p_ready[x][1], BT);
             mbar_init(&sm.o_done[x], 1);
         }
+        mbar_init(&sm.merge, BT);
+        mbar_init(&sm.merged, BT);
         mbar_init(&sm.drain, 1);
         mbar_init(&sm.never, 1);
         sm.abort_flag = 0;
@@ -539,18 +547,19 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     if (lane == 0)
         walk.begin(plan, Hk, blockIdx.x);
     __syncwarp();
-    const int total = walk.left, stall_at = total > 1 ? 1 : 0;   // test hook: the tile at which a role stalls
+    const bool any = walk.n > 0;
+    const int stall_at = walk.n > 1 ? 1 : 0;   // test hook: the tile at which a role stalls
 
     if (warp == 0) {
         // ---------------------------------------------------------------- MMA issuer
         const uint64_t q[2] = {rows_desc(smem_u32(sm.q[0])), rows_desc(smem_u32(sm.q[1]))};
-        bool ok = total > 0;
-        const bool any = ok;
-        int j0 = 0;                 // tiles before this run
-        int runs[2] = {0, 0};       // runs that a row tile has had
-        int had[2] = {0, 0};        // and tiles
+        bool ok = any;
+        int j0 = 0;              // tiles before this run
+        int runs[2] = {0, 0};    // runs before this one that a softmax group has had tiles of
+        int had[2] = {0, 0};     // and its tiles
         while (ok) {
-            const int tiles = walk.row_tiles(), n = walk.n;
+            // a tile's two turns, one for each row tile; or two tiles' turns, one for each group
+            const int n = walk.n, turns = walk.row_tiles() == 1, step = turns ? 2 : 1;
             auto issue_qk = [&](int w, int j) {
                 const int it = 2 * j;
                 if (!warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag))
@@ -560,26 +569,31 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 if (elect_one()) {
                     mma_rows<D>(tmem + BT * w, q[w], k);
                     umma_commit(&sm.s_full[w]);
-                    if (w == tiles - 1)   // the last reader of this key tile
+                    if (turns || w == 1)   // the last reader of this key tile
                         umma_commit(&sm.empty[it % NS]);
                 }
                 __syncwarp();
                 return true;
             };
-            for (int w = 0; ok && w < tiles; ++w) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int x = turns ? w : 0;
+                if (!ok || x >= n)
+                    continue;
                 ok = warp_wait(&sm.q_full[w], (uint32_t)(runs[w]++ & 1), &sm.wait_ns, abort_flag);
                 tc_fence_after();
-                ok = ok && issue_qk(w, j0);
+                ok = ok && issue_qk(w, j0 + x);
             }
-            for (int j = 0; ok && j < n; ++j) {
+            for (int x0 = 0; ok && x0 < n; x0 += step) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    if (!ok || w >= tiles)
+                    const int x = turns ? x0 + w : x0;
+                    if (!ok || x >= n)
                         continue;
-                    const int it = 2 * (j0 + j) + 1;
+                    const int it = 2 * (j0 + x) + 1;
                     const uint32_t phase = (uint32_t)(had[w] & 1);
                     ++had[w];
-                    const bool hook = stall == BDLA_STALL_MMA && j0 + j == stall_at;
+                    const bool hook = stall == BDLA_STALL_MMA && j0 + x == stall_at;
                     ok = warp_wait(&sm.full[it % NS], (it / NS) & 1, &sm.wait_ns, abort_flag) &&
                          warp_wait(hook ? &sm.never : &sm.p_ready[w][0], hook ? 0u : phase, &sm.wait_ns, abort_flag);
                     if (!ok)
@@ -588,7 +602,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     const uint64_t v = sum_desc(smem_u32(sm.ring[it % NS]));
                     const uint32_t acc = tmem + 2 * BT + BT * w, wt = tmem + BT * w;
                     if (elect_one())
-                        mma_sum<D, 32, 0, BT / 32>(acc, wt, v, j > 0);
+                        mma_sum<D, 32, 0, BT / 32>(acc, wt, v, x0 > 0);
                     __syncwarp();
                     ok = warp_wait(&sm.p_ready[w][1], phase, &sm.wait_ns, abort_flag);
                     if (!ok)
@@ -596,14 +610,14 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     tc_fence_after();
                     if (elect_one()) {
                         mma_sum<D, 32, BT / 32, BT / 16>(acc, wt, v, true);
-                        if (w == tiles - 1)
+                        if (turns || w == 1)
                             umma_commit(&sm.empty[it % NS]);
-                        if (j + 1 == n)
+                        if (x + step >= n)
                             umma_commit(&sm.o_done[w]);
                     }
                     __syncwarp();
-                    if (j + 1 < n)
-                        ok = issue_qk(w, j0 + j + 1);
+                    if (x + step < n)
+                        ok = issue_qk(w, j0 + x + step);
                 }
             }
             j0 += n;
@@ -630,12 +644,14 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         struct Tile {
             int t, end, len, kh, b;
         };
-        const auto tile_at = [&](int j) {   // j does not go back; j < total
+        const auto tile_at = [&](int j, Tile &x) {   // j does not go back; false: there is none
             while (j >= j1) {
-                walk.next(Hk);
+                if (!walk.next(Hk))
+                    return false;
                 j1 += walk.n;
             }
-            return Tile{walk.en.first + (walk.t0 + j - (j1 - walk.n)) * BT, walk.en.end, walk.en.len, walk.kh, walk.en.b};
+            x = {walk.en.first + (walk.t0 + j - (j1 - walk.n)) * BT, walk.en.end, walk.en.len, walk.kh, walk.en.b};
+            return true;
         };
         const auto lookup = [&](const Tile &x, int (&pg)[4]) {
             const int32_t *table = c.pages + (int64_t)x.b * c.max_pages;
@@ -647,11 +663,10 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         };
         Tile now{}, ahead{};
         int pg[4];
-        if (fw < total) {
-            ahead = tile_at(fw);
+        bool more = any && tile_at(fw, ahead);
+        if (more)
             lookup(ahead, pg);
-        }
-        for (int j = fw; ok && j < total; j += kFetchWarps) {
+        for (int j = fw; ok && more; j += kFetchWarps) {
             now = ahead;
             const uint64_t seen = now.t + BT > now.len ? sees_any(a.tree, now.b, T, lane) : 0;
             int row[4];
@@ -678,10 +693,9 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 *reinterpret_cast<int4 *>(&sm.row[fw][4 * lane]) = make_int4(row[0], row[1], row[2], row[3]);
                 __syncwarp();
             }
-            if (j + kFetchWarps < total) {
-                ahead = tile_at(j + kFetchWarps);
+            more = tile_at(j + kFetchWarps, ahead);
+            if (more)
                 lookup(ahead, pg);
-            }
 #pragma unroll 1
             for (int v = 0; ok && v < 2; ++v) {
                 const int it = 2 * j + v, s = it % NS;
@@ -745,18 +759,18 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         const uint32_t t_s = tmem + BT * w + lane_off, t_o = tmem + 2 * BT + BT * w + lane_off;
         const float cs = a.scale * kLog2e;
-        bool ok = total > 0;
-        const bool any = ok;
-        int j = 0, had = 0, runs = 0;   // tiles of the CTA; tiles and runs of this row tile
+        bool ok = any;
+        float2 *second = reinterpret_cast<float2 *>(sm.q[1]);   // group 1's maxima and sums (its queries are read by then)
+        int j0 = 0, had = 0, runs = 0, merges = 0;   // tiles before this run; tiles, runs and shared runs of this group
         while (ok) {
-            const int n = walk.n;
-            if (w >= walk.row_tiles()) {
-                j += n;
+            const int n = walk.n, turns = walk.row_tiles() == 1;
+            if (turns && w >= n) {   // one tile, which is the other group's
+                j0 += n;
                 if (!walk.next(Hk))
                     break;
                 continue;
             }
-            const int rr = walk.rb * kWideTile + w * BT + r, R = walk.en.R;
+            const int rr = walk.rb * kWideTile + (turns ? 0 : w * BT) + r, R = walk.en.R;
             const bool live_row = rr < R;
             const int i = live_row ? rr / G : 0;
             {
@@ -770,11 +784,12 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 tc_fence_before();   // the sums of the run before have been read
                 mbar_arrive(&sm.q_full[w]);
             }
-            const int len = walk.en.len;
-            int t0 = walk.en.first + walk.t0 * BT;
+            const int len = walk.en.len, step = turns ? 2 : 1, x0 = turns ? w : 0;
             const uint64_t see = walk.en.end > len ? sees(a.tree, walk.en.b, T, i) : 0;
             RowSoftmax row;
-            for (int x = 0; x < n; ++x, ++j, t0 += BT) {
+            int t0 = walk.en.first + (walk.t0 + x0) * BT;
+            for (int x = x0; x < n; x += step, t0 += step * BT) {
+                const int j = j0 + x;
                 const bool hook = stall == BDLA_STALL_EPILOGUE && j == stall_at;
                 ok = warp_wait(hook ? &sm.never : &sm.s_full[w], hook ? 0u : (uint32_t)(had & 1), &sm.wait_ns, abort_flag);
                 ++had;
@@ -794,24 +809,48 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // what this row sees of the 32 positions: the context, and its bits of the new tokens
-                        const int j0 = t0 + 32 * k - len;   // first of them as a new token
-                        uint32_t mask = j0 <= -32 ? 0xffffffffu
-                                                  : j0 < 0 ? ((1u << -j0) - 1) | (uint32_t)(see << -j0)
-                                                           : j0 < 64 ? (uint32_t)(see >> j0) : 0u;
+                        const int p0 = t0 + 32 * k - len;   // first of them as a new token
+                        uint32_t mask = p0 <= -32 ? 0xffffffffu
+                                                  : p0 < 0 ? ((1u << -p0) - 1) | (uint32_t)(see << -p0)
+                                                           : p0 < 64 ? (uint32_t)(see >> p0) : 0u;
                         mask &= sm.valid[j % SL][k];
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             s[k][e] = (mask >> e) & 1 ? s[k][e] : 0xff800000u;
                     }
                 }
-                row_weights<D>(s, cs, t_s, t_o, x == 0, row, [&](int half) { mbar_arrive(&sm.p_ready[w][half]); });
+                row_weights<D>(s, cs, t_s, t_o, x == x0, row, [&](int half) { mbar_arrive(&sm.p_ready[w][half]); });
             }
             if (ok)
-                ok = warp_wait(&sm.o_done[w], (uint32_t)(runs & 1), &sm.wait_ns, abort_flag);
-            ++runs;
+                ok = warp_wait(&sm.o_done[w], (uint32_t)(runs++ & 1), &sm.wait_ns, abort_flag);
             if (!ok)
                 break;
             tc_fence_after();
+            j0 += n;
+            float f0 = 1.0f, f1 = 0.0f;   // factors of this group's sums and of the other's
+            const bool both = turns && n > 1;
+            if (both) {
+                // the same rows: group 1 hands its maximum and sum over, and group 0 reads the output of both
+                if (w == 1) {
+                    second[r] = make_float2(row.m, row.l);
+                    tc_fence_before();
+                    mbar_arrive(&sm.merge);
+                    ok = warp_wait(&sm.merged, (uint32_t)(merges++ & 1), &sm.wait_ns, abort_flag);
+                    if (!ok || !walk.next(Hk))
+                        break;
+                    continue;
+                }
+                ok = warp_wait(&sm.merge, (uint32_t)(merges++ & 1), &sm.wait_ns, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const float2 o = second[r];
+                const float m = fmaxf(row.m, o.x);
+                f0 = row.m == m ? 1.0f : ex2((row.m - m) * cs);
+                f1 = o.x == m ? 1.0f : ex2((o.x - m) * cs);
+                row.m = m;
+                row.l = fmaf(row.l, f0, o.y * f1);
+            }
             const int64_t pt = (int64_t)walk.en.part + ((int64_t)walk.piece * Hk + walk.kh) * R + rr;
             // 32 rows of 128 bytes at a time through the warp's own rows of its query tile (read by now), so that whole
             // lines leave
@@ -820,7 +859,16 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t y[32];
                 tmem_ld32(t_o + 32 * k, y);
-                tmem_ld_wait();
+                if (both) {
+                    uint32_t y1[32];
+                    tmem_ld32(t_o + BT + 32 * k, y1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        y[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f0, __uint_as_float(y1[e]) * f1));
+                } else {
+                    tmem_ld_wait();
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     stage[lane * 8 + (e ^ (lane & 7))] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
@@ -833,6 +881,10 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                         *reinterpret_cast<uint4 *>(a.part_o + (pt - lane + x) * D + 32 * k + 4 * (lane & 7)) = z;
                 }
                 __syncwarp();
+            }
+            if (both) {
+                tc_fence_before();   // the other group's output has been read
+                mbar_arrive(&sm.merged);
             }
             if (live_row)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
@@ -880,7 +932,7 @@ shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan 
         step = (int64_t)Hk * x.R;
         if (x.nt == 0)
             return x.np;
-        const int begin = x.base + ((rr / kWideTile) * Hk + kh) * x.nt;
+        const int begin = x.base + ((rr / kWideTile) * Hk + kh) * (x.nt + kRunTiles) + kRunTiles;
         return (begin + x.nt - 1) / head.per_cta - begin / head.per_cta + 1;
     };
     int64_t f0 = 0, s0 = 0, f1 = 0, s1 = 0;
@@ -1019,7 +1071,7 @@ bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
     const Sizes z = sizes_of(d, n_groups);
     const int64_t R = (int64_t)d.T * z.G, groups = z.wide ? R * d.B / kWideTile + (n_groups < d.B / 2 ? n_groups : d.B / 2) : 0;
     const int64_t blocks = (groups + (z.own_wide ? (R + kWideTile - 1) / kWideTile * d.B : 0)) * d.Hk;
-    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1) <= INT32_MAX / 2;
+    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1 + kRunTiles) <= INT32_MAX / 2;
 }
 
 cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, const int32_t *cu_groups, const int32_t *shared,

@@ -6,7 +6,8 @@ import random
 import pytest
 
 SMS, TILE, WIDE, NARROW = 152, 128, 256, 32
-LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2, 8
+RUN = 3   # what a change of rows costs, in tiles
+LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2 + RUN, 8
 
 
 def up(a, b):
@@ -56,7 +57,7 @@ def plan(z, cu, shared, lens, cap):
         return R, tok0, wide, up(R, WIDE if wide else z.mr)
 
     entries = [entry(e) for e in range(E)]
-    tiles = sum(x[3] * z.Hk * up(n[e], TILE) for e, x in enumerate(entries) if x[2])
+    tiles = sum(x[3] * z.Hk * (up(n[e], TILE) + RUN) for e, x in enumerate(entries) if x[2] and n[e])
     positions = sum(x[3] * n[e] for e, x in enumerate(entries) if not x[2])
     per_cta = max(LEAST_TILES, up(tiles, SMS))
     size = min(up(up(positions, z.extra), 64) * 64, 2 ** 31 - 128) if z.most > 0 else 64
@@ -75,7 +76,7 @@ def plan(z, cu, shared, lens, cap):
         first = 0 if e < NG or g < 0 else n[g]
         b = e - NG if e >= NG else (cu[e] if n[e] > 0 else 0)
         np, direct, nt = 0, False, up(n[e], TILE) if wide else 0
-        w = blocks * z.Hk * nt
+        w = blocks * z.Hk * (nt + RUN) if nt else 0
         need = (up(nt, per_cta) + 1) * R * z.Hk if nt else 0
         if not wide:
             np = up(n[e], size)
@@ -107,21 +108,21 @@ def walk(z, wides, tiles, per_cta, first_entry, cta):
         return
     e = first_entry[cta]
     base, nt = wides[e][0], wides[e][6]
-    unit = (x - base) // nt
-    begin = base + unit * nt
-    t0, rb, kh, piece = x - begin, unit // z.Hk, unit % z.Hk, cta - begin // per_cta
-    while True:
-        n = min(wides[e][6] - t0, left)
+    unit = (x - base) // (nt + RUN)
+    begin = base + unit * (nt + RUN) + RUN
+    t0, rb, kh, piece = max(x - begin, 0), unit // z.Hk, unit % z.Hk, cta - begin // per_cta
+    left -= begin + t0 - x
+    n = min(nt - t0, left)
+    while n > 0:
         yield e, rb, kh, t0, n, piece
-        left -= n
-        if left <= 0:
-            return
+        left -= n + RUN
         t0 = piece = 0
         kh += 1
         if kh == z.Hk:
             kh, rb = 0, rb + 1
             if rb * WIDE >= wides[e][3]:
                 rb, e = 0, e + 1
+        n = min(wides[e][6], left) if left > 0 else 0
 
 
 def check(B, T, G, Hk, d, cu, shared, lens, cap):
@@ -154,7 +155,7 @@ def check(B, T, G, Hk, d, cu, shared, lens, cap):
         base, nt, R, part, np, tok0 = parts[e]
         rr, kh = (b * T + i - tok0) * G + h % G, h // G
         if nt:
-            begin = base + (rr // WIDE * Hk + kh) * nt
+            begin = base + (rr // WIDE * Hk + kh) * (nt + RUN) + RUN
             np = (begin + nt - 1) // per_cta - begin // per_cta + 1
         return [part + kh * R + rr + s * Hk * R for s in range(max(np, 0))] if np >= 0 else None
 
