@@ -3,10 +3,10 @@
 // cache.  Saves the keys' way through memory (4 bytes an element) and a launch
 // against bdla_qk_norm followed by bdla_cache_append, whose bits it gives.
 //
-// A group of lanes takes one token and a chunk of its query, key or value heads;
-// value heads are copied and run through the norm's shuffles along with their
-// warp.  The first heads are asked for before the token's place is looked up
-// (length, page), so that the two chains overlap.
+// A group of lanes takes one token and a chunk of its query, key or value heads,
+// and a warp the same chunk of four or eight tokens, so that values are copied by
+// whole warps without the norm's arithmetic.  The first heads are asked for before
+// the token's place is looked up (length, page), so that the two chains overlap.
 #include "bdla_cache.cuh"
 #include "bdla_norm.cuh"
 
@@ -34,10 +34,15 @@ norm_append_kernel(const __grid_constant__ NormParams p, const __grid_constant__
     if (blockIdx.x == 0 && p.cu != nullptr)
         attn::check_offsets(p.cu, p.n_docs, p.tokens, a.st);
     G g(p);
-    const int64_t item = (int64_t)blockIdx.x * G::kPerBlock + threadIdx.x / G::kLanes;
-    const bool any = item < (int64_t)p.tokens * p.n_chunks;
-    const int t = any ? (int)(item / p.n_chunks) : 0;
-    int c = any ? (int)(item - (int64_t)t * p.n_chunks) : 0;
+    // a warp takes one chunk (of queries, keys or values) of kTokens tokens
+    constexpr int kTokens = 32 / G::kLanes;
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), block = unit / p.n_chunks;
+    int c = (int)(unit - block * p.n_chunks);
+    const int64_t token = block * kTokens + (threadIdx.x & 31) / G::kLanes;
+    const bool any = token < p.tokens;
+    if (block * kTokens >= p.tokens)
+        return;   // the whole warp
+    const int t = any ? (int)token : 0;
     const int kind = c < p.q_chunks ? 0 : c < p.q_chunks + a.kv_chunks ? 1 : 2;   // queries, keys, values
     c -= kind == 0 ? 0 : kind == 1 ? p.q_chunks : p.q_chunks + a.kv_chunks;
     const int s = kind > 0, h0 = c * p.chunk;
@@ -100,6 +105,19 @@ norm_append_kernel(const __grid_constant__ NormParams p, const __grid_constant__
         }
         dst = static_cast<__nv_bfloat16 *>(kind == 1 ? a.c.k : a.c.v) + (row < 0 ? 0 : row) * p.heads[1] * D;
     }
+    if (kind == 2) {   // copied
+        for (int first = h0; first < h0 + p.chunk; first += kBatch) {
+            if (first > h0)
+                fetch(first);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (first + u < h1) {
+                    __stcs(reinterpret_cast<uint4 *>(dst + (first + u) * D + g.f0), in[u][0]);
+                    __stcs(reinterpret_cast<uint4 *>(dst + (first + u) * D + g.f1), in[u][1]);
+                }
+        }
+        return;
+    }
     Pairs own, other;
     {
         float cs[kPairs], sn[kPairs];
@@ -113,16 +131,9 @@ norm_append_kernel(const __grid_constant__ NormParams p, const __grid_constant__
             fetch(first);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int h = first + u;
             const Pairs y = normed<D, INTER>(in[u][0], in[u][1], p.eps, own, other);
-            if (h >= h1)
-                continue;
-            if (kind == 2) {
-                *reinterpret_cast<uint4 *>(dst + h * D + g.f0) = in[u][0];
-                *reinterpret_cast<uint4 *>(dst + h * D + g.f1) = in[u][1];
-            } else {
-                store16(dst + h * D, g.f0, g.f1, y);
-            }
+            if (first + u < h1)
+                store16(dst + (first + u) * D, g.f0, g.f1, y);
         }
     }
 }
@@ -140,9 +151,8 @@ cudaError_t launch_qk_norm_append(const bdla_qk_norm_args &a, const __nv_bfloat1
     p.q_chunks = (q_heads + p.chunk - 1) / p.chunk;
     p.n_chunks = p.q_chunks + 2 * ap.kv_chunks;
     const Turns &tu = turns_of(a);
-    const int64_t items = (int64_t)p.tokens * p.n_chunks;
-    const int per = kThreads / (d.d / kFeat);
-    const int64_t grid = (items + per - 1) / per;
+    const int per = 32 / (d.d / kFeat);   // tokens of a warp
+    const int64_t warps = ((int64_t)p.tokens + per - 1) / per * p.n_chunks, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
     auto *kern = d.d == 64 ? (a.interleaved ? norm_append_kernel<64, true> : norm_append_kernel<64, false>)
