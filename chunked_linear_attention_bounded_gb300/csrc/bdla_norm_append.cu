@@ -129,11 +129,20 @@ norm_append_kernel(const __grid_constant__ NormParams p, const __grid_constant__
     for (int first = h0; first < h0 + p.chunk; first += kBatch) {
         if (first > h0)
             fetch(first);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        const auto one = [&](int u) {
             const Pairs y = normed<D, INTER>(in[u][0], in[u][1], p.eps, own, other);
             if (first + u < h1)
                 store16(dst + (first + u) * D, g.f0, g.f1, y);
+        };
+        if (first + kBatch <= h0 + p.chunk) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                one(u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (first + u < h0 + p.chunk)   // (all lanes: a few tokens' few heads skip the arithmetic of the others)
+                    one(u);
         }
     }
 }
@@ -145,14 +154,18 @@ cudaError_t launch_qk_norm_append(const bdla_qk_norm_args &a, const __nv_bfloat1
                                   const bdla_attn_dims &d, DeviceStatus *st, cudaStream_t stream)
 {
     const int q_heads = a.q != nullptr ? d.Hq : 0;
-    NormParams p = norm_params(a, d, head_chunk(d, q_heads + 2 * d.Hk));
+    // heads of a warp: as few as put all warps onto the SMs at once (16 each), up to 8, which share the angles' cost
+    const int per = 32 / (d.d / kFeat);   // tokens of a warp
+    const int64_t blocks = ((int64_t)d.B * d.T + per - 1) / per, held = (int64_t)sm_count() * (kThreads / 32) * 2;
+    const int64_t even = (blocks * (q_heads + 2 * d.Hk) + held - 1) / held, widest = q_heads > d.Hk ? q_heads : d.Hk;
+    const int64_t chunk = even < 8 ? even : 8;
+    NormParams p = norm_params(a, d, (int)(chunk < widest ? chunk : widest));
     AppendParams ap = {v, v_token, v_head, c, rows, counts, (d.Hk + p.chunk - 1) / p.chunk, st};
     p.heads[0] = q_heads;
     p.q_chunks = (q_heads + p.chunk - 1) / p.chunk;
     p.n_chunks = p.q_chunks + 2 * ap.kv_chunks;
     const Turns &tu = turns_of(a);
-    const int per = 32 / (d.d / kFeat);   // tokens of a warp
-    const int64_t warps = ((int64_t)p.tokens + per - 1) / per * p.n_chunks, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t warps = blocks * p.n_chunks, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
     auto *kern = d.d == 64 ? (a.interleaved ? norm_append_kernel<64, true> : norm_append_kernel<64, false>)
