@@ -121,6 +121,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 using attn::ex2;
 
+__device__ __forceinline__ Work past_l1(const Work &w)
+{
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&w)), y = __ldcg(reinterpret_cast<const int4 *>(&w) + 1);
+    return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
+
 // LIST: the pieces are those of a list on the device, which an earlier kernel of
 // the same call has made (bdla_cache_shared.cu).
 template <int D, int WR, bool LIST>
@@ -144,12 +150,19 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     int64_t tok0, part;         // the rows' first token, and the partial sums' first row (-1: none)
     attn::next_may_start();
     if (LIST) {
-        attn::wait_for_previous();
+        // The list is there when this kernel may start: the one before waited for it, if it is not the one that made it
+        // (past_l1: nothing of it has been read on this SM by this grid, but by the call before).
+        if (!a.list_ready)
+            attn::wait_for_previous();
         kh = idx % Hk;
         idx /= Hk;
-        if (idx >= *a.n_list)
+        const Work w = past_l1(a.list[idx]);   // (there is room for every CTA's, and the counts come along)
+        const int2 n = __ldcg(a.n_list);
+        if (idx >= n.x && idx < n.y) {
+            if (tid == 0)
+                attn::wait_for_previous();
             return;
-        const Work w = a.list[idx];
+        }
         b = w.b;
         k0 = w.k0;
         k1 = w.k1;
@@ -210,11 +223,15 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
         }
         cp_commit();
     };
-    if (tid < kKeys)
-        for (int n = 0; n < 3; ++n) {
-            const int t = k0 + n * kKeys + tid;
-            place(n, t, lookup(t));
-        }
+    if (tid < kKeys) {
+        int pg[3];
+#pragma unroll
+        for (int n = 0; n < 3; ++n)   // together: a table's lines come from far
+            pg[n] = lookup(k0 + n * kKeys + tid);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+            place(n, k0 + n * kKeys + tid, pg[n]);
+    }
     __syncthreads();
     load(0, 0);
     load(0, 1);
@@ -400,6 +417,8 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
                 a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
         }
     }
+    if (LIST && a.list_ready && tid == 0)
+        attn::wait_for_previous();   // so that the end of this kernel is the end of that one too
 }
 
 // Joins the pieces of a row, W warps a row: each sums every W-th piece, and the

@@ -118,8 +118,9 @@ struct Call {
     PageDiv div;
     Pieces pieces;
     DeviceStatus *st;
-    const Work *list;     // of a planned call, n_list on the device
-    const int *n_list;
+    const Work *list;     // of a planned call: pieces 0 .. n_list->x - 1, and from n_list->y on
+    const int2 *n_list;
+    bool list_ready;      // the kernel before did not make it
 };
 
 }  // namespace cache

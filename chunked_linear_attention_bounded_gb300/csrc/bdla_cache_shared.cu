@@ -55,7 +55,7 @@ struct alignas(16) Parts {
 struct Head {
     int tiles;       // of the wide kernel, its runs' costs among them
     int per_cta;     // of a CTA
-    int n_list;      // pieces of the narrow kernel
+    int2 list;       // pieces of the narrow kernel: the long ones from the front, the others from `y` on to the end
 };
 
 // Entries are the groups, then the sequences.
@@ -153,14 +153,15 @@ __device__ __forceinline__ int tiles_of(int n) { return (int)(((uint32_t)n + BT 
 __device__ __forceinline__ int over(int n, int size) { return (int)(((uint32_t)n + (uint32_t)size - 1) / (uint32_t)size); }
 
 // What comes before an entry: tiles of the wide kernel, rows of partial sums,
-// pieces of the narrow list, entries of the wide one.
+// long and short pieces of the narrow list, entries of the wide one.
 struct Sums {
-    int tiles, rows, pieces, wides;
+    int tiles, rows, pieces, shorts, wides;
     __device__ __forceinline__ void add(const Sums &o)
     {
         tiles += o.tiles;
         rows += o.rows;
         pieces += o.pieces;
+        shorts += o.shorts;
         wides += o.wides;
     }
     // Sums over this and the lower lanes.
@@ -170,7 +171,8 @@ struct Sums {
 #pragma unroll
         for (int by = 1; by < 32; by <<= 1) {
             const Sums o = {__shfl_up_sync(0xffffffffu, s.tiles, by), __shfl_up_sync(0xffffffffu, s.rows, by),
-                            __shfl_up_sync(0xffffffffu, s.pieces, by), __shfl_up_sync(0xffffffffu, s.wides, by)};
+                            __shfl_up_sync(0xffffffffu, s.pieces, by), __shfl_up_sync(0xffffffffu, s.shorts, by),
+                            __shfl_up_sync(0xffffffffu, s.wides, by)};
             if ((int)(threadIdx.x & 31) >= by)
                 s.add(o);
         }
@@ -179,7 +181,8 @@ struct Sums {
     __device__ __forceinline__ Sums of_lane(int lane) const
     {
         return {__shfl_sync(0xffffffffu, tiles, lane), __shfl_sync(0xffffffffu, rows, lane),
-                __shfl_sync(0xffffffffu, pieces, lane), __shfl_sync(0xffffffffu, wides, lane)};
+                __shfl_sync(0xffffffffu, pieces, lane), __shfl_sync(0xffffffffu, shorts, lane),
+                __shfl_sync(0xffffffffu, wides, lane)};
     }
 };
 
@@ -347,7 +350,9 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
             } else {
                 np = n > 0 ? over(n, size) : e >= NG;
                 direct = first == 0 && np == 1 && e >= NG;
-                m.pieces = nb * np;
+                const bool shorter = n - (np - 1) * size < size / 2;   // the last piece: the others are whole
+                m.pieces = nb * (np - shorter);
+                m.shorts = nb * shorter;
                 m.rows = direct ? 0 : np * R * z.Hk;
             }
         }
@@ -368,6 +373,7 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
         at.tiles += upto.tiles - m.tiles;
         at.rows += upto.rows - m.rows;
         at.pieces += upto.pieces - m.pieces;
+        at.shorts += upto.shorts - m.shorts;
         at.wides += upto.wides - m.wides;
         // A lane writes what its entry has few of, the warp together where there are many: the pieces of the narrow
         // list, and the CTAs whose first tile lies in the entry.
@@ -383,33 +389,35 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
                 w1 = over(at.tiles + m.tiles, per_cta);
             }
         }
-        const auto write = [&](const Work &x, int pieces, int u, int i, int rb) {   // x: k1 positions, row0 blocks of rows
-            p.list[u] = {x.b, x.k0 + i * size, x.k0 + (i + 1 < pieces ? (i + 1) * size : x.k1), x.len, x.tok0, x.R, rb << mr_log,
-                         x.part < 0 ? -1 : x.part + i * z.Hk * x.R};
+        // piece i of `pieces` (x: k1 positions, row0 blocks of rows), u0 long and s0 short ones before the entry's
+        const auto write = [&](const Work &x, int pieces, int i, int u0, int s0) {
+            const int n = min(x.k1 - i * size, size), last = i + 1 == pieces && n < size / 2;
+            for (int rb = 0; rb < x.row0; ++rb)
+                p.list[last ? z.most - 1 - (s0 + rb) : u0 + i * x.row0 + rb] =
+                    {x.b, x.k0 + i * size, x.k0 + i * size + n, x.len, x.tok0, x.R, rb << mr_log,
+                     x.part < 0 ? -1 : x.part + i * z.Hk * x.R};
         };
         if (np <= kFew)
-            for (int i = 0, u = at.pieces; i < np; ++i)
-                for (int rb = 0; rb < nb; ++rb, ++u)
-                    write(piece, np, u, i, rb);
+            for (int i = 0; i < np; ++i)
+                write(piece, np, i, at.pieces, at.shorts);
         if (w1 - w0 <= kFew)
             for (int w = w0; w < w1; ++w)
                 p.first_entry[w] = at.wides;
         for (uint32_t left = __ballot_sync(0xffffffffu, np > kFew || w1 - w0 > kFew); left != 0; left &= left - 1) {
             const int l = __ffs(left) - 1;
             const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
-            const int pieces = of(np), to = of(w1), from = of(w0), which = of(at.wides), u0 = of(at.pieces);
+            const int pieces = of(np), to = of(w1), from = of(w0), which = of(at.wides), u0 = of(at.pieces), s0 = of(at.shorts);
             const Work x = {of(piece.b), of(piece.k0), of(piece.k1), of(piece.len), of(piece.tok0), of(piece.R), of(piece.row0),
                             of(piece.part)};
             if (pieces > kFew)
                 for (int i = lane; i < pieces; i += 32)
-                    for (int rb = 0; rb < x.row0; ++rb)
-                        write(x, pieces, u0 + i * x.row0 + rb, i, rb);
+                    write(x, pieces, i, u0, s0);
             for (int w = from + lane; w < to; w += 32)
                 p.first_entry[w] = which;
         }
     }
     if (tid == 0)
-        *p.head = {tiles, per_cta, done.pieces};
+        *p.head = {tiles, per_cta, {done.pieces, z.most - done.shorts}};
 }
 
 // ---------------------------------------------------------------- wide
@@ -507,7 +515,6 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bdla_cache &c = a.c;
     const int T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
-    next_may_start();
     if ((smem_u32(smem_raw) & 1023u) != 0u) {
         if (tid == 0)
             set_status(a.st, BDLA_ERR_DEVICE, 0xA11u);
@@ -541,6 +548,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     __syncthreads();
     tc_fence_after();
     wait_for_previous();   // the plan is there
+    next_may_start();      // and only then: the narrow kernel does not wait for it itself
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
     Walk &walk = sm.walk[warp];
@@ -1099,7 +1107,8 @@ cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.pieces = {1, 1, 1};
     a.st = st;
     a.list = p.list;
-    a.n_list = &p.head->n_list;
+    a.n_list = &p.head->list;
+    a.list_ready = z.wide;
     KernelMark mark_(BDLA_KERNEL_ATTN_SHARED, stream);
     const int entries = n_groups + d.B;
     plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? plan_ints(n_groups, d.B) * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
