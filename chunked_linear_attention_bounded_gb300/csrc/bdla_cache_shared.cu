@@ -108,7 +108,7 @@ Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
     s.narrow_tiles = (s.wide ? R : all) <= 16 ? 1 : 2;
     s.slots = s.ctas * (d.d == 128 ? 3 : 4);
     s.heads_per_slot = (float)d.Hk / (float)s.slots;
-    s.extra = 4 * ((s.slots + d.Hk - 1) / d.Hk);
+    s.extra = 2 * ((s.slots + d.Hk - 1) / d.Hk);
     const int groups = n_groups < d.B / 2 ? n_groups : d.B / 2;
     s.most = s.own_wide ? 0 : d.B + 2 * groups + s.extra;
     s.rows = 0;
