@@ -35,25 +35,29 @@ using namespace cache;
 
 constexpr int kNarrowRows = 32;   // rows a key head up to which warp MMAs take a group
 constexpr int kWideTile = 256;    // rows of a CTA of the wide kernel
-constexpr int kRunTiles = 3;      // what a change of rows costs the wide kernel, in tiles
+constexpr int kRun = 5;           // what a change of rows costs the wide kernel, in tiles of 128 rows
 constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
 
 // What the wide kernel walks: positions first .. end - 1 of sequence b's table
-// for the R rows from token tok0 on, as blocks of 256 rows times key heads, each
-// kRunTiles and then nt tiles of 128 positions on the line that the CTAs cut
-// evenly.  `base`: the line before it.
+// for the row blocks rb0 .. rb1 - 1 of the R rows from token tok0 on, times key
+// heads.  A block of 256 rows is two row tiles of 128, the last one may be one;
+// the blocks of an entry have `row_tiles` each.  On the line that the CTAs cut
+// evenly a block and head is kRun and then nt tiles of 128 positions, which count
+// row_tiles each; `base`: the line before the entry.
 struct alignas(16) WideEntry {
-    int base, b, tok0, R, first, end, len, nt, part;
+    int base, b, tok0, R, first, end, len, nt, part, rb0, rb1, row_tiles;
 };
 
-// Where an entry's partial sums are.  wide: pieces follow from the tiles' cut;
-// narrow: np pieces; np < 0: its rows are finished.
+// Where an entry's partial sums are.  wide (nt > 0): pieces follow from the cut of
+// the line, whose blocks of two row tiles start at `base` and the last one of one
+// row tile, block `full`, at `base1`; narrow: np pieces; np < 0: its rows are
+// finished.
 struct alignas(16) Parts {
-    int base, nt, R, part, np, tok0;
+    int base, nt, R, part, np, tok0, base1, full;
 };
 
 struct Head {
-    int tiles;       // of the wide kernel, its runs' costs among them
+    int line;        // of the wide kernel
     int per_cta;     // of a CTA
     int2 list;       // pieces of the narrow kernel: the long ones from the front, the others from `y` on to the end
 };
@@ -89,9 +93,9 @@ constexpr size_t plan_ints(int n_groups, int B) { return 3 * (size_t)n_groups + 
 // Bounds of the plan.  Narrow: a piece size of at least the (block-weighted)
 // positions over `extra` cuts at most `extra` pieces beyond the first of each
 // block; sequences have one block, groups of at most 32 rows one or two, and a
-// group that shares has two sequences or more.  Wide: nt tiles in a row lie in
-// nt / per_cta + 2 CTAs at most; nt R <= 256 tiles of the blocks, and all tiles
-// are at most ctas x per_cta.
+// group that shares has two sequences or more.  Wide: a block's tiles lie in
+// row_tiles nt / per_cta + 2 CTAs at most; 256 rows for each of that for all of an
+// entry's rows is at most 256 times its line, and the line at most ctas x per_cta.
 Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
 {
     Sizes s;
@@ -130,7 +134,7 @@ size_t carve(const Sizes &s, char *at, Plan *p)
         off += aligned(n * sizeof(*ptr));
     };
     take(p->head, 1);
-    take(p->wide, entries);
+    take(p->wide, 2 * entries);
     take(p->parts, entries);
     take(p->list, (size_t)s.most);
     take(p->first_entry, (size_t)s.ctas);
@@ -145,14 +149,14 @@ size_t carve(const Sizes &s, char *at, Plan *p)
 constexpr int kPlanThreads = 512;
 constexpr int kPlanEntries = 4000;   // whose offsets, groups and lengths fit into 48 KB of shared memory
 constexpr int kLeastShared = 64;     // shared positions that are worth a piece of their own
-constexpr int kLeastTiles = 2 + kRunTiles;   // of a wide CTA
+constexpr int kLeastLine = 2 + kRun;   // of a wide CTA
 constexpr int kFew = 4;               // pieces, or CTAs, of an entry that one lane writes
 constexpr int kSizes = 8;            // piece sizes of the narrow kernel that are weighed: 128, 256 .. 16384 positions
 
 __device__ __forceinline__ int tiles_of(int n) { return (int)(((uint32_t)n + BT - 1) / BT); }
 __device__ __forceinline__ int over(int n, int size) { return (int)(((uint32_t)n + (uint32_t)size - 1) / (uint32_t)size); }
 
-// What comes before an entry: tiles of the wide kernel, rows of partial sums,
+// What comes before an entry: line of the wide kernel, rows of partial sums,
 // long and short pieces of the narrow list, entries of the wide one.
 struct Sums {
     int tiles, rows, pieces, shorts, wides;
@@ -261,16 +265,20 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
     const int rows_of = z.T * z.G, mr_log = z.narrow_tiles == 1 ? 4 : 5;
     const auto rows = [&](int e, int n) { return e >= NG ? rows_of : n > 0 ? (cu[e + 1] - cu[e]) * rows_of : 0; };
     const auto wide = [&](int e, int R) { return e >= NG ? z.own_wide : R > kNarrowRows; };
-    const auto blocks = [&](int R, bool w) { return w ? (R + kWideTile - 1) / kWideTile : (R + (1 << mr_log) - 1) >> mr_log; };
+    // blocks of two row tiles and of one, and their line
+    const auto full = [](int R) { return (R + BT - 1) / kWideTile; };
+    const auto single = [](int R) { return (R + BT - 1) / BT & 1; };
+    const auto line_of = [&](int R, int nt) { return nt > 0 ? z.Hk * (full(R) * (2 * nt + kRun) + single(R) * (nt + kRun)) : 0; };
+    const auto blocks = [&](int R) { return (R + (1 << mr_log) - 1) >> mr_log; };
     int tiles = 0;
     int64_t positions = 0;
     for (int e = tid; e < E; e += kPlanThreads) {
         const int n = e < NG ? taken(e) : len[e] - taken(group[e - NG]), R = rows(e, n);
         len[e] = n;
         if (wide(e, R))
-            tiles += n > 0 ? blocks(R, true) * z.Hk * (tiles_of(n) + kRunTiles) : 0;
+            tiles += line_of(R, tiles_of(n));
         else
-            positions += (int64_t)blocks(R, false) * n;
+            positions += (int64_t)blocks(R) * n;
     }
     if (warp * 32 < E) {
         tiles = __reduce_add_sync(0xffffffffu, tiles);
@@ -285,7 +293,7 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
     __syncthreads();
     tiles = s_tiles;
     positions = s_positions;
-    const int per_cta = max(kLeastTiles, over(tiles, z.ctas));
+    const int per_cta = max(kLeastLine, over(tiles, z.ctas));
 
     // The narrow pieces' size: their work (a piece costs its start-up, about 128
     // positions) spread over the CTAs that the GPU holds, plus the last piece's
@@ -297,7 +305,7 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
         for (int e0 = warp * 32; e0 < E; e0 += kPlanThreads) {
             const int e = e0 + lane, n = e < E ? len[e] : 0, R = e < E ? rows(e, n) : 0;
             const bool mine = e < E && !wide(e, R);
-            const int x = mine ? blocks(R, false) : 0, some = mine && e >= NG ? 1 : 0;
+            const int x = mine ? blocks(R) : 0, some = mine && e >= NG ? 1 : 0;
             const int longest = __reduce_max_sync(0xffffffffu, mine ? n : 0);
             int sum = 0;
 #pragma unroll
@@ -340,13 +348,13 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
             n = len[e];
             R = rows(e, n);
             const bool w = wide(e, R);
-            nb = blocks(R, w);
+            nb = w ? 0 : blocks(R);
             first = e < NG ? 0 : taken(group[e - NG]);
             if (w) {
                 nt = tiles_of(n);
-                m.tiles = nt > 0 ? nb * z.Hk * (nt + kRunTiles) : 0;
-                m.rows = nt > 0 ? (over(nt, per_cta) + 1) * R * z.Hk : 0;
-                m.wides = nt > 0;
+                m.tiles = line_of(R, nt);
+                m.rows = nt > 0 ? (over(full(R) > 0 ? 2 * nt : nt, per_cta) + 1) * R * z.Hk : 0;
+                m.wides = nt > 0 ? (full(R) > 0) + single(R) : 0;
             } else {
                 np = n > 0 ? over(n, size) : e >= NG;
                 direct = first == 0 && np == 1 && e >= NG;
@@ -377,18 +385,29 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
         at.wides += upto.wides - m.wides;
         // A lane writes what its entry has few of, the warp together where there are many: the pieces of the narrow
         // list, and the CTAs whose first tile lies in the entry.
-        int w0 = 0, w1 = 0;
+        int w0 = 0, w1 = 0, w2 = 0;   // CTAs from w0 on begin in the entry's blocks of two row tiles, from w1 on in the last
         Work piece = {};
         if (e < E) {
-            const int b = e >= NG ? e - NG : n > 0 ? cu[e] : 0;
+            const int b = e >= NG ? e - NG : n > 0 ? cu[e] : 0, base1 = at.tiles + z.Hk * full(R) * (2 * nt + kRun);
             piece = {b, first, n, e < NG ? kSeen : max(c.lens[b], 0), b * z.T, R, nb, direct ? -1 : at.rows};
-            p.parts[e] = {at.tiles, nt, R, at.rows, direct ? -1 : np, piece.tok0};
+            p.parts[e] = {at.tiles, nt, R, at.rows, direct ? -1 : np, piece.tok0, base1, full(R)};
             if (nt > 0) {
-                p.wide[at.wides] = {at.tiles, b, piece.tok0, R, first, first + n, piece.len, nt, at.rows};
+                WideEntry x = {at.tiles, b, piece.tok0, R, first, first + n, piece.len, nt, at.rows, 0, full(R), 2};
+                WideEntry *to = p.wide + at.wides;
+                if (full(R) > 0)
+                    *to++ = x;
+                x.base = base1;
+                x.rb0 = full(R);
+                x.rb1 = x.rb0 + 1;
+                x.row_tiles = 1;
+                if (single(R))
+                    *to = x;
                 w0 = over(at.tiles, per_cta);
-                w1 = over(at.tiles + m.tiles, per_cta);
+                w1 = over(base1, per_cta);
+                w2 = over(at.tiles + m.tiles, per_cta);
             }
         }
+        const int second = at.wides + (full(R) > 0);   // the entry of one row tile
         // piece i of `pieces` (x: k1 positions, row0 blocks of rows), u0 long and s0 short ones before the entry's
         const auto write = [&](const Work &x, int pieces, int i, int u0, int s0) {
             const int n = min(x.k1 - i * size, size), last = i + 1 == pieces && n < size / 2;
@@ -400,20 +419,20 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
         if (np <= kFew)
             for (int i = 0; i < np; ++i)
                 write(piece, np, i, at.pieces, at.shorts);
-        if (w1 - w0 <= kFew)
-            for (int w = w0; w < w1; ++w)
-                p.first_entry[w] = at.wides;
-        for (uint32_t left = __ballot_sync(0xffffffffu, np > kFew || w1 - w0 > kFew); left != 0; left &= left - 1) {
+        if (w2 - w0 <= kFew)
+            for (int w = w0; w < w2; ++w)
+                p.first_entry[w] = w < w1 ? at.wides : second;
+        for (uint32_t left = __ballot_sync(0xffffffffu, np > kFew || w2 - w0 > kFew); left != 0; left &= left - 1) {
             const int l = __ffs(left) - 1;
             const auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
-            const int pieces = of(np), to = of(w1), from = of(w0), which = of(at.wides), u0 = of(at.pieces), s0 = of(at.shorts);
+            const int pieces = of(np), to = of(w2), turn = of(w1), from = of(w0), which = of(at.wides), then = of(second), u0 = of(at.pieces), s0 = of(at.shorts);
             const Work x = {of(piece.b), of(piece.k0), of(piece.k1), of(piece.len), of(piece.tok0), of(piece.R), of(piece.row0),
                             of(piece.part)};
             if (pieces > kFew)
                 for (int i = lane; i < pieces; i += 32)
                     write(x, pieces, i, u0, s0);
             for (int w = from + lane; w < to; w += 32)
-                p.first_entry[w] = which;
+                p.first_entry[w] = w < turn ? which : then;
         }
     }
     if (tid == 0)
@@ -430,49 +449,59 @@ constexpr int kThreads = 32 + 32 * kFetchWarps + 256;
 struct Walk {
     WideEntry en;
     const WideEntry *at;
-    int rb, kh, t0, n, piece, left;
+    int rb, kh, t0, n, piece, from, end;   // from: of the run's tile 0 on the line; end: of the CTA's part of it
+    __device__ __forceinline__ void settle()
+    {
+        const int x = from + t0 * en.row_tiles;
+        n = x < end ? min(en.nt - t0, (end - x + en.row_tiles - 1) / en.row_tiles) : 0;
+    }
+    __device__ __forceinline__ void step(int Hk)
+    {
+        from += en.nt * en.row_tiles + kRun;
+        t0 = piece = n = 0;
+        if (from >= end)
+            return;
+        if (++kh == Hk) {
+            kh = 0;
+            if (++rb == en.rb1) {
+                en = *++at;
+                rb = en.rb0;
+            }
+        }
+        settle();
+    }
     // One lane.  n = 0: there is no tile.
     __device__ __forceinline__ void begin(const Plan &p, int Hk, int cta)
     {
         const Head h = *p.head;
-        const int x = cta * h.per_cta;
-        left = x < h.tiles ? min(h.tiles - x, h.per_cta) : 0;
+        const int which = p.first_entry[cta], x = cta * h.per_cta;   // (which: if there is a line to walk)
+        end = min(h.line, x + h.per_cta);
         n = 0;
-        if (left == 0)
+        if (x >= h.line)
             return;
-        at = p.wide + p.first_entry[cta];
+        at = p.wide + which;
         en = *at;
-        const int whole = en.nt + kRunTiles, unit = (x - en.base) / whole, from = en.base + unit * whole + kRunTiles;
-        t0 = max(x - from, 0);
-        left -= from + t0 - x;   // (a run may be paid for by the CTA before)
+        const int whole = en.nt * en.row_tiles + kRun, unit = (x - en.base) / whole;
+        from = en.base + unit * whole + kRun;
+        t0 = x > from ? (x - from + en.row_tiles - 1) / en.row_tiles : 0;   // the first tile that starts at x or behind
         rb = unit / Hk;
         kh = unit - rb * Hk;
+        rb += en.rb0;
         piece = cta - from / h.per_cta;
-        n = max(min(en.nt - t0, left), 0);
+        settle();
+        if (n == 0)   // the last tile began before x
+            step(Hk);
     }
     // The next run, by the whole warp; false: there is none.
     __device__ __forceinline__ bool next(int Hk)
     {
         __syncwarp();   // all have looked at the run before
-        if ((threadIdx.x & 31) == 0) {
-            left -= n + kRunTiles;
-            n = 0;
-            if (left > 0) {
-                t0 = piece = 0;
-                if (++kh == Hk) {
-                    kh = 0;
-                    if (++rb * kWideTile >= en.R) {
-                        rb = 0;
-                        en = *++at;
-                    }
-                }
-                n = min(en.nt, left);
-            }
-        }
+        if ((threadIdx.x & 31) == 0)
+            step(Hk);
         __syncwarp();
         return n > 0;
     }
-    __device__ __forceinline__ int row_tiles() const { return en.R - rb * kWideTile > BT ? 2 : 1; }
+    __device__ __forceinline__ int row_tiles() const { return en.row_tiles; }
 };
 
 template <int D> struct WideSmem {
@@ -778,16 +807,19 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                     break;
                 continue;
             }
-            const int rr = walk.rb * kWideTile + (turns ? 0 : w * BT) + r, R = walk.en.R;
-            const bool live_row = rr < R;
-            const int i = live_row ? rr / G : 0;
+            int i;   // the row's token
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + (((int64_t)walk.en.tok0 + i) * Hq + walk.kh * G + (live_row ? rr - i * G : 0)) * D);
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch)
-                    *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(r, ch & 7)) =
-                        live_row ? src[ch] : make_uint4(0, 0, 0, 0);
+                // the warp's 32 rows, whole rows at a time
+                const int rr = walk.rb * kWideTile + (turns ? 0 : w * BT) + r, R = walk.en.R;
+                i = rr < R ? rr / G : 0;
+                const int mine = rr < R ? (walk.en.tok0 + i) * Hq + walk.kh * G + rr - i * G : -1;
+                const int ch = lane % kChunks;
+#pragma unroll 8
+                for (int x = 0; x < kChunks; ++x) {
+                    const int y = x * (32 / kChunks) + lane / kChunks, row = __shfl_sync(0xffffffffu, mine, y);
+                    *reinterpret_cast<uint4 *>(sm.q[w] + (ch >> 3) * kPanel + sw128_offset(32 * q4 + y, ch & 7)) =
+                        row >= 0 ? reinterpret_cast<const uint4 *>(a.q + (int64_t)row * D)[ch] : make_uint4(0, 0, 0, 0);
+                }
                 fence_proxy_async_smem();
                 tc_fence_before();   // the sums of the run before have been read
                 mbar_arrive(&sm.q_full[w]);
@@ -859,6 +891,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 row.m = m;
                 row.l = fmaf(row.l, f0, o.y * f1);
             }
+            const int R = walk.en.R, rr = walk.rb * kWideTile + (turns ? 0 : w * BT) + r;
             const int64_t pt = (int64_t)walk.en.part + ((int64_t)walk.piece * Hk + walk.kh) * R + rr;
             // 32 rows of 128 bytes at a time through the warp's own rows of its query tile (read by now), so that whole
             // lines leave
@@ -894,7 +927,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 tc_fence_before();   // the other group's output has been read
                 mbar_arrive(&sm.merged);
             }
-            if (live_row)
+            if (rr < R)
                 *reinterpret_cast<float2 *>(a.part_ml + 2 * pt) = make_float2(row.m, row.l);
             if (!walk.next(Hk))
                 break;
@@ -940,8 +973,9 @@ shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan 
         step = (int64_t)Hk * x.R;
         if (x.nt == 0)
             return x.np;
-        const int begin = x.base + ((rr / kWideTile) * Hk + kh) * (x.nt + kRunTiles) + kRunTiles;
-        return (begin + x.nt - 1) / head.per_cta - begin / head.per_cta + 1;
+        const int rb = rr / kWideTile, row_tiles = rb < x.full ? 2 : 1;
+        const int begin = kRun + (rb < x.full ? x.base + (rb * Hk + kh) * (2 * x.nt + kRun) : x.base1 + kh * (x.nt + kRun));
+        return (begin + (x.nt - 1) * row_tiles) / head.per_cta - begin / head.per_cta + 1;
     };
     int64_t f0 = 0, s0 = 0, f1 = 0, s1 = 0;
     const int n1 = pieces(n_groups + b, f1, s1);
@@ -1073,13 +1107,13 @@ size_t shared_bytes(const bdla_attn_dims &d, int n_groups)
     return carve(sizes_of(d, n_groups), nullptr, &p);
 }
 
-// Tiles (with a CTA's worth beyond them) and rows of the partial sums are 32-bit.
+// The line (with a CTA's worth beyond it) and rows of the partial sums are 32-bit.
 bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
 {
     const Sizes z = sizes_of(d, n_groups);
     const int64_t R = (int64_t)d.T * z.G, groups = z.wide ? R * d.B / kWideTile + (n_groups < d.B / 2 ? n_groups : d.B / 2) : 0;
     const int64_t blocks = (groups + (z.own_wide ? (R + kWideTile - 1) / kWideTile * d.B : 0)) * d.Hk;
-    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (max_keys / BT + 1 + kRunTiles) <= INT32_MAX / 2;
+    return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (2 * (max_keys / BT + 1) + kRun) <= INT32_MAX / 2;
 }
 
 cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, const int32_t *cu_groups, const int32_t *shared,

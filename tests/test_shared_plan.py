@@ -6,8 +6,8 @@ import random
 import pytest
 
 SMS, TILE, WIDE, NARROW = 152, 128, 256, 32
-RUN = 3   # what a change of rows costs, in tiles
-LEAST_SHARED, LEAST_TILES, N_SIZES = 64, 2 + RUN, 8
+RUN = 5   # what a change of rows costs, in tiles of 128 rows
+LEAST_SHARED, LEAST_LINE, N_SIZES = 64, 2 + RUN, 8
 
 
 def up(a, b):
@@ -54,12 +54,14 @@ def plan(z, cu, shared, lens, cap):
         if e < NG:
             tok0, R = (cu[e] * z.T, (cu[e + 1] - cu[e]) * z.T * z.G) if n[e] > 0 else (0, 0)
             wide = R > NARROW
-        return R, tok0, wide, up(R, WIDE if wide else z.mr)
+        return R, tok0, wide, up(R, z.mr)
 
     entries = [entry(e) for e in range(E)]
-    tiles = sum(x[3] * z.Hk * (up(n[e], TILE) + RUN) for e, x in enumerate(entries) if x[2] and n[e])
+    full, single = lambda R: up(R, TILE) // 2, lambda R: up(R, TILE) % 2   # blocks of two row tiles, and of one
+    line_of = lambda R, nt: z.Hk * (full(R) * (2 * nt + RUN) + single(R) * (nt + RUN)) if nt else 0
+    tiles = sum(line_of(x[0], up(n[e], TILE)) for e, x in enumerate(entries) if x[2])
     positions = sum(x[3] * n[e] for e, x in enumerate(entries) if not x[2])
-    per_cta = max(LEAST_TILES, up(tiles, SMS))
+    per_cta = max(LEAST_LINE, up(tiles, SMS))
     size = min(up(up(positions, z.extra), 64) * 64, 2 ** 31 - 128) if z.most > 0 else 64
     if z.most > 0 and size <= 128 << (N_SIZES - 1):
         best = None
@@ -76,21 +78,23 @@ def plan(z, cu, shared, lens, cap):
         first = 0 if e < NG or g < 0 else n[g]
         b = e - NG if e >= NG else (cu[e] if n[e] > 0 else 0)
         np, direct, nt = 0, False, up(n[e], TILE) if wide else 0
-        w = blocks * z.Hk * (nt + RUN) if nt else 0
-        need = (up(nt, per_cta) + 1) * R * z.Hk if nt else 0
+        w = line_of(R, nt)
+        need = (up(2 * nt if full(R) else nt, per_cta) + 1) * R * z.Hk if nt else 0
         if not wide:
             np = up(n[e], size)
             if e >= NG:
                 np = max(np, 1)
                 direct = np == 1 and (g < 0 or n[g] == 0)
             need = 0 if direct else np * R * z.Hk
-        parts.append((base, nt, R, rows, -1 if direct else np, tok0))
+        base1 = base + z.Hk * full(R) * (2 * nt + RUN)
+        parts.append((base, nt, R, rows, -1 if direct else np, tok0, base1, full(R)))
         if nt:
-            c = up(base, per_cta)
-            while c * per_cta < base + w:
-                first_entry[c] = len(wides)
-                c += 1
-            wides.append((base, b, tok0, R, first, first + n[e], nt, rows))
+            for start, end, rb0, rb1, rt in ((base, base1, 0, full(R), 2), (base1, base + w, full(R), full(R) + 1, 1)):
+                if start == end:
+                    continue
+                for c in range(up(start, per_cta), up(end, per_cta)):
+                    first_entry[c] = len(wides)
+                wides.append((start, b, tok0, R, first, first + n[e], nt, rows, rb0, rb1, rt))
         for i in range(np):
             for rb in range(blocks):
                 work.append((b, first + min(n[e], i * size), first + min(n[e], (i + 1) * size), tok0, R, rb * z.mr,
@@ -103,26 +107,30 @@ def plan(z, cu, shared, lens, cap):
 def walk(z, wides, tiles, per_cta, first_entry, cta):
     """(entry, block of rows, key head, first tile, tiles, piece) of each run of a CTA of the wide kernel."""
     x = cta * per_cta
-    left = min(tiles - x, per_cta) if x < tiles else 0
-    if not left:
+    end = min(tiles, x + per_cta)
+    if x >= tiles:
         return
     e = first_entry[cta]
-    base, nt = wides[e][0], wides[e][6]
-    unit = (x - base) // (nt + RUN)
-    begin = base + unit * (nt + RUN) + RUN
-    t0, rb, kh, piece = max(x - begin, 0), unit // z.Hk, unit % z.Hk, cta - begin // per_cta
-    left -= begin + t0 - x
-    n = min(nt - t0, left)
-    while n > 0:
-        yield e, rb, kh, t0, n, piece
-        left -= n + RUN
+    base, nt, rt = wides[e][0], wides[e][6], wides[e][10]
+    unit = (x - base) // (nt * rt + RUN)
+    start = base + unit * (nt * rt + RUN) + RUN
+    t0, rb, kh, piece = max(up(x - start, rt), 0), unit // z.Hk + wides[e][8], unit % z.Hk, cta - start // per_cta
+    while True:
+        nt, rt = wides[e][6], wides[e][10]
+        at = start + t0 * rt
+        n = min(nt - t0, up(end - at, rt)) if at < end else 0
+        if n > 0:
+            yield e, rb, kh, t0, n, piece
+        start += nt * rt + RUN
         t0 = piece = 0
+        if start >= end:
+            return
         kh += 1
         if kh == z.Hk:
             kh, rb = 0, rb + 1
-            if rb * WIDE >= wides[e][3]:
-                rb, e = 0, e + 1
-        n = min(wides[e][6], left) if left > 0 else 0
+            if rb == wides[e][9]:
+                e += 1
+                rb = wides[e][8]
 
 
 def check(B, T, G, Hk, d, cu, shared, lens, cap):
@@ -146,17 +154,19 @@ def check(B, T, G, Hk, d, cu, shared, lens, cap):
                 put(None if part < 0 else part + kh * R + r, tok0 + r // G, kh * G + r % G, a, e)
     for cta in range(SMS):
         for i, rb, kh, t0, n, piece in walk(z, wides, tiles, per_cta, first_entry, cta):
-            base, b, tok0, R, first, end, nt, part = wides[i]
+            base, b, tok0, R, first, end, nt, part, rb0, rb1, rt = wides[i]
+            assert rb0 <= rb < rb1 and up(min(R, rb * WIDE + WIDE) - rb * WIDE, TILE) == rt
             for r in range(rb * WIDE, min(R, rb * WIDE + WIDE)):
                 put(part + (piece * Hk + kh) * R + r, tok0 + r // G, kh * G + r % G, first + t0 * TILE,
                     min(end, first + (t0 + n) * TILE))
 
     def pieces(e, b, i, h):
-        base, nt, R, part, np, tok0 = parts[e]
+        base, nt, R, part, np, tok0, base1, full = parts[e]
         rr, kh = (b * T + i - tok0) * G + h % G, h // G
         if nt:
-            begin = base + (rr // WIDE * Hk + kh) * (nt + RUN) + RUN
-            np = (begin + nt - 1) // per_cta - begin // per_cta + 1
+            rb, rt = rr // WIDE, 2 if rr // WIDE < full else 1
+            begin = RUN + (base + (rb * Hk + kh) * (2 * nt + RUN) if rb < full else base1 + kh * (nt + RUN))
+            np = (begin + (nt - 1) * rt) // per_cta - begin // per_cta + 1
         return [part + kh * R + rr + s * Hk * R for s in range(max(np, 0))] if np >= 0 else None
 
     used = set()
