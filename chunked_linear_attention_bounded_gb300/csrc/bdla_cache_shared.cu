@@ -532,7 +532,8 @@ static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxS
 // row tile to turn to: both softmax groups then take the same rows and every
 // second tile of positions, and the first reads the output of both out of tensor
 // memory at the run's end.  `run` as there.
-template <int D>
+// DRAFTS: there are entries with new tokens among their positions (the sequences' own).
+template <int D, bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, int run,
                    const __grid_constant__ Call a, const __grid_constant__ Plan plan, uint64_t wait_ns, int stall)
@@ -705,13 +706,13 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
             lookup(ahead, pg);
         for (int j = fw; ok && more; j += kFetchWarps) {
             now = ahead;
-            const uint64_t seen = now.t + BT > now.len ? sees_any(a.tree, now.b, T, lane) : 0;
+            const uint64_t seen = DRAFTS && now.t + BT > now.len ? sees_any(a.tree, now.b, T, lane) : 0;
             int row[4];
             uint32_t bits = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int t = now.t + 4 * lane + u;
-                bool live = t < now.end && (t < now.len || ((seen >> (t - now.len)) & 1));
+                bool live = t < now.end && (!DRAFTS || t < now.len || ((seen >> (t - now.len)) & 1));
                 if (live && (pg[u] < 0 || pg[u] >= c.n_pages)) {
                     set_status(a.st, BDLA_ERR_DEVICE, (unsigned)now.b);
                     live = false;
@@ -824,8 +825,8 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                 tc_fence_before();   // the sums of the run before have been read
                 mbar_arrive(&sm.q_full[w]);
             }
-            const int len = walk.en.len, step = turns ? 2 : 1, x0 = turns ? w : 0;
-            const uint64_t see = walk.en.end > len ? sees(a.tree, walk.en.b, T, i) : 0;
+            const int len = DRAFTS ? walk.en.len : kSeen, step = turns ? 2 : 1, x0 = turns ? w : 0;
+            const uint64_t see = DRAFTS && walk.en.end > len ? sees(a.tree, walk.en.b, T, i) : 0;
             RowSoftmax row;
             int t0 = walk.en.first + (walk.t0 + x0) * BT;
             for (int x = x0; x < n; x += step, t0 += step * BT) {
@@ -845,7 +846,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     all &= sm.valid[j % SL][k];
-                if (all != 0xffffffffu || t0 + BT > len) {
+                if (all != 0xffffffffu || (DRAFTS && t0 + BT > len)) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // what this row sees of the 32 positions: the context, and its bits of the new tokens
@@ -853,7 +854,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
                         uint32_t mask = p0 <= -32 ? 0xffffffffu
                                                   : p0 < 0 ? ((1u << -p0) - 1) | (uint32_t)(see << -p0)
                                                            : p0 < 64 ? (uint32_t)(see >> p0) : 0u;
-                        mask &= sm.valid[j % SL][k];
+                        mask = (DRAFTS ? mask : 0xffffffffu) & sm.valid[j % SL][k];
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             s[k][e] = (mask >> e) & 1 ? s[k][e] : 0xff800000u;
@@ -1073,10 +1074,10 @@ shared_join_kernel(const __grid_constant__ Call a, const __grid_constant__ Plan 
         a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
 }
 
-template <int D> cudaError_t wide_go(const Call &a, const Plan &p, const Sizes &z, cudaStream_t stream)
+template <int D, bool DRAFTS> cudaError_t wide_go(const Call &a, const Plan &p, const Sizes &z, cudaStream_t stream)
 {
     const size_t smem = sizeof(WideSmem<D>);
-    const cudaError_t err = cudaFuncSetAttribute(shared_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = cudaFuncSetAttribute(shared_wide_kernel<D, DRAFTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
     CUtensorMap tk{}, tv{};
@@ -1087,7 +1088,7 @@ template <int D> cudaError_t wide_go(const Call &a, const Plan &p, const Sizes &
         run = 0;
     else if (!make_rows_map(&tk, a.c.k, width, rows, run) || !make_rows_map(&tv, a.c.v, width, rows, run))
         return cudaErrorInvalidValue;
-    return launch_second(shared_wide_kernel<D>, (unsigned)z.ctas, kThreads, smem, stream, tk, tv, run, a, p, g_wait_ns.load(),
+    return launch_second(shared_wide_kernel<D, DRAFTS>, (unsigned)z.ctas, kThreads, smem, stream, tk, tv, run, a, p, g_wait_ns.load(),
                          g_test_stall[BDLA_KERNEL_ATTN_SHARED].load());
 }
 
@@ -1148,7 +1149,8 @@ cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, cons
     plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? plan_ints(n_groups, d.B) * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
     cudaError_t err = cudaGetLastError();
     if (err == cudaSuccess && z.wide)
-        err = d.d == 64 ? wide_go<64>(a, p, z, stream) : wide_go<128>(a, p, z, stream);
+        err = d.d == 64 ? (z.own_wide ? wide_go<64, true>(a, p, z, stream) : wide_go<64, false>(a, p, z, stream))
+                        : (z.own_wide ? wide_go<128, true>(a, p, z, stream) : wide_go<128, false>(a, p, z, stream));
     if (err == cudaSuccess && z.most > 0)
         err = launch_cached_list(a, d.d, z.narrow_tiles, z.most, stream);
     if (err != cudaSuccess)
