@@ -421,6 +421,210 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
         attn::wait_for_previous();   // so that the end of this kernel is the end of that one too
 }
 
+// The pieces of a list with up to 16 rows, a warp each.  The list's sequences have
+// often no more than a few hundred positions of their own, so a piece's start (its
+// entry, its pages, its first keys: a chain of three trips to memory) is as long
+// as its work, and what counts is how many are under way: a warp by itself, with
+// 16 positions a tile and three tiles in flight, instead of four warps and two
+// barriers a tile.  256 sequences of up to 513 positions of their own, 8 key heads
+// of 128: BDLA_T1 us (four warps a piece 65).
+constexpr int kListKeys = 16, kListStages = 3;
+template <int D>
+__global__ void __launch_bounds__(32)
+list_kernel(const __grid_constant__ Call a)
+{
+    constexpr int kChunks = D / 8;
+    __shared__ __align__(128) unsigned char kv[kListStages][2][kListKeys * D * 2];
+    const int lane = threadIdx.x, T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
+    const bdla_cache &c = a.c;
+    attn::next_may_start();
+    // The list is there when this kernel may start: the one before waited for it, if it is not the one that made it
+    // (past_l1: nothing of it has been read on this SM by this grid, but by the call before).
+    if (!a.list_ready)
+        attn::wait_for_previous();
+    const int idx = blockIdx.x / Hk, kh = blockIdx.x - idx * Hk;
+    const Work w = past_l1(a.list[idx]);   // (there is room for every CTA's, and the counts come along)
+    const int2 count = __ldcg(a.n_list);
+    if (idx >= count.x && idx < count.y) {
+        attn::wait_for_previous();
+        return;
+    }
+    const int R = w.R, nt = (w.k1 - w.k0 + kListKeys - 1) / kListKeys;
+    const int32_t *table = c.pages + (int64_t)w.b * c.max_pages;
+    const bool drafts = w.k1 > w.len;   // the piece holds new tokens
+    const uint64_t seen = drafts ? sees_any(a.tree, w.b, T, lane) : 0;
+
+    // the first 16 lanes have a position of a tile each
+    auto lookup = [&](int n) {
+        const int t = w.k0 + n * kListKeys + lane;
+        return lane < kListKeys && t < w.k1 ? table[a.div.entry(t)] : -1;
+    };
+    // tile n into its stage, one cp.async group; its positions that may be seen
+    auto load = [&](int n, int pg) {
+        const int t = w.k0 + n * kListKeys + lane;
+        bool live = lane < kListKeys && t < w.k1 && (t < w.len || ((seen >> (t - w.len)) & 1));
+        if (live && (pg < 0 || pg >= c.n_pages)) {
+            set_status(a.st, BDLA_ERR_DEVICE, (unsigned)w.b);
+            live = false;
+        }
+        const int row = live ? pg * c.page + a.div.offset(t) : -1;
+        const uint32_t ok = __ballot_sync(0xffffffffu, live);
+        if (n < nt) {
+            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(kv[n % kListStages][0]));
+#pragma unroll
+            for (int u = 0; u < kListKeys * kChunks / 32; ++u) {
+                const int e = lane + 32 * u, r = e / kChunks, ch = e % kChunks, at = __shfl_sync(0xffffffffu, row, r);
+                const int64_t off = ((int64_t)max(at, 0) * Hk + kh) * D + 8 * ch;
+                const uint32_t to = dst + (r * kChunks + (ch ^ (r & 7))) * 16;
+                cp16(to, static_cast<const __nv_bfloat16 *>(c.k) + off, at >= 0);
+                cp16(to + kListKeys * D * 2, static_cast<const __nv_bfloat16 *>(c.v) + off, at >= 0);
+            }
+        }
+        cp_commit();
+        return ok;
+    };
+    int pg[kListStages + 1];
+#pragma unroll
+    for (int n = 0; n <= kListStages; ++n)
+        pg[n] = lookup(n);
+    uint32_t ok[kListStages];   // of tile n, n + 1, n + 2
+#pragma unroll
+    for (int n = 0; n < kListStages; ++n)
+        ok[n] = load(n, pg[n]);
+    int ahead = pg[kListStages];   // of tile n + 3
+
+    // query fragments: rows lane/4 and lane/4 + 8
+    const int r0 = w.row0 + (lane >> 2), r1 = r0 + 8;
+    const int i0 = min(r0, R - 1) / G, i1 = min(r1, R - 1) / G;
+    const __nv_bfloat16 *qa = a.q + (((int64_t)w.tok0 + i0) * Hq + kh * G + min(r0, R - 1) % G) * D + 2 * (lane & 3);
+    const __nv_bfloat16 *qb = a.q + (((int64_t)w.tok0 + i1) * Hq + kh * G + min(r1, R - 1) % G) * D + 2 * (lane & 3);
+    uint32_t fq[D / 16][4];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        fq[ks][0] = *reinterpret_cast<const uint32_t *>(qa + 16 * ks);
+        fq[ks][1] = *reinterpret_cast<const uint32_t *>(qb + 16 * ks);
+        fq[ks][2] = *reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8);
+        fq[ks][3] = *reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8);
+    }
+    const uint64_t see0 = drafts ? sees(a.tree, w.b, T, i0) : 0, see1 = drafts ? sees(a.tree, w.b, T, i1) : 0;
+    const float cs = a.scale * 1.4426950408889634f;
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+#pragma unroll 1
+    for (int n = 0; n < nt; ++n) {
+        cp_wait<kListStages - 1>();
+        __syncwarp();
+        const uint32_t sk = static_cast<uint32_t>(__cvta_generic_to_shared(kv[n % kListStages][0]));
+        const uint32_t sv = sk + kListKeys * D * 2;
+        float s[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * ks + ((lane >> 3) & 1);
+            uint32_t f[4];
+            ldm4(f, sk + (row * kChunks + (ch ^ (row & 7))) * 16);
+            mma16816(s[0], fq[ks], f[0], f[1]);
+            mma16816(s[1], fq[ks], f[2], f[3]);
+        }
+        const int t0 = w.k0 + n * kListKeys;
+        if (ok[0] != 0xffffu || t0 + kListKeys > w.len) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = 8 * i + 2 * (lane & 3) + u, j = t0 + kk - w.len;
+                    const bool live = (ok[0] >> kk) & 1;
+                    if (!(live && (j < 0 || ((see0 >> j) & 1))))
+                        s[i][u] = -INFINITY;
+                    if (!(live && (j < 0 || ((see1 >> j) & 1))))
+                        s[i][2 + u] = -INFINITY;
+                }
+        }
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, x));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, x));
+        }
+        if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float a0 = n0 == m0 ? 1.0f : ex2((m0 - n0) * cs), a1 = n1 == m1 ? 1.0f : ex2((m1 - n1) * cs);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                acc[i][0] *= a0;
+                acc[i][1] *= a0;
+                acc[i][2] *= a1;
+                acc[i][3] *= a1;
+            }
+        }
+        // rows that have seen nothing yet: every weight is e^(-inf)
+        const float b0 = m0 == -INFINITY ? 0.0f : m0 * cs, b1 = m1 == -INFINITY ? 0.0f : m1 * cs;
+        uint32_t fp[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float p0 = ex2(fmaf(s[u][0], cs, -b0)), p1 = ex2(fmaf(s[u][1], cs, -b0));
+            const float p2 = ex2(fmaf(s[u][2], cs, -b1)), p3 = ex2(fmaf(s[u][3], cs, -b1));
+            l0 += p0 + p1;
+            l1 += p2 + p3;
+            fp[2 * u] = sm100::pack_bf16(p0, p1);
+            fp[2 * u + 1] = sm100::pack_bf16(p2, p3);
+        }
+#pragma unroll
+        for (int dn = 0; dn < D / 16; ++dn) {
+            const int row = lane & 15, ch = 2 * dn + (lane >> 4);
+            uint32_t f[4];
+            ldm4t(f, sv + (row * kChunks + (ch ^ (row & 7))) * 16);
+            mma16816(acc[2 * dn], fp, f[0], f[1]);
+            mma16816(acc[2 * dn + 1], fp, f[2], f[3]);
+        }
+        __syncwarp();   // the stage has been read
+        ok[0] = ok[1];
+        ok[1] = ok[2];
+        ok[2] = load(n + kListStages, ahead);
+        ahead = lookup(n + kListStages + 1);
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int row = half ? r1 : r0;
+        const float m = half ? m1 : m0, l = half ? l1 : l0;
+        if (row >= R)
+            continue;
+        if (w.part >= 0) {
+            const int64_t at = (int64_t)w.part + (int64_t)kh * R + row;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2 *>(a.part_o + at * D + 8 * i + 2 * (lane & 3)) =
+                    make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+            if ((lane & 3) == 0)
+                *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m, l);
+        } else {
+            const int64_t at = ((int64_t)w.tok0 + row / G) * Hq + kh * G + row % G;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint32_t *>(a.o + at * D + 8 * i + 2 * (lane & 3)) =
+                    sm100::pack_bf16(acc[i][2 * half] * inv, acc[i][2 * half + 1] * inv);
+            if ((lane & 3) == 0)
+                a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
+        }
+    }
+    if (a.list_ready)
+        attn::wait_for_previous();   // so that the end of this kernel is the end of that one too
+}
+
 // Joins the pieces of a row, W warps a row: each sums every W-th piece, and the
 // warps' sums are added in order.  W follows the most pieces of a sequence: one
 // warp for up to 16, so that a CTA joins four rows, 16 beyond.
@@ -590,24 +794,22 @@ static cudaError_t cached_go(const Call &a, const bdla_attn_dims &d, cudaStream_
     return cudaGetLastError();
 }
 
-template <int D, int WR>
-static cudaError_t list_go(const Call &a, int most, cudaStream_t stream)
+// The pieces of a list of at most `most`, with 16 `row_tiles` rows at most.
+template <int D> static cudaError_t list_go(const Call &a, int row_tiles, int most, cudaStream_t stream)
 {
+    const unsigned grid = (unsigned)((int64_t)most * a.Hk);
+    if (row_tiles == 1)
+        return attn::launch_second(list_kernel<D>, grid, 32, 0, stream, a);
     const size_t smem = sizeof(CachedSmem<D>);
-    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, WR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess)
-        return err;
-    return attn::launch_second(cached_kernel<D, WR, true>, (unsigned)((int64_t)most * a.Hk), kCThreads, smem, stream, a, 1);
+    const cudaError_t err = cudaFuncSetAttribute(cached_kernel<D, 2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return err != cudaSuccess ? err : attn::launch_second(cached_kernel<D, 2, true>, grid, kCThreads, smem, stream, a, 1);
 }
 
-// The pieces of a list of at most `most`, with 16 `row_tiles` rows a CTA.
 cudaError_t launch_cached_list(const Call &a, int d, int row_tiles, int most, cudaStream_t stream)
 {
     if ((int64_t)most * a.Hk > INT32_MAX)
         return cudaErrorInvalidValue;
-    if (d == 64)
-        return row_tiles == 1 ? list_go<64, 1>(a, most, stream) : list_go<64, 2>(a, most, stream);
-    return row_tiles == 1 ? list_go<128, 1>(a, most, stream) : list_go<128, 2>(a, most, stream);
+    return d == 64 ? list_go<64>(a, row_tiles, most, stream) : list_go<128>(a, row_tiles, most, stream);
 }
 
 template <int D> static cudaError_t combine_go(const Call &a, int64_t rows, cudaStream_t stream)

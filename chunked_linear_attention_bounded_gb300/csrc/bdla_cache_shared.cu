@@ -110,7 +110,7 @@ Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
     s.wide = all > kNarrowRows;
     s.own_wide = R > kNarrowRows;
     s.narrow_tiles = (s.wide ? R : all) <= 16 ? 1 : 2;
-    s.slots = s.ctas * (d.d == 128 ? 3 : 4);
+    s.slots = s.ctas * (s.narrow_tiles == 1 ? (d.d == 128 ? 9 : 16) : d.d == 128 ? 3 : 4);
     s.heads_per_slot = (float)d.Hk / (float)s.slots;
     s.extra = 2 * ((s.slots + d.Hk - 1) / d.Hk);
     const int groups = n_groups < d.B / 2 ? n_groups : d.B / 2;

@@ -20,7 +20,7 @@ class Sizes:
         R, every = T * G, T * G * B
         s.wide, s.own_wide = every > NARROW, R > NARROW
         s.mr = 16 * (1 if (R if s.wide else every) <= 16 else 2)
-        s.slots = SMS * (3 if d == 128 else 4)
+        s.slots = SMS * ((9 if d == 128 else 16) if s.mr == 16 else 3 if d == 128 else 4)
         s.extra = 2 * up(s.slots, Hk)
         s.most = 0 if s.own_wide else B + 2 * min(n_groups, B // 2) + s.extra
         s.rows = 0
