@@ -427,7 +427,7 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
 // as its work, and what counts is how many are under way: a warp by itself, with
 // 16 positions a tile and three tiles in flight, instead of four warps and two
 // barriers a tile.  256 sequences of up to 513 positions of their own, 8 key heads
-// of 128: BDLA_T1 us (four warps a piece 65).
+// of 128: 50 us, 5.4 TB/s (four warps a piece 65).
 constexpr int kListKeys = 16, kListStages = 3;
 template <int D>
 __global__ void __launch_bounds__(32)

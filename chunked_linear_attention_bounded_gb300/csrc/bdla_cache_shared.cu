@@ -109,7 +109,7 @@ Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
     const int64_t R = (int64_t)d.T * s.G, all = R * d.B;
     s.wide = all > kNarrowRows;
     s.own_wide = R > kNarrowRows;
-    s.narrow_tiles = (s.wide ? R : all) <= 16 ? 1 : 2;
+    s.narrow_tiles = R <= 16 ? 1 : 2;
     s.slots = s.ctas * (s.narrow_tiles == 1 ? (d.d == 128 ? 9 : 16) : d.d == 128 ? 3 : 4);
     s.heads_per_slot = (float)d.Hk / (float)s.slots;
     s.extra = 2 * ((s.slots + d.Hk - 1) / d.Hk);

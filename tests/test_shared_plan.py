@@ -19,7 +19,7 @@ class Sizes:
         s.B, s.T, s.G, s.Hk, s.n_groups = B, T, G, Hk, n_groups
         R, every = T * G, T * G * B
         s.wide, s.own_wide = every > NARROW, R > NARROW
-        s.mr = 16 * (1 if (R if s.wide else every) <= 16 else 2)
+        s.mr = 16 if R <= 16 else 32
         s.slots = SMS * ((9 if d == 128 else 16) if s.mr == 16 else 3 if d == 128 else 4)
         s.extra = 2 * up(s.slots, Hk)
         s.most = 0 if s.own_wide else B + 2 * min(n_groups, B // 2) + s.extra
