@@ -41,7 +41,8 @@ EXPORTS = ("bdla_workspace_bytes", "bdla_decay", "bdla_fwd", "bdla_fwd_varlen", 
            "bdla_fwd_delta", "bdla_bwd_delta", "bdla_tile_states_bytes",
            "bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
            "bdla_attn_cached", "bdla_workspace_bytes_attn", "bdla_decode_delta",
-           "bdla_qk_norm_append", "bdla_attn_shared")
+           "bdla_qk_norm_append", "bdla_attn_shared",
+           "bdla_set_share_least")
 ATTN_FWD, ATTN_BWD, ATTN_NORM_BWD, ATTN_APPEND, ATTN_CACHED, ATTN_SHARED = 0, 1, 2, 3, 4, 5
 KERNEL_DECAY, KERNEL_FWD, KERNEL_BWD, KERNEL_STATES, KERNEL_SEG = 0, 1, 2, 3, 4
 KERNEL_ATTN_FWD, KERNEL_ATTN_BWD, KERNEL_ATTN_CACHED, KERNEL_ATTN_SHARED = 5, 6, 7, 8
@@ -115,6 +116,8 @@ def lib():
         L.bdla_fwd_noalloc.restype = ci
         L.bdla_set_seq_split.argtypes = [ci]
         L.bdla_set_seq_split.restype = ci
+        L.bdla_set_share_least.argtypes = [ctypes.c_int64]
+        L.bdla_set_share_least.restype = ci
         L.bdla_decode.argtypes = [vp, vp, vp, vp, f32, vp, vp, ci, Dims, ci, vp]
         L.bdla_decode.restype = ci
         L.bdla_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -191,6 +194,12 @@ def set_seq_split(blocks: int):
     global _seq_split
     lib().bdla_set_seq_split(int(blocks))
     _seq_split = int(blocks)
+
+
+def set_share_least(elements: int):
+    """Elements of keys and values that a group of attn_shared has to save from
+    being read again to be taken once: < 0 automatic, 0 always (process-wide)."""
+    lib().bdla_set_share_least(int(elements))
 
 
 def segments_engaged(q_shape, dv: int, n_docs: int = 0) -> bool:

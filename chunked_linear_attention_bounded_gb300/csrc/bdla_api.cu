@@ -12,6 +12,7 @@ namespace bdla {
 KernelEvents g_kernel_events[BDLA_KERNEL_COUNT];
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
 std::atomic<int> g_test_stall[BDLA_KERNEL_COUNT];
+std::atomic<int64_t> g_share_least{-1};
 
 bdla_status check_dims(const bdla_dims &d, bool varlen, int n_docs)
 {
@@ -465,6 +466,12 @@ bdla_status bdla_decode(const void *q, const void *k, const void *v, const float
                             static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v),
                             a, b, mode, state, o, o_dtype == BDLA_F32,
                             reinterpret_cast<cudaStream_t>(stream)));
+    return BDLA_OK;
+}
+
+bdla_status bdla_set_share_least(int64_t elements)
+{
+    g_share_least.store(elements);
     return BDLA_OK;
 }
 

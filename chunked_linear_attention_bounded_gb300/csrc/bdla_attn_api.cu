@@ -149,7 +149,7 @@ size_t bdla_workspace_bytes_attn(int op, bdla_attn_dims d, int n_docs, int64_t m
         if (check_attn_dims(d, false, 0) != BDLA_OK || max_keys < 0 || max_keys > INT32_MAX || d.T < 1 || d.T > 64 ||
             n_docs < 1 || n_docs > 65535 || (int64_t)d.B * d.T * d.Hq > INT32_MAX || !shared_fits(d, n_docs, max_keys))
             return 0;
-        return round_up(kStatusBytes) + shared_bytes(d, n_docs);
+        return round_up(kStatusBytes) + shared_bytes(d, n_docs, max_keys);
     }
     if (check_attn_dims(d, n_docs > 0, n_docs) != BDLA_OK)
         return 0;

@@ -51,7 +51,7 @@ cudaError_t launch_qk_norm_append(const bdla_qk_norm_args &a, const __nv_bfloat1
 int cached_splits(const bdla_attn_dims &d, int64_t max_keys);
 size_t cached_partial_bytes(const bdla_attn_dims &d, int splits);
 // Attention where groups of sequences share pages: bytes of scratch, and whether the sizes fit its 32-bit counts.
-size_t shared_bytes(const bdla_attn_dims &d, int n_groups);
+size_t shared_bytes(const bdla_attn_dims &d, int n_groups, int64_t max_keys);
 bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys);
 cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, const int32_t *cu_groups, const int32_t *shared,
                                int n_groups, const uint64_t *tree, float scale, __nv_bfloat16 *o, float *lse,

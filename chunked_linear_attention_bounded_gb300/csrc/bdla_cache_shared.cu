@@ -20,6 +20,16 @@
 // Everything that the cut depends on (group sizes, shared lengths, lengths) is on
 // the device and changes from step to step under a captured graph, so the grids
 // are sized from the tensors' shapes and the plan fills them.
+//
+// d = 128, 32 heads on 8, one token each: 256 sequences of up to 513 positions of
+// their own behind 32768 shared ones 170 us, of it the wide kernel 109 (tensor
+// cores; 1.44 PFLOP/s a further position, the whole-prompt forward's rate), the
+// narrow one 50 (HBM, 5.4 TB/s), the join 12, the plan 7, partly one over the
+// other; attention of each sequence by itself reads 34 GB, over 5 ms.  16 sequences
+// behind 131072: 116 us, the wide kernel 91 of it (HBM, 5.9 TB/s).  What is left:
+// the plan's chain of latencies, the first tiles and the last sums of each kernel
+// (about 45 us of the 170), and 168 registers a thread, of which 56 to 68 bytes
+// are spilled.
 #include <cudaTypedefs.h>
 
 #include "bdla_attn_sm100.cuh"
@@ -33,10 +43,27 @@ using namespace sm100;
 using namespace attn;
 using namespace cache;
 
-constexpr int kNarrowRows = 32;   // rows a key head up to which warp MMAs take a group
+// Rows a key head up to which warp MMAs take a group, 16 at a time (32 rows: 20 us
+// against 29 on the tensor cores behind 4096 positions, 83 against 71 behind 65536;
+// 16 rows behind 65536: 62 against 70).  Where the batch has twice as many and no
+// table more than kShortTable positions, the wide kernel is not launched at all (64
+// rows: 17 to 18 us against 26 to 33 behind 64 to 512 positions; behind 65536, 131
+// against 71).
+constexpr int kNarrowRows = 32, kShortTable = 4096;
 constexpr int kWideTile = 256;    // rows of a CTA of the wide kernel
-constexpr int kRun = 5;           // what a change of rows costs the wide kernel, in tiles of 128 rows
+// What a change of rows costs the wide kernel, in tiles of 128 rows: its sums out,
+// the next queries in, the first scores (64 sequences of 33 drafts, 484 us; 617
+// with 2, 520 with 5, 512 with 16).
+constexpr int kRun = 10;
 constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
+
+// Elements of keys and values that a group has to save from being read again for
+// its sums to be worth the joining, where the tensor cores take it and where not
+// (64 sequences, 32 heads on 8 of 128: 30.4 us against 29.1 each by itself with 128
+// shared positions, 35.7 against 40.2 with 512; 256 sequences: 62 against 58 with
+// 64, 62 against 76 with 256; 8 sequences, 2048 positions, 4 heads: 16.6 against
+// 18.6).
+constexpr int64_t kLeastWide = 32000000, kLeastNarrow = 2000000;
 
 // What the wide kernel walks: positions first .. end - 1 of sequence b's table
 // for the row blocks rb0 .. rb1 - 1 of the R rows from token tok0 on, times key
@@ -84,6 +111,7 @@ struct Sizes {
     int extra;           // pieces of the narrow list beyond one for every block of rows
     int most;            // pieces of the narrow list
     int64_t rows;        // of partial sums
+    int64_t least_wide, least_narrow;
 };
 
 // Integers that the plan keeps: offsets and shared lengths of the groups,
@@ -92,11 +120,12 @@ constexpr size_t plan_ints(int n_groups, int B) { return 3 * (size_t)n_groups + 
 
 // Bounds of the plan.  Narrow: a piece size of at least the (block-weighted)
 // positions over `extra` cuts at most `extra` pieces beyond the first of each
-// block; sequences have one block, groups of at most 32 rows one or two, and a
-// group that shares has two sequences or more.  Wide: a block's tiles lie in
+// block; sequences have one block, groups of at most 32 rows one or two, those of
+// at most 64 in all no more than four beyond one each, and a group that shares has
+// two sequences or more.  Wide: a block's tiles lie in
 // row_tiles nt / per_cta + 2 CTAs at most; 256 rows for each of that for all of an
 // entry's rows is at most 256 times its line, and the line at most ctas x per_cta.
-Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
+Sizes sizes_of(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
 {
     Sizes s;
     s.B = d.B;
@@ -105,16 +134,19 @@ Sizes sizes_of(const bdla_attn_dims &d, int n_groups)
     s.Hk = d.Hk;
     s.D = d.d;
     s.n_groups = n_groups;
+    const int64_t least = g_share_least.load();
+    s.least_narrow = least < 0 ? kLeastNarrow : least;
     s.ctas = sm_count();
     const int64_t R = (int64_t)d.T * s.G, all = R * d.B;
-    s.wide = all > kNarrowRows;
     s.own_wide = R > kNarrowRows;
+    s.least_wide = least < 0 && !s.own_wide ? kLeastWide : s.least_narrow;
+    s.wide = s.own_wide || all > (max_keys > kShortTable ? kNarrowRows : 2 * kNarrowRows);
     s.narrow_tiles = R <= 16 ? 1 : 2;
     s.slots = s.ctas * (s.narrow_tiles == 1 ? (d.d == 128 ? 9 : 16) : d.d == 128 ? 3 : 4);
     s.heads_per_slot = (float)d.Hk / (float)s.slots;
     s.extra = 2 * ((s.slots + d.Hk - 1) / d.Hk);
     const int groups = n_groups < d.B / 2 ? n_groups : d.B / 2;
-    s.most = s.own_wide ? 0 : d.B + 2 * groups + s.extra;
+    s.most = s.own_wide ? 0 : d.B + 2 * groups + 4 + s.extra;
     s.rows = 0;
     if (s.wide)
         s.rows += 2 * all * d.Hk * (s.own_wide ? 2 : 1) + (int64_t)kWideTile * s.ctas;
@@ -148,7 +180,6 @@ size_t carve(const Sizes &s, char *at, Plan *p)
 // ---------------------------------------------------------------- plan
 constexpr int kPlanThreads = 512;
 constexpr int kPlanEntries = 4000;   // whose offsets, groups and lengths fit into 48 KB of shared memory
-constexpr int kLeastShared = 64;     // shared positions that are worth a piece of their own
 constexpr int kLeastLine = 2 + kRun;   // of a wide CTA
 constexpr int kFew = 4;               // pieces, or CTAs, of an entry that one lane writes
 constexpr int kSizes = 8;            // piece sizes of the narrow kernel that are weighed: 128, 256 .. 16384 positions
@@ -261,10 +292,17 @@ plan_kernel(const __grid_constant__ bdla_cache c, const int32_t *cu_groups, cons
     }
     __syncthreads();
     // one sequence reads nothing twice, and a short prefix is not worth the joining
-    const auto taken = [&](int g) { return g < 0 || bad || cu[g + 1] - cu[g] < 2 || most[g] < kLeastShared ? 0 : most[g]; };
-    const int rows_of = z.T * z.G, mr_log = z.narrow_tiles == 1 ? 4 : 5;
+    const int rows_of = z.T * z.G;
+    const auto taken = [&](int g) {
+        if (g < 0 || bad)
+            return 0;
+        const int n = cu[g + 1] - cu[g];
+        const int64_t saved = (int64_t)(n - 1) * most[g] * z.Hk * z.D * 2;
+        return n < 2 || saved < (z.wide && n * rows_of > kNarrowRows ? z.least_wide : z.least_narrow) ? 0 : most[g];
+    };
+    const int mr_log = z.narrow_tiles == 1 ? 4 : 5;
     const auto rows = [&](int e, int n) { return e >= NG ? rows_of : n > 0 ? (cu[e + 1] - cu[e]) * rows_of : 0; };
-    const auto wide = [&](int e, int R) { return e >= NG ? z.own_wide : R > kNarrowRows; };
+    const auto wide = [&](int e, int R) { return e >= NG ? z.own_wide : z.wide && R > kNarrowRows; };
     // blocks of two row tiles and of one, and their line
     const auto full = [](int R) { return (R + BT - 1) / kWideTile; };
     const auto single = [](int R) { return (R + BT - 1) / BT & 1; };
@@ -1102,16 +1140,16 @@ template <int D> cudaError_t join_go(const Call &a, const Plan &p, const Sizes &
 
 }  // namespace
 
-size_t shared_bytes(const bdla_attn_dims &d, int n_groups)
+size_t shared_bytes(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
 {
     Plan p;
-    return carve(sizes_of(d, n_groups), nullptr, &p);
+    return carve(sizes_of(d, n_groups, max_keys), nullptr, &p);
 }
 
 // The line (with a CTA's worth beyond it) and rows of the partial sums are 32-bit.
 bool shared_fits(const bdla_attn_dims &d, int n_groups, int64_t max_keys)
 {
-    const Sizes z = sizes_of(d, n_groups);
+    const Sizes z = sizes_of(d, n_groups, max_keys);
     const int64_t R = (int64_t)d.T * z.G, groups = z.wide ? R * d.B / kWideTile + (n_groups < d.B / 2 ? n_groups : d.B / 2) : 0;
     const int64_t blocks = (groups + (z.own_wide ? (R + kWideTile - 1) / kWideTile * d.B : 0)) * d.Hk;
     return z.rows <= INT32_MAX && blocks <= INT32_MAX && blocks * (2 * (max_keys / BT + 1) + kRun) <= INT32_MAX / 2;
@@ -1121,7 +1159,7 @@ cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, cons
                                int n_groups, const uint64_t *tree, float scale, __nv_bfloat16 *o, float *lse,
                                const bdla_attn_dims &d, void *scratch, DeviceStatus *st, cudaStream_t stream)
 {
-    const Sizes z = sizes_of(d, n_groups);
+    const Sizes z = sizes_of(d, n_groups, (int64_t)c.max_pages * c.page);
     Plan p;
     carve(z, static_cast<char *>(scratch), &p);
     Call a;

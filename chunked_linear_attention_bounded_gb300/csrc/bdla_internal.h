@@ -87,6 +87,7 @@ inline const char *kernel_range_name(int kernel)
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 extern std::atomic<uint64_t> g_wait_ns;
 extern std::atomic<int> g_test_stall[BDLA_KERNEL_COUNT];
+extern std::atomic<int64_t> g_share_least;   // bdla_set_share_least
 struct WaitCfg {
     uint64_t ns;   // limit of the pipeline waits
     int stall;     // BDLA_STALL_* role that waits on a barrier nothing arrives at

@@ -1,7 +1,7 @@
 /*
  * bdla_tuning.h — process-wide settings of libbdla.so that are not part of
- * the operation itself: the sequence-segment policy, a measurement hook and
- * two test hooks for the bounded waits.  None of them changes a result
+ * the operation itself: the sequence-segment policy, when a shared prefix is
+ * taken once, a measurement hook and two test hooks for the bounded waits.  None of them changes a result
  * beyond floating-point rounding order; the defaults are what a user wants.
  *
  * Each setting is one value held by the library for the whole process and
@@ -38,6 +38,18 @@ extern "C" {
  * the workspace after changing it.  Always BDLA_OK.
  */
 bdla_status bdla_set_seq_split(int blocks);
+
+/*
+ * When bdla_attn_shared takes what a group of sequences shares once for all of
+ * them.  Joining the sums costs some microseconds, so a group has to save that
+ * many elements of keys and values from being read again, or its sequences are
+ * attended to by themselves.
+ *   elements <  0 (default): automatic, by whether the group's rows go to the
+ *                            tensor cores
+ *   elements >= 0: this many (0: whatever is shared)
+ * Always BDLA_OK.
+ */
+bdla_status bdla_set_share_least(int64_t elements);
 
 /*
  * Measurement hook.  Until called again with NULL events, every later call

@@ -42,6 +42,11 @@ def test_refusals(L):
         assert _call(L, **less) == bdla.ERR_WORKSPACE
 
 
+def test_the_threshold_is_a_setting(L):
+    for n in (0, 1 << 40, -1):
+        assert L.bdla_set_share_least(n) == bdla.OK
+
+
 def test_workspace_sizes(L):
     size = lambda dims, n, keys: L.bdla_workspace_bytes_attn(bdla.ATTN_SHARED, bdla.AttnDims(*dims), n, keys)
     d = (256, 1, 32, 8, 128)

@@ -10,6 +10,14 @@ pytestmark = pytest.mark.gpu
 BF16, I32 = torch.bfloat16, torch.int32
 
 
+@pytest.fixture(autouse=True)
+def whatever_is_shared():
+    """Small sizes too: by itself a call joins nothing that costs more than reading it again."""
+    bdla.set_share_least(0)
+    yield
+    bdla.set_share_least(-1)
+
+
 def _batch(groups, loose, own, T, Hq, Hk, d, page, seed=1, tree=False, spare=2, odd=0):
     """groups: (sequences, shared pages) each; then `loose` sequences; own: positions of each sequence behind what it
     shares.  Tables of a group begin with the same pages; what no table names, and what lies past a sequence's new tokens,
@@ -81,6 +89,10 @@ CASES = {  # groups, loose, own, T, Hq, Hk, d, page, tree
     "many blocks": ([(150, 9)], 3, [1, 40, 9], 1, 16, 2, 64, 64, False),
     "groups of all kinds": ([(1, 30), (0, 4), (2, 30), (11, 0), (13, 17), (3, 2), (20, 40)], 5, [0, 9, 200, 33], 1, 12, 4, 64, 16, False),
     "several tokens": ([(6, 20), (5, 7)], 2, [0, 9, 130], 5, 8, 4, 128, 16, False),
+    "rows of 32": ([(3, 20), (1, 4)], 2, [0, 9, 130], 8, 8, 2, 128, 16, True),
+    "rows of 24": ([(3, 20), (5, 14)], 2, [0, 9, 530], 3, 8, 1, 64, 32, False),
+    "64 rows in a short table": ([(16, 200)], 0, [0, 9, 130], 1, 8, 2, 128, 16, False),
+    "64 rows in a long table": ([(16, 300)], 0, [0, 9, 130], 1, 8, 2, 128, 16, False),
     "trees": ([(5, 20), (2, 7)], 2, [0, 9, 130], 17, 8, 4, 64, 48, True),
     "wide trees": ([(3, 20), (4, 7), (1, 5)], 2, [0, 9, 130, 400], 21, 8, 2, 128, 16, True),
     "trees of 64": ([(2, 12)], 1, [0, 190], 64, 8, 1, 64, 100, True),
@@ -89,8 +101,9 @@ CASES = {  # groups, loose, own, T, Hq, Hk, d, page, tree
 
 
 @pytest.mark.parametrize("name", CASES)
-@pytest.mark.parametrize("odd", [0, 7])
-def test_the_definition(name, odd):
+@pytest.mark.parametrize("odd,least", [(0, 0), (7, 0), (0, -1)])
+def test_the_definition(name, odd, least):
+    bdla.set_share_least(least)
     groups, loose, own, T, Hq, Hk, d, page, tree = CASES[name]
     _holds(_batch(groups, loose, own, T, Hq, Hk, d, page, seed=len(name), tree=tree, odd=odd))
 
@@ -214,6 +227,17 @@ def test_a_replayed_graph_follows_lengths_groups_and_tables(T):
         want_o, want_l = ref.cached(x["q"], x["kc"], x["vc"], x["table"], x["lens"].tolist(), None, 128 ** -0.5)
         ref.check("o", o, want_o)
         ref.check("lse", lse, want_l)
+
+
+def test_nothing_to_look_at():
+    """Tables and caches without pages."""
+    q, i32 = torch.randn((3, 1, 4, 64), device="cuda").to(BF16), lambda *v: torch.tensor(v, dtype=I32, device="cuda")
+    kc, none = torch.zeros((0, 16, 2, 64), dtype=BF16, device="cuda"), torch.zeros((3, 0), dtype=I32, device="cuda")
+    for table in (none, torch.zeros((3, 2), dtype=I32, device="cuda")):
+        ws = bdla.Workspace(256, "cuda")
+        o, lse = bdla.attn_shared(q, kc, kc, table, i32(0, 5, 9), i32(0, 3), i32(9), ws=ws)
+        assert ws.read_device_status() == bdla.ERR_DEVICE
+        assert not bool(o.any()) and bool((lse == -float("inf")).all())
 
 
 def _off(got, want):

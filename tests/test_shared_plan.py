@@ -6,8 +6,8 @@ import random
 import pytest
 
 SMS, TILE, WIDE, NARROW = 152, 128, 256, 32
-RUN = 5   # what a change of rows costs, in tiles of 128 rows
-LEAST_SHARED, LEAST_LINE, N_SIZES = 64, 2 + RUN, 8
+RUN = 10   # what a change of rows costs, in tiles of 128 rows
+LEAST_WIDE, LEAST_NARROW, SHORT_TABLE, LEAST_LINE, N_SIZES = 32_000_000, 2_000_000, 4096, 2 + RUN, 8
 
 
 def up(a, b):
@@ -15,14 +15,15 @@ def up(a, b):
 
 
 class Sizes:
-    def __init__(s, B, T, G, Hk, d, n_groups):
-        s.B, s.T, s.G, s.Hk, s.n_groups = B, T, G, Hk, n_groups
+    def __init__(s, B, T, G, Hk, d, n_groups, max_keys):
+        s.B, s.T, s.G, s.Hk, s.d, s.n_groups = B, T, G, Hk, d, n_groups
         R, every = T * G, T * G * B
-        s.wide, s.own_wide = every > NARROW, R > NARROW
+        s.own_wide = R > NARROW
+        s.wide = s.own_wide or every > (NARROW if max_keys > SHORT_TABLE else 2 * NARROW)
         s.mr = 16 if R <= 16 else 32
         s.slots = SMS * ((9 if d == 128 else 16) if s.mr == 16 else 3 if d == 128 else 4)
         s.extra = 2 * up(s.slots, Hk)
-        s.most = 0 if s.own_wide else B + 2 * min(n_groups, B // 2) + s.extra
+        s.most = 0 if s.own_wide else B + 2 * min(n_groups, B // 2) + 4 + s.extra
         s.rows = 0
         if s.wide:
             s.rows += 2 * every * Hk * (2 if s.own_wide else 1) + WIDE * SMS
@@ -30,7 +31,7 @@ class Sizes:
             s.rows += (2 * every + NARROW * s.extra) * Hk
 
 
-def plan(z, cu, shared, lens, cap):
+def plan(z, cu, shared, lens, cap, thrift=1):
     NG, E = z.n_groups, z.n_groups + z.B
     n = [min(max(x, 0), cap) for x in shared]
     bad = any(cu[g] < 0 or cu[g + 1] < cu[g] or cu[g + 1] > z.B for g in range(NG))
@@ -44,7 +45,11 @@ def plan(z, cu, shared, lens, cap):
             group[b] = lo if lo < NG and cu[lo] <= b else -1
         if group[b] >= 0:
             n[group[b]] = min(n[group[b]], max(lens[b], 0))
-    n = [0 if bad or cu[g + 1] - cu[g] < 2 or n[g] < LEAST_SHARED else n[g] for g in range(NG)]
+    for g in range(NG):
+        m = 0 if bad else cu[g + 1] - cu[g]
+        least = LEAST_WIDE if z.wide and not z.own_wide and m * z.T * z.G > NARROW else LEAST_NARROW
+        if m < 2 or (m - 1) * n[g] * z.Hk * z.d * 2 < least * thrift:
+            n[g] = 0
     for b in range(z.B):
         end = 0 if lens[b] < 0 else min(lens[b] + z.T, cap)
         n.append(end - (n[group[b]] if group[b] >= 0 else 0))
@@ -53,7 +58,7 @@ def plan(z, cu, shared, lens, cap):
         R, tok0, wide = z.T * z.G, (e - NG) * z.T, z.own_wide
         if e < NG:
             tok0, R = (cu[e] * z.T, (cu[e + 1] - cu[e]) * z.T * z.G) if n[e] > 0 else (0, 0)
-            wide = R > NARROW
+            wide = z.wide and R > NARROW
         return R, tok0, wide, up(R, z.mr)
 
     entries = [entry(e) for e in range(E)]
@@ -133,9 +138,9 @@ def walk(z, wides, tiles, per_cta, first_entry, cta):
                 rb = wides[e][8]
 
 
-def check(B, T, G, Hk, d, cu, shared, lens, cap):
-    z = Sizes(B, T, G, Hk, d, len(shared))
-    group, parts, wides, work, rows, tiles, per_cta, first_entry = plan(z, cu, shared, lens, cap)
+def check(B, T, G, Hk, d, cu, shared, lens, cap, thrift=0):
+    z = Sizes(B, T, G, Hk, d, len(shared), cap)
+    group, parts, wides, work, rows, tiles, per_cta, first_entry = plan(z, cu, shared, lens, cap, thrift)
     assert rows <= z.rows and len(work) <= z.most and tiles <= SMS * per_cta and all(0 <= c < SMS for c in first_entry)
     # what each piece leaves, by its row of the partial sums: (token, query head) and positions
     left, done = {}, {}
@@ -198,8 +203,10 @@ def test_small_and_odd():
     check(3, 1, 2, 2, 64, [2, 1], [5], [100, 100, 100], 1024)          # malformed: nobody shares
 
 
+# thrift 0: whatever is shared counts, so that small sizes show how it is cut
+@pytest.mark.parametrize("thrift", [0, 1])
 @pytest.mark.parametrize("seed", range(60))
-def test_every_position_once(seed):
+def test_every_position_once(seed, thrift):
     r = random.Random(seed)
     B = r.choice([1, 2, 3, 8, 17, 40])
     T, G, Hk = r.choice([1, 1, 2, 7, 20]), r.choice([1, 2, 4, 8]), r.choice([1, 2, 3, 8])
@@ -210,7 +217,8 @@ def test_every_position_once(seed):
     shared = [r.choice([0, 63, 64, r.randint(0, top), 10 ** 9]) for _ in range(NG)]
     if r.random() < 0.6:   # contexts that are longer than what is shared
         lens = [n + max(min(shared[g], top) for g in range(NG)) for n in lens]
-    check(B, T, G, Hk, r.choice([64, 128]), cu, shared, lens, max(lens) + r.choice([T, T + 77, 1]))
+    check(B, T, G, Hk, r.choice([64, 128]), cu, shared, lens, max(lens) + r.choice([T, T + 77, 1]),
+          thrift)
 
 
 def test_bounds_at_large_sizes():
@@ -218,10 +226,10 @@ def test_bounds_at_large_sizes():
     r = random.Random(1)
     for B, T, G, Hk, NG, top in ((256, 1, 4, 8, 1, 131072), (256, 1, 4, 8, 128, 131072), (256, 1, 1, 1, 100, 1 << 21),
                                  (600, 8, 4, 8, 3, 1 << 17), (5000, 1, 8, 1, 2500, 40000), (64, 64, 8, 8, 9, 1 << 16)):
-        z = Sizes(B, T, G, Hk, 128, NG)
+        z = Sizes(B, T, G, Hk, 128, NG, 1 << 30)
         cu = [B * g // NG for g in range(NG + 1)]
         for kind in range(3):
             shared = [r.randint(top // 2, top) if kind else top for _ in range(NG)]
             lens = [top + (r.randint(0, top) if kind == 2 else 5) for _ in range(B)]
-            _, _, _, work, rows, tiles, per_cta, first = plan(z, cu, shared, lens, 1 << 30)
+            _, _, _, work, rows, tiles, per_cta, first = plan(z, cu, shared, lens, 1 << 30, kind % 2)
             assert rows <= z.rows and len(work) <= z.most and tiles <= SMS * per_cta and all(c < SMS for c in first)
