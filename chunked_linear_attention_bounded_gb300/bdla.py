@@ -667,20 +667,21 @@ def decode_delta(q, k, v, a, beta, state, slots=None, counts=None, b: float = -5
     keep the accepted.  Returns o [B, T, H, dv].  What the device refuses (a slot out of range or named twice, a bad
     count) is recorded in `ws`."""
     _check(q, "q", torch.bfloat16, 4, here=True)
-    _check(v, "v", torch.bfloat16, 4)
-    B, T, H, dk = q.shape
-    dv, device = v.shape[3], q.device
-    rows = (B, T, H)
-    pk, pv = _on(k, "k", torch.bfloat16, q.shape, device), _on(v, "v", torch.bfloat16, (B, T, H, dv), device)
+    shape, device = q.shape, q.device
+    B, T, H, dk = shape
+    dv = v.shape[-1] if isinstance(v, torch.Tensor) and v.dim() == 4 else 0
+    n = state.shape[0] if slots is not None and isinstance(state, torch.Tensor) and state.dim() == 4 else B
+    rows, wide = (B, T, H), (B, T, H, dv)
+    pk, pv = _on(k, "k", torch.bfloat16, shape, device), _on(v, "v", torch.bfloat16, wide, device)
     pa, pb = _on(a, "a", torch.float32, rows, device), _on(beta, "beta", torch.float32, rows, device)
-    _check(state, "state", torch.float32, 4)
-    n = state.shape[0] if slots is not None else B
     ps = _on(state, "state", torch.float32, (n, H, dk, dv), device)
     pi = None if slots is None else _on(slots, "slots", torch.int32, (B,), device)
     pc = None if counts is None else _on(counts, "counts", torch.int32, (B,), device)
     if out is None:
-        out, = _new(device, stream, ((B, T, H, dv), o_dtype))
-    po = _on(out, "out", out.dtype, (B, T, H, dv), device)
+        out, = _new(device, stream, (wide, o_dtype))
+        po = out.data_ptr()
+    else:
+        po = _on(out, "out", out.dtype, wide, device)
     if ws is not None or pi is not None or pc is not None:
         ws = _workspace(256, device, ws, stream)
     st = lib().bdla_decode_delta(q.data_ptr(), pk, pv, pa, pb, b, ps, pi, n, pc, po, _dtype_code(out.dtype),

@@ -746,6 +746,6 @@ bdla_status bdla_set_test_stall(int kernel, int role)
     return BDLA_OK;
 }
 
-int bdla_version(void) { return 300; }
+int bdla_version(void) { return 400; }
 
 }  // extern "C"

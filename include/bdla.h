@@ -307,7 +307,7 @@ bdla_status bdla_bwd_delta(const void *q, const void *k, const void *v, const fl
  *   o        bf16 or fp32 [B, T, H, dv]
  * T >= 1 (the tokens run one after the other: long prompts belong to
  * bdla_fwd_delta).  dk in {64, 128}, dv in {64, 128}; same b / mode rules as
- * bdla_fwd.  A slot below -1 or not in the pool, and one that an earlier
+ * bdla_fwd; tensors 16-byte aligned.  A slot below -1 or not in the pool, and one that an earlier
  * sequence of the batch has named, are recorded as BDLA_ERR_DEVICE and treated
  * as -1; a count outside 0 .. T is recorded and leaves the state as it was.
  * Workspace: 256 bytes, the status word alone; NULL will do where slots and

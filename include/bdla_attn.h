@@ -179,12 +179,13 @@ bdla_status bdla_attn_cached(const void *q, bdla_cache c, const uint64_t *tree, 
  *   cu_groups  device int32 [n_groups + 1], 0 <= cu[0] <= cu[1] .. <= B: group g
  *              is the sequences cu[g] .. cu[g + 1] - 1 (sequences outside all
  *              groups share nothing; groups may be empty)
- *   shared     device int32 [n_groups]: positions that the group's sequences share.
- *              The first shared[g] positions of all of them lie in the same
- *              pages: those positions are taken from the table of the group's
- *              first sequence, and the other tables are not read there.  What
- *              goes beyond the shortest committed context of a group's sequences
- *              (lens) is not counted as shared
+ *   shared     device int32 [n_groups]: positions that the group's sequences share:
+ *              the first shared[g] positions of all of them lie in the same pages,
+ *              and each of their tables names those.  They are read as the table
+ *              of the group's first sequence says, or, where reading them once
+ *              would not pay (bdla_set_share_least), as each sequence's own does.
+ *              What goes beyond the shortest committed context of a group's
+ *              sequences (lens) is not counted as shared
  * n_groups is 1 .. 65535, T 1 .. 64.  Both arrays may change between replays of a
  * captured call, as lens and the tables may.  Malformed cu_groups (then no
  * sequence shares anything) and negative shared[g] are recorded as
