@@ -12,9 +12,10 @@
 //            group shares, tiles for the wide kernel, pieces for the narrow one
 //   wide     groups (and trees of drafts) of more than 32 rows a key head, on
 //            the tensor cores: this file
-//   narrow   everything of up to 32 rows: the kernel of bdla_cache.cu over the
-//            plan's list; a sequence of one piece that shares nothing is
-//            finished there
+//   narrow   everything of up to 32 rows, over the plan's list, by the kernels of
+//            bdla_cache.cu: a warp a piece for sequences of up to 16 rows, four
+//            warps above; a sequence of one piece that shares nothing is finished
+//            there
 //   join     the sums of a row's pieces, in their order
 //
 // Everything that the cut depends on (group sizes, shared lengths, lengths) is on

@@ -17,7 +17,8 @@
 // tokens: bound by fp32 arithmetic (8 paired operations a row, token and four
 // columns; 48 x 33 tokens of 16 heads of 128 x 64: 65 us in two rounds of warps).
 // 128 registers a thread are what 16 warps an SM allow; 96 spill in the token
-// loop (95 us), and 32 rows a lane with 168 registers spill as well (62).
+// loop (95 us), and 32 rows a lane with 168 registers spill as well (62, but 3.1 for
+// one sequence and 10.0 for 37 x 5 tokens, where 16 rows take 7.9).
 #include "bdla_attn_sm100.cuh"
 #include "bdla_cache.cuh"
 
