@@ -152,8 +152,8 @@ def lib():
         L.bdla_qk_norm_append.argtypes = [QkNormArgs, vp, ctypes.c_int64, ctypes.c_int64, CacheArgs, vp, vp, vp, AttnDims, vp,
                                           sz, vp]
         L.bdla_attn_shared.argtypes = [vp, CacheArgs, vp, vp, ci, vp, f32, vp, vp, AttnDims, vp, sz, vp]
-        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_qk_norm_append", "bdla_attn_shared", "bdla_attn_fwd", "bdla_attn_bwd", "bdla_cache_append",
-                     "bdla_attn_cached"):
+        for name in ("bdla_qk_norm", "bdla_qk_norm_bwd", "bdla_qk_norm_append", "bdla_attn_fwd", "bdla_attn_bwd",
+                     "bdla_cache_append", "bdla_attn_cached", "bdla_attn_shared"):
             getattr(L, name).restype = ci
         L.bdla_workspace_bytes_attn.argtypes = [ci, AttnDims, ci, ctypes.c_int64]
         L.bdla_workspace_bytes_attn.restype = sz

@@ -11,8 +11,9 @@
 // Bound by HBM: 65536 packed tokens of 8 sequences, 32 + 8 + 8 heads of 128, in 250
 // us (6.4 TB/s; 304 where a warp's groups took different kinds of heads).  Few
 // tokens are bound by the chain of length, page and first line, and take as few
-// heads a warp as put all warps on the SMs at once: 256 single tokens 4.7 us (9.4
-// with eight heads a warp), one token 4.0 (5.2), 91 x 61 chosen rows 13.0 (15.6).
+// heads a warp as put all warps on the SMs at once: 256 single tokens 4.7 to 5.1 us
+// (9.4 with eight heads a warp), one token 3.9 to 4.5 (5.2), 91 x 61 chosen rows
+// 13.0 (15.6).
 #include "bdla_cache.cuh"
 #include "bdla_norm.cuh"
 
