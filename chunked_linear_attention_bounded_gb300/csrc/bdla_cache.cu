@@ -121,14 +121,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 using attn::ex2;
 
-__device__ __forceinline__ Work past_l1(const Work &w)
-{
-    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&w)), y = __ldcg(reinterpret_cast<const int4 *>(&w) + 1);
-    return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-}
-
 // LIST: the pieces are those of a list on the device, which an earlier kernel of
-// the same call has made (bdla_cache_shared.cu).
+// the same call has made (bdla_cache_shared.cu).  Nothing in memory is looked at
+// before the kernel ahead of this one has ended, queries, tables and masks
+// included: a start ahead of that end orders no reads.
 template <int D, int WR, bool LIST>
 __global__ void __launch_bounds__(kCThreads, D == 128 ? 3 : 4)
 cached_kernel(const __grid_constant__ Call a, int row_blocks)
@@ -149,20 +145,15 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
     int k0, k1, len, R, row0;   // positions, committed ones, rows of the key head and the CTA's first
     int64_t tok0, part;         // the rows' first token, and the partial sums' first row (-1: none)
     attn::next_may_start();
+    if (LIST)
+        attn::wait_for_previous();
     if (LIST) {
-        // The list is there when this kernel may start: the one before waited for it, if it is not the one that made it
-        // (past_l1: nothing of it has been read on this SM by this grid, but by the call before).
-        if (!a.list_ready)
-            attn::wait_for_previous();
         kh = idx % Hk;
         idx /= Hk;
-        const Work w = past_l1(a.list[idx]);   // (there is room for every CTA's, and the counts come along)
-        const int2 n = __ldcg(a.n_list);
-        if (idx >= n.x && idx < n.y) {
-            if (tid == 0)
-                attn::wait_for_previous();
+        const Work w = a.list[idx];   // (there is room for every CTA's, and the counts come along)
+        const int2 n = *a.n_list;
+        if (idx >= n.x && idx < n.y)
             return;
-        }
         b = w.b;
         k0 = w.k0;
         k1 = w.k1;
@@ -417,8 +408,6 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
                 a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
         }
     }
-    if (LIST && a.list_ready && tid == 0)
-        attn::wait_for_previous();   // so that the end of this kernel is the end of that one too
 }
 
 // The pieces of a list with up to 16 rows, a warp each.  The list's sequences have
@@ -438,17 +427,12 @@ list_kernel(const __grid_constant__ Call a)
     const int lane = threadIdx.x, T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
     const bdla_cache &c = a.c;
     attn::next_may_start();
-    // The list is there when this kernel may start: the one before waited for it, if it is not the one that made it
-    // (past_l1: nothing of it has been read on this SM by this grid, but by the call before).
-    if (!a.list_ready)
-        attn::wait_for_previous();
+    attn::wait_for_previous();   // ahead of every read, as above
     const int idx = blockIdx.x / Hk, kh = blockIdx.x - idx * Hk;
-    const Work w = past_l1(a.list[idx]);   // (there is room for every CTA's, and the counts come along)
-    const int2 count = __ldcg(a.n_list);
-    if (idx >= count.x && idx < count.y) {
-        attn::wait_for_previous();
+    const Work w = a.list[idx];   // (there is room for every CTA's, and the counts come along)
+    const int2 count = *a.n_list;
+    if (idx >= count.x && idx < count.y)
         return;
-    }
     const int R = w.R, nt = (w.k1 - w.k0 + kListKeys - 1) / kListKeys;
     const int32_t *table = c.pages + (int64_t)w.b * c.max_pages;
     const bool drafts = w.k1 > w.len;   // the piece holds new tokens
@@ -621,8 +605,6 @@ list_kernel(const __grid_constant__ Call a)
                 a.lse[at] = l == 0.0f ? -INFINITY : fmaf(m, a.scale, logf(l));
         }
     }
-    if (a.list_ready)
-        attn::wait_for_previous();   // so that the end of this kernel is the end of that one too
 }
 
 // Joins the pieces of a row, W warps a row: each sums every W-th piece, and the

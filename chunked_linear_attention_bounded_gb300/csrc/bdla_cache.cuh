@@ -120,7 +120,6 @@ struct Call {
     DeviceStatus *st;
     const Work *list;     // of a planned call: pieces 0 .. n_list->x - 1, and from n_list->y on
     const int2 *n_list;
-    bool list_ready;      // the kernel before did not make it
 };
 
 }  // namespace cache

@@ -6,7 +6,8 @@
 // shared positions of a group are taken once, with the rows of all its sequences
 // (new tokens times query heads of the key head) as one matrix, and each
 // sequence's own positions by themselves.  Four kernels in stream order, each
-// launched ahead of the end of the one before:
+// launched ahead of the end of the one before, for which it waits ahead of its
+// first read:
 //
 //   plan     one CTA reads offsets and lengths and cuts the work: how far each
 //            group shares, tiles for the wide kernel, pieces for the narrow one
@@ -584,6 +585,7 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bdla_cache &c = a.c;
     const int T = a.T, Hq = a.Hq, Hk = a.Hk, G = Hq / Hk;
+    next_may_start();
     if ((smem_u32(smem_raw) & 1023u) != 0u) {
         if (tid == 0)
             set_status(a.st, BDLA_ERR_DEVICE, 0xA11u);
@@ -617,7 +619,6 @@ shared_wide_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     __syncthreads();
     tc_fence_after();
     wait_for_previous();   // the plan is there
-    next_may_start();      // and only then: the narrow kernel does not wait for it itself
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort_flag;
     Walk &walk = sm.walk[warp];
@@ -1182,7 +1183,6 @@ cudaError_t launch_attn_shared(const __nv_bfloat16 *q, const bdla_cache &c, cons
     a.st = st;
     a.list = p.list;
     a.n_list = &p.head->list;
-    a.list_ready = z.wide;
     KernelMark mark_(BDLA_KERNEL_ATTN_SHARED, stream);
     const int entries = n_groups + d.B;
     plan_kernel<<<1, kPlanThreads, entries <= kPlanEntries ? plan_ints(n_groups, d.B) * sizeof(int) : 0, stream>>>(c, cu_groups, shared, z, p, st);
