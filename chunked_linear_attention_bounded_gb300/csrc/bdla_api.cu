@@ -713,8 +713,7 @@ bdla_status bdla_decode_delta(const void *q, const void *k, const void *v, const
     if (d.T < 1 || (slots && n_slots < 0))
         return BDLA_ERR_SHAPE;
     BDLA_TRY(check_decay(b, kChunk, mode));
-    // warps are a grid extent, a quarter of it
-    if ((int64_t)d.B * d.T > INT32_MAX || (int64_t)d.B * d.H * (d.dv / 32) > INT32_MAX)
+    if ((int64_t)d.B * d.T > INT32_MAX || delta_step_ctas(d) > INT32_MAX)   // CTAs are a grid extent
         return BDLA_ERR_TOO_LARGE;
     if (!q || !k || !v || !a || !beta || !o || (!state && !(slots && n_slots == 0)))
         return BDLA_ERR_NULL;

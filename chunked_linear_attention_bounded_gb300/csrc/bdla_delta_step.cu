@@ -238,18 +238,20 @@ delta_step_kernel(const __grid_constant__ StepParams p)
 
 }  // namespace
 
+int64_t delta_step_ctas(const bdla_dims &d)
+{
+    return (int64_t)d.B * d.H * (d.dv / (d.dk == 64 ? Split<64>::kCols : Split<128>::kCols));
+}
+
 cudaError_t launch_delta_step(const bdla_dims &d, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                               const __nv_bfloat16 *v, const float *a, const float *beta, float b, int mode, float *state,
                               const int32_t *slots, int n_slots, const int32_t *counts, void *o, int o_f32,
                               DeviceStatus *st, cudaStream_t stream)
 {
     const StepParams p = {q, k, v, a, beta, b, mode, state, slots, counts, n_slots, o, o_f32, d.B, d.T, d.H, st};
-    const int64_t grid = (int64_t)d.B * d.H * (d.dv / (d.dk == 64 ? Split<64>::kCols : Split<128>::kCols));
-    if (grid > INT32_MAX)
-        return cudaErrorInvalidValue;
     auto *kern = d.dk == 64 ? (d.dv == 64 ? delta_step_kernel<64, 64> : delta_step_kernel<64, 128>)
                             : (d.dv == 64 ? delta_step_kernel<128, 64> : delta_step_kernel<128, 128>);
-    kern<<<(unsigned)grid, 32, 0, stream>>>(p);
+    kern<<<(unsigned)delta_step_ctas(d), 32, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

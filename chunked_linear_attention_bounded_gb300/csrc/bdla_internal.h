@@ -206,7 +206,9 @@ cudaError_t launch_delta_bwd(const Problem &p, const __nv_bfloat16 *q, const __n
                              const __nv_bfloat16 *states, const float *dhT, float *dq, float *dk, float *dv,
                              float *da, float *dbeta, float *dh0, const int32_t *order);
 
-// T recurrent steps of the gated delta rule per sequence, from and to the states that `slots` names.
+// T recurrent steps of the gated delta rule per sequence, from and to the states that `slots` names, by so many CTAs
+// (at most INT32_MAX).
+int64_t delta_step_ctas(const bdla_dims &d);
 cudaError_t launch_delta_step(const bdla_dims &d, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                               const __nv_bfloat16 *v, const float *a, const float *beta, float b, int mode, float *state,
                               const int32_t *slots, int n_slots, const int32_t *counts, void *o, int o_f32,

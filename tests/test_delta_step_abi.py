@@ -43,3 +43,12 @@ def test_refusals(L):
     for less in (dict(ws=None), dict(ws_bytes=255), dict(ws=P + 8)):
         assert _call(L, **less) == bdla.ERR_WORKSPACE
         assert _call(L, slots=None, **less) == _call(L, counts=None, **less) == bdla.ERR_WORKSPACE
+
+
+def test_the_grid_is_a_limit_of_its_own(L):
+    """A CTA takes 16 columns of a state of 128 rows and 32 of one of 64; 65535 x 8192 states of 128 columns lie between
+    the two."""
+    assert _call(L, dims=(65535, 1, 8192, 128, 128)) == bdla.ERR_TOO_LARGE
+    assert _call(L, dims=(65535, 1, 8192, 128, 64), ws=None) == bdla.ERR_WORKSPACE   # the last check before the launch
+    assert _call(L, dims=(65535, 1, 8192, 64, 128), ws=None) == bdla.ERR_WORKSPACE
+    assert _call(L, dims=(65535, 1, 8193, 64, 128)) == bdla.ERR_TOO_LARGE
