@@ -60,12 +60,20 @@ constexpr int kRun = 10;
 constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
 
 // Elements of keys and values that a group has to save from being read again for
-// its sums to be worth the joining, where the tensor cores take it and where not
-// (64 sequences, 32 heads on 8 of 128: 30.4 us against 29.1 each by itself with 128
-// shared positions, 35.7 against 40.2 with 512; 256 sequences: 62 against 58 with
-// 64, 62 against 76 with 256; 8 sequences, 2048 positions, 4 heads: 16.6 against
-// 18.6).
-constexpr int64_t kLeastWide = 32000000, kLeastNarrow = 2000000;
+// its sums to be worth the joining (us with and without it, up to 401 positions of
+// a sequence's own).  Where the tensor cores take the group and run for nothing
+// else, their kernel's set-up has to be earned too: 64 sequences, 32 heads on 8 of
+// 128: 35 against 32 with 17e6 elements (128 shared positions), 36 against 37 with
+// 33e6, 40 against 42 with 66e6; 256 sequences: 72 against 58 with 33e6, 70 against
+// 66 with 67e6, 70 against 71 with 100e6, 75 against 104 with 267e6.  Where warps
+// take the group (8 sequences, 16 heads on 4: 16.4 against 16.7 with 1.8e6, 17.2
+// against 19.2 with 15e6), and where the tensor cores run for the sequences' own
+// positions anyway (more than kNarrowRows rows of one): 8 sequences of 17 tokens 30
+// against 32 with 3.7e6 and 31 against 35 with 29e6, 29 of them 57 against 55 with 7e6
+// and 70 against 82 with 117e6; with many rows and little shared it costs more than
+// it gives (64 of 33 tokens, 151 against 129 with 17e6, 194 against 213 with 264e6),
+// but the larger bound would leave short prompts of few trees unjoined.
+constexpr int64_t kLeastWide = 64000000, kLeastNarrow = 2000000;
 
 // What the wide kernel walks: positions first .. end - 1 of sequence b's table
 // for the row blocks rb0 .. rb1 - 1 of the R rows from token tok0 on, times key

@@ -44,8 +44,9 @@ bdla_status bdla_set_seq_split(int blocks);
  * them.  Joining the sums costs some microseconds, so a group has to save that
  * many elements of keys and values from being read again, or its sequences are
  * attended to by themselves.
- *   elements <  0 (default): automatic, by whether the group's rows go to the
- *                            tensor cores
+ *   elements <  0 (default): automatic: 64 million where the tensor cores take the
+ *                            group and nothing else of the call (sequences of up to
+ *                            32 rows a key head, groups of more), else 2 million
  *   elements >= 0: this many (0: whatever is shared)
  * Always BDLA_OK.
  */
