@@ -2,8 +2,8 @@
 
 A delta-rule layer and a softmax layer of a hybrid stack.  The prompt runs once, whole.  Its state is copied to a slot for
 each sample, and the samples' page tables begin with the prompt's pages; a page that the prompt leaves part empty is copied.
-Then every step is three calls: queries and keys normed, rotated and appended; attention that reads the prompt once for all
-samples; a recurrent step of the delta rule.  A drafted chain is verified by the same calls over several tokens: the states
+Then every step is three calls: queries and keys normed, rotated and appended; attention that reads the prompt's whole pages
+once for all samples (where that saves enough, as here: bdla.set_share_least); a recurrent step of the delta rule.  A drafted chain is verified by the same calls over several tokens: the states
 stay where they are until it is known how many drafts are kept.
 
     python examples/sample_batch.py
@@ -93,7 +93,7 @@ def inputs(n, T, Hq=8, Hk=2, H=4, d=128, seed=1, device="cuda"):
 
 
 def main():
-    n, T = 12, 203
+    n, T = 12, 403
     s = Samples(n, T, room=40)
     outs = [*s.prefill(*inputs(1, T, seed=1))]
     for i in range(3):

@@ -60,3 +60,33 @@ def test_samples_are_what_their_whole_sequences_give(T):
             f = lambda i: whole(i, m, tail)[0].double().cpu().numpy()
             want_d, _ = oracle.fwd_delta(f(1), f(2), f(3), f(4), f(5), -5.0, 0, cu_seqlens=np.array([0, L]))
             assert_close("delta", delta.float().cpu().numpy(), want_d[at:at + count])
+
+
+@pytest.mark.parametrize("T", [203, 32])
+def test_samples_whose_prompt_is_read_once(T):
+    """At these sizes a call joins nothing by itself."""
+    sample_batch.bdla.set_share_least(0)
+    try:
+        test_samples_are_what_their_whole_sequences_give(T)
+    finally:
+        sample_batch.bdla.set_share_least(-1)
+
+
+@pytest.mark.parametrize("n,T,least,once", [(12, 403, -1, True), (6, 203, -1, False), (6, 203, 0, True)])
+def test_whether_a_step_reads_the_prompt_once(n, T, least, once):
+    """What is read once is read as the first sample's table says: without the others' entries the outputs are the same.
+    The first size is the example's own."""
+    outs = []
+    for cut in (False, True):
+        s = sample_batch.Samples(n, T, room=40)
+        s.prefill(*sample_batch.inputs(1, T, seed=41))
+        if cut:
+            s.pages[1:, :s.whole] = -1
+        sample_batch.bdla.set_share_least(least)
+        try:
+            outs.append(s.step(*sample_batch.inputs(n, 1, seed=42)))
+        finally:
+            sample_batch.bdla.set_share_least(-1)
+        assert s.ws.read_device_status() == (sample_batch.bdla.ERR_DEVICE if cut and not once else sample_batch.bdla.OK)
+    assert torch.equal(outs[0][1], outs[1][1]) and torch.equal(outs[0][0][:1], outs[1][0][:1])
+    assert torch.equal(outs[0][0], outs[1][0]) == once
