@@ -247,3 +247,55 @@ def test_arguments_are_refused_by_name(monkeypatch):
     monkeypatch.setattr(bdla, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device is cuda:1"):
         call()
+
+
+def _held(c, kc):
+    """Rows [sequence, position] of the cache as the tables order them."""
+    return kc[c["pages"].long()].flatten(1, 2)
+
+
+@pytest.mark.parametrize("cu,covered", [([1, 8, 9, 20], (1, 20)), ([0, 8, 9, 19], (0, 19)), ([0, 8, 9, 40], (0, 20)),
+                                        ([20, 20, 20, 20], (20, 20)), ([-3, 2, 2, 9], (0, 9))])
+def test_tokens_of_no_sequence_are_not_written(cu, covered):
+    """Offsets in order that leave tokens out, or go past them: what is theirs is written, every other row stays as it was."""
+    lens, T = [3, 0, 30], 20
+    q, k, v, wq, wk, c = _case(1, T, 4, 2, 64, 16, lens, news=[T, T, T], seed=12)
+    qn, kc, vc, status = _append(q, k, v, wq, wk, c, cu_seqlens=torch.tensor(cu, dtype=I32, device="cuda"))
+    assert status == bdla.ERR_DEVICE
+    want_k, want_v = c["kc"].clone(), c["vc"].clone()
+    pos = torch.zeros((1, T), dtype=I32, device="cuda")
+    at = {}
+    for b, n in enumerate(lens):
+        for t in range(max(cu[b], 0), min(cu[b + 1], T)):
+            pos[0, t] = n + t - cu[b]
+            at[t] = (c["pages"][b].long()[int(pos[0, t]) // 16], int(pos[0, t]) % 16)
+    assert sorted(at) == list(range(*covered))
+    all_q, all_k = bdla.qk_norm(q, k, wq, wk, positions=pos)
+    for t, (page, row) in at.items():
+        want_k[page, row], want_v[page, row] = all_k[0, t], v[0, t]
+    assert _same(kc, want_k) and _same(vc, want_v)
+    assert _same(qn[:, slice(*covered)], all_q[:, slice(*covered)]) and bool(qn.isfinite().all())
+
+
+@pytest.mark.parametrize("cu", [[0, 8, 5, 20], [0, 30, 9, 20], [5, 4, 3, 2], [0, -9, 2 ** 31 - 1, 20], [2 ** 31 - 1, -(2 ** 31), 0, 20]])
+def test_offsets_out_of_order_write_nothing_outside(cu):
+    """Whatever they hold: pages that no table names and positions of the contexts stay as they were, and a row that is
+    written is a token's, once."""
+    lens, T = [3, 0, 30], 20
+    q, k, v, wq, wk, c = _case(1, T, 4, 2, 64, 16, lens, news=[T, T, T], seed=13)
+    qn, kc, vc, status = _append(q, k, v, wq, wk, c, cu_seqlens=torch.tensor(cu, dtype=I32, device="cuda"))
+    assert status == bdla.ERR_DEVICE and bool(qn.isfinite().all())
+    named = torch.zeros(kc.shape[0], dtype=torch.bool, device="cuda").index_fill_(0, c["pages"].flatten().long(), True)
+    assert not bool(named.all())
+    tokens = []
+    for new, old in ((kc, c["kc"]), (vc, c["vc"])):
+        assert _same(new[~named], old[~named])
+        held = _held(c, new)
+        wrote = ~held.isnan().all(-1).all(-1)
+        for b, n in enumerate(lens):
+            assert not bool(wrote[b, :n].any())
+        assert not bool(held[wrote].isnan().any()) and int(wrote.sum()) <= T
+        tokens.append((held, wrote))
+    assert torch.equal(tokens[0][1], tokens[1][1])
+    is_token = (tokens[1][0][tokens[1][1]][:, None] == v[0][None]).flatten(2).all(2)   # [written, T]
+    assert bool((is_token.sum(1) == 1).all()) and bool((is_token.sum(0) <= 1).all())
