@@ -245,3 +245,25 @@ def test_arguments_are_refused_by_name():
     with pytest.raises(bdla.BdlaError) as e:
         bdla.decode_delta(*args, b=1.0)
     assert e.value.status == bdla.ERR_RANGE
+
+
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_an_output_of_the_callers_is_filled(o_dtype):
+    t = _tokens(5, 3, 4, 64, 128, seed=21)
+    want = _step(t, t["state"].clone(), o_dtype=o_dtype)
+    pool = torch.cat((t["state"], torch.zeros_like(t["state"][:2])))
+    slots = torch.tensor([3, -1, 0, 1, 4], dtype=torch.int32, device="cuda")
+    src = slots.long()
+    buf = torch.full((7, 3, 4, 128), float("nan"), dtype=o_dtype, device="cuda")
+    state = t["state"].clone()
+    got = _step(t, state, out=buf[1:6])
+    assert got.data_ptr() == buf[1:6].data_ptr() and torch.equal(buf[1:6], want)
+    assert bool(buf[0].isnan().all()) and bool(buf[6].isnan().all())
+    buf.fill_(float("nan"))
+    got = _step(t, pool, slots=slots, out=buf[1:6])
+    t["state"] = t["state"][src.clamp(min=0)]
+    want = _step(t, t["state"], o_dtype=o_dtype)
+    assert not bool(buf[2].any())   # the unused place
+    for b in (0, 2, 3, 4):
+        assert torch.equal(buf[1 + b], want[b]) and torch.equal(pool[src[b]], t["state"][b])
+    assert bool(buf[0].isnan().all()) and bool(buf[6].isnan().all())
