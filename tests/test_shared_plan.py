@@ -233,3 +233,26 @@ def test_bounds_at_large_sizes():
             lens = [top + (r.randint(0, top) if kind == 2 else 5) for _ in range(B)]
             _, _, _, work, rows, tiles, per_cta, first = plan(z, cu, shared, lens, 1 << 30, kind % 2)
             assert rows <= z.rows and len(work) <= z.most and tiles <= SMS * per_cta and all(c < SMS for c in first)
+
+
+def _bytes(z):
+    """The workspace: the status word, then each table of the plan on its own lines of 256 bytes."""
+    entries = z.n_groups + z.B
+    ints = 3 * z.n_groups + 2 * z.B + 1
+    sizes = (24, 2 * entries * 48, entries * 32, z.most * 32, SMS * 4, z.B * 4, ints * 4, z.rows * z.d * 4, z.rows * 8)
+    return 256 + sum(up(n, 256) * 256 for n in sizes)
+
+
+def test_the_library_asks_for_what_is_restated_here():
+    """Rows of partial sums, the list's length and the tables' sizes, by the bytes of workspace that they come to."""
+    from chunked_linear_attention_bounded_gb300 import bdla
+    from chunked_linear_attention_bounded_gb300.build import build
+    build()
+    r = random.Random(7)
+    for _ in range(400):
+        B, T = r.choice([1, 2, 7, 60, 256, 1000]), r.choice([1, 1, 2, 5, 17, 64])
+        G, Hk, d = r.choice([1, 2, 4, 8]), r.choice([1, 2, 4, 8]), r.choice([64, 128])
+        n_groups, keys = r.randint(1, min(2 * B, 300)), r.choice([0, 64, 4096, 4097, 1 << 17])
+        got = bdla.lib().bdla_workspace_bytes_attn(bdla.ATTN_SHARED, bdla.AttnDims(B, T, G * Hk, Hk, d), n_groups, keys)
+        z = Sizes(B, T, G, Hk, d, n_groups, keys)
+        assert got == (_bytes(z) if z.rows < 1 << 31 else 0), (B, T, G, Hk, d, n_groups, keys)
