@@ -978,8 +978,9 @@ def attn_shared(q, kcache, vcache, pages, lens, cu_groups, shared, tree=None, sc
                 ws: Optional[Workspace] = None, stream=None):
     """attn_cached for a batch in which groups of consecutive sequences share the positions that they begin with: group g
     is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [n_groups + 1]), whose tables name the same pages for
-    their first shared[g] positions (int32 [n_groups]).  Those are read once for the whole group.  Returns (o, lse) as
-    attn_cached does, up to rounding."""
+    their first shared[g] positions (int32 [n_groups]).  Those are read once for the whole group where
+    that saves enough (set_share_least); a batch that shares little is attn_cached's.  Returns (o, lse) as attn_cached
+    does, up to rounding."""
     c, pt, dims, o, lse, scale = _newest(q, kcache, vcache, pages, lens, tree, scale, stream)
     n = shared.shape[0] if isinstance(shared, torch.Tensor) and shared.dim() == 1 else 0
     ps = _on(shared, "shared", torch.int32, (n,), q.device)

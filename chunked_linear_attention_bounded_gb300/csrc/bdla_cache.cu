@@ -74,7 +74,9 @@ cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, co
 // buffers each, and a buffer is filled again as soon as its own product is done:
 // 64 KB a CTA, three CTAs an SM.  256 ragged sequences, 676 us (6.3 TB/s; three
 // whole tiles a CTA, two CTAs an SM: 736); one of 262144 positions, with the
-// join, 170 us (6.3 TB/s).  With 32 rows 12 to 16 bytes of registers are spilled.
+// join, 170 us (6.3 TB/s).  With 32 rows of 128 features 24 bytes of
+// registers are spilled (4 in the list's form, none with 64 features): 64 sequences
+// of 8 tokens behind 4096 to 8192 positions, 8 heads of 128, 319 us.
 // Pieces are counted from the table's width, so a table for 262144 positions over
 // sequences of up to 8192 launches CTAs that find nothing to do: 856 us for 688 (both
 // from cold).  A CTA's four warps split the rows first and the
@@ -416,7 +418,9 @@ cached_kernel(const __grid_constant__ Call a, int row_blocks)
 // as its work, and what counts is how many are under way: a warp by itself, with
 // 16 positions a tile and three tiles in flight, instead of four warps and two
 // barriers a tile.  256 sequences of up to 513 positions of their own, 8 key heads
-// of 128: 50 us, 5.4 TB/s (four warps a piece 65).
+// of 128: 51 us, 5.7 TB/s (four warps a piece 65).  The weights are rounded to bf16
+// for their product with the values (an MMA takes both operands in one type), as in
+// the kernel above; their sum is not.
 constexpr int kListKeys = 16, kListStages = 3;
 template <int D>
 __global__ void __launch_bounds__(32)

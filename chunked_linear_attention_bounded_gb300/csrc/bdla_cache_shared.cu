@@ -24,14 +24,22 @@
 // are sized from the tensors' shapes and the plan fills them.
 //
 // d = 128, 32 heads on 8, one token each: 256 sequences of up to 513 positions of
-// their own behind 32768 shared ones 170 us, of it the wide kernel 109 (tensor
+// their own behind 32768 shared ones 174 to 175 us, of it the wide kernel 107 (tensor
 // cores; 1.44 PFLOP/s a further position, the whole-prompt forward's rate), the
-// narrow one 50 (HBM, 5.4 TB/s), the join 12, the plan 7, partly one over the
-// other; attention of each sequence by itself reads 34 GB, over 5 ms.  16 sequences
-// behind 131072: 116 us, the wide kernel 91 of it (HBM, 5.9 TB/s).  What is left:
-// the plan's chain of latencies, the first tiles and the last sums of each kernel
-// (about 45 us of the 170), and 168 registers a thread, of which 56 to 68 bytes
-// are spilled.
+// narrow one 51 (HBM, 5.7 TB/s), the join 12, the plan 7, one after the other but
+// for their set-up; attention of each sequence by itself reads 34 GB, 4.2 ms.  16
+// sequences behind 131072: 119 to 121 us, the wide kernel 91 of it (HBM, 5.9 TB/s).
+// Where the narrow kernel read the plan's list without waiting for the wide one's
+// end, as only the order of launches had it, the two took 170 and 116 us, and 64
+// sequences behind 512 positions 36 for 40.  What is left: the plan's chain of
+// latencies, the first tiles and the last sums of each kernel (about 45 us of the
+// 174), and 168 registers a thread, beside which 48 to 68 bytes are spilled.
+//
+// Rounding: scores, weights, their sums and the sums of pieces are fp32; the
+// weights are rounded to bf16 as they enter their product with the values, in both
+// kernels, because the tensor cores take both operands in one type, and o once more
+// at the end.  The error against 64 bits is then 1.7e-3 to 2.3e-3 of the norm, where
+// weights of fp32 leave o's own 1.5e-3 to 1.7e-3.
 #include <cudaTypedefs.h>
 
 #include "bdla_attn_sm100.cuh"
@@ -46,15 +54,15 @@ using namespace attn;
 using namespace cache;
 
 // Rows a key head up to which warp MMAs take a group, 16 at a time (32 rows: 20 us
-// against 29 on the tensor cores behind 4096 positions, 83 against 71 behind 65536;
-// 16 rows behind 65536: 62 against 70).  Where the batch has twice as many and no
+// against 36 on the tensor cores behind 4096 positions, 82 against 73 behind 65536;
+// 16 rows behind 65536: 61 against 73).  Where the batch has twice as many and no
 // table more than kShortTable positions, the wide kernel is not launched at all (64
-// rows: 17 to 18 us against 26 to 33 behind 64 to 512 positions; behind 65536, 131
-// against 71).
+// rows: 17 to 21 us against 32 to 39 behind 64 to 3500 positions; behind 65536, 131
+// against 75).
 constexpr int kNarrowRows = 32, kShortTable = 4096;
 constexpr int kWideTile = 256;    // rows of a CTA of the wide kernel
 // What a change of rows costs the wide kernel, in tiles of 128 rows: its sums out,
-// the next queries in, the first scores (64 sequences of 33 drafts, 484 us; 617
+// the next queries in, the first scores (64 sequences of 33 drafts, 490 us; 617
 // with 2, 520 with 5, 512 with 16).
 constexpr int kRun = 10;
 constexpr int kSeen = INT32_MAX;  // "committed positions" where no new token is among those seen
@@ -576,7 +584,7 @@ static_assert(sizeof(WideSmem<128>) <= kMaxSmem && sizeof(WideSmem<64>) <= kMaxS
 // run of tiles to the next: tiles, ring stages and barrier phases count on, keys
 // and values of the next run are fetched while the last of this one is worked
 // on, and only the rows (queries in, sums out) change hands.  All CTAs get the
-// same number of tiles.  Where a block has 128 rows or fewer there is no second
+// same length of the line, on which tiles and changes of rows are weighed.  Where a block has 128 rows or fewer there is no second
 // row tile to turn to: both softmax groups then take the same rows and every
 // second tile of positions, and the first reads the output of both out of tensor
 // memory at the run's end.  `run` as there.

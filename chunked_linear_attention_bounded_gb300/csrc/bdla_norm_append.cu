@@ -13,7 +13,9 @@
 // tokens are bound by the chain of length, page and first line, and take as few
 // heads a warp as put all warps on the SMs at once: 256 single tokens 4.7 to 5.1 us
 // (9.4 with eight heads a warp), one token 3.9 to 4.5 (5.2), 91 x 61 chosen rows
-// 13.0 (15.6).
+// 13.0 (15.6).  The 128 registers of two CTAs an SM hold the eight heads in flight,
+// angles and weights but for 24 to 40 bytes, which cost 36 to 220 bytes of reloads a
+// thread and nothing that HBM's rate shows.
 #include "bdla_cache.cuh"
 #include "bdla_norm.cuh"
 
